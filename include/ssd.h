@@ -8,7 +8,10 @@
  * step (ssd_step), the steps just before and after the scan in a Mamba-2
  * mixer (ssd_conv1d_silu, ssd_gated_norm, and both with the scan in one call:
  * ssd_mixer_forward), the deterministic gradient pass
- * (ssd_chunk_scan_bwd), and the pieces of a sequence split into segments
+ * (ssd_chunk_scan_bwd), the products around a mixer (ssd_linear and its
+ * gradient ssd_linear_bwd), a gated linear recurrence per channel
+ * (ssd_gated_scan, its gradient ssd_gated_scan_bwd, and its decode step
+ * ssd_gated_step), and the pieces of a sequence split into segments
  * (ssd_segment_log_decay, ssd_combine_segments); plus workspace queries
  * and status strings.
  *
@@ -53,7 +56,7 @@
 extern "C" {
 #endif
 
-#define SSD_ABI_VERSION 6
+#define SSD_ABI_VERSION 7
 
 /* io dtype of x, dt, B, C and y */
 enum ssd_dtype { SSD_F32 = 0, SSD_BF16 = 1 };
@@ -432,6 +435,155 @@ int32_t ssd_chunk_scan_bwd(const void *x, const void *dt, const float *A, const 
 size_t ssd_chunk_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
                                           int64_t head_dim, int64_t state_dim, int64_t groups,
                                           int64_t chunk, int32_t io_dtype);
+
+/*
+ * ssd_linear -- a matrix product with what follows it in its epilogue, the
+ * projections before and after a mixer (in: x rows -> z | x | B | C | dt or
+ * a recurrence's gates; out: back to the model's width, plus the residual):
+ *
+ *   pre = x W^T + bias
+ *   out = act(pre) + residual
+ *
+ *   x           [rows, in_dim] io dtype
+ *   weight      [out_dim, in_dim] io dtype
+ *   bias        [out_dim] fp32 or NULL (zero)
+ *   residual    [rows, out_dim] io dtype or NULL; may be out
+ *   out         [rows, out_dim] io dtype, written
+ *   pre         [rows, out_dim] io dtype or NULL: also written, for
+ *               ssd_linear_bwd
+ *   activation  enum ssd_activation; GELU is v (1 + erf(v / sqrt 2)) / 2
+ *   workspace   ssd_linear_workspace_bytes(...) bytes, 256-byte aligned
+ *               (NULL where that is 0)
+ *
+ * Alignment: each tensor to the largest power of two up to 16 bytes that
+ * divides one of its rows (so that any run of a tensor's rows qualifies),
+ * bias to 4.  Any row count (one decoded token upwards) and any widths up to
+ * 2^20; operands whose rows are not multiples of 16 bytes are first laid out
+ * again in the workspace.  Matrix-core products with fp32
+ * accumulation in a fixed order (bf16 io: bf16 operands exactly as given;
+ * fp32 io: fp32 operands); bias, activation and residual in fp32; one
+ * rounding to nearest even at each output.  out and pre must not overlap
+ * anything else (out may be the residual).
+ */
+enum ssd_activation {
+    SSD_ACT_NONE = 0, SSD_ACT_SILU = 1, SSD_ACT_GELU = 2, SSD_ACT_SIGMOID = 3
+};
+int32_t ssd_linear(const void *x, const void *weight, const float *bias, const void *residual,
+                   void *out, void *pre, int32_t activation, int64_t rows, int64_t in_dim,
+                   int64_t out_dim, int32_t io_dtype, void *workspace, size_t workspace_bytes,
+                   void *hip_stream);
+
+/* Bytes of workspace ssd_linear needs (a pure function of its arguments; may
+ * be 0; 0 for invalid sizes too). */
+size_t ssd_linear_workspace_bytes(int64_t rows, int64_t in_dim, int64_t out_dim, int32_t io_dtype);
+
+/*
+ * ssd_linear_bwd -- gradients of ssd_linear's out (cotangent dy) with
+ * respect to x, weight and bias, deterministic (the residual's gradient is
+ * dy itself):
+ *
+ *   e = dy act'(pre),  dx = e W,  dweight = e^T x,  dbias = sum over rows of e
+ *
+ *   dy          [rows, out_dim] io dtype
+ *   x, weight   the forward's (x may be NULL without dweight, weight without dx)
+ *   pre         [rows, out_dim] io dtype, the forward's; NULL only for
+ *               SSD_ACT_NONE (not read then)
+ *   dx          [rows, in_dim] io dtype or NULL (not computed)
+ *   dweight     [out_dim, in_dim] io dtype or NULL
+ *   dbias       [out_dim] fp32 or NULL
+ *   workspace   ssd_linear_bwd_workspace_bytes(...) bytes, 256-byte aligned
+ *
+ * Alignment as for ssd_linear.  bf16 io: with an activation, e is rounded
+ * to bf16 as the products' operand (their accumulation is fp32); dbias sums
+ * the fp32 values of e.  rows == 0 writes zeros to dweight and dbias.
+ */
+int32_t ssd_linear_bwd(const void *dy, const void *x, const void *weight, const void *pre,
+                       int32_t activation, void *dx, void *dweight, float *dbias, int64_t rows,
+                       int64_t in_dim, int64_t out_dim, int32_t io_dtype, void *workspace,
+                       size_t workspace_bytes, void *hip_stream);
+
+/* Bytes of workspace ssd_linear_bwd needs (0 for invalid sizes). */
+size_t ssd_linear_bwd_workspace_bytes(int64_t rows, int64_t in_dim, int64_t out_dim,
+                                      int32_t activation, int32_t io_dtype);
+
+/*
+ * ssd_gated_scan -- a gated linear recurrence over a whole sequence, one
+ * state per channel (the per-channel counterpart of ssd_chunk_scan):
+ *
+ *   u_t = scale softplus(lam) sigmoid(r_t),  a_t = exp(-u_t)
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t,   y_t = h_t
+ *
+ *   x            [batch, seqlen, dim] io dtype
+ *   gates        [batch, seqlen, 2 dim] io dtype: r (channels 0 .. dim-1) and
+ *                i (dim .. 2 dim-1), both before their sigmoids (one
+ *                ssd_linear gives both)
+ *   lam          [dim] fp32; scale >= 0, finite
+ *   init_state   [batch, dim] fp32 or NULL (zeros)
+ *   seq_idx      [batch, seqlen] int32 or NULL, as for ssd_chunk_scan_ex: the
+ *                state is zero before a token whose index differs from the
+ *                token's before it; init_state belongs to the first document
+ *   y            [batch, seqlen, dim] io dtype, written
+ *   final_state  [batch, dim] fp32 or NULL, written; may equal init_state
+ *   states       [batch, ceil(seqlen / SSD_GATED_CHUNK), dim] fp32 or NULL:
+ *                entry c is the state after token min(SSD_GATED_CHUNK (c + 1),
+ *                seqlen) - 1, what ssd_gated_scan_bwd can start from
+ *   workspace    ssd_gated_scan_workspace_bytes(...) bytes, 256-byte aligned
+ *
+ * Tensors aligned to their element.  Any dim; 4 (or 2) channels move at once
+ * where dim is a multiple and the tensors are aligned to as many elements.  fp32 arithmetic and states, y rounded to nearest even;
+ * 1 - a^2 is taken without cancellation as a goes to 1.  Deterministic.
+ * seqlen == 0 gives final_state = init_state or zeros.
+ */
+#define SSD_GATED_CHUNK 64
+int32_t ssd_gated_scan(const void *x, const void *gates, const float *lam, float scale,
+                       const float *init_state, const int32_t *seq_idx, void *y,
+                       float *final_state, float *states, int64_t batch, int64_t seqlen,
+                       int64_t dim, int32_t io_dtype, void *workspace, size_t workspace_bytes,
+                       void *hip_stream);
+
+/* Bytes of workspace ssd_gated_scan needs (0 for invalid or empty sizes). */
+size_t ssd_gated_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
+
+/*
+ * ssd_gated_scan_bwd -- gradients of ssd_gated_scan's y (cotangent dy) and
+ * final state (d_final), deterministic:
+ *
+ *   g_t = dy_t + a_{t+1} g_{t+1}   (inside a document; the last token's also
+ *                                   gets d_final)
+ *   dx = g beta s_i,  di = g beta x s_i (1 - s_i),
+ *   p  = g (a^2 (u / beta) s_i x - u a h_{t-1}),  dr = p (1 - s_r),
+ *   dlam = sum p sigmoid(lam) / softplus(lam),  d_init = a_0 g_0
+ *
+ * with s_r, s_i the gates' sigmoids and beta = sqrt(1 - a^2); u / beta goes
+ * to zero with u, so a gate that closes fully has a zero gradient.
+ *
+ *   states    the forward's states output for the same inputs, or NULL (they
+ *             are then computed again)
+ *   dy        [batch, seqlen, dim] io dtype;  d_final [batch, dim] fp32 or NULL
+ *   dx        [batch, seqlen, dim] io dtype;  dgates [batch, seqlen, 2 dim]
+ *             io dtype;  dlam [dim] fp32;  d_init [batch, dim] fp32 or NULL
+ *   workspace ssd_gated_scan_bwd_workspace_bytes(...) bytes, 256-byte aligned
+ *
+ * batch and seqlen >= 1; tensors aligned to their element.
+ */
+int32_t ssd_gated_scan_bwd(const void *x, const void *gates, const float *lam, float scale,
+                           const float *init_state, const int32_t *seq_idx, const float *states,
+                           const void *dy, const float *d_final, void *dx, void *dgates,
+                           float *dlam, float *d_init, int64_t batch, int64_t seqlen, int64_t dim,
+                           int32_t io_dtype, void *workspace, size_t workspace_bytes,
+                           void *hip_stream);
+
+/* Bytes of workspace ssd_gated_scan_bwd needs (0 for invalid sizes). */
+size_t ssd_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim);
+
+/*
+ * ssd_gated_step -- one token of ssd_gated_scan: state [batch, dim] fp32 read
+ * and overwritten, x [batch, dim], gates [batch, 2 dim], y [batch, dim] io
+ * dtype; tensors aligned to their element.
+ */
+int32_t ssd_gated_step(float *state, const void *x, const void *gates, const float *lam,
+                       float scale, void *y, int64_t batch, int64_t dim, int32_t io_dtype,
+                       void *hip_stream);
 
 /*
  * Sequence segments (one per GPU for contexts beyond one GPU).  The state

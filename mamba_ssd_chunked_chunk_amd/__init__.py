@@ -25,6 +25,9 @@ from ._lib import LibraryMissing, load, status_string  # noqa: F401
 __all__ = ["chunk_scan", "chunk_scan_noalloc", "chunk_scan_bwd", "step", "conv1d_silu", "gated_norm",
            "mixer_forward", "mixer_workspace_bytes",
            "segment_log_decay", "combine_segments",
+           "linear", "linear_bwd", "linear_workspace_bytes", "linear_bwd_workspace_bytes",
+           "gated_scan", "gated_scan_bwd", "gated_step", "gated_scan_workspace_bytes",
+           "gated_scan_bwd_workspace_bytes",
            "workspace_bytes", "state_chunks", "abi_version",
            "LibraryMissing", "SsdError"]
 
@@ -480,3 +483,240 @@ def mixer_forward(xbc, dt, A, conv_weight, heads, head_dim, state_dim, groups, z
         return y
     return (y,) + ((fin,) if return_final_state else ()) + \
         ((cfin,) if return_conv_state else ())
+
+
+def _activation(name) -> int:
+    try:
+        return _lib.ACTIVATIONS[name]
+    except KeyError:
+        raise ValueError("activation must be one of %s, got %r"
+                         % (", ".join(sorted(_lib.ACTIVATIONS)), name)) from None
+
+
+def _launch(name, dev, *args) -> None:
+    """Calls the library's `name` on the current stream of `dev` (its last
+    argument), with `dev` the current device, and raises its errors."""
+    cuda = _torch().cuda
+    fn = getattr(load(), name)
+    if dev.index == cuda.current_device():
+        rc = fn(*args, cuda.current_stream(dev).cuda_stream)
+    else:
+        with cuda.device(dev):
+            rc = fn(*args, cuda.current_stream(dev).cuda_stream)
+    if rc != 0:
+        raise SsdError(name, rc)
+
+
+def _scratch(workspace, nbytes, dev):
+    """The caller's workspace, or one of nbytes from torch's allocator."""
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    _check("workspace", workspace, torch.uint8, None, dev)
+    return workspace
+
+
+def linear_workspace_bytes(rows, in_dim, out_dim, io="bf16") -> int:
+    """Workspace bytes of one linear call (ssd_linear_workspace_bytes)."""
+    code = _lib.SSD_BF16 if io == "bf16" else _lib.SSD_F32
+    return int(load().ssd_linear_workspace_bytes(rows, in_dim, out_dim, code))
+
+
+def linear_bwd_workspace_bytes(rows, in_dim, out_dim, activation="none", io="bf16") -> int:
+    """Workspace bytes of one linear_bwd call (ssd_linear_bwd_workspace_bytes)."""
+    code = _lib.SSD_BF16 if io == "bf16" else _lib.SSD_F32
+    return int(load().ssd_linear_bwd_workspace_bytes(rows, in_dim, out_dim,
+                                                     _activation(activation), code))
+
+
+def linear(x, weight, bias=None, activation: str = "none", residual=None,
+           return_pre: bool = False, out=None, pre_out=None, workspace=None):
+    """out = act(x W^T + bias) + residual in one product (ssd_linear).
+
+    x [..., in_dim] and weight [out_dim, in_dim] in the io dtype, bias
+    [out_dim] fp32, residual [..., out_dim] in the io dtype; activation
+    "none", "silu", "gelu" (erf) or "sigmoid".  Returns out [..., out_dim],
+    and with return_pre also the pre-activation in the io dtype, which
+    linear_bwd takes.  `out` may be the residual."""
+    torch = _torch()
+    lib = load()
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("x must be a GPU tensor")
+    io = x.dtype
+    code = _io_code(io)
+    act = _activation(activation)
+    if x.dim() < 1 or weight.dim() != 2:
+        raise ValueError("x must be [..., in_dim] and weight [out_dim, in_dim]")
+    n, k = weight.shape
+    shape = tuple(x.shape[:-1]) + (n,)
+    _check("x", x, io, tuple(x.shape[:-1]) + (k,))
+    _check("weight", weight, io, None, dev)
+    _check("bias", bias, torch.float32, (n,), dev)
+    _check("residual", residual, io, shape, dev)
+    o = torch.empty(shape, dtype=io, device=dev) if out is None else out
+    _check("out", o, io, shape, dev)
+    pre = None
+    if return_pre:
+        pre = torch.empty(shape, dtype=io, device=dev) if pre_out is None else pre_out
+        _check("pre_out", pre, io, shape, dev)
+    m = x.numel() // k if k else 0
+    wsb = int(lib.ssd_linear_workspace_bytes(m, k, n, code))
+    ws = _scratch(workspace, wsb, dev) if wsb or workspace is not None else None
+    _launch("ssd_linear", dev, _ptr(x), _ptr(weight), _ptr(bias), _ptr(residual), _ptr(o),
+            _ptr(pre), act, m, k, n, code, _ptr(ws), 0 if ws is None else ws.numel())
+    return (o, pre) if return_pre else o
+
+
+def linear_bwd(dy, x, weight, pre=None, activation: str = "none", bias: bool = False,
+               workspace=None):
+    """Gradients of linear's out (cotangent dy [..., out_dim]) with respect to
+    x, weight and, with `bias`, the bias (ssd_linear_bwd), deterministic.
+    pre: the pre-activation that linear returned (not needed for "none").
+    Returns a dict: dx, dweight (io dtype), dbias (fp32); the residual's
+    gradient is dy."""
+    torch = _torch()
+    lib = load()
+    dev = dy.device
+    if dev.type != "cuda":
+        raise ValueError("dy must be a GPU tensor")
+    io = dy.dtype
+    code = _io_code(io)
+    act = _activation(activation)
+    if dy.dim() < 1 or weight.dim() != 2:
+        raise ValueError("dy must be [..., out_dim] and weight [out_dim, in_dim]")
+    n, k = weight.shape
+    lead = tuple(dy.shape[:-1])
+    _check("dy", dy, io, lead + (n,))
+    _check("x", x, io, lead + (k,), dev)
+    _check("weight", weight, io, None, dev)
+    if act and pre is None:
+        raise ValueError("pre is needed for the gradient of %s" % activation)
+    _check("pre", pre, io, lead + (n,), dev)
+    res = dict(dx=torch.empty_like(x), dweight=torch.empty_like(weight))
+    if bias:
+        res["dbias"] = torch.empty((n,), dtype=torch.float32, device=dev)
+    m = dy.numel() // n if n else 0
+    ws = _scratch(workspace, int(lib.ssd_linear_bwd_workspace_bytes(m, k, n, act, code)), dev)
+    _launch("ssd_linear_bwd", dev, _ptr(dy), _ptr(x), _ptr(weight), _ptr(pre), act,
+            _ptr(res["dx"]), _ptr(res["dweight"]), _ptr(res.get("dbias")), m, k, n, code,
+            _ptr(ws), ws.numel())
+    return res
+
+
+def gated_scan_workspace_bytes(batch, seqlen, dim) -> int:
+    """Workspace bytes of one gated_scan call (ssd_gated_scan_workspace_bytes)."""
+    return int(load().ssd_gated_scan_workspace_bytes(batch, seqlen, dim))
+
+
+def gated_scan_bwd_workspace_bytes(batch, seqlen, dim) -> int:
+    """Workspace bytes of one gated_scan_bwd call (ssd_gated_scan_bwd_workspace_bytes)."""
+    return int(load().ssd_gated_scan_bwd_workspace_bytes(batch, seqlen, dim))
+
+
+def gated_scan(x, gates, lam, scale: float = 8.0, initial_state=None, seq_idx=None,
+               return_final_state: bool = False, return_states: bool = False, out=None,
+               final_out=None, states_out=None, workspace=None):
+    """The gated linear recurrence over a whole sequence (ssd_gated_scan):
+    h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t per channel, with
+    a_t = exp(-scale softplus(lam) sigmoid(r_t)).
+
+    x [b, l, d] and gates [b, l, 2d] (r | i, before their sigmoids) in the io
+    dtype, lam [d] fp32, initial_state [b, d] fp32, seq_idx [b, l] int32.
+    Returns y [b, l, d], followed by the final state [b, d] and by the states
+    after every 64 tokens [b, ceil(l / 64), d] (fp32, for gated_scan_bwd) when
+    asked for.  final_out may be initial_state."""
+    torch = _torch()
+    lib = load()
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, seqlen, dim]")
+    b, l, d = x.shape
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("x must be a GPU tensor")
+    io = x.dtype
+    code = _io_code(io)
+    _check("x", x, io)
+    _check("gates", gates, io, (b, l, 2 * d), dev)
+    _check("lam", lam, torch.float32, (d,), dev)
+    _check("initial_state", initial_state, torch.float32, (b, d), dev)
+    _check("seq_idx", seq_idx, torch.int32, (b, l), dev)
+    y = torch.empty_like(x) if out is None else out
+    _check("out", y, io, (b, l, d), dev)
+    fin = states = None
+    if return_final_state:
+        fin = torch.empty((b, d), dtype=torch.float32, device=dev) \
+            if final_out is None else final_out
+        _check("final_out", fin, torch.float32, (b, d), dev)
+    if return_states:
+        ns = -(-l // _lib.SSD_GATED_CHUNK)
+        states = torch.empty((b, ns, d), dtype=torch.float32, device=dev) \
+            if states_out is None else states_out
+        _check("states_out", states, torch.float32, (b, ns, d), dev)
+    ws = _scratch(workspace, int(lib.ssd_gated_scan_workspace_bytes(b, l, d)), dev)
+    _launch("ssd_gated_scan", dev, _ptr(x), _ptr(gates), _ptr(lam), float(scale),
+            _ptr(initial_state), _ptr(seq_idx), _ptr(y), _ptr(fin), _ptr(states), b, l, d,
+            code, _ptr(ws), ws.numel())
+    if not return_final_state and not return_states:
+        return y
+    return (y,) + ((fin,) if return_final_state else ()) + ((states,) if return_states else ())
+
+
+def gated_scan_bwd(x, gates, lam, dy, scale: float = 8.0, initial_state=None, d_final=None,
+                   seq_idx=None, states=None, workspace=None):
+    """Gradients of gated_scan's y (cotangent dy) and final state (d_final)
+    with respect to every input (ssd_gated_scan_bwd), deterministic.  states:
+    what gated_scan returned for these inputs (None: computed again).
+    Returns a dict: dx, dgates (io dtype), dlam, and d_init (fp32) if
+    initial_state was given."""
+    torch = _torch()
+    lib = load()
+    if x.dim() != 3:
+        raise ValueError("x must be [batch, seqlen, dim]")
+    b, l, d = x.shape
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("x must be a GPU tensor")
+    io = x.dtype
+    code = _io_code(io)
+    _check("x", x, io)
+    _check("gates", gates, io, (b, l, 2 * d), dev)
+    _check("lam", lam, torch.float32, (d,), dev)
+    _check("dy", dy, io, (b, l, d), dev)
+    _check("initial_state", initial_state, torch.float32, (b, d), dev)
+    _check("d_final", d_final, torch.float32, (b, d), dev)
+    _check("seq_idx", seq_idx, torch.int32, (b, l), dev)
+    _check("states", states, torch.float32, (b, -(-l // _lib.SSD_GATED_CHUNK), d), dev)
+    res = dict(dx=torch.empty_like(x), dgates=torch.empty_like(gates), dlam=torch.empty_like(lam))
+    if initial_state is not None:
+        res["d_init"] = torch.empty_like(initial_state)
+    ws = _scratch(workspace, int(lib.ssd_gated_scan_bwd_workspace_bytes(b, l, d)), dev)
+    _launch("ssd_gated_scan_bwd", dev, _ptr(x), _ptr(gates), _ptr(lam), float(scale),
+            _ptr(initial_state), _ptr(seq_idx), _ptr(states), _ptr(dy), _ptr(d_final),
+            _ptr(res["dx"]), _ptr(res["dgates"]), _ptr(res["dlam"]),
+            _ptr(res.get("d_init")), b, l, d, code, _ptr(ws), ws.numel())
+    return res
+
+
+def gated_step(state, x, gates, lam, scale: float = 8.0, out=None):
+    """One token of gated_scan (ssd_gated_step): updates `state` [b, d] (fp32)
+    in place, returns y [b, d].  x [b, d], gates [b, 2d] in the io dtype."""
+    torch = _torch()
+    lib = load()
+    if x.dim() != 2:
+        raise ValueError("x must be [batch, dim]")
+    b, d = x.shape
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("x must be a GPU tensor")
+    io = x.dtype
+    code = _io_code(io)
+    _check("state", state, torch.float32, (b, d), dev)
+    _check("x", x, io)
+    _check("gates", gates, io, (b, 2 * d), dev)
+    _check("lam", lam, torch.float32, (d,), dev)
+    y = torch.empty_like(x) if out is None else out
+    _check("out", y, io, (b, d), dev)
+    _launch("ssd_gated_step", dev, _ptr(state), _ptr(x), _ptr(gates), _ptr(lam), float(scale),
+            _ptr(y), b, d, code)
+    return y

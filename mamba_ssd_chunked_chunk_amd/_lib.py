@@ -29,7 +29,17 @@ EXPORTS = ("ssd_chunk_scan", "ssd_chunk_scan_ex", "ssd_chunk_scan_noalloc",
            "ssd_conv1d_silu", "ssd_gated_norm", "ssd_mixer_forward",
            "ssd_mixer_workspace_bytes", "ssd_chunk_scan_bwd",
            "ssd_segment_log_decay", "ssd_combine_segments",
-           "ssd_chunk_scan_bwd_workspace_bytes", "ssd_status_string", "ssd_abi_version")
+           "ssd_chunk_scan_bwd_workspace_bytes",
+           "ssd_linear", "ssd_linear_workspace_bytes", "ssd_linear_bwd",
+           "ssd_linear_bwd_workspace_bytes", "ssd_gated_scan",
+           "ssd_gated_scan_workspace_bytes", "ssd_gated_scan_bwd",
+           "ssd_gated_scan_bwd_workspace_bytes", "ssd_gated_step",
+           "ssd_status_string", "ssd_abi_version")
+
+# ssd_linear's activations by name
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "sigmoid": 3}
+# tokens between the states that ssd_gated_scan keeps for its gradient
+SSD_GATED_CHUNK = 64
 
 _lib = None
 
@@ -89,6 +99,26 @@ def load() -> ctypes.CDLL:
     lib.ssd_segment_log_decay.argtypes = [P, P, P, I32, F, F, P, P, I64, I64, I64, I32, P]
     lib.ssd_combine_segments.restype = I32
     lib.ssd_combine_segments.argtypes = [P, P, P, P, P, P, I64, I64, I64, I64, I64, P]
+    Z = ctypes.c_size_t
+    lib.ssd_linear.restype = I32
+    lib.ssd_linear.argtypes = [P, P, P, P, P, P, I32, I64, I64, I64, I32, P, Z, P]
+    lib.ssd_linear_workspace_bytes.restype = Z
+    lib.ssd_linear_workspace_bytes.argtypes = [I64, I64, I64, I32]
+    lib.ssd_linear_bwd.restype = I32
+    lib.ssd_linear_bwd.argtypes = [P, P, P, P, I32, P, P, P, I64, I64, I64, I32, P, Z, P]
+    lib.ssd_linear_bwd_workspace_bytes.restype = Z
+    lib.ssd_linear_bwd_workspace_bytes.argtypes = [I64, I64, I64, I32, I32]
+    lib.ssd_gated_scan.restype = I32
+    lib.ssd_gated_scan.argtypes = [P, P, P, F, P, P, P, P, P, I64, I64, I64, I32, P, Z, P]
+    lib.ssd_gated_scan_workspace_bytes.restype = Z
+    lib.ssd_gated_scan_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.ssd_gated_scan_bwd.restype = I32
+    lib.ssd_gated_scan_bwd.argtypes = [P, P, P, F, P, P, P, P, P, P, P, P, P, I64, I64, I64, I32,
+                                       P, Z, P]
+    lib.ssd_gated_scan_bwd_workspace_bytes.restype = Z
+    lib.ssd_gated_scan_bwd_workspace_bytes.argtypes = [I64, I64, I64]
+    lib.ssd_gated_step.restype = I32
+    lib.ssd_gated_step.argtypes = [P, P, P, P, F, P, I64, I64, I32, P]
     lib.ssd_status_string.restype = ctypes.c_char_p
     lib.ssd_status_string.argtypes = [I32]
     lib.ssd_abi_version.restype = I32
