@@ -6,8 +6,8 @@
 // with r_t = gates[.., c] and i_t = gates[.., d + c] raw (before their
 // sigmoids), its gradient, and one decode step of it.
 //
-// A tile is T = kSeg * NW tokens of 64 * V channels: a lane owns V channels,
-// a wave a run of kSeg consecutive tokens, so every load of a wave is one
+// A tile is 64 tokens of 64 * V channels: a lane owns V channels, a wave a run
+// of SEG consecutive tokens, so every load of a wave is one
 // contiguous piece of a token's row.  A run is the map h -> A h + S of the
 // state entering it (A = prod a_t, S its result from zero); runs compose in
 // order: waves through LDS inside a tile, tiles through the workspace.
@@ -22,10 +22,8 @@ namespace ssd {
 
 namespace {
 
-constexpr int kSeg = 8;    // tokens per wave
-constexpr int kGW = 8;     // waves per workgroup
-constexpr int kGT = kSeg * kGW;  // tokens per tile
-static_assert(kGT % SSD_GATED_CHUNK == 0 && SSD_GATED_CHUNK % kSeg == 0, "tile and state spacing");
+constexpr int kGT = 64;  // tokens per tile, SEG to a wave
+static_assert(kGT == SSD_GATED_CHUNK, "a tile ends where a state is kept");
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <typename IO, int V> struct alignas(sizeof(IO) * V) VecIO { IO e[V]; };
@@ -52,6 +50,28 @@ __device__ __forceinline__ void decay(float u2, float &a, float &beta) {
     beta = __builtin_amdgcn_sqrtf(t < 0.25f ? s : 1.f - a * a);
 }
 
+// How the tiles of one column (64 V channels of one sequence) hand states
+// along in one pass.  A tile publishes its own map as soon as its rows are
+// read; a tile then needs the maps of the earlier tiles of its group of
+// kGroup and the state after the group before, which the last tile of that
+// group publishes.  So a state crosses kGroup tiles per hand-over, and each
+// sum has one order whatever runs first.  Tiles are numbered as their
+// workgroups start (a ticket per column): every tile waits only for lower
+// tickets of its own column, which are running and wait for lower ones in
+// turn, so every wait ends.  The words are written and read at agent scope
+// (the XCDs' L2 caches are not coherent inside a kernel), a flag after its
+// data has reached memory.
+constexpr int kGroup = 16;
+constexpr int kTicketWords = 32;  // a 128-byte line per column's ticket
+
+struct Chain {
+    uint32_t *ticket;   // [cols][kTicketWords]
+    uint32_t *flag;     // [cols][tiles]   the tile's map is there
+    uint32_t *gflag;    // [cols][groups]  the state after the group is there
+    uint64_t *map;      // [cols][tiles][64 V]  (A, S) of a channel
+    uint32_t *after;    // [cols][groups][64 V] the state after the group
+};
+
 struct GArgs {
     const void *x, *gates;
     const float *lam;
@@ -61,28 +81,44 @@ struct GArgs {
     const float *kept;    // backward: states after every SSD_GATED_CHUNK tokens
     const void *dy;       // backward
     const float *dfin;    // backward
-    void *y;              // forward output, or dx
+    void *y;              // forward output (NULL: states only), or dx
     void *dgates;
     float *fin;           // final state, or d_init
     float *states;        // forward output: states after every SSD_GATED_CHUNK tokens
     float *part;          // backward: per tile sums behind dlam [b, tiles, d]
-    float *A, *S, *R;     // workspace: per tile maps [b, tiles, d]
-    int64_t b, l, d, tiles;
+    Chain ch;
+    int64_t b, l, d, tiles, ncol;
 };
 
+__device__ __forceinline__ uint32_t get32(const uint32_t *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void put32(uint32_t *p, uint32_t v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Waits until *p is set.  The bound (many seconds) only turns a broken
+// promise of the scheduler into NaN results instead of a hang.
+__device__ __forceinline__ bool wait_flag(const uint32_t *p) {
+    for (uint32_t n = 0; n < (1u << 25); ++n) {
+        if (get32(p)) return true;
+        __builtin_amdgcn_s_sleep(1);
+    }
+    return false;
+}
+
 // What one tile's loads need: this lane's channels and its rows.
-template <typename IO, int V> struct Tile {
+template <typename IO, int V, int SEG> struct Tile {
     int64_t c;       // first channel of this lane (clamped to a valid one)
     bool live;       // the lane's channels exist
     int64_t row0;    // the sequence's first row in [b * l]
     int64_t t0;      // the wave's first token
-    __device__ Tile(const GArgs &g, int64_t bi, int64_t tile) {
+    __device__ Tile(const GArgs &g, int64_t col, int64_t tile) {
         const int lane = threadIdx.x & 63;
-        c = ((int64_t)blockIdx.x * 64 + lane) * V;
+        c = (col % g.ncol * 64 + lane) * V;
         live = c < g.d;
         if (!live) c = 0;
-        row0 = bi * g.l;
-        t0 = tile * kGT + wave_id() * kSeg;
+        row0 = col / g.ncol * g.l;
+        t0 = tile * kGT + wave_id() * SEG;
     }
 };
 
@@ -96,11 +132,11 @@ __device__ __forceinline__ void stv(void *p, int64_t at, const VecIO<IO, V> &v) 
 }
 
 // The wave's rows of x, r and i (rows past the end read the last row).
-template <typename IO, int V> struct Rows {
-    VecIO<IO, V> x[kSeg], r[kSeg], i[kSeg];
-    __device__ void load(const GArgs &g, const Tile<IO, V> &w) {
+template <typename IO, int V, int SEG> struct Rows {
+    VecIO<IO, V> x[SEG], r[SEG], i[SEG];
+    __device__ void load(const GArgs &g, const Tile<IO, V, SEG> &w) {
 #pragma unroll
-        for (int k = 0; k < kSeg; ++k) {
+        for (int k = 0; k < SEG; ++k) {
             int64_t t = w.t0 + k;
             if (t >= g.l) t = g.l - 1;
             const int64_t at = (w.row0 + t) * g.d + w.c;
@@ -119,12 +155,12 @@ __device__ __forceinline__ bool same_document(const GArgs &g, int64_t row0, int6
 }
 
 // Decay and added value of the wave's tokens; identity past the end.
-template <typename IO, int V>
-__device__ __forceinline__ void terms(const GArgs &g, const Tile<IO, V> &w, const Rows<IO, V> &rw,
-                                      const float (&m2)[V], float (&a)[kSeg][V],
-                                      float (&v)[kSeg][V]) {
+template <typename IO, int V, int SEG>
+__device__ __forceinline__ void terms(const GArgs &g, const Tile<IO, V, SEG> &w, const Rows<IO, V, SEG> &rw,
+                                      const float (&m2)[V], float (&a)[SEG][V],
+                                      float (&v)[SEG][V]) {
 #pragma unroll
-    for (int k = 0; k < kSeg; ++k) {
+    for (int k = 0; k < SEG; ++k) {
         const int64_t t = w.t0 + k;
         const bool in = t < g.l, same = same_document(g, w.row0, t);
 #pragma unroll
@@ -138,147 +174,172 @@ __device__ __forceinline__ void terms(const GArgs &g, const Tile<IO, V> &w, cons
     }
 }
 
-template <typename IO, int V>
-__device__ __forceinline__ void rates(const GArgs &g, const Tile<IO, V> &w, float (&m2)[V]) {
+template <typename IO, int V, int SEG>
+__device__ __forceinline__ void rates(const GArgs &g, const Tile<IO, V, SEG> &w, float (&m2)[V]) {
 #pragma unroll
     for (int e = 0; e < V; ++e) m2[e] = g.scale * softplus_f(g.lam[w.c + e]) * kLog2e;
 }
 
-// ------------------------------------------------------------- forward ----
-// Every tile's map (A, S), and for the backward pass the adjoint's R.
-template <typename IO, int V, bool FWD, bool ADJ>
-__global__ __launch_bounds__(kGW * 64, 2) void k_gated_map(GArgs g) {
-    __shared__ VecF<V> sA[kGW][64], sS[kGW][64], sR[kGW][64];
+// This workgroup's tile of its column, in the order of the chain.
+__device__ __forceinline__ int64_t take_ticket(const GArgs &g, int64_t col, uint32_t *slot) {
+    if (threadIdx.x == 0)
+        *slot = __hip_atomic_fetch_add(g.ch.ticket + col * kTicketWords, 1u, __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*slot);
+}
+
+template <int V, int NW> struct Lds {
+    VecF<V> A[NW][64], S[NW][64];             // the waves' maps
+    VecF<V> pA[kGroup][64], pS[kGroup][64];     // the maps of the group's earlier tiles
+    VecF<V> before[64];                         // the state after the group before
+    uint32_t slot;
+};
+
+// Composes the tile's waves (in chain order: BACK takes them from the last),
+// publishes, gathers what is before the tile and leaves the state entering it
+// in h.  `first`: the state entering the chain, at the lane's channels (NULL:
+// zero); the tiles that take it have read it before they publish anything, so
+// the chain's end may overwrite it.  Every wave of the workgroup
+// calls it; the waves' maps are in lds.A, lds.S already.
+template <int V, int NW, bool BACK>
+__device__ __forceinline__ void enter_tile(const GArgs &g, Lds<V, NW> &lds, int64_t col, int64_t j,
+                                           const float *first, float (&h)[V]) {
     const int lane = threadIdx.x & 63, wv = wave_id();
-    const int64_t tile = blockIdx.y, bi = blockIdx.z;
-    const Tile<IO, V> w(g, bi, tile);
-    float m2[V];
-    rates(g, w, m2);
-    Rows<IO, V> rw;
-    rw.load(g, w);
-    float a[kSeg][V], v[kSeg][V];
-    terms(g, w, rw, m2, a, v);
-    VecF<V> A, S, R;
+    const int64_t grp = j / kGroup, groups = (g.tiles + kGroup - 1) / kGroup;
+    const int in = (int)(j % kGroup);
+    const bool last = in == kGroup - 1 && j + 1 < g.tiles;
+    constexpr int W = 64 * V;
+    if (wv == NW - 1 && grp == 0) {
+        VecF<V> p;
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        float p = 1.f, s = 0.f;
-#pragma unroll
-        for (int k = 0; k < kSeg; ++k) {
-            p *= a[k][e];
-            s = a[k][e] * s + v[k][e];
-        }
-        A.e[e] = p;
-        S.e[e] = s;
+        for (int e = 0; e < V; ++e) p.e[e] = first ? first[e] : 0.f;
+        lds.before[lane] = p;
     }
-    if constexpr (ADJ) {
+    __syncthreads();
+    VecF<V> tA, tS;
+    if (wv == 0 && j + 1 < g.tiles) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) R.e[e] = 0.f;
+        for (int e = 0; e < V; ++e) tA.e[e] = 1.f, tS.e[e] = 0.f;
 #pragma unroll
-        for (int k = kSeg - 1; k >= 0; --k) {
-            const int64_t t = w.t0 + k;
-            const VecIO<IO, V> dy = ldv<IO, V>(
-                g.dy, (w.row0 + (t < g.l ? t : g.l - 1)) * g.d + w.c);
+        for (int k = 0; k < NW; ++k) {
+            const VecF<V> A = lds.A[BACK ? NW - 1 - k : k][lane];
+            const VecF<V> S = lds.S[BACK ? NW - 1 - k : k][lane];
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                tA.e[e] *= A.e[e];
+                tS.e[e] = A.e[e] * tS.e[e] + S.e[e];
+            }
+        }
+        if (!last) {
+            uint64_t *m = g.ch.map + (col * g.tiles + j) * W + lane * V;
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                if (t < g.l) R.e[e] = a[k][e] * (to_f32(dy.e[e]) + R.e[e]);
+                __hip_atomic_store(m + e,
+                                   ((uint64_t)__builtin_bit_cast(uint32_t, tS.e[e]) << 32) |
+                                       __builtin_bit_cast(uint32_t, tA.e[e]),
+                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            vm_wait<0>();
+            if (lane == 0) put32(g.ch.flag + col * g.tiles + j, 1);
         }
-        sR[wv][lane] = R;
     }
-    sA[wv][lane] = A;
-    sS[wv][lane] = S;
+    // the earlier tiles of the group, a wave each; the group before by the last wave
+#pragma unroll
+    for (int k0 = 0; k0 < kGroup; k0 += NW) {
+        const int k = k0 + wv;
+        if (k >= in) continue;
+        const int64_t t = grp * kGroup + k;
+        const bool ok = wait_flag(g.ch.flag + col * g.tiles + t);
+        const uint64_t *m = g.ch.map + (col * g.tiles + t) * W + lane * V;
+        VecF<V> A, S;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const uint64_t w = __hip_atomic_load(m + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            A.e[e] = ok ? __builtin_bit_cast(float, (uint32_t)w) : NAN;
+            S.e[e] = __builtin_bit_cast(float, (uint32_t)(w >> 32));
+        }
+        lds.pA[k][lane] = A;
+        lds.pS[k][lane] = S;
+    }
+    if (wv == NW - 1 && grp > 0) {
+        const bool ok = wait_flag(g.ch.gflag + col * groups + grp - 1);
+        const uint32_t *m = g.ch.after + (col * groups + grp - 1) * W + lane * V;
+        VecF<V> p;
+#pragma unroll
+        for (int e = 0; e < V; ++e) p.e[e] = ok ? __builtin_bit_cast(float, get32(m + e)) : NAN;
+        lds.before[lane] = p;
+    }
     __syncthreads();
-    if (wv != 0 || !w.live) return;
-    VecF<V> tA, tS, tR;
+    const VecF<V> p = lds.before[lane];
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-        float p = 1.f, s = 0.f, q = 0.f;
+    for (int e = 0; e < V; ++e) h[e] = p.e[e];
+    for (int k = 0; k < in; ++k) {
+        const VecF<V> A = lds.pA[k][lane], S = lds.pS[k][lane];
 #pragma unroll
-        for (int j = 0; j < kGW; ++j) {
-            p *= sA[j][lane].e[e];
-            s = sA[j][lane].e[e] * s + sS[j][lane].e[e];
-        }
-        if constexpr (ADJ) {
-#pragma unroll
-            for (int j = kGW - 1; j >= 0; --j) q = sA[j][lane].e[e] * q + sR[j][lane].e[e];
-        }
-        tA.e[e] = p;
-        tS.e[e] = s;
-        tR.e[e] = q;
+        for (int e = 0; e < V; ++e) h[e] = A.e[e] * h[e] + S.e[e];
     }
-    const int64_t at = (bi * g.tiles + tile) * g.d + w.c;
-    *reinterpret_cast<VecF<V> *>(g.A + at) = tA;
-    if constexpr (FWD) *reinterpret_cast<VecF<V> *>(g.S + at) = tS;
-    if constexpr (ADJ) *reinterpret_cast<VecF<V> *>(g.R + at) = tR;
+    if (wv == 0 && last) {
+        uint32_t *m = g.ch.after + (col * groups + grp) * W + lane * V;
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+            put32(m + e, __builtin_bit_cast(uint32_t, tA.e[e] * h[e] + tS.e[e]));
+        vm_wait<0>();
+        if (lane == 0) put32(g.ch.gflag + col * groups + grp, 1);
+    }
+    // the waves before this one
+#pragma unroll
+    for (int k = 0; k < NW - 1; ++k) {
+        const int w = BACK ? NW - 1 - k : k;
+        if (BACK ? w > wv : w < wv) {
+            const VecF<V> A = lds.A[w][lane], S = lds.S[w][lane];
+#pragma unroll
+            for (int e = 0; e < V; ++e) h[e] = A.e[e] * h[e] + S.e[e];
+        }
+    }
 }
 
-// Turns every tile's S into the state entering it and (backward) every
-// tile's R into the adjoint carry entering it from its right.
-template <bool FWD, bool ADJ>
-__global__ __launch_bounds__(256) void k_gated_chain(GArgs g) {
+// Clears the tickets and flags.
+__global__ __launch_bounds__(256) void k_gated_clear(uint32_t *p, int64_t n) {
     const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k >= g.b * g.d) return;
-    const int64_t bi = k / g.d, c = k % g.d, base = bi * g.tiles * g.d + c;
-    if constexpr (FWD) {
-        float h = g.init ? g.init[k] : 0.f;
-        for (int64_t j = 0; j < g.tiles; ++j) {
-            const float A = g.A[base + j * g.d], S = g.S[base + j * g.d];
-            g.S[base + j * g.d] = h;
-            h = A * h + S;
-        }
-    }
-    if constexpr (ADJ) {
-        float q = g.dfin ? g.dfin[k] : 0.f;
-        for (int64_t j = g.tiles - 1; j >= 0; --j) {
-            const float A = g.A[base + j * g.d], R = g.R[base + j * g.d];
-            g.R[base + j * g.d] = q;
-            q = A * q + R;
-        }
-    }
+    if (k < n) p[k] = 0;
 }
 
-// The states of a tile's tokens from the state entering it.
-template <typename IO, int V>
-__global__ __launch_bounds__(kGW * 64, 2) void k_gated_out(GArgs g) {
-    __shared__ VecF<V> sA[kGW][64], sS[kGW][64];
+// ------------------------------------------------------------- forward ----
+template <typename IO, int V, int SEG>
+__global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_fwd(GArgs g) {
+    constexpr int NW = kGT / SEG;
+    __shared__ Lds<V, NW> lds;
     const int lane = threadIdx.x & 63, wv = wave_id();
-    const int64_t tile = blockIdx.y, bi = blockIdx.z;
-    const Tile<IO, V> w(g, bi, tile);
+    const int64_t cols = g.b * g.ncol, col = blockIdx.x % cols;
+    const int64_t tile = g.tiles > 1 ? take_ticket(g, col, &lds.slot) : 0;
+    const Tile<IO, V, SEG> w(g, col, tile);
+    const int64_t bi = col / g.ncol;
     float m2[V];
     rates(g, w, m2);
-    Rows<IO, V> rw;
+    Rows<IO, V, SEG> rw;
     rw.load(g, w);
-    float h[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-        h[e] = g.tiles > 1 ? g.S[(bi * g.tiles + tile) * g.d + w.c + e]
-                           : (g.init ? g.init[bi * g.d + w.c + e] : 0.f);
-    float a[kSeg][V], v[kSeg][V];
+    const float *first = g.init ? g.init + bi * g.d + w.c : nullptr;
+    float a[SEG][V], v[SEG][V];
     terms(g, w, rw, m2, a, v);
     VecF<V> A, S;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         float p = 1.f, s = 0.f;
 #pragma unroll
-        for (int k = 0; k < kSeg; ++k) {
+        for (int k = 0; k < SEG; ++k) {
             p *= a[k][e];
             s = a[k][e] * s + v[k][e];
         }
         A.e[e] = p;
         S.e[e] = s;
     }
-    sA[wv][lane] = A;
-    sS[wv][lane] = S;
-    __syncthreads();
-    if (w.t0 >= g.l) return;
+    lds.A[wv][lane] = A;
+    lds.S[wv][lane] = S;
+    float h[V];
+    enter_tile<V, NW, false>(g, lds, col, tile, first, h);
+    if (!w.live || w.t0 >= g.l) return;
 #pragma unroll
-    for (int j = 0; j < kGW - 1; ++j)
-        if (j < wv) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) h[e] = sA[j][lane].e[e] * h[e] + sS[j][lane].e[e];
-        }
-    if (!w.live) return;
-#pragma unroll
-    for (int k = 0; k < kSeg; ++k) {
+    for (int k = 0; k < SEG; ++k) {
         const int64_t t = w.t0 + k;
         VecIO<IO, V> o;
 #pragma unroll
@@ -286,9 +347,9 @@ __global__ __launch_bounds__(kGW * 64, 2) void k_gated_out(GArgs g) {
             h[e] = a[k][e] * h[e] + v[k][e];
             o.e[e] = (IO)h[e];
         }
-        if (t < g.l) stv<IO, V>(g.y, (w.row0 + t) * g.d + w.c, o);
+        if (g.y && t < g.l) stv<IO, V>(g.y, (w.row0 + t) * g.d + w.c, o);
     }
-    const int64_t end = w.t0 + kSeg < g.l ? w.t0 + kSeg : g.l;
+    const int64_t end = w.t0 + SEG < g.l ? w.t0 + SEG : g.l;
     VecF<V> o;
 #pragma unroll
     for (int e = 0; e < V; ++e) o.e[e] = h[e];
@@ -308,73 +369,68 @@ __global__ __launch_bounds__(kGW * 64, 2) void k_gated_out(GArgs g) {
 //   dr = p (1 - sigmoid(r)),  dlam = sum p sigmoid(lam) / softplus(lam).
 // u / beta = u / sqrt(1 - e^{-2u}) goes to zero with u, so nothing divides by
 // zero where the decay rounds to one.
-template <typename IO, int V>
-__global__ __launch_bounds__(kGW * 64, 2) void k_gated_bwd(GArgs g) {
-    __shared__ VecF<V> sA[kGW][64], sS[kGW][64], sR[kGW][64];
+template <typename IO, int V, int SEG>
+__global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_bwd(GArgs g) {
+    constexpr int NW = kGT / SEG;
+    __shared__ Lds<V, NW> lds;
+    __shared__ VecF<V> sS[NW][64];  // the waves' maps of the states; A is the adjoint's too
     const int lane = threadIdx.x & 63, wv = wave_id();
-    const int64_t tile = blockIdx.y, bi = blockIdx.z;
-    const Tile<IO, V> w(g, bi, tile);
+    const int64_t cols = g.b * g.ncol, col = blockIdx.x % cols, bi = col / g.ncol;
+    // the chain runs from the last tile to the first
+    const int64_t turn = g.tiles > 1 ? take_ticket(g, col, &lds.slot) : 0;
+    const int64_t tile = g.tiles - 1 - turn;
+    const Tile<IO, V, SEG> w(g, col, tile);
     float m2[V];
     rates(g, w, m2);
-    Rows<IO, V> rw;
+    Rows<IO, V, SEG> rw;
     rw.load(g, w);
-    VecIO<IO, V> dy[kSeg];
+    VecIO<IO, V> dy[SEG];
 #pragma unroll
-    for (int k = 0; k < kSeg; ++k) {
+    for (int k = 0; k < SEG; ++k) {
         const int64_t t = w.t0 + k < g.l ? w.t0 + k : g.l - 1;
         dy[k] = ldv<IO, V>(g.dy, (w.row0 + t) * g.d + w.c);
     }
     float h[V], q[V];
+    const float *first = g.dfin ? g.dfin + bi * g.d + w.c : nullptr;
     const int64_t ns = (g.l + SSD_GATED_CHUNK - 1) / SSD_GATED_CHUNK;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const int64_t ch = w.c + e, at = (bi * g.tiles + tile) * g.d + ch;
-        if (tile == 0)
-            h[e] = g.init ? g.init[bi * g.d + ch] : 0.f;
-        else if (g.kept)
-            h[e] = g.kept[(bi * ns + tile * kGT / SSD_GATED_CHUNK - 1) * g.d + ch];
-        else
-            h[e] = g.S[at];
-        q[e] = tile < g.tiles - 1 ? g.R[at] : (g.dfin ? g.dfin[bi * g.d + ch] : 0.f);
+        const int64_t ch = w.c + e;
+        h[e] = tile > 0 ? g.kept[(bi * ns + tile * kGT / SSD_GATED_CHUNK - 1) * g.d + ch]
+                        : (g.init ? g.init[bi * g.d + ch] : 0.f);
     }
-    float a[kSeg][V], v[kSeg][V];
+    float a[SEG][V], v[SEG][V];
     terms(g, w, rw, m2, a, v);
     VecF<V> A, S, R;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         float p = 1.f, s = 0.f, r = 0.f;
 #pragma unroll
-        for (int k = 0; k < kSeg; ++k) {
+        for (int k = 0; k < SEG; ++k) {
             p *= a[k][e];
             s = a[k][e] * s + v[k][e];
         }
 #pragma unroll
-        for (int k = kSeg - 1; k >= 0; --k)
+        for (int k = SEG - 1; k >= 0; --k)
             if (w.t0 + k < g.l) r = a[k][e] * (to_f32(dy[k].e[e]) + r);
         A.e[e] = p;
         S.e[e] = s;
         R.e[e] = r;
     }
-    sA[wv][lane] = A;
+    lds.A[wv][lane] = A;
+    lds.S[wv][lane] = R;
     sS[wv][lane] = S;
-    sR[wv][lane] = R;
-    __syncthreads();
+    enter_tile<V, NW, true>(g, lds, col, turn, first, q);
 #pragma unroll
-    for (int j = 0; j < kGW; ++j)
+    for (int j = 0; j < NW; ++j)
         if (j < wv) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) h[e] = sA[j][lane].e[e] * h[e] + sS[j][lane].e[e];
-        }
-#pragma unroll
-    for (int j = kGW - 1; j >= 0; --j)
-        if (j > wv) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) q[e] = sA[j][lane].e[e] * q[e] + sR[j][lane].e[e];
+            for (int e = 0; e < V; ++e) h[e] = lds.A[j][lane].e[e] * h[e] + sS[j][lane].e[e];
         }
     __syncthreads();
     // the states before every token, in place of the added values
 #pragma unroll
-    for (int k = 0; k < kSeg; ++k)
+    for (int k = 0; k < SEG; ++k)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const float hn = a[k][e] * h[e] + v[k][e];
@@ -385,7 +441,7 @@ __global__ __launch_bounds__(kGW * 64, 2) void k_gated_bwd(GArgs g) {
 #pragma unroll
     for (int e = 0; e < V; ++e) acc.e[e] = 0.f;
 #pragma unroll
-    for (int k = kSeg - 1; k >= 0; --k) {
+    for (int k = SEG - 1; k >= 0; --k) {
         const int64_t t = w.t0 + k;
         if (t >= g.l) continue;
         VecIO<IO, V> ox, orr, oi;
@@ -420,7 +476,7 @@ __global__ __launch_bounds__(kGW * 64, 2) void k_gated_bwd(GArgs g) {
     for (int e = 0; e < V; ++e) {
         s.e[e] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kGW; ++j) s.e[e] += sS[j][lane].e[e];
+        for (int j = 0; j < NW; ++j) s.e[e] += sS[j][lane].e[e];
     }
     *reinterpret_cast<VecF<V> *>(g.part + (bi * g.tiles + tile) * g.d + w.c) = s;
     if (g.fin && tile == 0) {
@@ -484,19 +540,32 @@ __global__ void k_gated_copy(float *dst, const float *src, int64_t n) {
 
 bool al(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-// Workspace: A, S (the backward pass also R and the sums behind dlam), each
-// [b, tiles, d] fp32.
-size_t gated_ws(int64_t b, int64_t l, int64_t d, int parts) {
-    const int64_t tiles = (l + kGT - 1) / kGT;
-    const size_t one = ((size_t)b * tiles * d * 4 + 255) & ~(size_t)255;
-    return parts * one;
-}
+// Workspace: the tickets and flags of every column, the columns' maps and the
+// states after their groups, for any lane width; the backward pass also the
+// states it starts from and the sums behind dlam.
+struct GatedWs {
+    int64_t words;  // tickets and flags
+    size_t map, after, kept, part, total;
+    GatedWs(int64_t b, int64_t l, int64_t d, bool bwd) {
+        auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
+        const int64_t tiles = (l + kGT - 1) / kGT, groups = (tiles + kGroup - 1) / kGroup;
+        const int64_t cols = b * ((d + 63) / 64), wide = b * ((d + 255) / 256 * 256);
+        const bool one = tiles == 1;
+        words = one ? 0 : cols * (kTicketWords + tiles + groups);
+        size_t o = up(words * 4);
+        map = o, o += one ? 0 : up((size_t)wide * tiles * 8);
+        after = o, o += one ? 0 : up((size_t)wide * groups * 4);
+        kept = o, o += bwd && !one ? up((size_t)b * ((l + SSD_GATED_CHUNK - 1) / SSD_GATED_CHUNK) * d * 4) : 0;
+        part = o, o += bwd ? up((size_t)b * tiles * d * 4) : 0;
+        total = o > 256 ? o : 256;
+    }
+};
 
-// Channels a lane moves at once: 4 or 2 where the width and every tensor allow
+// Channels a lane moves at once: `most` (4 or 2) or 2 where the width and every tensor allow
 // vector accesses of as many elements, else 1.
-template <typename... P> int lanes(int io, int64_t d, const float *f0, const float *f1,
-                                   P... p) {
-    for (int v = 4; v > 1; v /= 2) {
+template <typename... P> int lanes(int io, int64_t d, int most, const float *f0,
+                                   const float *f1, P... p) {
+    for (int v = most; v > 1; v /= 2) {
         const uintptr_t a = v * (io == SSD_BF16 ? 2 : 4), f = 4 * v;
         if (d % v == 0 && al(f0, f) && al(f1, f) && (al(p, a) && ...))
             return v;
@@ -509,33 +578,47 @@ template <typename... P> bool io_aligned(int io, P... p) {
 
 // sizes whose element offsets and grids fit
 bool gated_sizes(int64_t b, int64_t l, int64_t d) {
-    return b <= 65535 && d <= ((int64_t)1 << 24) && l <= (int64_t)65535 * kGT;
+    return b <= 65535 && d <= ((int64_t)1 << 24) && l <= ((int64_t)1 << 28) &&
+           b * ((d + 63) / 64) * ((l + kGT - 1) / kGT) <= ((int64_t)1 << 30);
 }
 
-template <typename IO, int V> hipError_t fwd(GArgs &g, hipStream_t s) {
-    const dim3 grid((unsigned)((g.d + 64 * V - 1) / (64 * V)), (unsigned)g.tiles, (unsigned)g.b);
-    if (g.tiles > 1) {
-        hipLaunchKernelGGL((k_gated_map<IO, V, true, false>), grid, dim3(kGW * 64), 0, s, g);
-        hipLaunchKernelGGL((k_gated_chain<true, false>),
-                           dim3((unsigned)((g.b * g.d + 255) / 256)), dim3(256), 0, s, g);
-    }
-    hipLaunchKernelGGL((k_gated_out<IO, V>), grid, dim3(kGW * 64), 0, s, g);
+// The columns' layout at lane width v, and the cleared tickets and flags.
+void set_chain(GArgs &g, const GatedWs &W, char *ws, int v, hipStream_t s) {
+    g.ncol = (g.d + 64 * v - 1) / (64 * v);
+    if (g.tiles == 1) return;
+    const int64_t cols = g.b * g.ncol, groups = (g.tiles + kGroup - 1) / kGroup;
+    g.ch.ticket = reinterpret_cast<uint32_t *>(ws);
+    g.ch.flag = g.ch.ticket + cols * kTicketWords;
+    g.ch.gflag = g.ch.flag + cols * g.tiles;
+    g.ch.map = reinterpret_cast<uint64_t *>(ws + W.map);
+    g.ch.after = reinterpret_cast<uint32_t *>(ws + W.after);
+    const int64_t n = cols * (kTicketWords + g.tiles + groups);
+    hipLaunchKernelGGL(k_gated_clear, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
+                       g.ch.ticket, n);
+}
+
+constexpr int kSegF = 8, kSegB = 4;  // tokens per wave of the two passes
+
+template <typename IO, int V>
+hipError_t fwd(GArgs g, const GatedWs &W, char *ws, hipStream_t s) {
+    set_chain(g, W, ws, V, s);
+    hipLaunchKernelGGL((k_gated_fwd<IO, V, kSegF>), dim3((unsigned)(g.b * g.ncol * g.tiles)),
+                       dim3(kGT / kSegF * 64), 0, s, g);
     return hipGetLastError();
 }
 
-template <typename IO, int V> hipError_t bwd(GArgs &g, float *dlam, hipStream_t s) {
-    const dim3 grid((unsigned)((g.d + 64 * V - 1) / (64 * V)), (unsigned)g.tiles, (unsigned)g.b);
-    const dim3 line((unsigned)((g.b * g.d + 255) / 256));
-    if (g.tiles > 1) {
-        if (g.kept) {
-            hipLaunchKernelGGL((k_gated_map<IO, V, false, true>), grid, dim3(kGW * 64), 0, s, g);
-            hipLaunchKernelGGL((k_gated_chain<false, true>), line, dim3(256), 0, s, g);
-        } else {
-            hipLaunchKernelGGL((k_gated_map<IO, V, true, true>), grid, dim3(kGW * 64), 0, s, g);
-            hipLaunchKernelGGL((k_gated_chain<true, true>), line, dim3(256), 0, s, g);
-        }
+template <typename IO, int V>
+hipError_t bwd(GArgs g, const GatedWs &W, char *ws, float *dlam, hipStream_t s) {
+    if (g.tiles > 1 && !g.kept) {
+        GArgs f = g;
+        f.y = nullptr, f.fin = nullptr, f.states = reinterpret_cast<float *>(ws + W.kept);
+        const hipError_t e = fwd<IO, V>(f, W, ws, s);
+        if (e != hipSuccess) return e;
+        g.kept = f.states;
     }
-    hipLaunchKernelGGL((k_gated_bwd<IO, V>), grid, dim3(kGW * 64), 0, s, g);
+    set_chain(g, W, ws, V, s);
+    hipLaunchKernelGGL((k_gated_bwd<IO, V, kSegB>), dim3((unsigned)(g.b * g.ncol * g.tiles)),
+                       dim3(kGT / kSegB * 64), 0, s, g);
     hipLaunchKernelGGL(k_gated_lam, dim3((unsigned)((g.d + 31) / 32)), dim3(256), 0, s, g.part,
                        g.lam, dlam, g.b * g.tiles, g.d);
     return hipGetLastError();
@@ -551,12 +634,12 @@ extern "C" {
 
 size_t ssd_gated_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
     if (batch <= 0 || seqlen <= 0 || dim <= 0 || !gated_sizes(batch, seqlen, dim)) return 0;
-    return gated_ws(batch, seqlen, dim, 2);
+    return GatedWs(batch, seqlen, dim, false).total;
 }
 
 size_t ssd_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim) {
     if (batch <= 0 || seqlen <= 0 || dim <= 0 || !gated_sizes(batch, seqlen, dim)) return 0;
-    return gated_ws(batch, seqlen, dim, 4);
+    return GatedWs(batch, seqlen, dim, true).total;
 }
 
 int32_t ssd_gated_scan(const void *x, const void *gates, const float *lam, float scale,
@@ -582,21 +665,20 @@ int32_t ssd_gated_scan(const void *x, const void *gates, const float *lam, float
     }
     if (!x || !gates || !lam || !y) return SSD_ERR_NULL;
     if (!io_aligned(io_dtype, x, gates, y) || !al(lam, 4) || !al(seq_idx, 4)) return SSD_ERR_ALIGN;
-    if (!workspace || workspace_bytes < gated_ws(batch, seqlen, dim, 2)) return SSD_ERR_WORKSPACE;
+    const GatedWs W(batch, seqlen, dim, false);
+    if (!workspace || workspace_bytes < W.total) return SSD_ERR_WORKSPACE;
     if (!al(workspace, 256)) return SSD_ERR_ALIGN;
     GArgs g{};
     g.x = x, g.gates = gates, g.lam = lam, g.scale = scale, g.init = init_state, g.seq = seq_idx;
     g.y = y, g.fin = final_state, g.states = states;
     g.b = batch, g.l = seqlen, g.d = dim, g.tiles = (seqlen + kGT - 1) / kGT;
-    g.A = static_cast<float *>(workspace);
-    g.S = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                    gated_ws(batch, seqlen, dim, 1));
-    const int v = lanes(io_dtype, dim, final_state, states, x, gates, y);
+    char *ws = static_cast<char *>(workspace);
+    const int v = lanes(io_dtype, dim, io_dtype == SSD_BF16 ? 4 : 2, final_state, states, x, gates, y);
     const hipError_t e = io_dtype == SSD_BF16
-                             ? (v == 4 ? fwd<bf16, 4>(g, s) : v == 2 ? fwd<bf16, 2>(g, s)
-                                                                     : fwd<bf16, 1>(g, s))
-                             : (v == 4 ? fwd<float, 4>(g, s) : v == 2 ? fwd<float, 2>(g, s)
-                                                                      : fwd<float, 1>(g, s));
+                             ? (v == 4   ? fwd<bf16, 4>(g, W, ws, s)
+                                : v == 2 ? fwd<bf16, 2>(g, W, ws, s)
+                                         : fwd<bf16, 1>(g, W, ws, s))
+                             : (v == 2 ? fwd<float, 2>(g, W, ws, s) : fwd<float, 1>(g, W, ws, s));
     return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
@@ -614,7 +696,8 @@ int32_t ssd_gated_scan_bwd(const void *x, const void *gates, const float *lam, f
     if (!io_aligned(io_dtype, x, gates, dy, dx, dgates) || !al(lam, 4) || !al(init_state, 4) ||
         !al(seq_idx, 4) || !al(states, 4) || !al(d_final, 4) || !al(dlam, 4) || !al(d_init, 4))
         return SSD_ERR_ALIGN;
-    if (!workspace || workspace_bytes < gated_ws(batch, seqlen, dim, 4)) return SSD_ERR_WORKSPACE;
+    const GatedWs W(batch, seqlen, dim, true);
+    if (!workspace || workspace_bytes < W.total) return SSD_ERR_WORKSPACE;
     if (!al(workspace, 256)) return SSD_ERR_ALIGN;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     GArgs g{};
@@ -622,18 +705,12 @@ int32_t ssd_gated_scan_bwd(const void *x, const void *gates, const float *lam, f
     g.kept = states, g.dy = dy, g.dfin = d_final, g.y = dx, g.dgates = dgates, g.fin = d_init;
     g.b = batch, g.l = seqlen, g.d = dim, g.tiles = (seqlen + kGT - 1) / kGT;
     char *ws = static_cast<char *>(workspace);
-    const size_t one = gated_ws(batch, seqlen, dim, 1);
-    g.A = reinterpret_cast<float *>(ws);
-    g.S = reinterpret_cast<float *>(ws + one);
-    g.R = reinterpret_cast<float *>(ws + 2 * one);
-    g.part = reinterpret_cast<float *>(ws + 3 * one);
-    const int v = lanes(io_dtype, dim, d_init, nullptr, x, gates, dy, dx, dgates);
+    g.part = reinterpret_cast<float *>(ws + W.part);
+    const int v = lanes(io_dtype, dim, 2, d_init, nullptr, x, gates, dy, dx, dgates);
     const hipError_t e =
         io_dtype == SSD_BF16
-            ? (v == 4 ? bwd<bf16, 4>(g, dlam, s) : v == 2 ? bwd<bf16, 2>(g, dlam, s)
-                                                          : bwd<bf16, 1>(g, dlam, s))
-            : (v == 4 ? bwd<float, 4>(g, dlam, s) : v == 2 ? bwd<float, 2>(g, dlam, s)
-                                                           : bwd<float, 1>(g, dlam, s));
+            ? (v == 2 ? bwd<bf16, 2>(g, W, ws, dlam, s) : bwd<bf16, 1>(g, W, ws, dlam, s))
+            : (v == 2 ? bwd<float, 2>(g, W, ws, dlam, s) : bwd<float, 1>(g, W, ws, dlam, s));
     return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
@@ -647,7 +724,7 @@ int32_t ssd_gated_step(float *state, const void *x, const void *gates, const flo
     if (!state || !x || !gates || !lam || !y) return SSD_ERR_NULL;
     if (!al(state, 4) || !al(lam, 4) || !io_aligned(io_dtype, x, gates, y)) return SSD_ERR_ALIGN;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
-    const int v = lanes(io_dtype, dim, state, lam, x, gates, y);
+    const int v = lanes(io_dtype, dim, 4, state, lam, x, gates, y);
     const int64_t n = batch * (dim / v), blocks = (n + 255) / 256;
     if (blocks > ((int64_t)1 << 31) - 1) return SSD_ERR_UNSUPPORTED;
 #define SSD_GSTEP(IO, VV)                                                                         \
