@@ -18,6 +18,10 @@
 #include "../../include/ssd.h"
 #include "ssd_device.hpp"
 
+// Products and sums are fused only where the code says so: every lane width
+// then gives the same bits.
+#pragma clang fp contract(off)
+
 namespace ssd {
 
 namespace {
@@ -33,21 +37,33 @@ __device__ __forceinline__ float sigmoid_f(float z) {
     return __builtin_amdgcn_rcpf(1.f + exp2_fast(-z * kLog2e));
 }
 
-// softplus(v) = max(v, 0) + log1p(e^-|v|)
+// softplus(v) = max(v, 0) + log1p(y), y = e^-|v|: the exponential with the
+// rounding of its argument put back, and log1p(y) = 2 atanh(z), z = y / (2 + y)
+// <= 1/3, from seven terms (the eighth is below 2^-26 of the sum).
 __device__ __forceinline__ float softplus_f(float v) {
-    return fmaxf(v, 0.f) + log1pf(expf(-fabsf(v)));
+    const float w = -fabsf(v), p = w * kLog2e;
+    // log2(e) = kLog2e + 1.9e-8
+    const float lo = fmaf(w, kLog2e, -p) + w * 1.925963033e-8f;
+    const float y = exp2_fast(p) * fmaf(lo, kLn2, 1.f);
+    const float z = y * __builtin_amdgcn_rcpf(2.f + y), q = z * z;
+    float s = fmaf(q, 1.f / 13, 1.f / 11);
+    s = fmaf(q, s, 1.f / 9);
+    s = fmaf(q, s, 1.f / 7);
+    s = fmaf(q, s, 1.f / 5);
+    s = fmaf(q, s, 1.f / 3);
+    return fmaxf(v, 0.f) + 2.f * fmaf(z * q, s, z);
 }
 
-// a = e^-u and beta = sqrt(1 - a^2) for u = u2 ln 2 >= 0.  1 - a^2 =
-// -expm1(-2u) is taken from its series where the subtraction would cancel:
-// t = 2u < 1/4, six terms, relative error t^6 / 5040 < 2^-24; above, the
-// subtraction loses at most two bits of fp32.
-__device__ __forceinline__ void decay(float u2, float &a, float &beta) {
+// a = e^-u and 1 - a^2 = -expm1(-2u) for u = u2 ln 2 >= 0.  Where the
+// subtraction would cancel (2u < 1/8) the difference is u2 times the cubic of
+// least largest relative error (1.6e-8 there, before rounding); above, the
+// subtraction loses at most three bits of fp32.
+__device__ __forceinline__ void decay(float u2, float &a, float &om) {
     a = exp2_fast(-u2);
-    const float t = 2.f * kLn2 * u2;
-    const float s =
-        t * (1.f - t * (0.5f - t * (1.f / 6 - t * (1.f / 24 - t * (1.f / 120 - t * (1.f / 720))))));
-    beta = __builtin_amdgcn_sqrtf(t < 0.25f ? s : 1.f - a * a);
+    const float s = u2 * fmaf(u2, fmaf(u2, fmaf(u2, -0.1463926534f, 0.4436125999f),
+                                       -0.9608984357f), 1.386294340f);
+    const float m = fmaf(-a, a, 1.f);
+    om = u2 < 0.09016844f ? s : m;
 }
 
 // How the tiles of one column (64 V channels of one sequence) hand states
@@ -70,6 +86,7 @@ struct Chain {
     uint32_t *gflag;    // [cols][groups]  the state after the group is there
     uint64_t *map;      // [cols][tiles][64 V]  (A, S) of a channel
     uint32_t *after;    // [cols][groups][64 V] the state after the group
+    float *rate;        // [d] scale softplus(lam) in binary orders (NULL without a chain)
 };
 
 struct GArgs {
@@ -156,20 +173,31 @@ __device__ __forceinline__ bool same_document(const GArgs &g, int64_t row0, int6
 
 // Decay and added value of the wave's tokens; identity past the end.
 template <typename IO, int V, int SEG>
-__device__ __forceinline__ void terms(const GArgs &g, const Tile<IO, V, SEG> &w, const Rows<IO, V, SEG> &rw,
-                                      const float (&m2)[V], float (&a)[SEG][V],
-                                      float (&v)[SEG][V]) {
+__device__ __forceinline__ void terms(const GArgs &g, const Tile<IO, V, SEG> &w,
+                                      const Rows<IO, V, SEG> &rw, const float (&m2)[V],
+                                      float (&a)[SEG][V], float (&v)[SEG][V]) {
+#pragma unroll
+    for (int k = 0; k < SEG; ++k) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            float om;
+            decay(m2[e] * sigmoid_f(to_f32(rw.r[k].e[e])), a[k][e], om);
+            v[k][e] = __builtin_amdgcn_sqrtf(om) * sigmoid_f(to_f32(rw.i[k].e[e])) *
+                      to_f32(rw.x[k].e[e]);
+        }
+        // a row's temporaries are dead before the next row's begin: without
+        // this the scheduler interleaves the rows and spills
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    if (w.t0 + SEG <= g.l && !g.seq) return;
 #pragma unroll
     for (int k = 0; k < SEG; ++k) {
         const int64_t t = w.t0 + k;
         const bool in = t < g.l, same = same_document(g, w.row0, t);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            float aa, beta;
-            decay(m2[e] * sigmoid_f(to_f32(rw.r[k].e[e])), aa, beta);
-            const float vv = beta * sigmoid_f(to_f32(rw.i[k].e[e])) * to_f32(rw.x[k].e[e]);
-            a[k][e] = in ? (same ? aa : 0.f) : 1.f;
-            v[k][e] = in ? vv : 0.f;
+            a[k][e] = in ? (same ? a[k][e] : 0.f) : 1.f;
+            v[k][e] = in ? v[k][e] : 0.f;
         }
     }
 }
@@ -177,7 +205,8 @@ __device__ __forceinline__ void terms(const GArgs &g, const Tile<IO, V, SEG> &w,
 template <typename IO, int V, int SEG>
 __device__ __forceinline__ void rates(const GArgs &g, const Tile<IO, V, SEG> &w, float (&m2)[V]) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) m2[e] = g.scale * softplus_f(g.lam[w.c + e]) * kLog2e;
+    for (int e = 0; e < V; ++e)
+        m2[e] = g.ch.rate ? g.ch.rate[w.c + e] : g.scale * softplus_f(g.lam[w.c + e]) * kLog2e;
 }
 
 // This workgroup's tile of its column, in the order of the chain.
@@ -228,7 +257,7 @@ __device__ __forceinline__ void enter_tile(const GArgs &g, Lds<V, NW> &lds, int6
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 tA.e[e] *= A.e[e];
-                tS.e[e] = A.e[e] * tS.e[e] + S.e[e];
+                tS.e[e] = fmaf(A.e[e], tS.e[e], S.e[e]);
             }
         }
         if (!last) {
@@ -276,13 +305,13 @@ __device__ __forceinline__ void enter_tile(const GArgs &g, Lds<V, NW> &lds, int6
     for (int k = 0; k < in; ++k) {
         const VecF<V> A = lds.pA[k][lane], S = lds.pS[k][lane];
 #pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = A.e[e] * h[e] + S.e[e];
+        for (int e = 0; e < V; ++e) h[e] = fmaf(A.e[e], h[e], S.e[e]);
     }
     if (wv == 0 && last) {
         uint32_t *m = g.ch.after + (col * groups + grp) * W + lane * V;
 #pragma unroll
         for (int e = 0; e < V; ++e)
-            put32(m + e, __builtin_bit_cast(uint32_t, tA.e[e] * h[e] + tS.e[e]));
+            put32(m + e, __builtin_bit_cast(uint32_t, fmaf(tA.e[e], h[e], tS.e[e])));
         vm_wait<0>();
         if (lane == 0) put32(g.ch.gflag + col * groups + grp, 1);
     }
@@ -293,15 +322,18 @@ __device__ __forceinline__ void enter_tile(const GArgs &g, Lds<V, NW> &lds, int6
         if (BACK ? w > wv : w < wv) {
             const VecF<V> A = lds.A[w][lane], S = lds.S[w][lane];
 #pragma unroll
-            for (int e = 0; e < V; ++e) h[e] = A.e[e] * h[e] + S.e[e];
+            for (int e = 0; e < V; ++e) h[e] = fmaf(A.e[e], h[e], S.e[e]);
         }
     }
 }
 
-// Clears the tickets and flags.
-__global__ __launch_bounds__(256) void k_gated_clear(uint32_t *p, int64_t n) {
+// Clears the tickets and flags, and works out the channels' rates once (a
+// softplus is as much work as a token's decay).
+__global__ __launch_bounds__(256) void k_gated_setup(uint32_t *p, int64_t n, const float *lam,
+                                                     float scale, float *rate, int64_t d) {
     const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (k < n) p[k] = 0;
+    if (k < d) rate[k] = scale * softplus_f(lam[k]) * kLog2e;
 }
 
 // ------------------------------------------------------------- forward ----
@@ -328,7 +360,7 @@ __global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_fwd(GArgs g) {
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             p *= a[k][e];
-            s = a[k][e] * s + v[k][e];
+            s = fmaf(a[k][e], s, v[k][e]);
         }
         A.e[e] = p;
         S.e[e] = s;
@@ -344,7 +376,7 @@ __global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_fwd(GArgs g) {
         VecIO<IO, V> o;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            h[e] = a[k][e] * h[e] + v[k][e];
+            h[e] = fmaf(a[k][e], h[e], v[k][e]);
             o.e[e] = (IO)h[e];
         }
         if (g.y && t < g.l) stv<IO, V>(g.y, (w.row0 + t) * g.d + w.c, o);
@@ -408,7 +440,7 @@ __global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_bwd(GArgs g) {
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             p *= a[k][e];
-            s = a[k][e] * s + v[k][e];
+            s = fmaf(a[k][e], s, v[k][e]);
         }
 #pragma unroll
         for (int k = SEG - 1; k >= 0; --k)
@@ -425,7 +457,7 @@ __global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_bwd(GArgs g) {
     for (int j = 0; j < NW; ++j)
         if (j < wv) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) h[e] = lds.A[j][lane].e[e] * h[e] + sS[j][lane].e[e];
+            for (int e = 0; e < V; ++e) h[e] = fmaf(lds.A[j][lane].e[e], h[e], sS[j][lane].e[e]);
         }
     __syncthreads();
     // the states before every token, in place of the added values
@@ -433,7 +465,7 @@ __global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_bwd(GArgs g) {
     for (int k = 0; k < SEG; ++k)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const float hn = a[k][e] * h[e] + v[k][e];
+            const float hn = fmaf(a[k][e], h[e], v[k][e]);
             v[k][e] = h[e];
             h[e] = hn;
         }
@@ -449,17 +481,19 @@ __global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_bwd(GArgs g) {
         for (int e = 0; e < V; ++e) {
             const float gt = to_f32(dy[k].e[e]) + q[e];
             const float sr = sigmoid_f(to_f32(rw.r[k].e[e])), si = sigmoid_f(to_f32(rw.i[k].e[e]));
-            const float x = to_f32(rw.x[k].e[e]), u2 = m2[e] * sr, u = kLn2 * u2;
-            float aa, beta;
-            decay(u2, aa, beta);
-            const float ratio = beta > 0.f ? u * __builtin_amdgcn_rcpf(beta) : 0.f;
-            const float gx = gt * si;
-            const float p = aa * aa * ratio * gx * x - u * a[k][e] * gt * v[k][e];
-            ox.e[e] = (IO)(gx * beta);
-            oi.e[e] = (IO)(gx * beta * x * (1.f - si));
+            const float x = to_f32(rw.x[k].e[e]), u2 = m2[e] * sr;
+            float aa, om;
+            decay(u2, aa, om);
+            // beta and its inverse; a shut gate (om = 0) has beta = 0 and a
+            // finite stand-in for the inverse, which u = 0 then cancels
+            const float rb = __builtin_amdgcn_rsqf(fmaxf(om, 1e-30f));
+            const float gx = gt * si, gb = gx * (om * rb), gxx = gx * x;
+            q[e] = a[k][e] * gt;
+            const float p = kLn2 * u2 * fmaf(aa * aa * rb, gxx, -q[e] * v[k][e]);
+            ox.e[e] = (IO)gb;
+            oi.e[e] = (IO)(gb * x * (1.f - si));
             orr.e[e] = (IO)(p * (1.f - sr));
             acc.e[e] += p;
-            q[e] = a[k][e] * gt;
         }
         if (w.live) {
             const int64_t at = (w.row0 + t) * g.d + w.c;
@@ -487,20 +521,29 @@ __global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_bwd(GArgs g) {
 }
 
 // dlam: the tiles' sums, added in a fixed order in fp64.  One workgroup: 32
-// channels by 8 runs of tiles.
-__global__ __launch_bounds__(256) void k_gated_lam(const float *part, const float *lam, float *dlam,
-                                                   int64_t rows, int64_t d) {
-    __shared__ double s[8][32];
+// channels by 32 runs of tiles, four loads in flight a thread.
+__global__ __launch_bounds__(1024) void k_gated_lam(const float *part, const float *lam,
+                                                    float *dlam, int64_t rows, int64_t d) {
+    __shared__ double s[32][33];
     const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
     const int64_t ch = (int64_t)blockIdx.x * 32 + c;
     double t = 0;
-    if (ch < d)
-        for (int64_t j = k; j < rows; j += 8) t += part[j * d + ch];
+    if (ch < d) {
+        int64_t j = k;
+        for (; j + 96 < rows; j += 128) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = part[(j + 32 * i) * d + ch];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t += v[i];
+        }
+        for (; j < rows; j += 32) t += part[j * d + ch];
+    }
     s[k][c] = t;
     __syncthreads();
     if (k != 0 || ch >= d) return;
 #pragma unroll
-    for (int j = 1; j < 8; ++j) t += s[j][c];
+    for (int j = 1; j < 32; ++j) t += s[j][c];
     // sigmoid(v) / softplus(v) tends to one as v goes to minus infinity
     const double v = lam[ch];
     const double ratio = v < -30. ? 1. : 1. / ((1. + exp(-v)) * (fmax(v, 0.) + log1p(exp(-fabs(v)))));
@@ -523,9 +566,10 @@ __global__ __launch_bounds__(256) void k_gated_step(float *state, const IO *x, c
     VecIO<IO, V> o;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        float a, beta;
-        decay(scale * softplus_f(lm.e[e]) * kLog2e * sigmoid_f(to_f32(r.e[e])), a, beta);
-        h.e[e] = a * h.e[e] + beta * sigmoid_f(to_f32(i.e[e])) * to_f32(xv.e[e]);
+        float a, om;
+        decay(scale * softplus_f(lm.e[e]) * kLog2e * sigmoid_f(to_f32(r.e[e])), a, om);
+        h.e[e] = fmaf(a, h.e[e], __builtin_amdgcn_sqrtf(om) * sigmoid_f(to_f32(i.e[e])) *
+                                     to_f32(xv.e[e]));
         o.e[e] = (IO)h.e[e];
     }
     *reinterpret_cast<VecF<V> *>(state + at) = h;
@@ -545,7 +589,7 @@ bool al(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 // states it starts from and the sums behind dlam.
 struct GatedWs {
     int64_t words;  // tickets and flags
-    size_t map, after, kept, part, total;
+    size_t map, after, rate, kept, part, total;
     GatedWs(int64_t b, int64_t l, int64_t d, bool bwd) {
         auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
         const int64_t tiles = (l + kGT - 1) / kGT, groups = (tiles + kGroup - 1) / kGroup;
@@ -555,6 +599,7 @@ struct GatedWs {
         size_t o = up(words * 4);
         map = o, o += one ? 0 : up((size_t)wide * tiles * 8);
         after = o, o += one ? 0 : up((size_t)wide * groups * 4);
+        rate = o, o += one ? 0 : up((size_t)d * 4);
         kept = o, o += bwd && !one ? up((size_t)b * ((l + SSD_GATED_CHUNK - 1) / SSD_GATED_CHUNK) * d * 4) : 0;
         part = o, o += bwd ? up((size_t)b * tiles * d * 4) : 0;
         total = o > 256 ? o : 256;
@@ -592,12 +637,13 @@ void set_chain(GArgs &g, const GatedWs &W, char *ws, int v, hipStream_t s) {
     g.ch.gflag = g.ch.flag + cols * g.tiles;
     g.ch.map = reinterpret_cast<uint64_t *>(ws + W.map);
     g.ch.after = reinterpret_cast<uint32_t *>(ws + W.after);
-    const int64_t n = cols * (kTicketWords + g.tiles + groups);
-    hipLaunchKernelGGL(k_gated_clear, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
-                       g.ch.ticket, n);
+    g.ch.rate = reinterpret_cast<float *>(ws + W.rate);
+    const int64_t n = cols * (kTicketWords + g.tiles + groups), most = n > g.d ? n : g.d;
+    hipLaunchKernelGGL(k_gated_setup, dim3((unsigned)((most + 255) / 256)), dim3(256), 0, s,
+                       g.ch.ticket, n, g.lam, g.scale, g.ch.rate, g.d);
 }
 
-constexpr int kSegF = 8, kSegB = 4;  // tokens per wave of the two passes
+constexpr int kSegF = 8, kSegB = 8;  // tokens per wave of the two passes
 
 template <typename IO, int V>
 hipError_t fwd(GArgs g, const GatedWs &W, char *ws, hipStream_t s) {
@@ -619,7 +665,7 @@ hipError_t bwd(GArgs g, const GatedWs &W, char *ws, float *dlam, hipStream_t s) 
     set_chain(g, W, ws, V, s);
     hipLaunchKernelGGL((k_gated_bwd<IO, V, kSegB>), dim3((unsigned)(g.b * g.ncol * g.tiles)),
                        dim3(kGT / kSegB * 64), 0, s, g);
-    hipLaunchKernelGGL(k_gated_lam, dim3((unsigned)((g.d + 31) / 32)), dim3(256), 0, s, g.part,
+    hipLaunchKernelGGL(k_gated_lam, dim3((unsigned)((g.d + 31) / 32)), dim3(1024), 0, s, g.part,
                        g.lam, dlam, g.b * g.tiles, g.d);
     return hipGetLastError();
 }
