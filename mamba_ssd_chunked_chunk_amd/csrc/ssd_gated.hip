@@ -6,8 +6,8 @@
 // with r_t = gates[.., c] and i_t = gates[.., d + c] raw (before their
 // sigmoids), its gradient, and one decode step of it.
 //
-// A tile is 64 tokens of 64 * V channels: a lane owns V channels, a wave a run
-// of SEG consecutive tokens, so every load of a wave is one
+// A tile is SEG * NW tokens of 64 * V channels: a lane owns V channels, each of
+// the workgroup's NW waves a run of SEG consecutive tokens, so every load of a wave is one
 // contiguous piece of a token's row.  A run is the map h -> A h + S of the
 // state entering it (A = prod a_t, S its result from zero); runs compose in
 // order: waves through LDS inside a tile, tiles through the workspace.
@@ -26,8 +26,6 @@ namespace ssd {
 
 namespace {
 
-constexpr int kGT = 64;  // tokens per tile, SEG to a wave
-static_assert(kGT == SSD_GATED_CHUNK, "a tile ends where a state is kept");
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <typename IO, int V> struct alignas(sizeof(IO) * V) VecIO { IO e[V]; };
@@ -77,7 +75,7 @@ __device__ __forceinline__ void decay(float u2, float &a, float &om) {
 // turn, so every wait ends.  The words are written and read at agent scope
 // (the XCDs' L2 caches are not coherent inside a kernel), a flag after its
 // data has reached memory.
-constexpr int kGroup = 16;
+constexpr int kGroup = 8;
 constexpr int kTicketWords = 32;  // a 128-byte line per column's ticket
 
 struct Chain {
@@ -129,13 +127,13 @@ template <typename IO, int V, int SEG> struct Tile {
     bool live;       // the lane's channels exist
     int64_t row0;    // the sequence's first row in [b * l]
     int64_t t0;      // the wave's first token
-    __device__ Tile(const GArgs &g, int64_t col, int64_t tile) {
+    __device__ Tile(const GArgs &g, int64_t col, int64_t tile, int tokens) {
         const int lane = threadIdx.x & 63;
         c = (col % g.ncol * 64 + lane) * V;
         live = c < g.d;
         if (!live) c = 0;
         row0 = col / g.ncol * g.l;
-        t0 = tile * kGT + wave_id() * SEG;
+        t0 = tile * tokens + wave_id() * SEG;
     }
 };
 
@@ -337,14 +335,15 @@ __global__ __launch_bounds__(256) void k_gated_setup(uint32_t *p, int64_t n, con
 }
 
 // ------------------------------------------------------------- forward ----
-template <typename IO, int V, int SEG>
-__global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_fwd(GArgs g) {
-    constexpr int NW = kGT / SEG;
+template <typename IO, int V, int SEG, int NW>
+__global__ __launch_bounds__(NW * 64, 4) void k_gated_fwd(GArgs g) {
+    constexpr int T = SEG * NW;
+    static_assert(T % SSD_GATED_CHUNK == 0 && SSD_GATED_CHUNK % SEG == 0, "where states are kept");
     __shared__ Lds<V, NW> lds;
     const int lane = threadIdx.x & 63, wv = wave_id();
     const int64_t cols = g.b * g.ncol, col = blockIdx.x % cols;
     const int64_t tile = g.tiles > 1 ? take_ticket(g, col, &lds.slot) : 0;
-    const Tile<IO, V, SEG> w(g, col, tile);
+    const Tile<IO, V, SEG> w(g, col, tile, T);
     const int64_t bi = col / g.ncol;
     float m2[V];
     rates(g, w, m2);
@@ -401,9 +400,10 @@ __global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_fwd(GArgs g) {
 //   dr = p (1 - sigmoid(r)),  dlam = sum p sigmoid(lam) / softplus(lam).
 // u / beta = u / sqrt(1 - e^{-2u}) goes to zero with u, so nothing divides by
 // zero where the decay rounds to one.
-template <typename IO, int V, int SEG>
-__global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_bwd(GArgs g) {
-    constexpr int NW = kGT / SEG;
+template <typename IO, int V, int SEG, int NW>
+__global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
+    constexpr int T = SEG * NW;
+    static_assert(T % SSD_GATED_CHUNK == 0 && SSD_GATED_CHUNK % SEG == 0, "where states are kept");
     __shared__ Lds<V, NW> lds;
     __shared__ VecF<V> sS[NW][64];  // the waves' maps of the states; A is the adjoint's too
     const int lane = threadIdx.x & 63, wv = wave_id();
@@ -411,7 +411,7 @@ __global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_bwd(GArgs g) {
     // the chain runs from the last tile to the first
     const int64_t turn = g.tiles > 1 ? take_ticket(g, col, &lds.slot) : 0;
     const int64_t tile = g.tiles - 1 - turn;
-    const Tile<IO, V, SEG> w(g, col, tile);
+    const Tile<IO, V, SEG> w(g, col, tile, T);
     float m2[V];
     rates(g, w, m2);
     Rows<IO, V, SEG> rw;
@@ -428,7 +428,7 @@ __global__ __launch_bounds__(kGT / SEG * 64, 4) void k_gated_bwd(GArgs g) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         const int64_t ch = w.c + e;
-        h[e] = tile > 0 ? g.kept[(bi * ns + tile * kGT / SSD_GATED_CHUNK - 1) * g.d + ch]
+        h[e] = tile > 0 ? g.kept[(bi * ns + tile * T / SSD_GATED_CHUNK - 1) * g.d + ch]
                         : (g.init ? g.init[bi * g.d + ch] : 0.f);
     }
     float a[SEG][V], v[SEG][V];
@@ -584,6 +584,8 @@ __global__ void k_gated_copy(float *dst, const float *src, int64_t n) {
 
 bool al(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+constexpr int kLeastTile = 64;  // tokens of the shortest tile
+
 // Workspace: the tickets and flags of every column, the columns' maps and the
 // states after their groups, for any lane width; the backward pass also the
 // states it starts from and the sums behind dlam.
@@ -592,7 +594,7 @@ struct GatedWs {
     size_t map, after, rate, kept, part, total;
     GatedWs(int64_t b, int64_t l, int64_t d, bool bwd) {
         auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
-        const int64_t tiles = (l + kGT - 1) / kGT, groups = (tiles + kGroup - 1) / kGroup;
+        const int64_t tiles = (l + kLeastTile - 1) / kLeastTile, groups = (tiles + kGroup - 1) / kGroup;
         const int64_t cols = b * ((d + 63) / 64), wide = b * ((d + 255) / 256 * 256);
         const bool one = tiles == 1;
         words = one ? 0 : cols * (kTicketWords + tiles + groups);
@@ -624,12 +626,18 @@ template <typename... P> bool io_aligned(int io, P... p) {
 // sizes whose element offsets and grids fit
 bool gated_sizes(int64_t b, int64_t l, int64_t d) {
     return b <= 65535 && d <= ((int64_t)1 << 24) && l <= ((int64_t)1 << 28) &&
-           b * ((d + 63) / 64) * ((l + kGT - 1) / kGT) <= ((int64_t)1 << 30);
+           b * ((d + 63) / 64) * ((l + kLeastTile - 1) / kLeastTile) <= ((int64_t)1 << 30);
 }
 
-// The columns' layout at lane width v, and the cleared tickets and flags.
-void set_chain(GArgs &g, const GatedWs &W, char *ws, int v, hipStream_t s) {
+// Tokens per wave and waves per workgroup of the two passes.
+template <typename IO> struct FwdShape { static constexpr int SEG = sizeof(IO) == 2 ? 16 : 8, NW = 8; };
+struct BwdShape { static constexpr int SEG = 4, NW = 16; };
+
+// The columns' layout at lane width v and `tokens` a tile, the cleared tickets
+// and flags and the rates.
+void set_chain(GArgs &g, const GatedWs &W, char *ws, int v, int tokens, hipStream_t s) {
     g.ncol = (g.d + 64 * v - 1) / (64 * v);
+    g.tiles = (g.l + tokens - 1) / tokens;
     if (g.tiles == 1) return;
     const int64_t cols = g.b * g.ncol, groups = (g.tiles + kGroup - 1) / kGroup;
     g.ch.ticket = reinterpret_cast<uint32_t *>(ws);
@@ -643,28 +651,28 @@ void set_chain(GArgs &g, const GatedWs &W, char *ws, int v, hipStream_t s) {
                        g.ch.ticket, n, g.lam, g.scale, g.ch.rate, g.d);
 }
 
-constexpr int kSegF = 8, kSegB = 8;  // tokens per wave of the two passes
-
 template <typename IO, int V>
 hipError_t fwd(GArgs g, const GatedWs &W, char *ws, hipStream_t s) {
-    set_chain(g, W, ws, V, s);
-    hipLaunchKernelGGL((k_gated_fwd<IO, V, kSegF>), dim3((unsigned)(g.b * g.ncol * g.tiles)),
-                       dim3(kGT / kSegF * 64), 0, s, g);
+    typedef FwdShape<IO> F;
+    set_chain(g, W, ws, V, F::SEG * F::NW, s);
+    hipLaunchKernelGGL((k_gated_fwd<IO, V, F::SEG, F::NW>),
+                       dim3((unsigned)(g.b * g.ncol * g.tiles)), dim3(F::NW * 64), 0, s, g);
     return hipGetLastError();
 }
 
 template <typename IO, int V>
 hipError_t bwd(GArgs g, const GatedWs &W, char *ws, float *dlam, hipStream_t s) {
-    if (g.tiles > 1 && !g.kept) {
+    typedef BwdShape B;
+    if (!g.kept && g.l > B::SEG * B::NW) {
         GArgs f = g;
         f.y = nullptr, f.fin = nullptr, f.states = reinterpret_cast<float *>(ws + W.kept);
         const hipError_t e = fwd<IO, V>(f, W, ws, s);
         if (e != hipSuccess) return e;
         g.kept = f.states;
     }
-    set_chain(g, W, ws, V, s);
-    hipLaunchKernelGGL((k_gated_bwd<IO, V, kSegB>), dim3((unsigned)(g.b * g.ncol * g.tiles)),
-                       dim3(kGT / kSegB * 64), 0, s, g);
+    set_chain(g, W, ws, V, B::SEG * B::NW, s);
+    hipLaunchKernelGGL((k_gated_bwd<IO, V, B::SEG, B::NW>),
+                       dim3((unsigned)(g.b * g.ncol * g.tiles)), dim3(B::NW * 64), 0, s, g);
     hipLaunchKernelGGL(k_gated_lam, dim3((unsigned)((g.d + 31) / 32)), dim3(1024), 0, s, g.part,
                        g.lam, dlam, g.b * g.tiles, g.d);
     return hipGetLastError();
@@ -717,13 +725,11 @@ int32_t ssd_gated_scan(const void *x, const void *gates, const float *lam, float
     GArgs g{};
     g.x = x, g.gates = gates, g.lam = lam, g.scale = scale, g.init = init_state, g.seq = seq_idx;
     g.y = y, g.fin = final_state, g.states = states;
-    g.b = batch, g.l = seqlen, g.d = dim, g.tiles = (seqlen + kGT - 1) / kGT;
+    g.b = batch, g.l = seqlen, g.d = dim;
     char *ws = static_cast<char *>(workspace);
-    const int v = lanes(io_dtype, dim, io_dtype == SSD_BF16 ? 4 : 2, final_state, states, x, gates, y);
+    const int v = lanes(io_dtype, dim, 2, final_state, states, x, gates, y);
     const hipError_t e = io_dtype == SSD_BF16
-                             ? (v == 4   ? fwd<bf16, 4>(g, W, ws, s)
-                                : v == 2 ? fwd<bf16, 2>(g, W, ws, s)
-                                         : fwd<bf16, 1>(g, W, ws, s))
+                             ? (v == 2 ? fwd<bf16, 2>(g, W, ws, s) : fwd<bf16, 1>(g, W, ws, s))
                              : (v == 2 ? fwd<float, 2>(g, W, ws, s) : fwd<float, 1>(g, W, ws, s));
     return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
@@ -749,7 +755,7 @@ int32_t ssd_gated_scan_bwd(const void *x, const void *gates, const float *lam, f
     GArgs g{};
     g.x = x, g.gates = gates, g.lam = lam, g.scale = scale, g.init = init_state, g.seq = seq_idx;
     g.kept = states, g.dy = dy, g.dfin = d_final, g.y = dx, g.dgates = dgates, g.fin = d_init;
-    g.b = batch, g.l = seqlen, g.d = dim, g.tiles = (seqlen + kGT - 1) / kGT;
+    g.b = batch, g.l = seqlen, g.d = dim;
     char *ws = static_cast<char *>(workspace);
     g.part = reinterpret_cast<float *>(ws + W.part);
     const int v = lanes(io_dtype, dim, 2, d_init, nullptr, x, gates, dy, dx, dgates);
