@@ -169,7 +169,24 @@ __device__ __forceinline__ bool same_document(const GArgs &g, int64_t row0, int6
     return g.seq[row0 + t] == g.seq[row0 + t - 1];
 }
 
-// Decay and added value of the wave's tokens; identity past the end.
+// Zero decay into a document's first token, and the identity past the end.
+template <typename IO, int V, int SEG>
+__device__ __forceinline__ void mask(const GArgs &g, const Tile<IO, V, SEG> &w,
+                                     float (&a)[SEG][V], float (&v)[SEG][V]) {
+    if (w.t0 + SEG <= g.l && !g.seq) return;
+#pragma unroll
+    for (int k = 0; k < SEG; ++k) {
+        const int64_t t = w.t0 + k;
+        const bool in = t < g.l, same = same_document(g, w.row0, t);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            a[k][e] = in ? (same ? a[k][e] : 0.f) : 1.f;
+            v[k][e] = in ? v[k][e] : 0.f;
+        }
+    }
+}
+
+// Decay and added value of the wave's tokens.
 template <typename IO, int V, int SEG>
 __device__ __forceinline__ void terms(const GArgs &g, const Tile<IO, V, SEG> &w,
                                       const Rows<IO, V, SEG> &rw, const float (&m2)[V],
@@ -187,17 +204,7 @@ __device__ __forceinline__ void terms(const GArgs &g, const Tile<IO, V, SEG> &w,
         // this the scheduler interleaves the rows and spills
         __builtin_amdgcn_sched_barrier(0);
     }
-    if (w.t0 + SEG <= g.l && !g.seq) return;
-#pragma unroll
-    for (int k = 0; k < SEG; ++k) {
-        const int64_t t = w.t0 + k;
-        const bool in = t < g.l, same = same_document(g, w.row0, t);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            a[k][e] = in ? (same ? a[k][e] : 0.f) : 1.f;
-            v[k][e] = in ? v[k][e] : 0.f;
-        }
-    }
+    mask(g, w, a, v);
 }
 
 template <typename IO, int V, int SEG>
@@ -431,8 +438,20 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
         h[e] = tile > 0 ? g.kept[(bi * ns + tile * T / SSD_GATED_CHUNK - 1) * g.d + ch]
                         : (g.init ? g.init[bi * g.d + ch] : 0.f);
     }
-    float a[SEG][V], v[SEG][V];
-    terms(g, w, rw, m2, a, v);
+    // kept for the second half: the decay, both gates and 1 - a^2
+    float a[SEG][V], v[SEG][V], sr[SEG][V], si[SEG][V], om[SEG][V];
+#pragma unroll
+    for (int k = 0; k < SEG; ++k) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            sr[k][e] = sigmoid_f(to_f32(rw.r[k].e[e]));
+            si[k][e] = sigmoid_f(to_f32(rw.i[k].e[e]));
+            decay(m2[e] * sr[k][e], a[k][e], om[k][e]);
+            v[k][e] = __builtin_amdgcn_sqrtf(om[k][e]) * si[k][e] * to_f32(rw.x[k].e[e]);
+        }
+        __builtin_amdgcn_sched_barrier(0);  // as in terms()
+    }
+    mask(g, w, a, v);
     VecF<V> A, S, R;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -471,7 +490,7 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
         }
     VecF<V> acc;
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc.e[e] = 0.f;
+    for (int e = 0; e < V; ++e) acc.e[e] = 0.f, m2[e] *= kLn2;
 #pragma unroll
     for (int k = SEG - 1; k >= 0; --k) {
         const int64_t t = w.t0 + k;
@@ -479,22 +498,21 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
         VecIO<IO, V> ox, orr, oi;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const float gt = to_f32(dy[k].e[e]) + q[e];
-            const float sr = sigmoid_f(to_f32(rw.r[k].e[e])), si = sigmoid_f(to_f32(rw.i[k].e[e]));
-            const float x = to_f32(rw.x[k].e[e]), u2 = m2[e] * sr;
-            float aa, om;
-            decay(u2, aa, om);
-            // beta and its inverse; a shut gate (om = 0) has beta = 0 and a
-            // finite stand-in for the inverse, which u = 0 then cancels
-            const float rb = __builtin_amdgcn_rsqf(fmaxf(om, 1e-30f));
-            const float gx = gt * si, gb = gx * (om * rb), gxx = gx * x;
+            const float x = to_f32(rw.x[k].e[e]), gt = to_f32(dy[k].e[e]) + q[e];
+            // 1 / beta; a shut gate (om = 0) has beta = om rb = 0 and a finite
+            // stand-in for the inverse, which u = 0 then cancels
+            const float rb = __builtin_amdgcn_rsqf(fmaxf(om[k][e], 1e-30f));
+            const float gx = gt * si[k][e], gb = gx * (om[k][e] * rb), gbx = gb * x;
             q[e] = a[k][e] * gt;
-            const float p = kLn2 * u2 * fmaf(aa * aa * rb, gxx, -q[e] * v[k][e]);
+            // a^2 = 1 - om also where a token starts a document (a = 0 there)
+            const float p = m2[e] * sr[k][e] *
+                            fmaf((1.f - om[k][e]) * rb, gx * x, -q[e] * v[k][e]);
             ox.e[e] = (IO)gb;
-            oi.e[e] = (IO)(gb * x * (1.f - si));
-            orr.e[e] = (IO)(p * (1.f - sr));
+            oi.e[e] = (IO)fmaf(-gbx, si[k][e], gbx);
+            orr.e[e] = (IO)fmaf(-p, sr[k][e], p);
             acc.e[e] += p;
         }
+        __builtin_amdgcn_sched_barrier(0);
         if (w.live) {
             const int64_t at = (w.row0 + t) * g.d + w.c;
             stv<IO, V>(g.y, at, ox);
@@ -631,7 +649,7 @@ bool gated_sizes(int64_t b, int64_t l, int64_t d) {
 
 // Tokens per wave and waves per workgroup of the two passes.
 template <typename IO> struct FwdShape { static constexpr int SEG = sizeof(IO) == 2 ? 16 : 8, NW = 8; };
-struct BwdShape { static constexpr int SEG = 4, NW = 16; };
+struct BwdShape { static constexpr int SEG = 8, NW = 8; };
 
 // The columns' layout at lane width v and `tokens` a tile, the cleared tickets
 // and flags and the rates.
