@@ -10,6 +10,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 #include "../../include/ssd.h"
 #include "ssd_device.hpp"
 
@@ -66,7 +68,7 @@ template <> struct Mma<float> {
 
 // What becomes of a product's elements.
 struct Epi {
-    void *out;           // io elements, or fp32 parts [split][m][n]
+    void *out;           // [m][n]
     const float *bias;   // [n] or NULL
     const void *res;     // [m][n] or NULL
     void *pre;           // [m][n] or NULL
@@ -79,6 +81,7 @@ struct GemmArgs {
     int64_t m, n, k;
     int64_t tm, tn;      // tiles
     int64_t split, kper; // contraction parts, elements per part (a multiple of the step)
+    float *parts;        // [split][m][n] where split > 1
     Epi ep;
 };
 
@@ -124,38 +127,49 @@ template <typename IO, bool TR, int BM> struct OpTile {
     static constexpr int BYTES = ROWS * CH * 16;
     static __device__ __forceinline__ int f(int r) {
         if (!TR) return r & 7;
-        if (sizeof(IO) == 2) return (((r & 3) | ((r >> 1) & 4)) << 1) & (CH - 1);
-        return (((r >> 2) & 3) << 2) & (CH - 1);
+        constexpr int M = (CH & -CH) - 1;  // the swap stays inside aligned runs of a row's chunks
+        if (sizeof(IO) == 2) return (((r & 3) | ((r >> 1) & 4)) << 1) & M;
+        return (((r >> 2) & 3) << 2) & M;
     }
 };
 
-template <typename IO, bool TR, int BM, int NT>
-__device__ __forceinline__ void stage(const GemmArgs &g, const void *src, int64_t ld, int64_t m0,
-                                      int64_t mEnd, int64_t k0, int64_t kEnd, char *lds) {
+// This thread's share of an operand tile's copies into LDS: byte offsets from
+// the tile's first element, the same in every step of the contraction.
+template <typename IO, bool TR, int BM, int NT> struct Copies {
     typedef OpTile<IO, TR, BM> T;
-    const int tid = threadIdx.x;
-    const IO *base;
-    int64_t bytes;
-    if (TR) {
-        base = static_cast<const IO *>(src) + k0 * ld + m0;
-        bytes = ((kEnd - k0) * ld - m0) * (int64_t)sizeof(IO);
-    } else {
-        base = static_cast<const IO *>(src) + m0 * ld + k0;
-        bytes = ((mEnd - m0) * ld - k0) * (int64_t)sizeof(IO);
+    static constexpr int N = T::BYTES / 16 / NT;
+    static_assert(T::BYTES % (16 * NT) == 0, "every wave copies as much");
+    uint32_t off[N];
+    static __device__ __forceinline__ int chunk(int slot) {
+        return slot % T::CH ^ T::f(slot / T::CH);
     }
-    // offsets inside a tile stay below 2^31, so a resource never has to reach
-    // further, and the offset of a masked piece lies past every resource
-    const RsrcW r = make_rsrc_w(base, bytes < 0x7fffffff ? bytes : 0x7fffffff);
-    constexpr int N = T::BYTES / 16 / NT;
-    static_assert(T::BYTES % (16 * NT) == 0, "tile copies");
+    __device__ __forceinline__ void init(int64_t ld) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int slot = i * NT + tid, row = slot / T::CH, ch = (slot % T::CH) ^ T::f(row);
-        uint32_t off = (uint32_t)(row * ld + ch * T::EPC) * (uint32_t)sizeof(IO);
-        if (!TR && k0 + ch * T::EPC >= kEnd) off = 0xffffff00u;
-        lds_dma16(r, (lds_void *)(lds + (i * NT + (tid & ~63)) * 16), off);
+        for (int i = 0; i < N; ++i) {
+            const int slot = i * NT + (int)threadIdx.x;
+            off[i] = (uint32_t)(slot / T::CH * ld + chunk(slot) * T::EPC) * (uint32_t)sizeof(IO);
+        }
     }
-}
+    // Rows m0 .. of the operand (it has mEnd), contraction k0 .. kEnd.  What
+    // lies past either end is written as zeros; k0 >= kEnd writes zeros only.
+    // Offsets inside a tile stay below 2^31, so a resource never has to reach
+    // further, and the offset of a masked piece lies past every resource.
+    __device__ __forceinline__ void go(const void *src, int64_t ld, int64_t m0, int64_t mEnd,
+                                       int64_t k0, int64_t kEnd, char *lds) const {
+        const int64_t first = TR ? k0 * ld + m0 : m0 * ld + k0;
+        const int64_t end = TR ? kEnd * ld : mEnd * ld;
+        int64_t bytes = k0 < kEnd ? (end - first) * (int64_t)sizeof(IO) : 0;
+        if (bytes > 0x7fffffff) bytes = 0x7fffffff;
+        const RsrcW r = make_rsrc_w(static_cast<const IO *>(src) + first, bytes);
+        const bool tail = !TR && k0 + T::BK > kEnd;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            uint32_t o = off[i];
+            if (tail && k0 + chunk(i * NT + (int)threadIdx.x) * T::EPC >= kEnd) o = 0xffffff00u;
+            lds_dma16(r, (lds_void *)(lds + (i * NT + (threadIdx.x & ~63)) * 16), o);
+        }
+    }
+};
 
 // The 16-byte operand piece of lane l: tile row m = r0 + (l & 15), contraction
 // chunk 4 j + (l >> 4) of the step.
@@ -189,19 +203,25 @@ __device__ __forceinline__ u32x4 piece(const char *lds, int r0, int j, int lane)
     }
 }
 
-// One workgroup: a BM x BN tile of D over one contraction part.  WM x WN waves.
-template <typename IO, bool TA, bool TB, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64) void k_gemm(GemmArgs g) {
+constexpr int64_t kBand = 8;
+
+// One workgroup: a BM x BN tile of D over one contraction part, WM x WN waves,
+// ST steps of both operands in LDS: ST - 1 are in flight while one is
+// multiplied.
+template <typename IO, bool TA, bool TB, int BM, int BN, int WM, int WN, int ST>
+__device__ __forceinline__ void gemm_tile(const GemmArgs &g, int64_t item, char *lds) {
     constexpr int NT = WM * WN * 64;
     typedef OpTile<IO, TA, BM> OA;
     typedef OpTile<IO, TB, BN> OB;
-    constexpr int BK = OA::BK;
+    constexpr int BK = OA::BK, SIZE = OA::BYTES + OB::BYTES;
     constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
-    __shared__ __align__(16) char lds[2][OA::BYTES + OB::BYTES];
     const int lane = threadIdx.x & 63, wv = wave_id();
-    const int64_t item = xcd_item(blockIdx.x, gridDim.x);
     const int64_t part = item / (g.tm * g.tn), tile = item % (g.tm * g.tn);
-    const int64_t m0 = tile / g.tn * BM, n0 = tile % g.tn * BN;
+    // tiles in bands of kBand tile rows, down the rows first: the tiles that run
+    // at one time on an XCD (consecutive items) share rows of both operands
+    const int64_t band = tile / (kBand * g.tn), in = tile % (kBand * g.tn);
+    const int64_t rows = g.tm - band * kBand < kBand ? g.tm - band * kBand : kBand;
+    const int64_t m0 = (band * kBand + in % rows) * BM, n0 = in / rows * BN;
     const int64_t k0 = part * g.kper, kEnd = k0 + g.kper < g.k ? k0 + g.kper : g.k;
     const int wm = wv / WN * (BM / WM), wn = wv % WN * (BN / WN);
     f32x4 acc[MI][NI];
@@ -209,17 +229,25 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm(GemmArgs g) {
     for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < NI; ++j) acc[i][j] = zero4();
-    auto copy = [&](int64_t k, int buf) {
-        stage<IO, TA, BM, NT>(g, g.A, g.lda, m0, g.m, k, kEnd, lds[buf]);
-        stage<IO, TB, BN, NT>(g, g.B, g.ldb, n0, g.n, k, kEnd, lds[buf] + OA::BYTES);
+    Copies<IO, TA, BM, NT> ca;
+    Copies<IO, TB, BN, NT> cb;
+    ca.init(g.lda);
+    cb.init(g.ldb);
+    auto copy = [&](int64_t k, int slot) {
+        ca.go(g.A, g.lda, m0, g.m, k, kEnd, lds + slot * SIZE);
+        cb.go(g.B, g.ldb, n0, g.n, k, kEnd, lds + slot * SIZE + OA::BYTES);
     };
-    int buf = 0;
-    copy(k0, 0);
+    constexpr int PER = ca.N + cb.N;  // copies a wave issues per step
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) copy(k0 + i * BK, i);
+    int slot = 0;
     for (int64_t k = k0; k < kEnd; k += BK) {
-        vm_wait<0>();
+        // this step's copies have landed (the ST - 2 steps after it may be in
+        // flight), and everyone has read the step before, whose slot is next
+        vm_wait<(ST - 2) * PER>();
         lds_barrier();
-        if (k + BK < kEnd) copy(k + BK, buf ^ 1);
-        const char *a = lds[buf], *b = lds[buf] + OA::BYTES;
+        copy(k + (ST - 1) * BK, slot == 0 ? ST - 1 : slot - 1);
+        const char *a = lds + slot * SIZE, *b = a + OA::BYTES;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             u32x4 pa[MI], pb[NI];
@@ -232,8 +260,9 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm(GemmArgs g) {
 #pragma unroll
                 for (int n = 0; n < NI; ++n) acc[i][n] = Mma<IO>::go(pb[n], pa[i], acc[i][n]);
         }
-        buf ^= 1;
+        slot = slot + 1 == ST ? 0 : slot + 1;
     }
+    vm_wait<0>();  // the copies of zeros behind the last step
     // element r of a lane: row m of lane & 15, column 4 (lane >> 4) + r
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -244,7 +273,7 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm(GemmArgs g) {
             const int64_t n = n0 + wn + 16 * j + 4 * (lane >> 4);
             if (n >= g.n) continue;
             if (g.split > 1) {
-                float *p = static_cast<float *>(g.ep.out) + (part * g.m + m) * g.n + n;
+                float *p = g.parts + (part * g.m + m) * g.n + n;
                 if (g.n % 4 == 0)
                     *reinterpret_cast<f32x4 *>(p) = acc[i][j];
                 else
@@ -256,64 +285,250 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm(GemmArgs g) {
     }
 }
 
-// Sums the contraction parts in order and finishes the elements.
-template <typename IO>
-__global__ __launch_bounds__(256) void k_gemm_sum(const float *parts, int64_t split, int64_t m,
-                                                  int64_t n, Epi ep) {
-    const int64_t q = (n + 3) / 4, k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k >= m * q) return;
-    const int64_t row = k / q, col = k % q * 4;
+template <typename IO, bool TA, bool TB, int BM, int BN, int ST> constexpr int lds_bytes() {
+    return ST * (OpTile<IO, TA, BM>::BYTES + OpTile<IO, TB, BN>::BYTES);
+}
+
+// The forward product.
+template <typename IO, int BM, int BN, int WM, int WN, int ST>
+__global__ __launch_bounds__(WM * WN * 64) void k_gemm(GemmArgs g) {
+    __shared__ __align__(16) char lds[lds_bytes<IO, false, false, BM, BN, ST>()];
+    gemm_tile<IO, false, false, BM, BN, WM, WN, ST>(g, xcd_item(blockIdx.x, gridDim.x), lds);
+}
+
+// The gradient's two products in one launch: dx = e W, then dW = e^T x.
+template <typename IO, int BM, int BN, int WM, int WN, int ST>
+__global__ __launch_bounds__(WM * WN * 64) void k_gemm_bwd(GemmArgs gx, GemmArgs gw) {
+    __shared__ __align__(16) char lds[lds_bytes<IO, true, true, BM, BN, ST>()];
+    const int64_t item = xcd_item(blockIdx.x, gridDim.x), nx = gx.tm * gx.tn * gx.split;
+    if (item < nx)
+        gemm_tile<IO, false, true, BM, BN, WM, WN, ST>(gx, item, lds);
+    else
+        gemm_tile<IO, true, true, BM, BN, WM, WN, ST>(gw, item - nx, lds);
+}
+
+// Four consecutive elements of a product in parts: their sum in the parts'
+// order, and what follows it.
+template <typename IO> __device__ __forceinline__ void sum_parts(const GemmArgs &g, int64_t k) {
+    const int64_t q = (g.n + 3) / 4, row = k / q, col = k % q * 4;
     f32x4 v = zero4();
-    for (int64_t s = 0; s < split; ++s) {
-        const float *p = parts + (s * m + row) * n + col;
-        if (n % 4 == 0)
+    for (int64_t s = 0; s < g.split; ++s) {
+        const float *p = g.parts + (s * g.m + row) * g.n + col;
+        if (g.n % 4 == 0)
             v += *reinterpret_cast<const f32x4 *>(p);
         else
-            for (int r = 0; r < 4 && col + r < n; ++r) v[r] += p[r];
+            for (int r = 0; r < 4 && col + r < g.n; ++r) v[r] += p[r];
     }
-    finish4<IO>(ep, row, col, n, v);
+    finish4<IO>(g.ep, row, col, g.n, v);
+}
+template <typename IO> __global__ __launch_bounds__(256) void k_gemm_sum(GemmArgs g) {
+    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (k < g.m * ((g.n + 3) / 4)) sum_parts<IO>(g, k);
 }
 
-// --------------------------------------------------------------- helpers ----
-// Rows of `cols` elements laid out again with `ld` elements a row, zeros behind them.
-template <typename IO>
-__global__ __launch_bounds__(256) void k_pad_rows(const IO *src, IO *dst, int64_t rows, int64_t cols,
-                                                  int64_t ld) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
-        if (c < ld) dst[r * ld + c] = c < cols ? src[r * cols + c] : (IO)0.f;
-}
+// ------------------------------------------------------------- few rows ----
+// Up to 16 MT rows of x (decoded tokens): bound by the weight's bytes.  A
+// workgroup owns 16 weight rows, its waves 128-byte pieces of them in turn,
+// loaded from memory straight into operands; the waves' sums meet in LDS and
+// are added in order.
+constexpr int kFewWaves = 8;
+constexpr int kFewUnroll = 4;  // weight pieces in flight a wave
 
-// e = dy act'(pre) in the io type (e NULL: not written) with ld elements a row
-// and zeros behind the row, and its fp32 sums over runs of kBiasRows rows.
-constexpr int kBiasRows = 64;
-template <typename IO>
-__global__ __launch_bounds__(256) void k_act_bwd(const IO *dy, const IO *pre, IO *e, float *part,
-                                                 int64_t m, int64_t n, int64_t ld, int act) {
-    const int64_t c = (int64_t)blockIdx.y * 256 + threadIdx.x;
-    if (c >= ld) return;
-    const int64_t r0 = (int64_t)blockIdx.x * kBiasRows;
-    const int64_t r1 = r0 + kBiasRows < m ? r0 + kBiasRows : m;
-    float s = 0.f;
-    for (int64_t r = r0; r < r1; ++r) {
-        float v = 0.f;
-        if (c < n) {
-            v = to_f32(dy[r * n + c]);
-            if (pre) v *= act_grad(to_f32(pre[r * n + c]), act);
+template <typename IO, int MT>
+__global__ __launch_bounds__(kFewWaves * 64) void k_few(GemmArgs g) {
+    constexpr int EPC = 16 / (int)sizeof(IO), BK = 8 * EPC;
+    __shared__ f32x4 part[kFewWaves][MT][64];
+    const int lane = threadIdx.x & 63, wv = wave_id();
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int c = lane & 15, q = lane >> 4;
+    const int64_t nr = n0 + c < g.n ? n0 + c : g.n - 1;
+    const IO *w = static_cast<const IO *>(g.B) + nr * g.ldb;
+    const IO *x[MT];
+    bool live[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        live[t] = t * 16 + c < g.m;
+        x[t] = static_cast<const IO *>(g.A) + (live[t] ? t * 16 + c : 0) * g.lda;
+    }
+    f32x4 acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = zero4();
+    const u32x4 none = {0, 0, 0, 0};
+    auto steps = [&](int64_t k, auto whole) {
+        u32x4 pw[2 * kFewUnroll], px[2 * kFewUnroll][MT];
+#pragma unroll
+        for (int i = 0; i < 2 * kFewUnroll; ++i) {
+            const int64_t at = k + i / 2 * (kFewWaves * BK) + (4 * (i & 1) + q) * EPC;
+            const bool in = decltype(whole)::value || at < g.k;
+            pw[i] = *reinterpret_cast<const u32x4 *>(w + (in ? at : 0));
+            if (!in) pw[i] = none;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                px[i][t] = *reinterpret_cast<const u32x4 *>(x[t] + (in ? at : 0));
+                if (!in || !live[t]) px[i][t] = none;
+            }
         }
-        s += v;
-        if (e) e[r * ld + c] = (IO)v;
+#pragma unroll
+        for (int i = 0; i < 2 * kFewUnroll; ++i)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) acc[t] = Mma<IO>::go(pw[i], px[i][t], acc[t]);
+    };
+    constexpr int64_t RUN = (int64_t)kFewUnroll * kFewWaves * BK;
+    for (int64_t k = wv * BK; k < g.k; k += RUN) {
+        if (k + RUN <= g.k)
+            steps(k, std::true_type{});
+        else
+            steps(k, std::false_type{});
     }
-    if (part && c < n) part[blockIdx.x * n + c] = s;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) part[wv][t][lane] = acc[t];
+    __syncthreads();
+    if (wv >= MT) return;
+    f32x4 v = part[0][wv][lane];
+#pragma unroll
+    for (int k = 1; k < kFewWaves; ++k) v += part[k][wv][lane];
+    const int64_t m = wv * 16 + c, n = n0 + 4 * q;
+    if (m < g.m && n < g.n) finish4<IO>(g.ep, m, n, g.n, v);
 }
 
-__global__ __launch_bounds__(256) void k_bias_sum(const float *part, float *db, int64_t rows,
-                                                  int64_t n) {
-    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (c >= n) return;
-    float s = 0.f;
-    for (int64_t r = 0; r < rows; ++r) s += part[r * n + c];
-    db[c] = s;
+// ------------------------------------------------------------ gradient ----
+// Everything before the gradient's products in one launch, in 8-element pieces
+// of rows (rows of odd widths start at any element; the memory takes vector
+// accesses there too): e = dy act'(pre), with its fp32 column sums over runs
+// of kBiasRows rows, and x and W laid out again with padded rows.
+constexpr int kBiasRows = 64;
+
+struct PrepArgs {
+    const void *dy, *pre, *x, *w;
+    void *e, *px, *pw;        // NULL: not wanted
+    float *part;              // [runs][n] column sums of e, or NULL
+    int64_t m, n, k, ln, lk;  // ln, lk: elements per padded row
+    int act;
+    int64_t eb, xb, wb;       // workgroups of each piece of work
+};
+
+template <typename IO> struct alignas(16) Piece { IO v[8]; };
+
+// Elements c .. c + 7 of a row of `width`, zeros past its end.
+template <typename IO>
+__device__ __forceinline__ Piece<IO> row_piece(const IO *row, int64_t c, int64_t width) {
+    Piece<IO> p;
+    if (c + 8 <= width) {
+        __builtin_memcpy(&p, row + c, sizeof(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p.v[i] = c + i < width ? row[c + i] : (IO)0.f;
+    }
+    return p;
+}
+
+// Rows of `cols` elements laid out with `ld` a row (a multiple of 8), zeros
+// behind them; workgroup `block` of a grid of them.
+template <typename IO>
+__device__ __forceinline__ void pad_rows(const void *src, void *dst, int64_t rows, int64_t cols,
+                                         int64_t ld, int64_t block) {
+    const int64_t per = ld / 8, k = block * 256 + threadIdx.x;
+    if (k >= rows * per) return;
+    const int64_t r = k / per, c = k % per * 8;
+    *reinterpret_cast<Piece<IO> *>(static_cast<IO *>(dst) + r * ld + c) =
+        row_piece(static_cast<const IO *>(src) + r * cols, c, cols);
+}
+
+template <typename IO> __global__ __launch_bounds__(256) void k_pad(PrepArgs g) {
+    const int64_t b = blockIdx.x;
+    if (b < g.xb)
+        pad_rows<IO>(g.x, g.px, g.m, g.k, g.lk, b);
+    else
+        pad_rows<IO>(g.w, g.pw, g.n, g.k, g.lk, b - g.xb);
+}
+
+template <typename IO> __global__ __launch_bounds__(256) void k_bwd_prep(PrepArgs g) {
+    __shared__ float sums[4][64 * 8];
+    int64_t b = blockIdx.x;
+    if (b >= g.eb) {
+        b -= g.eb;
+        if (b < g.xb)
+            pad_rows<IO>(g.x, g.px, g.m, g.k, g.lk, b);
+        else
+            pad_rows<IO>(g.w, g.pw, g.n, g.k, g.lk, b - g.xb);
+        return;
+    }
+    // a wave: 512 columns of a quarter of the run's rows
+    const int lane = threadIdx.x & 63, wv = wave_id();
+    const int64_t cols = (g.ln + 511) / 512, run = b / cols, c = (b % cols * 64 + lane) * 8;
+    constexpr int R = kBiasRows / 4, U = 4;
+    const int64_t r0 = run * kBiasRows + wv * R;
+    const IO *dy = static_cast<const IO *>(g.dy), *pre = static_cast<const IO *>(g.pre);
+    float s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = 0.f;
+    if (c < g.ln) {
+        for (int64_t r = r0; r < r0 + R && r < g.m; r += U) {
+            Piece<IO> d[U], p[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t row = r + u < g.m ? r + u : g.m - 1;
+                d[u] = row_piece(dy + row * g.n, c, g.n);
+                if (pre) p[u] = row_piece(pre + row * g.n, c, g.n);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (r + u >= g.m) break;
+                Piece<IO> o;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float v = to_f32(d[u].v[i]);
+                    if (pre) v *= act_grad(to_f32(p[u].v[i]), g.act);
+                    s[i] += v;
+                    o.v[i] = (IO)v;
+                }
+                if (g.e)
+                    *reinterpret_cast<Piece<IO> *>(static_cast<IO *>(g.e) + (r + u) * g.ln + c) = o;
+            }
+        }
+    }
+    if (!g.part) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[wv][i * 64 + lane] = s[i];
+    __syncthreads();
+    for (int k = threadIdx.x; k < 512; k += 256) {
+        const int64_t col = b % cols * 512 + (k & 63) * 8 + (k >> 6);
+        if (col < g.n)
+            g.part[run * g.n + col] = (sums[0][k] + sums[1][k]) + (sums[2][k] + sums[3][k]);
+    }
+}
+
+// Everything after them in one launch: the sums of products in parts, and the
+// bias gradient from its runs' sums (a workgroup: 32 columns by 8 runs at a
+// time, added in a fixed order).
+template <typename IO>
+__global__ __launch_bounds__(256) void k_bwd_finish(GemmArgs gx, GemmArgs gw, int64_t xb, int64_t wb,
+                                                    const float *part, int64_t runs, float *db) {
+    __shared__ float s[8][32];
+    int64_t b = blockIdx.x;
+    if (b < xb) {
+        const int64_t k = b * 256 + threadIdx.x;
+        if (k < gx.m * ((gx.n + 3) / 4)) sum_parts<IO>(gx, k);
+        return;
+    }
+    b -= xb;
+    if (b < wb) {
+        const int64_t k = b * 256 + threadIdx.x;
+        if (k < gw.m * ((gw.n + 3) / 4)) sum_parts<IO>(gw, k);
+        return;
+    }
+    b -= wb;
+    const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const int64_t col = b * 32 + c, n = gw.m;
+    float t = 0.f;
+    if (col < n)
+        for (int64_t r = q; r < runs; r += 8) t += part[r * n + col];
+    s[q][c] = t;
+    __syncthreads();
+    if (q != 0 || col >= n) return;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) t += s[k][c];
+    db[col] = t;
 }
 
 template <typename IO>
@@ -324,91 +539,163 @@ __global__ __launch_bounds__(256) void k_zero(IO *p, int64_t n) {
 
 // --------------------------------------------------------------- the plan ----
 size_t up(size_t v) { return (v + 255) & ~(size_t)255; }
-int64_t pad(int64_t v, int io) { return io == SSD_BF16 ? (v + 7) / 8 * 8 : (v + 3) / 4 * 4; }
+int64_t pad(int64_t v) { return (v + 7) / 8 * 8; }
+// Whether rows of v elements have to be laid out again: not whole 16-byte pieces.
+bool odd_rows(int64_t v, int io) { return v % (io == SSD_BF16 ? 8 : 4) != 0; }
 int64_t esz(int io) { return io == SSD_BF16 ? 2 : 4; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int kBM = 128, kBN = 128;
+constexpr int64_t kCus = 256;       // compute units of the part this is written for
+constexpr int64_t kFewRows = 32;    // rows up to which k_few runs
 
-// Contraction parts of a product: as many as it takes to give every compute
-// unit a workgroup, none shorter than 8 steps.
-int64_t parts_of(int64_t m, int64_t n, int64_t k, int io) {
-    const int64_t tiles = (m + kBM - 1) / kBM * ((n + kBN - 1) / kBN), step = 128 / esz(io);
-    const int64_t steps = (k + step - 1) / step;
-    int64_t s = 256 / tiles;
-    if (s > steps / 8) s = steps / 8;
-    return s < 1 ? 1 : s;
+// Tile shapes.  A bigger tile moves fewer bytes per product (from L2, which
+// gives 17 TB/s: a 128 x 128 tile runs at that limit) but comes in bigger
+// rounds.
+enum Tile { kT64, kT128, kT128Deep, kT256, kT320, kTiles };
+struct Shape { int bm, bn, per_cu; float step; };
+// per_cu: workgroups a compute unit holds; step: us of one contraction step
+// with all of them running
+constexpr Shape kShape16[] = {{64, 64, 4, 0.60f}, {128, 128, 2, 1.22f}, {128, 128, 1, 0.70f},
+                              {256, 256, 1, 1.90f}, {256, 320, 1, 2.70f}};
+constexpr Shape kShape32[] = {{64, 64, 4, 2.2f}, {128, 128, 2, 4.2f}};
+
+struct Choice { Tile t; int64_t split; };
+
+// Rounds of workgroups times the time of a round, over the products of one
+// launch; with split > 1, also the parts written and read back.
+inline float cost(const Shape &h, int64_t tiles, int64_t steps, int64_t split, int64_t out) {
+    const int64_t rounds = cdiv(tiles * split, kCus * h.per_cu);
+    return rounds * cdiv(steps, split) * h.step +
+           (split > 1 ? 3.f + split * out * 8e-6f / 4.f : 0.f);
 }
-size_t parts_bytes(int64_t m, int64_t n, int64_t k, int io) {
-    const int64_t s = parts_of(m, n, k, io);
-    return s > 1 ? up((size_t)s * m * n * 4) : 0;
+Choice choose(const int64_t (*mnk)[3], int count, int io) {
+    const bool b16 = io == SSD_BF16;
+    Choice best{kT128, 1};
+    float least = 1e30f;
+    const int64_t bk = 128 / esz(io);
+    for (int t = 0; t < (b16 ? kTiles : 2); ++t) {
+        const Shape &h = b16 ? kShape16[t] : kShape32[t];
+        for (int64_t split = 1; split <= 16; split = split < 4 ? split + 1 : split + 4) {
+            int64_t tiles = 0, steps = 0, out = 0;
+            bool ok = true;
+            for (int i = 0; i < count; ++i) {
+                tiles += cdiv(mnk[i][0], h.bm) * cdiv(mnk[i][1], h.bn);
+                const int64_t s = cdiv(mnk[i][2], bk);
+                steps = s > steps ? s : steps;
+                out += mnk[i][0] * mnk[i][1];
+                ok = ok && s / split >= 4;
+            }
+            if (split > 1 && !ok) break;
+            const float c = cost(h, tiles, steps, split, out);
+            if (c < least) least = c, best = {(Tile)t, split};
+        }
+    }
+    return best;
 }
 
-template <typename IO, bool TA, bool TB>
-hipError_t product(const void *A, int64_t lda, const void *B, int64_t ldb, int64_t m, int64_t n,
-                   int64_t k, const Epi &ep, float *parts, hipStream_t s) {
-    const int io = sizeof(IO) == 2 ? SSD_BF16 : SSD_F32;
-    const int64_t step = 128 / (int64_t)sizeof(IO), steps = (k + step - 1) / step;
+GemmArgs plan(const void *A, int64_t lda, const void *B, int64_t ldb, int64_t m, int64_t n,
+              int64_t k, Choice c, const Epi &ep, float *parts, int io) {
+    const Shape &h = io == SSD_BF16 ? kShape16[c.t] : kShape32[c.t];
+    const int64_t bk = 128 / esz(io), steps = cdiv(k, bk);
     GemmArgs g{};
     g.A = A, g.B = B, g.lda = lda, g.ldb = ldb, g.m = m, g.n = n, g.k = k;
-    g.tm = (m + kBM - 1) / kBM, g.tn = (n + kBN - 1) / kBN;
-    g.split = parts_of(m, n, k, io);
-    g.kper = (steps + g.split - 1) / g.split * step;
-    g.split = (k + g.kper - 1) / g.kper;
-    g.ep = ep;
-    if (g.split > 1) g.ep.out = parts;
-    hipLaunchKernelGGL((k_gemm<IO, TA, TB, kBM, kBN, 2, 2>), dim3((unsigned)(g.tm * g.tn * g.split)),
-                       dim3(256), 0, s, g);
-    if (g.split > 1)
-        hipLaunchKernelGGL((k_gemm_sum<IO>), dim3((unsigned)((m * ((n + 3) / 4) + 255) / 256)),
-                           dim3(256), 0, s, parts, g.split, m, n, ep);
-    return hipGetLastError();
+    g.tm = cdiv(m, h.bm), g.tn = cdiv(n, h.bn);
+    g.kper = cdiv(steps, c.split) * bk;
+    g.split = cdiv(k, g.kper);
+    g.parts = parts, g.ep = ep;
+    return g;
+}
+size_t parts_bytes(const GemmArgs &g) {
+    return g.split > 1 ? up((size_t)g.split * g.m * g.n * 4) : 0;
 }
 
-template <typename IO>
-void pad_rows(const void *src, void *dst, int64_t rows, int64_t cols, int64_t ld, hipStream_t s) {
-    const int64_t y = rows < 4096 ? rows : 4096;
-    hipLaunchKernelGGL((k_pad_rows<IO>), dim3((unsigned)((ld + 255) / 256), (unsigned)y), dim3(256), 0,
-                       s, static_cast<const IO *>(src), static_cast<IO *>(dst), rows, cols, ld);
+Choice choose_fwd(int64_t m, int64_t n, int64_t k, int io) {
+    const int64_t mnk[1][3] = {{m, n, k}};
+    return choose(mnk, 1, io);
+}
+Choice choose_bwd(int64_t m, int64_t n, int64_t k, int io) {
+    const int64_t mnk[2][3] = {{m, k, n}, {n, k, m}};
+    return choose(mnk, 2, io);
 }
 
 // Widths up to 2^20 elements and rows up to 2^31: a tile's byte offsets stay
 // below 2^31 and every grid below 2^31 workgroups.
 bool linear_sizes(int64_t m, int64_t n, int64_t k) {
-    const int64_t w = (int64_t)1 << 20;
-    if (n > w || k > w || m >= ((int64_t)1 << 31)) return false;
-    const int64_t big = ((int64_t)1 << 31) - 1;
-    return (m + 127) / 128 * ((n + 127) / 128) <= big && m * ((n + 3) / 4) / 256 < big;
+    const int64_t w = (int64_t)1 << 20, big = ((int64_t)1 << 31) - 1;
+    if (n > w || k > w || m > big) return false;
+    return m * cdiv(n, 4) / 64 < big && m * cdiv(k, 4) / 64 < big && n * cdiv(k, 4) / 64 < big;
+}
+
+size_t fwd_bytes(int64_t m, int64_t n, int64_t k, int io, size_t *copies) {
+    *copies = odd_rows(k, io) ? up(m * pad(k) * esz(io)) + up(n * pad(k) * esz(io)) : 0;
+    if (m <= kFewRows) return *copies;
+    return *copies + parts_bytes(plan(nullptr, 0, nullptr, 0, m, n, k, choose_fwd(m, n, k, io),
+                                      Epi{}, nullptr, io));
 }
 
 template <typename IO>
 int32_t run_linear(const void *x, const void *w, const Epi &ep, int64_t m, int64_t n, int64_t k,
                    char *ws, hipStream_t s) {
     const int io = sizeof(IO) == 2 ? SSD_BF16 : SSD_F32;
-    const int64_t ld = pad(k, io);
-    if (ld != k) {
-        char *px = ws, *pw = ws + up(m * ld * sizeof(IO));
-        pad_rows<IO>(x, px, m, k, ld, s);
-        pad_rows<IO>(w, pw, n, k, ld, s);
-        x = px, w = pw;
-        ws = pw + up(n * ld * sizeof(IO));
+    int64_t ld = k;
+    if (odd_rows(k, io)) {
+        PrepArgs p{};
+        ld = pad(k);
+        p.x = x, p.w = w, p.px = ws, p.pw = ws + up(m * ld * sizeof(IO));
+        p.m = m, p.n = n, p.k = k, p.lk = ld;
+        p.xb = cdiv(m * (ld / 8), 256), p.wb = cdiv(n * (ld / 8), 256);
+        hipLaunchKernelGGL((k_pad<IO>), dim3((unsigned)(p.xb + p.wb)), dim3(256), 0, s, p);
+        x = p.px, w = p.pw;
+        ws = static_cast<char *>(p.pw) + up(n * ld * sizeof(IO));
     }
-    const hipError_t e = product<IO, false, false>(x, ld, w, ld, m, n, k, ep,
-                                                   reinterpret_cast<float *>(ws), s);
-    return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+    if (m <= kFewRows) {
+        GemmArgs g{};
+        g.A = x, g.B = w, g.lda = g.ldb = ld, g.m = m, g.n = n, g.k = ld, g.ep = ep;
+        const dim3 grid((unsigned)cdiv(n, 16)), block(kFewWaves * 64);
+        if (m <= 16)
+            hipLaunchKernelGGL((k_few<IO, 1>), grid, block, 0, s, g);
+        else
+            hipLaunchKernelGGL((k_few<IO, 2>), grid, block, 0, s, g);
+        return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+    }
+    const Choice c = choose_fwd(m, n, k, io);
+    const GemmArgs g = plan(x, ld, w, ld, m, n, k, c, ep, reinterpret_cast<float *>(ws), io);
+    const dim3 grid((unsigned)(g.tm * g.tn * g.split));
+#define SSD_GEMM(BM, BN, WM, WN, ST)                                                              \
+    hipLaunchKernelGGL((k_gemm<IO, BM, BN, WM, WN, ST>), grid, dim3(WM * WN * 64), 0, s, g)
+    if (c.t == kT64) SSD_GEMM(64, 64, 2, 2, 2);
+    else if (c.t == kT128) SSD_GEMM(128, 128, 2, 2, 2);
+    if constexpr (sizeof(IO) == 2) {
+        if (c.t == kT128Deep) SSD_GEMM(128, 128, 2, 2, 4);
+        else if (c.t == kT256) SSD_GEMM(256, 256, 2, 4, 2);
+        else if (c.t == kT320) SSD_GEMM(256, 320, 2, 4, 2);
+    }
+#undef SSD_GEMM
+    if (g.split > 1)
+        hipLaunchKernelGGL((k_gemm_sum<IO>), dim3((unsigned)cdiv(m * cdiv(n, 4), 256)), dim3(256), 0,
+                           s, g);
+    return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
 // Parts of the gradient's workspace.
 struct BwdWs {
-    size_t e, w, x, part, prod, total;
+    bool own_e;
+    int64_t ln, lk, runs;
+    Choice c;
+    size_t e, w, x, part, px, pw, total;
     BwdWs(int64_t m, int64_t n, int64_t k, int act, int io) {
-        const int64_t ln = pad(n, io), lk = pad(k, io), es = esz(io);
+        const int64_t es = esz(io);
+        own_e = act != SSD_ACT_NONE || odd_rows(n, io);
+        ln = own_e ? pad(n) : n, lk = odd_rows(k, io) ? pad(k) : k;
+        runs = cdiv(m, kBiasRows);
+        c = choose_bwd(m, n, k, io);
         size_t o = 0;
-        e = o, o += act != SSD_ACT_NONE || ln != n ? up(m * ln * es) : 0;
+        e = o, o += own_e ? up(m * ln * es) : 0;
         w = o, o += lk != k ? up(n * lk * es) : 0;
         x = o, o += lk != k ? up(m * lk * es) : 0;
-        part = o, o += up((m + kBiasRows - 1) / kBiasRows * n * 4);
-        const size_t p1 = parts_bytes(m, k, n, io), p2 = parts_bytes(n, k, m, io);
-        prod = o, o += p1 > p2 ? p1 : p2;
+        part = o, o += up(runs * n * 4);
+        px = o, o += parts_bytes(plan(nullptr, 0, nullptr, 0, m, k, n, c, Epi{}, nullptr, io));
+        pw = o, o += parts_bytes(plan(nullptr, 0, nullptr, 0, n, k, m, c, Epi{}, nullptr, io));
         total = o;
     }
 };
@@ -418,38 +705,46 @@ int32_t run_linear_bwd(const void *dy, const void *x, const void *w, const void 
                        void *dx, void *dw, float *db, int64_t m, int64_t n, int64_t k, char *ws,
                        hipStream_t s) {
     const int io = sizeof(IO) == 2 ? SSD_BF16 : SSD_F32;
-    const int64_t ln = pad(n, io), lk = pad(k, io);
     const BwdWs L(m, n, k, act, io);
-    const bool own_e = act != SSD_ACT_NONE || ln != n;
-    const void *e = own_e ? ws + L.e : dy;
-    if (own_e || db) {
-        const int64_t rows = (m + kBiasRows - 1) / kBiasRows;
-        hipLaunchKernelGGL((k_act_bwd<IO>), dim3((unsigned)rows, (unsigned)((ln + 255) / 256)),
-                           dim3(256), 0, s, static_cast<const IO *>(dy),
-                           static_cast<const IO *>(act != SSD_ACT_NONE ? pre : nullptr),
-                           own_e ? reinterpret_cast<IO *>(ws + L.e) : nullptr,
-                           db ? reinterpret_cast<float *>(ws + L.part) : nullptr, m, n, ln, act);
-        if (db)
-            hipLaunchKernelGGL(k_bias_sum, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
-                               reinterpret_cast<const float *>(ws + L.part), db, rows, n);
+    PrepArgs p{};
+    p.dy = dy, p.pre = act != SSD_ACT_NONE ? pre : nullptr, p.x = x, p.w = w, p.act = act;
+    p.m = m, p.n = n, p.k = k, p.ln = L.ln, p.lk = L.lk;
+    if (L.own_e) p.e = ws + L.e;
+    if (db) p.part = reinterpret_cast<float *>(ws + L.part);
+    if (p.e || db) p.eb = L.runs * cdiv(pad(L.ln), 512);
+    if (L.lk != k && dw) p.px = ws + L.x, p.xb = cdiv(m * (L.lk / 8), 256);
+    if (L.lk != k && dx) p.pw = ws + L.w, p.wb = cdiv(n * (L.lk / 8), 256);
+    if (p.eb + p.xb + p.wb > 0)
+        hipLaunchKernelGGL((k_bwd_prep<IO>), dim3((unsigned)(p.eb + p.xb + p.wb)), dim3(256), 0, s, p);
+    const void *e = p.e ? p.e : dy;
+    if (p.px) x = p.px;
+    if (p.pw) w = p.pw;
+    GemmArgs gx = plan(e, L.ln, w, L.lk, m, k, n, L.c, Epi{dx, nullptr, nullptr, nullptr, 0},
+                       reinterpret_cast<float *>(ws + L.px), io);
+    GemmArgs gw = plan(e, L.ln, x, L.lk, n, k, m, L.c, Epi{dw, nullptr, nullptr, nullptr, 0},
+                       reinterpret_cast<float *>(ws + L.pw), io);
+    if (!dx) gx.tm = 0;
+    const int64_t items = gx.tm * gx.tn * gx.split + (dw ? gw.tm * gw.tn * gw.split : 0);
+    if (items > 0) {
+#define SSD_GEMM(BM, BN, WM, WN, ST)                                                              \
+    hipLaunchKernelGGL((k_gemm_bwd<IO, BM, BN, WM, WN, ST>), dim3((unsigned)items),               \
+                       dim3(WM * WN * 64), 0, s, gx, gw)
+        if (L.c.t == kT64) SSD_GEMM(64, 64, 2, 2, 2);
+        else if (L.c.t == kT128) SSD_GEMM(128, 128, 2, 2, 2);
+        if constexpr (sizeof(IO) == 2) {
+            if (L.c.t == kT128Deep) SSD_GEMM(128, 128, 2, 2, 4);
+            else if (L.c.t == kT256) SSD_GEMM(256, 256, 2, 4, 2);
+            else if (L.c.t == kT320) SSD_GEMM(256, 320, 2, 4, 2);
+        }
+#undef SSD_GEMM
     }
-    if (lk != k) {
-        if (dx) pad_rows<IO>(w, ws + L.w, n, k, lk, s);
-        if (dw) pad_rows<IO>(x, ws + L.x, m, k, lk, s);
-        w = ws + L.w, x = ws + L.x;
-    }
-    float *parts = reinterpret_cast<float *>(ws + L.prod);
-    hipError_t r = hipGetLastError();
-    Epi ep{};
-    if (dx && r == hipSuccess) {
-        ep.out = dx;
-        r = product<IO, false, true>(e, ln, w, lk, m, k, n, ep, parts, s);
-    }
-    if (dw && r == hipSuccess) {
-        ep.out = dw;
-        r = product<IO, true, true>(e, ln, x, lk, n, k, m, ep, parts, s);
-    }
-    return r == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+    const int64_t xb = dx && gx.split > 1 ? cdiv(m * cdiv(k, 4), 256) : 0;
+    const int64_t wb = dw && gw.split > 1 ? cdiv(n * cdiv(k, 4), 256) : 0;
+    const int64_t bb = db ? cdiv(n, 32) : 0;
+    if (xb + wb + bb > 0)
+        hipLaunchKernelGGL((k_bwd_finish<IO>), dim3((unsigned)(xb + wb + bb)), dim3(256), 0, s, gx, gw,
+                           xb, wb, p.part, L.runs, db);
+    return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
 bool act_ok(int act) { return act >= SSD_ACT_NONE && act <= SSD_ACT_SIGMOID; }
@@ -466,9 +761,8 @@ size_t ssd_linear_workspace_bytes(int64_t rows, int64_t in_dim, int64_t out_dim,
     if ((io_dtype != SSD_F32 && io_dtype != SSD_BF16) || rows <= 0 || in_dim <= 0 || out_dim <= 0 ||
         !linear_sizes(rows, out_dim, in_dim))
         return 0;
-    const int64_t ld = pad(in_dim, io_dtype), es = esz(io_dtype);
-    const size_t copies = ld != in_dim ? up(rows * ld * es) + up(out_dim * ld * es) : 0;
-    return copies + parts_bytes(rows, out_dim, in_dim, io_dtype);
+    size_t copies;
+    return fwd_bytes(rows, out_dim, in_dim, io_dtype, &copies);
 }
 
 size_t ssd_linear_bwd_workspace_bytes(int64_t rows, int64_t in_dim, int64_t out_dim,
@@ -508,8 +802,7 @@ int32_t ssd_linear_bwd(const void *dy, const void *x, const void *weight, const 
                        size_t workspace_bytes, void *hip_stream) {
     if (io_dtype != SSD_F32 && io_dtype != SSD_BF16) return SSD_ERR_UNSUPPORTED;
     if (rows < 0 || in_dim <= 0 || out_dim <= 0) return SSD_ERR_SHAPE;
-    if (!act_ok(activation) || !linear_sizes(rows, out_dim, in_dim) ||
-        !linear_sizes(out_dim, in_dim, 1))
+    if (!act_ok(activation) || !linear_sizes(rows, out_dim, in_dim))
         return SSD_ERR_UNSUPPORTED;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     const int64_t es = esz(io_dtype);
