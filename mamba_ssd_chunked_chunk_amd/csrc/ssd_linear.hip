@@ -203,25 +203,26 @@ __device__ __forceinline__ u32x4 piece(const char *lds, int r0, int j, int lane)
     }
 }
 
-constexpr int64_t kBand = 8;
+constexpr uint32_t kBand = 8;
 
 // One workgroup: a BM x BN tile of D over one contraction part, WM x WN waves,
 // ST steps of both operands in LDS: ST - 1 are in flight while one is
 // multiplied.
 template <typename IO, bool TA, bool TB, int BM, int BN, int WM, int WN, int ST>
-__device__ __forceinline__ void gemm_tile(const GemmArgs &g, int64_t item, char *lds) {
+__device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint32_t item, char *lds) {
     constexpr int NT = WM * WN * 64;
     typedef OpTile<IO, TA, BM> OA;
     typedef OpTile<IO, TB, BN> OB;
     constexpr int BK = OA::BK, SIZE = OA::BYTES + OB::BYTES;
     constexpr int MI = BM / WM / 16, NI = BN / WN / 16;
     const int lane = threadIdx.x & 63, wv = wave_id();
-    const int64_t part = item / (g.tm * g.tn), tile = item % (g.tm * g.tn);
+    const uint32_t tn = (uint32_t)g.tn, all = (uint32_t)g.tm * tn;
+    const uint32_t part = item / all, tile = item % all;
     // tiles in bands of kBand tile rows, down the rows first: the tiles that run
     // at one time on an XCD (consecutive items) share rows of both operands
-    const int64_t band = tile / (kBand * g.tn), in = tile % (kBand * g.tn);
-    const int64_t rows = g.tm - band * kBand < kBand ? g.tm - band * kBand : kBand;
-    const int64_t m0 = (band * kBand + in % rows) * BM, n0 = in / rows * BN;
+    const uint32_t band = tile / (kBand * tn), in = tile % (kBand * tn);
+    const uint32_t left = (uint32_t)g.tm - band * kBand, rows = left < kBand ? left : kBand;
+    const int64_t m0 = (int64_t)(band * kBand + in % rows) * BM, n0 = (int64_t)(in / rows) * BN;
     const int64_t k0 = part * g.kper, kEnd = k0 + g.kper < g.k ? k0 + g.kper : g.k;
     const int wm = wv / WN * (BM / WM), wn = wv % WN * (BN / WN);
     f32x4 acc[MI][NI];
@@ -293,14 +294,16 @@ template <typename IO, bool TA, bool TB, int BM, int BN, int ST> constexpr int l
 template <typename IO, int BM, int BN, int WM, int WN, int ST>
 __global__ __launch_bounds__(WM * WN * 64) void k_gemm(GemmArgs g) {
     __shared__ __align__(16) char lds[lds_bytes<IO, false, false, BM, BN, ST>()];
-    gemm_tile<IO, false, false, BM, BN, WM, WN, ST>(g, xcd_item(blockIdx.x, gridDim.x), lds);
+    gemm_tile<IO, false, false, BM, BN, WM, WN, ST>(
+        g, (uint32_t)xcd_item(blockIdx.x, gridDim.x), lds);
 }
 
 // The gradient's two products in one launch: dx = e W, then dW = e^T x.
 template <typename IO, int BM, int BN, int WM, int WN, int ST>
 __global__ __launch_bounds__(WM * WN * 64) void k_gemm_bwd(GemmArgs gx, GemmArgs gw) {
     __shared__ __align__(16) char lds[lds_bytes<IO, true, true, BM, BN, ST>()];
-    const int64_t item = xcd_item(blockIdx.x, gridDim.x), nx = gx.tm * gx.tn * gx.split;
+    const uint32_t item = (uint32_t)xcd_item(blockIdx.x, gridDim.x);
+    const uint32_t nx = (uint32_t)(gx.tm * gx.tn * gx.split);
     if (item < nx)
         gemm_tile<IO, false, true, BM, BN, WM, WN, ST>(gx, item, lds);
     else
@@ -309,8 +312,9 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_bwd(GemmArgs gx, GemmArgs
 
 // Four consecutive elements of a product in parts: their sum in the parts'
 // order, and what follows it.
-template <typename IO> __device__ __forceinline__ void sum_parts(const GemmArgs &g, int64_t k) {
-    const int64_t q = (g.n + 3) / 4, row = k / q, col = k % q * 4;
+template <typename IO> __device__ __forceinline__ void sum_parts(const GemmArgs &g, uint32_t k) {
+    const uint32_t q = (uint32_t)((g.n + 3) / 4);
+    const int64_t row = k / q, col = (int64_t)(k % q) * 4;
     f32x4 v = zero4();
     for (int64_t s = 0; s < g.split; ++s) {
         const float *p = g.parts + (s * g.m + row) * g.n + col;
@@ -323,7 +327,7 @@ template <typename IO> __device__ __forceinline__ void sum_parts(const GemmArgs 
 }
 template <typename IO> __global__ __launch_bounds__(256) void k_gemm_sum(GemmArgs g) {
     const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k < g.m * ((g.n + 3) / 4)) sum_parts<IO>(g, k);
+    if (k < g.m * ((g.n + 3) / 4)) sum_parts<IO>(g, (uint32_t)k);
 }
 
 // ------------------------------------------------------------- few rows ----
@@ -427,9 +431,9 @@ __device__ __forceinline__ Piece<IO> row_piece(const IO *row, int64_t c, int64_t
 template <typename IO>
 __device__ __forceinline__ void pad_rows(const void *src, void *dst, int64_t rows, int64_t cols,
                                          int64_t ld, int64_t block) {
-    const int64_t per = ld / 8, k = block * 256 + threadIdx.x;
+    const uint32_t per = (uint32_t)(ld / 8), k = (uint32_t)block * 256 + threadIdx.x;
     if (k >= rows * per) return;
-    const int64_t r = k / per, c = k % per * 8;
+    const int64_t r = k / per, c = (int64_t)(k % per) * 8;
     *reinterpret_cast<Piece<IO> *>(static_cast<IO *>(dst) + r * ld + c) =
         row_piece(static_cast<const IO *>(src) + r * cols, c, cols);
 }
@@ -444,9 +448,9 @@ template <typename IO> __global__ __launch_bounds__(256) void k_pad(PrepArgs g) 
 
 template <typename IO> __global__ __launch_bounds__(256) void k_bwd_prep(PrepArgs g) {
     __shared__ float sums[4][64 * 8];
-    int64_t b = blockIdx.x;
+    uint32_t b = blockIdx.x;
     if (b >= g.eb) {
-        b -= g.eb;
+        b -= (uint32_t)g.eb;
         if (b < g.xb)
             pad_rows<IO>(g.x, g.px, g.m, g.k, g.lk, b);
         else
@@ -455,7 +459,8 @@ template <typename IO> __global__ __launch_bounds__(256) void k_bwd_prep(PrepArg
     }
     // a wave: 512 columns of a quarter of the run's rows
     const int lane = threadIdx.x & 63, wv = wave_id();
-    const int64_t cols = (g.ln + 511) / 512, run = b / cols, c = (b % cols * 64 + lane) * 8;
+    const uint32_t cols = (uint32_t)((g.ln + 511) / 512);
+    const int64_t run = b / cols, c = (int64_t)(b % cols * 64 + lane) * 8;
     constexpr int R = kBiasRows / 4, U = 4;
     const int64_t r0 = run * kBiasRows + wv * R;
     const IO *dy = static_cast<const IO *>(g.dy), *pre = static_cast<const IO *>(g.pre);
@@ -492,7 +497,7 @@ template <typename IO> __global__ __launch_bounds__(256) void k_bwd_prep(PrepArg
     for (int i = 0; i < 8; ++i) sums[wv][i * 64 + lane] = s[i];
     __syncthreads();
     for (int k = threadIdx.x; k < 512; k += 256) {
-        const int64_t col = b % cols * 512 + (k & 63) * 8 + (k >> 6);
+        const int64_t col = (int64_t)(b % cols) * 512 + (k & 63) * 8 + (k >> 6);
         if (col < g.n)
             g.part[run * g.n + col] = (sums[0][k] + sums[1][k]) + (sums[2][k] + sums[3][k]);
     }
@@ -508,13 +513,13 @@ __global__ __launch_bounds__(256) void k_bwd_finish(GemmArgs gx, GemmArgs gw, in
     int64_t b = blockIdx.x;
     if (b < xb) {
         const int64_t k = b * 256 + threadIdx.x;
-        if (k < gx.m * ((gx.n + 3) / 4)) sum_parts<IO>(gx, k);
+        if (k < gx.m * ((gx.n + 3) / 4)) sum_parts<IO>(gx, (uint32_t)k);
         return;
     }
     b -= xb;
     if (b < wb) {
         const int64_t k = b * 256 + threadIdx.x;
-        if (k < gw.m * ((gw.n + 3) / 4)) sum_parts<IO>(gw, k);
+        if (k < gw.m * ((gw.n + 3) / 4)) sum_parts<IO>(gw, (uint32_t)k);
         return;
     }
     b -= wb;
@@ -548,15 +553,9 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 constexpr int64_t kCus = 256;       // compute units of the part this is written for
 constexpr int64_t kFewRows = 32;    // rows up to which k_few runs
 
-// Tile shapes.  A bigger tile moves fewer bytes per product (from L2, which
-// gives 17 TB/s: a 128 x 128 tile runs at that limit) but comes in bigger
-// rounds.
-enum Tile { kT64, kT128, kT128Deep, kT256, kT320, kTiles };
+enum Tile { kT64, kT128, kT192, kTiles };
 struct Shape { int bm, bn, per_cu; float step; };
-// per_cu: workgroups a compute unit holds; step: us of one contraction step
-// with all of them running
-constexpr Shape kShape16[] = {{64, 64, 4, 0.60f}, {128, 128, 2, 1.22f}, {128, 128, 1, 0.70f},
-                              {256, 256, 1, 1.90f}, {256, 320, 1, 2.70f}};
+constexpr Shape kShape16[] = {{64, 64, 4, 0.78f}, {128, 128, 2, 1.05f}, {128, 192, 2, 1.22f}};
 constexpr Shape kShape32[] = {{64, 64, 4, 2.2f}, {128, 128, 2, 4.2f}};
 
 struct Choice { Tile t; int64_t split; };
@@ -618,12 +617,12 @@ Choice choose_bwd(int64_t m, int64_t n, int64_t k, int io) {
     return choose(mnk, 2, io);
 }
 
-// Widths up to 2^20 elements and rows up to 2^31: a tile's byte offsets stay
-// below 2^31 and every grid below 2^31 workgroups.
+// Widths up to 2^20 elements and tensors up to 2^34: a tile's byte offsets stay
+// below 2^31, and pieces of four elements and workgroups are counted in 32 bits.
 bool linear_sizes(int64_t m, int64_t n, int64_t k) {
-    const int64_t w = (int64_t)1 << 20, big = ((int64_t)1 << 31) - 1;
-    if (n > w || k > w || m > big) return false;
-    return m * cdiv(n, 4) / 64 < big && m * cdiv(k, 4) / 64 < big && n * cdiv(k, 4) / 64 < big;
+    const int64_t w = (int64_t)1 << 20, big = (int64_t)1 << 32;
+    if (n > w || k > w || m >= ((int64_t)1 << 31)) return false;
+    return m * cdiv(n, 4) < big && m * cdiv(k, 4) < big && n * cdiv(k, 4) < big;
 }
 
 size_t fwd_bytes(int64_t m, int64_t n, int64_t k, int io, size_t *copies) {
@@ -661,15 +660,12 @@ int32_t run_linear(const void *x, const void *w, const Epi &ep, int64_t m, int64
     const Choice c = choose_fwd(m, n, k, io);
     const GemmArgs g = plan(x, ld, w, ld, m, n, k, c, ep, reinterpret_cast<float *>(ws), io);
     const dim3 grid((unsigned)(g.tm * g.tn * g.split));
-#define SSD_GEMM(BM, BN, WM, WN, ST)                                                              \
-    hipLaunchKernelGGL((k_gemm<IO, BM, BN, WM, WN, ST>), grid, dim3(WM * WN * 64), 0, s, g)
-    if (c.t == kT64) SSD_GEMM(64, 64, 2, 2, 2);
-    else if (c.t == kT128) SSD_GEMM(128, 128, 2, 2, 2);
-    if constexpr (sizeof(IO) == 2) {
-        if (c.t == kT128Deep) SSD_GEMM(128, 128, 2, 2, 4);
-        else if (c.t == kT256) SSD_GEMM(256, 256, 2, 4, 2);
-        else if (c.t == kT320) SSD_GEMM(256, 320, 2, 4, 2);
-    }
+#define SSD_GEMM(BM, BN, WM, WN)                                                                  \
+    hipLaunchKernelGGL((k_gemm<IO, BM, BN, WM, WN, 2>), grid, dim3(WM * WN * 64), 0, s, g)
+    if (c.t == kT64) SSD_GEMM(64, 64, 2, 2);
+    else if (c.t == kT128) SSD_GEMM(128, 128, 2, 4);
+    if constexpr (sizeof(IO) == 2)
+        if (c.t == kT192) SSD_GEMM(128, 192, 2, 4);
 #undef SSD_GEMM
     if (g.split > 1)
         hipLaunchKernelGGL((k_gemm_sum<IO>), dim3((unsigned)cdiv(m * cdiv(n, 4), 256)), dim3(256), 0,
@@ -726,16 +722,13 @@ int32_t run_linear_bwd(const void *dy, const void *x, const void *w, const void 
     if (!dx) gx.tm = 0;
     const int64_t items = gx.tm * gx.tn * gx.split + (dw ? gw.tm * gw.tn * gw.split : 0);
     if (items > 0) {
-#define SSD_GEMM(BM, BN, WM, WN, ST)                                                              \
-    hipLaunchKernelGGL((k_gemm_bwd<IO, BM, BN, WM, WN, ST>), dim3((unsigned)items),               \
+#define SSD_GEMM(BM, BN, WM, WN)                                                                  \
+    hipLaunchKernelGGL((k_gemm_bwd<IO, BM, BN, WM, WN, 2>), dim3((unsigned)items),               \
                        dim3(WM * WN * 64), 0, s, gx, gw)
-        if (L.c.t == kT64) SSD_GEMM(64, 64, 2, 2, 2);
-        else if (L.c.t == kT128) SSD_GEMM(128, 128, 2, 2, 2);
-        if constexpr (sizeof(IO) == 2) {
-            if (L.c.t == kT128Deep) SSD_GEMM(128, 128, 2, 2, 4);
-            else if (L.c.t == kT256) SSD_GEMM(256, 256, 2, 4, 2);
-            else if (L.c.t == kT320) SSD_GEMM(256, 320, 2, 4, 2);
-        }
+        if (L.c.t == kT64) SSD_GEMM(64, 64, 2, 2);
+        else if (L.c.t == kT128) SSD_GEMM(128, 128, 2, 4);
+        if constexpr (sizeof(IO) == 2)
+            if (L.c.t == kT192) SSD_GEMM(128, 192, 2, 4);
 #undef SSD_GEMM
     }
     const int64_t xb = dx && gx.split > 1 ? cdiv(m * cdiv(k, 4), 256) : 0;
