@@ -133,41 +133,58 @@ template <typename IO, bool TR, int BM> struct OpTile {
     }
 };
 
-// This thread's share of an operand tile's copies into LDS: byte offsets from
-// the tile's first element, the same in every step of the contraction.
+// A wave's share of an operand's copies into LDS, a step of the contraction at
+// a time: byte offsets from the step's first element, the same in every step,
+// and the resource that the step reads through, moved on by one scalar
+// addition.  What lies past the operand's rows or its contraction is read as
+// zeros: contraction contiguous, the resource ends with the rows (the pieces
+// of a row past its end are masked in the last step); contraction outermost,
+// it ends with the contraction, which only the last step can reach.  Offsets
+// inside a tile stay below 2^30, so where nothing ends kOpen is far enough.
+constexpr int64_t kOpen = 0x7fffffff;
+
 template <typename IO, bool TR, int BM, int NT> struct Copies {
     typedef OpTile<IO, TR, BM> T;
     static constexpr int N = T::BYTES / 16 / NT;
     static_assert(T::BYTES % (16 * NT) == 0, "every wave copies as much");
     uint32_t off[N];
+    const char *base;
+    int64_t stride;   // bytes from step to step
+    int bytes, last;  // reach of the resource in a step, and in the last one
+    int tail;         // contraction elements in the last step
     static __device__ __forceinline__ int chunk(int slot) {
         return slot % T::CH ^ T::f(slot / T::CH);
     }
-    __device__ __forceinline__ void init(int64_t ld) {
+    // Rows m0 .. of the operand (it has mEnd), `steps` steps from k0 to kEnd.
+    __device__ __forceinline__ Copies(const void *src, int64_t ld, int64_t m0, int64_t mEnd,
+                                      int64_t k0, int64_t kEnd, int steps) {
+        constexpr int64_t ES = sizeof(IO);
+        const int64_t kLast = k0 + (int64_t)(steps - 1) * T::BK;
+        base = static_cast<const char *>(src) + (TR ? k0 * ld + m0 : m0 * ld + k0) * ES;
+        stride = TR ? T::BK * ld * ES : T::BK * ES;
+        const int64_t end = (TR ? (kEnd - kLast) * ld - m0 : (mEnd - m0) * ld) * ES;
+        last = (int)(end < kOpen ? end : kOpen);
+        bytes = TR ? (int)kOpen : last;
+        tail = (int)(kEnd - kLast);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int slot = i * NT + (int)threadIdx.x;
-            off[i] = (uint32_t)(slot / T::CH * ld + chunk(slot) * T::EPC) * (uint32_t)sizeof(IO);
+            off[i] = (uint32_t)(slot / T::CH * ld + chunk(slot) * T::EPC) * (uint32_t)ES;
         }
     }
-    // Rows m0 .. of the operand (it has mEnd), contraction k0 .. kEnd.  What
-    // lies past either end is written as zeros; k0 >= kEnd writes zeros only.
-    // Offsets inside a tile stay below 2^31, so a resource never has to reach
-    // further, and the offset of a masked piece lies past every resource.
-    __device__ __forceinline__ void go(const void *src, int64_t ld, int64_t m0, int64_t mEnd,
-                                       int64_t k0, int64_t kEnd, char *lds) const {
-        const int64_t first = TR ? k0 * ld + m0 : m0 * ld + k0;
-        const int64_t end = TR ? kEnd * ld : mEnd * ld;
-        int64_t bytes = k0 < kEnd ? (end - first) * (int64_t)sizeof(IO) : 0;
-        if (bytes > 0x7fffffff) bytes = 0x7fffffff;
-        const RsrcW r = make_rsrc_w(static_cast<const IO *>(src) + first, bytes);
-        const bool tail = !TR && k0 + T::BK > kEnd;
+    __device__ __forceinline__ void next(char *lds, bool final) {
+        const RsrcW r = make_rsrc_w(base, final ? last : bytes);
+        char *dst = lds + wave_id() * 1024;
+        if (!TR && final && tail < T::BK) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            uint32_t o = off[i];
-            if (tail && k0 + chunk(i * NT + (int)threadIdx.x) * T::EPC >= kEnd) o = 0xffffff00u;
-            lds_dma16(r, (lds_void *)(lds + (i * NT + (threadIdx.x & ~63)) * 16), o);
+            for (int i = 0; i < N; ++i)
+                lds_dma16(r, (lds_void *)(dst + i * NT * 16),
+                          chunk(i * NT + (int)threadIdx.x) * T::EPC < tail ? off[i] : 0xffffff00u);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) lds_dma16(r, (lds_void *)(dst + i * NT * 16), off[i]);
         }
+        base += stride;
     }
 };
 
@@ -206,9 +223,8 @@ __device__ __forceinline__ u32x4 piece(const char *lds, int r0, int j, int lane)
 constexpr uint32_t kBand = 8;
 
 // One workgroup: a BM x BN tile of D over one contraction part, WM x WN waves,
-// ST steps of both operands in LDS: ST - 1 are in flight while one is
-// multiplied.
-template <typename IO, bool TA, bool TB, int BM, int BN, int WM, int WN, int ST>
+// two steps of both operands in LDS.
+template <typename IO, bool TA, bool TB, int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint32_t item, char *lds) {
     constexpr int NT = WM * WN * 64;
     typedef OpTile<IO, TA, BM> OA;
@@ -230,24 +246,21 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint32_t item, char
     for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < NI; ++j) acc[i][j] = zero4();
-    Copies<IO, TA, BM, NT> ca;
-    Copies<IO, TB, BN, NT> cb;
-    ca.init(g.lda);
-    cb.init(g.ldb);
-    auto copy = [&](int64_t k, int slot) {
-        ca.go(g.A, g.lda, m0, g.m, k, kEnd, lds + slot * SIZE);
-        cb.go(g.B, g.ldb, n0, g.n, k, kEnd, lds + slot * SIZE + OA::BYTES);
+    const int steps = (int)((kEnd - k0 + BK - 1) / BK);
+    Copies<IO, TA, BM, NT> ca(g.A, g.lda, m0, g.m, k0, kEnd, steps);
+    Copies<IO, TB, BN, NT> cb(g.B, g.ldb, n0, g.n, k0, kEnd, steps);
+    auto copy = [&](int slot, bool final) {
+        ca.next(lds + slot * SIZE, final);
+        cb.next(lds + slot * SIZE + OA::BYTES, final);
     };
-    constexpr int PER = ca.N + cb.N;  // copies a wave issues per step
-#pragma unroll
-    for (int i = 0; i < ST - 1; ++i) copy(k0 + i * BK, i);
-    int slot = 0;
-    for (int64_t k = k0; k < kEnd; k += BK) {
-        // this step's copies have landed (the ST - 2 steps after it may be in
-        // flight), and everyone has read the step before, whose slot is next
-        vm_wait<(ST - 2) * PER>();
+    // One step from the LDS slot it was copied to, while the next is copied to
+    // the other one: this step's copies have landed, and everyone has read the
+    // step before.
+    auto step = [&](int k, auto s) {
+        constexpr int slot = decltype(s)::value;
+        vm_wait<0>();
         lds_barrier();
-        copy(k + (ST - 1) * BK, slot == 0 ? ST - 1 : slot - 1);
+        if (k + 1 < steps) copy(1 - slot, k + 2 == steps);
         const char *a = lds + slot * SIZE, *b = a + OA::BYTES;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -261,9 +274,12 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint32_t item, char
 #pragma unroll
                 for (int n = 0; n < NI; ++n) acc[i][n] = Mma<IO>::go(pb[n], pa[i], acc[i][n]);
         }
-        slot = slot + 1 == ST ? 0 : slot + 1;
+    };
+    copy(0, steps == 1);
+    for (int k = 0; k < steps; k += 2) {
+        step(k, std::integral_constant<int, 0>{});
+        if (k + 1 < steps) step(k + 1, std::integral_constant<int, 1>{});
     }
-    vm_wait<0>();  // the copies of zeros behind the last step
     // element r of a lane: row m of lane & 15, column 4 (lane >> 4) + r
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -286,28 +302,28 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint32_t item, char
     }
 }
 
-template <typename IO, bool TA, bool TB, int BM, int BN, int ST> constexpr int lds_bytes() {
-    return ST * (OpTile<IO, TA, BM>::BYTES + OpTile<IO, TB, BN>::BYTES);
+template <typename IO, bool TA, bool TB, int BM, int BN> constexpr int lds_bytes() {
+    return 2 * (OpTile<IO, TA, BM>::BYTES + OpTile<IO, TB, BN>::BYTES);
 }
 
 // The forward product.
-template <typename IO, int BM, int BN, int WM, int WN, int ST>
+template <typename IO, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM * WN * 64) void k_gemm(GemmArgs g) {
-    __shared__ __align__(16) char lds[lds_bytes<IO, false, false, BM, BN, ST>()];
-    gemm_tile<IO, false, false, BM, BN, WM, WN, ST>(
+    __shared__ __align__(16) char lds[lds_bytes<IO, false, false, BM, BN>()];
+    gemm_tile<IO, false, false, BM, BN, WM, WN>(
         g, (uint32_t)xcd_item(blockIdx.x, gridDim.x), lds);
 }
 
 // The gradient's two products in one launch: dx = e W, then dW = e^T x.
-template <typename IO, int BM, int BN, int WM, int WN, int ST>
+template <typename IO, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM * WN * 64) void k_gemm_bwd(GemmArgs gx, GemmArgs gw) {
-    __shared__ __align__(16) char lds[lds_bytes<IO, true, true, BM, BN, ST>()];
+    __shared__ __align__(16) char lds[lds_bytes<IO, true, true, BM, BN>()];
     const uint32_t item = (uint32_t)xcd_item(blockIdx.x, gridDim.x);
     const uint32_t nx = (uint32_t)(gx.tm * gx.tn * gx.split);
     if (item < nx)
-        gemm_tile<IO, false, true, BM, BN, WM, WN, ST>(gx, item, lds);
+        gemm_tile<IO, false, true, BM, BN, WM, WN>(gx, item, lds);
     else
-        gemm_tile<IO, true, true, BM, BN, WM, WN, ST>(gw, item - nx, lds);
+        gemm_tile<IO, true, true, BM, BN, WM, WN>(gw, item - nx, lds);
 }
 
 // Four consecutive elements of a product in parts: their sum in the parts'
@@ -335,7 +351,7 @@ template <typename IO> __global__ __launch_bounds__(256) void k_gemm_sum(GemmArg
 // workgroup owns 16 weight rows, its waves 128-byte pieces of them in turn,
 // loaded from memory straight into operands; the waves' sums meet in LDS and
 // are added in order.
-constexpr int kFewWaves = 8;
+constexpr int kFewWaves = 4;
 constexpr int kFewUnroll = 4;  // weight pieces in flight a wave
 
 template <typename IO, int MT>
@@ -399,13 +415,13 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_few(GemmArgs g) {
 // Everything before the gradient's products in one launch, in 8-element pieces
 // of rows (rows of odd widths start at any element; the memory takes vector
 // accesses there too): e = dy act'(pre), with its fp32 column sums over runs
-// of kBiasRows rows, and x and W laid out again with padded rows.
-constexpr int kBiasRows = 64;
+// of `run` rows, and x and W laid out again with padded rows.
 
 struct PrepArgs {
     const void *dy, *pre, *x, *w;
     void *e, *px, *pw;        // NULL: not wanted
     float *part;              // [runs][n] column sums of e, or NULL
+    int run;                  // rows of a workgroup: a multiple of 16
     int64_t m, n, k, ln, lk;  // ln, lk: elements per padded row
     int act;
     int64_t eb, xb, wb;       // workgroups of each piece of work
@@ -413,15 +429,22 @@ struct PrepArgs {
 
 template <typename IO> struct alignas(16) Piece { IO v[8]; };
 
-// Elements c .. c + 7 of a row of `width`, zeros past its end.
+// Elements c .. c + 7 of a row of `width`, zeros past its end.  What lies past
+// the row but before `end`, the tensor's end, is read and dropped.
 template <typename IO>
-__device__ __forceinline__ Piece<IO> row_piece(const IO *row, int64_t c, int64_t width) {
+__device__ __forceinline__ Piece<IO> row_piece(const IO *row, int64_t c, int64_t width,
+                                               const IO *end) {
     Piece<IO> p;
-    if (c + 8 <= width) {
+    if (row + c + 8 <= end) {
         __builtin_memcpy(&p, row + c, sizeof(p));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) p.v[i] = c + i < width ? row[c + i] : (IO)0.f;
+    }
+    if (c + 8 > width) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i >= width) p.v[i] = (IO)0.f;
     }
     return p;
 }
@@ -435,7 +458,8 @@ __device__ __forceinline__ void pad_rows(const void *src, void *dst, int64_t row
     if (k >= rows * per) return;
     const int64_t r = k / per, c = (int64_t)(k % per) * 8;
     *reinterpret_cast<Piece<IO> *>(static_cast<IO *>(dst) + r * ld + c) =
-        row_piece(static_cast<const IO *>(src) + r * cols, c, cols);
+        row_piece(static_cast<const IO *>(src) + r * cols, c, cols,
+                  static_cast<const IO *>(src) + rows * cols);
 }
 
 template <typename IO> __global__ __launch_bounds__(256) void k_pad(PrepArgs g) {
@@ -461,8 +485,9 @@ template <typename IO> __global__ __launch_bounds__(256) void k_bwd_prep(PrepArg
     const int lane = threadIdx.x & 63, wv = wave_id();
     const uint32_t cols = (uint32_t)((g.ln + 511) / 512);
     const int64_t run = b / cols, c = (int64_t)(b % cols * 64 + lane) * 8;
-    constexpr int R = kBiasRows / 4, U = 4;
-    const int64_t r0 = run * kBiasRows + wv * R;
+    constexpr int U = 4;
+    const int R = g.run / 4;
+    const int64_t r0 = run * g.run + wv * R;
     const IO *dy = static_cast<const IO *>(g.dy), *pre = static_cast<const IO *>(g.pre);
     float s[8];
 #pragma unroll
@@ -473,8 +498,8 @@ template <typename IO> __global__ __launch_bounds__(256) void k_bwd_prep(PrepArg
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int64_t row = r + u < g.m ? r + u : g.m - 1;
-                d[u] = row_piece(dy + row * g.n, c, g.n);
-                if (pre) p[u] = row_piece(pre + row * g.n, c, g.n);
+                d[u] = row_piece(dy + row * g.n, c, g.n, dy + g.m * g.n);
+                if (pre) p[u] = row_piece(pre + row * g.n, c, g.n, pre + g.m * g.n);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -505,7 +530,7 @@ template <typename IO> __global__ __launch_bounds__(256) void k_bwd_prep(PrepArg
 
 // Everything after them in one launch: the sums of products in parts, and the
 // bias gradient from its runs' sums (a workgroup: 32 columns by 8 runs at a
-// time, added in a fixed order).
+// time, four loads in flight, added in a fixed order).
 template <typename IO>
 __global__ __launch_bounds__(256) void k_bwd_finish(GemmArgs gx, GemmArgs gw, int64_t xb, int64_t wb,
                                                     const float *part, int64_t runs, float *db) {
@@ -526,8 +551,16 @@ __global__ __launch_bounds__(256) void k_bwd_finish(GemmArgs gx, GemmArgs gw, in
     const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
     const int64_t col = b * 32 + c, n = gw.m;
     float t = 0.f;
-    if (col < n)
-        for (int64_t r = q; r < runs; r += 8) t += part[r * n + col];
+    if (col < n) {
+        int64_t r = q;
+        for (; r + 24 < runs; r += 32) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = part[(r + 8 * i) * n + col];
+            t += (v[0] + v[1]) + (v[2] + v[3]);
+        }
+        for (; r < runs; r += 8) t += part[r * n + col];
+    }
     s[q][c] = t;
     __syncthreads();
     if (q != 0 || col >= n) return;
@@ -544,7 +577,9 @@ __global__ __launch_bounds__(256) void k_zero(IO *p, int64_t n) {
 
 // --------------------------------------------------------------- the plan ----
 size_t up(size_t v) { return (v + 255) & ~(size_t)255; }
-int64_t pad(int64_t v) { return (v + 7) / 8 * 8; }
+// Elements of a row laid out again: whole cache lines, so that a tile's pieces of
+// a row meet no line of its neighbours.
+int64_t pad(int64_t v) { return (v + 63) / 64 * 64; }
 // Whether rows of v elements have to be laid out again: not whole 16-byte pieces.
 bool odd_rows(int64_t v, int io) { return v % (io == SSD_BF16 ? 8 : 4) != 0; }
 int64_t esz(int io) { return io == SSD_BF16 ? 2 : 4; }
@@ -554,52 +589,68 @@ constexpr int64_t kCus = 256;       // compute units of the part this is written
 constexpr int64_t kFewRows = 32;    // rows up to which k_few runs
 
 enum Tile { kT64, kT128, kT192, kTiles };
-struct Shape { int bm, bn, per_cu; float step; };
-constexpr Shape kShape16[] = {{64, 64, 4, 0.78f}, {128, 128, 2, 1.05f}, {128, 192, 2, 1.22f}};
-constexpr Shape kShape32[] = {{64, 64, 4, 2.2f}, {128, 128, 2, 4.2f}};
+struct Shape {
+    int bm, bn;
+    int per_cu;        // workgroups a compute unit holds
+    float alone, full; // us of a contraction step with one and with all of them (measured)
+};
+constexpr Shape kShape16[] = {{64, 64, 5, 0.27f, 0.90f}, {128, 128, 2, 0.62f, 1.0f},
+                              {128, 192, 2, 0.83f, 1.13f}};
+constexpr Shape kShape32[] = {{64, 64, 5, 0.55f, 2.6f}, {128, 128, 2, 2.0f, 3.9f}};
 
-struct Choice { Tile t; int64_t split; };
+struct Product { int64_t m, n, k; };
+struct Choice { Tile t; int64_t split[2]; };  // contraction parts of each product
 
-// Rounds of workgroups times the time of a round, over the products of one
-// launch; with split > 1, also the parts written and read back.
-inline float cost(const Shape &h, int64_t tiles, int64_t steps, int64_t split, int64_t out) {
-    const int64_t rounds = cdiv(tiles * split, kCus * h.per_cu);
-    return rounds * cdiv(steps, split) * h.step +
-           (split > 1 ? 3.f + split * out * 8e-6f / 4.f : 0.f);
-}
-Choice choose(const int64_t (*mnk)[3], int count, int io) {
-    const bool b16 = io == SSD_BF16;
-    Choice best{kT128, 1};
-    float least = 1e30f;
-    const int64_t bk = 128 / esz(io);
-    for (int t = 0; t < (b16 ? kTiles : 2); ++t) {
-        const Shape &h = b16 ? kShape16[t] : kShape32[t];
-        for (int64_t split = 1; split <= 16; split = split < 4 ? split + 1 : split + 4) {
-            int64_t tiles = 0, steps = 0, out = 0;
-            bool ok = true;
-            for (int i = 0; i < count; ++i) {
-                tiles += cdiv(mnk[i][0], h.bm) * cdiv(mnk[i][1], h.bn);
-                const int64_t s = cdiv(mnk[i][2], bk);
-                steps = s > steps ? s : steps;
-                out += mnk[i][0] * mnk[i][1];
-                ok = ok && s / split >= 4;
-            }
-            if (split > 1 && !ok) break;
-            const float c = cost(h, tiles, steps, split, out);
-            if (c < least) least = c, best = {(Tile)t, split};
-        }
+// Time of a launch of products (us): rounds of workgroups times a step's time
+// at the load of the last round; with several products, their work at full
+// load and half a round's loss, but no less than the longest workgroup; and
+// parts written and read back.
+float cost(const Shape &h, const Product *p, int count, const int64_t *split, int64_t bk) {
+    int64_t all = 0, longest = 0;
+    float work = 0.f, parts = 0.f;
+    for (int i = 0; i < count; ++i) {
+        const int64_t wgs = cdiv(p[i].m, h.bm) * cdiv(p[i].n, h.bn) * split[i];
+        const int64_t steps = cdiv(cdiv(p[i].k, bk), split[i]);
+        all += wgs;
+        longest = steps > longest ? steps : longest;
+        work += (float)wgs * steps;
+        if (split[i] > 1) parts += 2.f + (float)split[i] * p[i].m * p[i].n * 8 / 4e6f;
     }
+    const int64_t slots = kCus * h.per_cu, rounds = all / slots, rest = all % slots;
+    const float load = (float)cdiv(rest, kCus);
+    const float last = h.alone + (h.full - h.alone) * (load - 1) / (h.per_cu - 1);
+    if (count == 1 || rounds == 0)
+        return parts + longest * (rounds * h.full + (rest ? last : 0.f));
+    return parts + work / slots * h.full + 0.5f * longest * h.full;
+}
+
+Choice choose(const Product *p, int count, int io) {
+    constexpr int64_t kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+    const int64_t bk = 128 / esz(io);
+    Choice best{kT128, {1, 1}};
+    float least = 1e30f;
+    for (int t = 0; t < (io == SSD_BF16 ? kTiles : 2); ++t)
+        for (int64_t s0 : kSplits)
+            for (int64_t s1 : kSplits) {
+                const int64_t split[2] = {s0, s1};
+                bool ok = count == 2 || s1 == 1;
+                for (int i = 0; i < count; ++i)  // parts of four steps at least
+                    ok = ok && (split[i] == 1 || cdiv(p[i].k, bk) / split[i] >= 4);
+                if (!ok) continue;
+                const float c = cost(io == SSD_BF16 ? kShape16[t] : kShape32[t], p, count, split, bk);
+                if (c < least) least = c, best = {(Tile)t, {s0, s1}};
+            }
     return best;
 }
 
 GemmArgs plan(const void *A, int64_t lda, const void *B, int64_t ldb, int64_t m, int64_t n,
-              int64_t k, Choice c, const Epi &ep, float *parts, int io) {
+              int64_t k, const Choice &c, int which, const Epi &ep, float *parts, int io) {
     const Shape &h = io == SSD_BF16 ? kShape16[c.t] : kShape32[c.t];
     const int64_t bk = 128 / esz(io), steps = cdiv(k, bk);
     GemmArgs g{};
     g.A = A, g.B = B, g.lda = lda, g.ldb = ldb, g.m = m, g.n = n, g.k = k;
     g.tm = cdiv(m, h.bm), g.tn = cdiv(n, h.bn);
-    g.kper = cdiv(steps, c.split) * bk;
+    g.kper = cdiv(steps, c.split[which]) * bk;
     g.split = cdiv(k, g.kper);
     g.parts = parts, g.ep = ep;
     return g;
@@ -609,12 +660,12 @@ size_t parts_bytes(const GemmArgs &g) {
 }
 
 Choice choose_fwd(int64_t m, int64_t n, int64_t k, int io) {
-    const int64_t mnk[1][3] = {{m, n, k}};
-    return choose(mnk, 1, io);
+    const Product p[1] = {{m, n, k}};
+    return choose(p, 1, io);
 }
 Choice choose_bwd(int64_t m, int64_t n, int64_t k, int io) {
-    const int64_t mnk[2][3] = {{m, k, n}, {n, k, m}};
-    return choose(mnk, 2, io);
+    const Product p[2] = {{m, k, n}, {n, k, m}};
+    return choose(p, 2, io);
 }
 
 // Widths up to 2^20 elements and tensors up to 2^34: a tile's byte offsets stay
@@ -628,7 +679,7 @@ bool linear_sizes(int64_t m, int64_t n, int64_t k) {
 size_t fwd_bytes(int64_t m, int64_t n, int64_t k, int io, size_t *copies) {
     *copies = odd_rows(k, io) ? up(m * pad(k) * esz(io)) + up(n * pad(k) * esz(io)) : 0;
     if (m <= kFewRows) return *copies;
-    return *copies + parts_bytes(plan(nullptr, 0, nullptr, 0, m, n, k, choose_fwd(m, n, k, io),
+    return *copies + parts_bytes(plan(nullptr, 0, nullptr, 0, m, n, k, choose_fwd(m, n, k, io), 0,
                                       Epi{}, nullptr, io));
 }
 
@@ -658,10 +709,10 @@ int32_t run_linear(const void *x, const void *w, const Epi &ep, int64_t m, int64
         return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
     }
     const Choice c = choose_fwd(m, n, k, io);
-    const GemmArgs g = plan(x, ld, w, ld, m, n, k, c, ep, reinterpret_cast<float *>(ws), io);
+    const GemmArgs g = plan(x, ld, w, ld, m, n, k, c, 0, ep, reinterpret_cast<float *>(ws), io);
     const dim3 grid((unsigned)(g.tm * g.tn * g.split));
 #define SSD_GEMM(BM, BN, WM, WN)                                                                  \
-    hipLaunchKernelGGL((k_gemm<IO, BM, BN, WM, WN, 2>), grid, dim3(WM * WN * 64), 0, s, g)
+    hipLaunchKernelGGL((k_gemm<IO, BM, BN, WM, WN>), grid, dim3(WM * WN * 64), 0, s, g)
     if (c.t == kT64) SSD_GEMM(64, 64, 2, 2);
     else if (c.t == kT128) SSD_GEMM(128, 128, 2, 4);
     if constexpr (sizeof(IO) == 2)
@@ -676,22 +727,24 @@ int32_t run_linear(const void *x, const void *w, const Epi &ep, int64_t m, int64
 // Parts of the gradient's workspace.
 struct BwdWs {
     bool own_e;
-    int64_t ln, lk, runs;
+    int64_t ln, lk, run, runs;
     Choice c;
     size_t e, w, x, part, px, pw, total;
     BwdWs(int64_t m, int64_t n, int64_t k, int act, int io) {
         const int64_t es = esz(io);
         own_e = act != SSD_ACT_NONE || odd_rows(n, io);
         ln = own_e ? pad(n) : n, lk = odd_rows(k, io) ? pad(k) : k;
-        runs = cdiv(m, kBiasRows);
+        // 64 rows a workgroup, or 16 where that leaves compute units without one
+        run = cdiv(m, 64) * cdiv(n, 512) >= 4 * kCus ? 64 : 16;
+        runs = cdiv(m, run);
         c = choose_bwd(m, n, k, io);
         size_t o = 0;
         e = o, o += own_e ? up(m * ln * es) : 0;
         w = o, o += lk != k ? up(n * lk * es) : 0;
         x = o, o += lk != k ? up(m * lk * es) : 0;
         part = o, o += up(runs * n * 4);
-        px = o, o += parts_bytes(plan(nullptr, 0, nullptr, 0, m, k, n, c, Epi{}, nullptr, io));
-        pw = o, o += parts_bytes(plan(nullptr, 0, nullptr, 0, n, k, m, c, Epi{}, nullptr, io));
+        px = o, o += parts_bytes(plan(nullptr, 0, nullptr, 0, m, k, n, c, 0, Epi{}, nullptr, io));
+        pw = o, o += parts_bytes(plan(nullptr, 0, nullptr, 0, n, k, m, c, 1, Epi{}, nullptr, io));
         total = o;
     }
 };
@@ -704,10 +757,10 @@ int32_t run_linear_bwd(const void *dy, const void *x, const void *w, const void 
     const BwdWs L(m, n, k, act, io);
     PrepArgs p{};
     p.dy = dy, p.pre = act != SSD_ACT_NONE ? pre : nullptr, p.x = x, p.w = w, p.act = act;
-    p.m = m, p.n = n, p.k = k, p.ln = L.ln, p.lk = L.lk;
+    p.m = m, p.n = n, p.k = k, p.ln = L.ln, p.lk = L.lk, p.run = (int)L.run;
     if (L.own_e) p.e = ws + L.e;
     if (db) p.part = reinterpret_cast<float *>(ws + L.part);
-    if (p.e || db) p.eb = L.runs * cdiv(pad(L.ln), 512);
+    if (p.e || db) p.eb = L.runs * cdiv(L.ln, 512);
     if (L.lk != k && dw) p.px = ws + L.x, p.xb = cdiv(m * (L.lk / 8), 256);
     if (L.lk != k && dx) p.pw = ws + L.w, p.wb = cdiv(n * (L.lk / 8), 256);
     if (p.eb + p.xb + p.wb > 0)
@@ -715,15 +768,15 @@ int32_t run_linear_bwd(const void *dy, const void *x, const void *w, const void 
     const void *e = p.e ? p.e : dy;
     if (p.px) x = p.px;
     if (p.pw) w = p.pw;
-    GemmArgs gx = plan(e, L.ln, w, L.lk, m, k, n, L.c, Epi{dx, nullptr, nullptr, nullptr, 0},
+    GemmArgs gx = plan(e, L.ln, w, L.lk, m, k, n, L.c, 0, Epi{dx, nullptr, nullptr, nullptr, 0},
                        reinterpret_cast<float *>(ws + L.px), io);
-    GemmArgs gw = plan(e, L.ln, x, L.lk, n, k, m, L.c, Epi{dw, nullptr, nullptr, nullptr, 0},
+    GemmArgs gw = plan(e, L.ln, x, L.lk, n, k, m, L.c, 1, Epi{dw, nullptr, nullptr, nullptr, 0},
                        reinterpret_cast<float *>(ws + L.pw), io);
     if (!dx) gx.tm = 0;
     const int64_t items = gx.tm * gx.tn * gx.split + (dw ? gw.tm * gw.tn * gw.split : 0);
     if (items > 0) {
 #define SSD_GEMM(BM, BN, WM, WN)                                                                  \
-    hipLaunchKernelGGL((k_gemm_bwd<IO, BM, BN, WM, WN, 2>), dim3((unsigned)items),               \
+    hipLaunchKernelGGL((k_gemm_bwd<IO, BM, BN, WM, WN>), dim3((unsigned)items),               \
                        dim3(WM * WN * 64), 0, s, gx, gw)
         if (L.c.t == kT64) SSD_GEMM(64, 64, 2, 2);
         else if (L.c.t == kT128) SSD_GEMM(128, 128, 2, 4);
