@@ -493,16 +493,34 @@ def _activation(name) -> int:
                          % (", ".join(sorted(_lib.ACTIVATIONS)), name)) from None
 
 
+def _fit(name, t, dtype, shape, device):
+    """_check with everything given, at the cost of four comparisons where all
+    is well (a decode step makes several such checks per launch)."""
+    if t is None or (t.dtype is dtype and t.shape == shape and t.device == device
+                     and t.is_contiguous()):
+        return
+    _check(name, t, dtype, shape, device)
+
+
+def _raw_stream(index: int) -> int:
+    """The current stream's handle on device `index`; torch's own accessor of
+    the bare handle where it has one (building a Stream object costs as much
+    as half a launch)."""
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _launch(name, dev, *args) -> None:
     """Calls the library's `name` on the current stream of `dev` (its last
     argument), with `dev` the current device, and raises its errors."""
     cuda = _torch().cuda
     fn = getattr(load(), name)
     if dev.index == cuda.current_device():
-        rc = fn(*args, cuda.current_stream(dev).cuda_stream)
+        rc = fn(*args, _raw_stream(dev.index))
     else:
         with cuda.device(dev):
-            rc = fn(*args, cuda.current_stream(dev).cuda_stream)
+            rc = fn(*args, _raw_stream(dev.index))
     if rc != 0:
         raise SsdError(name, rc)
 
@@ -552,14 +570,14 @@ def linear(x, weight, bias=None, activation: str = "none", residual=None,
     shape = tuple(x.shape[:-1]) + (n,)
     _check("x", x, io, tuple(x.shape[:-1]) + (k,))
     _check("weight", weight, io, None, dev)
-    _check("bias", bias, torch.float32, (n,), dev)
-    _check("residual", residual, io, shape, dev)
+    _fit("bias", bias, torch.float32, (n,), dev)
+    _fit("residual", residual, io, shape, dev)
     o = torch.empty(shape, dtype=io, device=dev) if out is None else out
-    _check("out", o, io, shape, dev)
+    _fit("out", o, io, shape, dev)
     pre = None
     if return_pre:
         pre = torch.empty(shape, dtype=io, device=dev) if pre_out is None else pre_out
-        _check("pre_out", pre, io, shape, dev)
+        _fit("pre_out", pre, io, shape, dev)
     m = x.numel() // k if k else 0
     wsb = int(lib.ssd_linear_workspace_bytes(m, k, n, code))
     ws = _scratch(workspace, wsb, dev) if wsb or workspace is not None else None
@@ -588,11 +606,11 @@ def linear_bwd(dy, x, weight, pre=None, activation: str = "none", bias: bool = F
     n, k = weight.shape
     lead = tuple(dy.shape[:-1])
     _check("dy", dy, io, lead + (n,))
-    _check("x", x, io, lead + (k,), dev)
+    _fit("x", x, io, lead + (k,), dev)
     _check("weight", weight, io, None, dev)
     if act and pre is None:
         raise ValueError("pre is needed for the gradient of %s" % activation)
-    _check("pre", pre, io, lead + (n,), dev)
+    _fit("pre", pre, io, lead + (n,), dev)
     res = dict(dx=torch.empty_like(x), dweight=torch.empty_like(weight))
     if bias:
         res["dbias"] = torch.empty((n,), dtype=torch.float32, device=dev)
@@ -637,22 +655,22 @@ def gated_scan(x, gates, lam, scale: float = 8.0, initial_state=None, seq_idx=No
     io = x.dtype
     code = _io_code(io)
     _check("x", x, io)
-    _check("gates", gates, io, (b, l, 2 * d), dev)
-    _check("lam", lam, torch.float32, (d,), dev)
-    _check("initial_state", initial_state, torch.float32, (b, d), dev)
-    _check("seq_idx", seq_idx, torch.int32, (b, l), dev)
+    _fit("gates", gates, io, (b, l, 2 * d), dev)
+    _fit("lam", lam, torch.float32, (d,), dev)
+    _fit("initial_state", initial_state, torch.float32, (b, d), dev)
+    _fit("seq_idx", seq_idx, torch.int32, (b, l), dev)
     y = torch.empty_like(x) if out is None else out
-    _check("out", y, io, (b, l, d), dev)
+    _fit("out", y, io, (b, l, d), dev)
     fin = states = None
     if return_final_state:
         fin = torch.empty((b, d), dtype=torch.float32, device=dev) \
             if final_out is None else final_out
-        _check("final_out", fin, torch.float32, (b, d), dev)
+        _fit("final_out", fin, torch.float32, (b, d), dev)
     if return_states:
         ns = -(-l // _lib.SSD_GATED_CHUNK)
         states = torch.empty((b, ns, d), dtype=torch.float32, device=dev) \
             if states_out is None else states_out
-        _check("states_out", states, torch.float32, (b, ns, d), dev)
+        _fit("states_out", states, torch.float32, (b, ns, d), dev)
     ws = _scratch(workspace, int(lib.ssd_gated_scan_workspace_bytes(b, l, d)), dev)
     _launch("ssd_gated_scan", dev, _ptr(x), _ptr(gates), _ptr(lam), float(scale),
             _ptr(initial_state), _ptr(seq_idx), _ptr(y), _ptr(fin), _ptr(states), b, l, d,
@@ -680,13 +698,13 @@ def gated_scan_bwd(x, gates, lam, dy, scale: float = 8.0, initial_state=None, d_
     io = x.dtype
     code = _io_code(io)
     _check("x", x, io)
-    _check("gates", gates, io, (b, l, 2 * d), dev)
-    _check("lam", lam, torch.float32, (d,), dev)
-    _check("dy", dy, io, (b, l, d), dev)
-    _check("initial_state", initial_state, torch.float32, (b, d), dev)
-    _check("d_final", d_final, torch.float32, (b, d), dev)
-    _check("seq_idx", seq_idx, torch.int32, (b, l), dev)
-    _check("states", states, torch.float32, (b, -(-l // _lib.SSD_GATED_CHUNK), d), dev)
+    _fit("gates", gates, io, (b, l, 2 * d), dev)
+    _fit("lam", lam, torch.float32, (d,), dev)
+    _fit("dy", dy, io, (b, l, d), dev)
+    _fit("initial_state", initial_state, torch.float32, (b, d), dev)
+    _fit("d_final", d_final, torch.float32, (b, d), dev)
+    _fit("seq_idx", seq_idx, torch.int32, (b, l), dev)
+    _fit("states", states, torch.float32, (b, -(-l // _lib.SSD_GATED_CHUNK), d), dev)
     res = dict(dx=torch.empty_like(x), dgates=torch.empty_like(gates), dlam=torch.empty_like(lam))
     if initial_state is not None:
         res["d_init"] = torch.empty_like(initial_state)
@@ -711,12 +729,12 @@ def gated_step(state, x, gates, lam, scale: float = 8.0, out=None):
         raise ValueError("x must be a GPU tensor")
     io = x.dtype
     code = _io_code(io)
-    _check("state", state, torch.float32, (b, d), dev)
+    _fit("state", state, torch.float32, (b, d), dev)
     _check("x", x, io)
-    _check("gates", gates, io, (b, 2 * d), dev)
-    _check("lam", lam, torch.float32, (d,), dev)
+    _fit("gates", gates, io, (b, 2 * d), dev)
+    _fit("lam", lam, torch.float32, (d,), dev)
     y = torch.empty_like(x) if out is None else out
-    _check("out", y, io, (b, d), dev)
+    _fit("out", y, io, (b, d), dev)
     _launch("ssd_gated_step", dev, _ptr(state), _ptr(x), _ptr(gates), _ptr(lam), float(scale),
             _ptr(y), b, d, code)
     return y

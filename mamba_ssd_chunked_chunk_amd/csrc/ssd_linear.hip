@@ -85,27 +85,40 @@ struct GemmArgs {
     Epi ep;
 };
 
+// Four consecutive elements as fp32, and back, at any element alignment (rows
+// of odd widths; the memory takes vector accesses there too).
+__device__ __forceinline__ f32x4 ldu4(const float *p) {
+    f32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+__device__ __forceinline__ f32x4 ldu4(const bf16 *p) {
+    bf16x4 v;
+    __builtin_memcpy(&v, p, 8);
+    return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]};
+}
+__device__ __forceinline__ void stu4(float *p, f32x4 v) { __builtin_memcpy(p, &v, 16); }
+__device__ __forceinline__ void stu4(bf16 *p, f32x4 v) {
+    bf16x4 o;
+    o[0] = (bf16)v[0]; o[1] = (bf16)v[1]; o[2] = (bf16)v[2]; o[3] = (bf16)v[3];
+    __builtin_memcpy(p, &o, 8);
+}
+
 // Four consecutive n of one row m.
 template <typename IO>
 __device__ __forceinline__ void finish4(const Epi &ep, int64_t m, int64_t n, int64_t N, f32x4 v) {
     const int64_t at = m * N + n;
-    if (n + 4 <= N && N % 4 == 0) {
-        if (ep.bias) {
-            f32x4 b;
-            __builtin_memcpy(&b, ep.bias + n, 16);
-            v += b;
-        }
-        if (ep.pre) st4<IO>(static_cast<IO *>(ep.pre) + at, v);
+    if (n + 4 <= N) {
+        if (ep.bias) v += ldu4(ep.bias + n);
+        if (ep.pre) stu4(static_cast<IO *>(ep.pre) + at, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = act_f(v[i], ep.act);
-        if (ep.res) v += ld4<IO>(static_cast<const IO *>(ep.res) + at);
-        st4<IO>(static_cast<IO *>(ep.out) + at, v);
+        if (ep.res) v += ldu4(static_cast<const IO *>(ep.res) + at);
+        stu4(static_cast<IO *>(ep.out) + at, v);
         return;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (n + i >= N) break;
-        float x = v[i];
+    for (int i = 0; n + i < N; ++i) {
+        float x = i == 0 ? v[0] : i == 1 ? v[1] : v[2];
         if (ep.bias) x += ep.bias[n + i];
         if (ep.pre) static_cast<IO *>(ep.pre)[at + i] = (IO)x;
         x = act_f(x, ep.act);
@@ -291,8 +304,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint32_t item, char
             if (n >= g.n) continue;
             if (g.split > 1) {
                 float *p = g.parts + (part * g.m + m) * g.n + n;
-                if (g.n % 4 == 0)
-                    *reinterpret_cast<f32x4 *>(p) = acc[i][j];
+                if (n + 4 <= g.n)
+                    stu4(p, acc[i][j]);
                 else
                     for (int r = 0; r < 4 && n + r < g.n; ++r) p[r] = acc[i][j][r];
             } else {
@@ -334,8 +347,8 @@ template <typename IO> __device__ __forceinline__ void sum_parts(const GemmArgs 
     f32x4 v = zero4();
     for (int64_t s = 0; s < g.split; ++s) {
         const float *p = g.parts + (s * g.m + row) * g.n + col;
-        if (g.n % 4 == 0)
-            v += *reinterpret_cast<const f32x4 *>(p);
+        if (col + 4 <= g.n)
+            v += ldu4(p);
         else
             for (int r = 0; r < 4 && col + r < g.n; ++r) v[r] += p[r];
     }
