@@ -138,11 +138,15 @@ template <typename IO, bool TR, int BM> struct OpTile {
     static constexpr int ROWS = TR ? BK : BM;
     static constexpr int CH = TR ? BM / EPC : 8;
     static constexpr int BYTES = ROWS * CH * 16;
+    static_assert(!TR || (sizeof(IO) == 2 ? CH % 8 : CH % 16) == 0, "f stays inside a row");
     static __device__ __forceinline__ int f(int r) {
         if (!TR) return r & 7;
-        constexpr int M = (CH & -CH) - 1;  // the swap stays inside aligned runs of a row's chunks
-        if (sizeof(IO) == 2) return (((r & 3) | ((r >> 1) & 4)) << 1) & M;
-        return (((r >> 2) & 3) << 2) & M;
+        // The transposing loads of 32 lanes take 32 bytes of rows 0-3 and 8-11
+        // (4-7 and 12-15): f moves them to eight different eighths of the banks.
+        // Rows of an odd number of 128 bytes alternate halves by themselves.
+        if (sizeof(IO) == 2)
+            return CH % 16 == 0 ? ((r & 3) | ((r >> 1) & 4)) << 1 : (r & 2) | ((r >> 1) & 4);
+        return ((r >> 2) & 3) << 2;  // fp32: 64 bytes of rows 4 apart
     }
 };
 
@@ -327,16 +331,21 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm(GemmArgs g) {
         g, (uint32_t)xcd_item(blockIdx.x, gridDim.x), lds);
 }
 
-// The gradient's two products in one launch: dx = e W, then dW = e^T x.
+// The gradient's two products in one launch: dx = e W and dW = e^T x, the one
+// with the longer contraction first so that the other fills the last round.
+// Each is dealt over all XCDs by itself: one run of items over both would give
+// some XCDs only long ones (477 against 385 us for 8192 x 2560 -> 5120).
 template <typename IO, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64) void k_gemm_bwd(GemmArgs gx, GemmArgs gw) {
+__global__ __launch_bounds__(WM * WN * 64) void k_gemm_bwd(GemmArgs gx, GemmArgs gw, int wfirst) {
     __shared__ __align__(16) char lds[lds_bytes<IO, true, true, BM, BN>()];
-    const uint32_t item = (uint32_t)xcd_item(blockIdx.x, gridDim.x);
-    const uint32_t nx = (uint32_t)(gx.tm * gx.tn * gx.split);
-    if (item < nx)
-        gemm_tile<IO, false, true, BM, BN, WM, WN>(gx, item, lds);
+    const uint32_t nx = (uint32_t)(gx.tm * gx.tn * gx.split), nw = (uint32_t)(gw.tm * gw.tn * gw.split);
+    const uint32_t lead = wfirst ? nw : nx, b = blockIdx.x;
+    const bool w = (b < lead) == (wfirst != 0);
+    const uint32_t item = (uint32_t)xcd_item(b < lead ? b : b - lead, w ? nw : nx);
+    if (w)
+        gemm_tile<IO, true, true, BM, BN, WM, WN>(gw, item, lds);
     else
-        gemm_tile<IO, true, true, BM, BN, WM, WN>(gw, item - nx, lds);
+        gemm_tile<IO, false, true, BM, BN, WM, WN>(gx, item, lds);
 }
 
 // Four consecutive elements of a product in parts: their sum in the parts'
@@ -786,11 +795,13 @@ int32_t run_linear_bwd(const void *dy, const void *x, const void *w, const void 
     GemmArgs gw = plan(e, L.ln, x, L.lk, n, k, m, L.c, 1, Epi{dw, nullptr, nullptr, nullptr, 0},
                        reinterpret_cast<float *>(ws + L.pw), io);
     if (!dx) gx.tm = 0;
-    const int64_t items = gx.tm * gx.tn * gx.split + (dw ? gw.tm * gw.tn * gw.split : 0);
+    if (!dw) gw.tm = 0;
+    const int64_t items = gx.tm * gx.tn * gx.split + gw.tm * gw.tn * gw.split;
+    const int wfirst = gw.kper > gx.kper;
     if (items > 0) {
 #define SSD_GEMM(BM, BN, WM, WN)                                                                  \
     hipLaunchKernelGGL((k_gemm_bwd<IO, BM, BN, WM, WN>), dim3((unsigned)items),               \
-                       dim3(WM * WN * 64), 0, s, gx, gw)
+                       dim3(WM * WN * 64), 0, s, gx, gw, wfirst)
         if (L.c.t == kT64) SSD_GEMM(64, 64, 2, 2);
         else if (L.c.t == kT128) SSD_GEMM(128, 128, 2, 4);
         if constexpr (sizeof(IO) == 2)
