@@ -66,16 +66,16 @@ __device__ __forceinline__ void decay(float u2, float &a, float &om) {
 
 // How the tiles of one column (64 V channels of one sequence) hand states
 // along in one pass.  A tile publishes its own map as soon as its rows are
-// read; a tile then needs the maps of the earlier tiles of its group of
-// kGroup and the state after the group before, which the last tile of that
-// group publishes.  So a state crosses kGroup tiles per hand-over, and each
+// read; a tile then needs the maps of the earlier tiles of its group
+// and the state after the group before, which the last tile of that
+// group publishes.  So a state crosses a group per hand-over, and each
 // sum has one order whatever runs first.  Tiles are numbered as their
 // workgroups start (a ticket per column): every tile waits only for lower
 // tickets of its own column, which are running and wait for lower ones in
 // turn, so every wait ends.  The words are written and read at agent scope
 // (the XCDs' L2 caches are not coherent inside a kernel), a flag after its
 // data has reached memory.
-constexpr int kGroup = 8;
+constexpr int kMostGroup = 32;  // tiles of a group: 8 to 32, see group_of
 constexpr int kTicketWords = 32;  // a 128-byte line per column's ticket
 
 struct Chain {
@@ -103,6 +103,7 @@ struct GArgs {
     float *part;          // backward: per tile sums behind dlam [b, tiles, d]
     Chain ch;
     int64_t b, l, d, tiles, ncol;
+    int group;  // tiles of a group
 };
 
 __device__ __forceinline__ uint32_t get32(const uint32_t *p) {
@@ -225,7 +226,7 @@ __device__ __forceinline__ int64_t take_ticket(const GArgs &g, int64_t col, uint
 
 template <int V, int NW> struct Lds {
     VecF<V> A[NW][64], S[NW][64];             // the waves' maps
-    VecF<V> pA[kGroup][64], pS[kGroup][64];     // the maps of the group's earlier tiles
+    VecF<V> pA[kMostGroup][64], pS[kMostGroup][64];     // the maps of the group's earlier tiles
     VecF<V> before[64];                         // the state after the group before
     uint32_t slot;
 };
@@ -240,9 +241,9 @@ template <int V, int NW, bool BACK>
 __device__ __forceinline__ void enter_tile(const GArgs &g, Lds<V, NW> &lds, int64_t col, int64_t j,
                                            const float *first, float (&h)[V]) {
     const int lane = threadIdx.x & 63, wv = wave_id();
-    const int64_t grp = j / kGroup, groups = (g.tiles + kGroup - 1) / kGroup;
-    const int in = (int)(j % kGroup);
-    const bool last = in == kGroup - 1 && j + 1 < g.tiles;
+    const int grp = (int)j / g.group, in = (int)j % g.group;
+    const int64_t groups = (g.tiles + g.group - 1) / g.group;
+    const bool last = in == g.group - 1 && j + 1 < g.tiles;
     constexpr int W = 64 * V;
     if (wv == NW - 1 && grp == 0) {
         VecF<V> p;
@@ -278,11 +279,8 @@ __device__ __forceinline__ void enter_tile(const GArgs &g, Lds<V, NW> &lds, int6
         }
     }
     // the earlier tiles of the group, a wave each; the group before by the last wave
-#pragma unroll
-    for (int k0 = 0; k0 < kGroup; k0 += NW) {
-        const int k = k0 + wv;
-        if (k >= in) continue;
-        const int64_t t = grp * kGroup + k;
+    for (int k = wv; k < in; k += NW) {
+        const int64_t t = (int64_t)grp * g.group + k;
         const bool ok = wait_flag(g.ch.flag + col * g.tiles + t);
         const uint64_t *m = g.ch.map + (col * g.tiles + t) * W + lane * V;
         VecF<V> A, S;
@@ -612,7 +610,7 @@ struct GatedWs {
     size_t map, after, rate, kept, part, total;
     GatedWs(int64_t b, int64_t l, int64_t d, bool bwd) {
         auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
-        const int64_t tiles = (l + kLeastTile - 1) / kLeastTile, groups = (tiles + kGroup - 1) / kGroup;
+        const int64_t tiles = (l + kLeastTile - 1) / kLeastTile, groups = (tiles + 7) / 8;
         const int64_t cols = b * ((d + 63) / 64), wide = b * ((d + 255) / 256 * 256);
         const bool one = tiles == 1;
         words = one ? 0 : cols * (kTicketWords + tiles + groups);
@@ -651,13 +649,20 @@ bool gated_sizes(int64_t b, int64_t l, int64_t d) {
 template <typename IO> struct FwdShape { static constexpr int SEG = sizeof(IO) == 2 ? 16 : 8, NW = 8; };
 struct BwdShape { static constexpr int SEG = 8, NW = 8; };
 
+// Tiles of a group.  A column's states cross a group per hand-over (2-3 us),
+// and each tile reads the maps of half a group: with few columns the chain of
+// hand-overs is what a call waits for, with many the maps are traffic.
+int group_of(int64_t cols) { return cols <= 4 ? 32 : cols <= 12 ? 16 : 8; }
+
 // The columns' layout at lane width v and `tokens` a tile, the cleared tickets
 // and flags and the rates.
 void set_chain(GArgs &g, const GatedWs &W, char *ws, int v, int tokens, hipStream_t s) {
     g.ncol = (g.d + 64 * v - 1) / (64 * v);
     g.tiles = (g.l + tokens - 1) / tokens;
+    const int64_t cols = g.b * g.ncol;
+    g.group = group_of(cols);  // a call of one tile divides by it too
     if (g.tiles == 1) return;
-    const int64_t cols = g.b * g.ncol, groups = (g.tiles + kGroup - 1) / kGroup;
+    const int64_t groups = (g.tiles + g.group - 1) / g.group;
     g.ch.ticket = reinterpret_cast<uint32_t *>(ws);
     g.ch.flag = g.ch.ticket + cols * kTicketWords;
     g.ch.gflag = g.ch.flag + cols * g.tiles;
