@@ -124,41 +124,49 @@ __device__ __forceinline__ bool wait_flag(const uint32_t *p) {
 
 // What one tile's loads need: this lane's channels and its rows.
 template <typename IO, int V, int SEG> struct Tile {
-    int64_t c;       // first channel of this lane (clamped to a valid one)
+    uint32_t c;      // first channel of this lane (clamped to a valid one)
     bool live;       // the lane's channels exist
     int64_t row0;    // the sequence's first row in [b * l]
     int64_t t0;      // the wave's first token
     __device__ Tile(const GArgs &g, int64_t col, int64_t tile, int tokens) {
         const int lane = threadIdx.x & 63;
-        c = (col % g.ncol * 64 + lane) * V;
+        c = ((uint32_t)col % (uint32_t)g.ncol * 64 + lane) * V;
         live = c < g.d;
         if (!live) c = 0;
-        row0 = col / g.ncol * g.l;
+        row0 = (int64_t)((uint32_t)col / (uint32_t)g.ncol) * g.l;
         t0 = tile * tokens + wave_id() * SEG;
     }
 };
 
+// V elements at element `row` + `lane` of p.  With the row wave-uniform and the
+// lane's channel apart, the access is a scalar address plus a 32-bit offset
+// (the forward pass: 296 -> 291 us at 65536 x 2560); the gradient, short of
+// registers, is faster with whole addresses in them (174 -> 163 us at
+// 4 x 4096 x 2560), and adds the channel to the row.
 template <typename IO, int V>
-__device__ __forceinline__ VecIO<IO, V> ldv(const void *p, int64_t at) {
-    return *reinterpret_cast<const VecIO<IO, V> *>(static_cast<const IO *>(p) + at);
+__device__ __forceinline__ VecIO<IO, V> ldv(const void *p, int64_t row, uint32_t lane = 0) {
+    const char *q = reinterpret_cast<const char *>(static_cast<const IO *>(p) + row);
+    return *reinterpret_cast<const VecIO<IO, V> *>(q + lane * (uint32_t)sizeof(IO));
 }
 template <typename IO, int V>
-__device__ __forceinline__ void stv(void *p, int64_t at, const VecIO<IO, V> &v) {
-    *reinterpret_cast<VecIO<IO, V> *>(static_cast<IO *>(p) + at) = v;
+__device__ __forceinline__ void stv(void *p, int64_t row, uint32_t lane, const VecIO<IO, V> &v) {
+    char *q = reinterpret_cast<char *>(static_cast<IO *>(p) + row);
+    *reinterpret_cast<VecIO<IO, V> *>(q + lane * (uint32_t)sizeof(IO)) = v;
 }
 
 // The wave's rows of x, r and i (rows past the end read the last row).
 template <typename IO, int V, int SEG> struct Rows {
     VecIO<IO, V> x[SEG], r[SEG], i[SEG];
-    __device__ void load(const GArgs &g, const Tile<IO, V, SEG> &w) {
+    template <bool WHOLE> __device__ void load(const GArgs &g, const Tile<IO, V, SEG> &w) {
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             int64_t t = w.t0 + k;
             if (t >= g.l) t = g.l - 1;
-            const int64_t at = (w.row0 + t) * g.d + w.c;
-            x[k] = ldv<IO, V>(g.x, at);
-            r[k] = ldv<IO, V>(g.gates, at + (w.row0 + t) * g.d);
-            i[k] = ldv<IO, V>(g.gates, at + (w.row0 + t + 1) * g.d);
+            const int64_t row = (w.row0 + t) * g.d, in = WHOLE ? w.c : 0;
+            const uint32_t lane = WHOLE ? 0 : w.c;
+            x[k] = ldv<IO, V>(g.x, row + in, lane);
+            r[k] = ldv<IO, V>(g.gates, 2 * row + in, lane);
+            i[k] = ldv<IO, V>(g.gates, 2 * row + g.d + in, lane);
         }
     }
 };
@@ -346,14 +354,15 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_fwd(GArgs g) {
     static_assert(T % SSD_GATED_CHUNK == 0 && SSD_GATED_CHUNK % SEG == 0, "where states are kept");
     __shared__ Lds<V, NW> lds;
     const int lane = threadIdx.x & 63, wv = wave_id();
-    const int64_t cols = g.b * g.ncol, col = blockIdx.x % cols;
+    const uint32_t cols = (uint32_t)(g.b * g.ncol);
+    const int64_t col = blockIdx.x % cols;
     const int64_t tile = g.tiles > 1 ? take_ticket(g, col, &lds.slot) : 0;
     const Tile<IO, V, SEG> w(g, col, tile, T);
-    const int64_t bi = col / g.ncol;
+    const int64_t bi = (uint32_t)col / (uint32_t)g.ncol;
     float m2[V];
     rates(g, w, m2);
     Rows<IO, V, SEG> rw;
-    rw.load(g, w);
+    rw.template load<false>(g, w);
     const float *first = g.init ? g.init + bi * g.d + w.c : nullptr;
     float a[SEG][V], v[SEG][V];
     terms(g, w, rw, m2, a, v);
@@ -383,7 +392,7 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_fwd(GArgs g) {
             h[e] = fmaf(a[k][e], h[e], v[k][e]);
             o.e[e] = (IO)h[e];
         }
-        if (g.y && t < g.l) stv<IO, V>(g.y, (w.row0 + t) * g.d + w.c, o);
+        if (g.y && t < g.l) stv<IO, V>(g.y, (w.row0 + t) * g.d, w.c, o);
     }
     const int64_t end = w.t0 + SEG < g.l ? w.t0 + SEG : g.l;
     VecF<V> o;
@@ -412,7 +421,8 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
     __shared__ Lds<V, NW> lds;
     __shared__ VecF<V> sS[NW][64];  // the waves' maps of the states; A is the adjoint's too
     const int lane = threadIdx.x & 63, wv = wave_id();
-    const int64_t cols = g.b * g.ncol, col = blockIdx.x % cols, bi = col / g.ncol;
+    const uint32_t cols = (uint32_t)(g.b * g.ncol);
+    const int64_t col = blockIdx.x % cols, bi = (uint32_t)col / (uint32_t)g.ncol;
     // the chain runs from the last tile to the first
     const int64_t turn = g.tiles > 1 ? take_ticket(g, col, &lds.slot) : 0;
     const int64_t tile = g.tiles - 1 - turn;
@@ -420,7 +430,7 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
     float m2[V];
     rates(g, w, m2);
     Rows<IO, V, SEG> rw;
-    rw.load(g, w);
+    rw.template load<true>(g, w);
     VecIO<IO, V> dy[SEG];
 #pragma unroll
     for (int k = 0; k < SEG; ++k) {
@@ -512,10 +522,10 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
         }
         __builtin_amdgcn_sched_barrier(0);
         if (w.live) {
-            const int64_t at = (w.row0 + t) * g.d + w.c;
-            stv<IO, V>(g.y, at, ox);
-            stv<IO, V>(g.dgates, at + (w.row0 + t) * g.d, orr);
-            stv<IO, V>(g.dgates, at + (w.row0 + t + 1) * g.d, oi);
+            const int64_t row = (w.row0 + t) * g.d;
+            stv<IO, V>(g.y, row + w.c, 0, ox);
+            stv<IO, V>(g.dgates, 2 * row + w.c, 0, orr);
+            stv<IO, V>(g.dgates, 2 * row + g.d + w.c, 0, oi);
         }
     }
     sS[wv][lane] = acc;
@@ -589,7 +599,7 @@ __global__ __launch_bounds__(256) void k_gated_step(float *state, const IO *x, c
         o.e[e] = (IO)h.e[e];
     }
     *reinterpret_cast<VecF<V> *>(state + at) = h;
-    stv<IO, V>(y, at, o);
+    stv<IO, V>(y, at, 0, o);
 }
 
 // batch > 0, seqlen == 0: the final state is the initial one, or zeros
