@@ -371,10 +371,26 @@ template <typename IO> __global__ __launch_bounds__(256) void k_gemm_sum(GemmArg
 // ------------------------------------------------------------- few rows ----
 // Up to 16 MT rows of x (decoded tokens): bound by the weight's bytes.  A
 // workgroup owns 16 weight rows, its waves 128-byte pieces of them in turn,
-// loaded from memory straight into operands; the waves' sums meet in LDS and
-// are added in order.
+// loaded from memory straight into operands (at any alignment: rows of odd
+// widths are read where they are); the waves' sums meet in LDS and are added
+// in order.
 constexpr int kFewWaves = 4;
 constexpr int kFewUnroll = 4;  // weight pieces in flight a wave
+
+// The 16 bytes of a row of `width` elements from element c, zeros past its end.
+template <typename IO> __device__ __forceinline__ u32x4 row16(const IO *row, int64_t c, int64_t width) {
+    constexpr int N = 16 / (int)sizeof(IO);
+    u32x4 v = {0, 0, 0, 0};
+    if (c + N <= width) {
+        __builtin_memcpy(&v, row + c, 16);
+    } else if (c < width) {
+        IO e[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) e[i] = c + i < width ? row[c + i] : (IO)0.f;
+        __builtin_memcpy(&v, e, 16);
+    }
+    return v;
+}
 
 template <typename IO, int MT>
 __global__ __launch_bounds__(kFewWaves * 64) void k_few(GemmArgs g) {
@@ -401,13 +417,18 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_few(GemmArgs g) {
 #pragma unroll
         for (int i = 0; i < 2 * kFewUnroll; ++i) {
             const int64_t at = k + i / 2 * (kFewWaves * BK) + (4 * (i & 1) + q) * EPC;
-            const bool in = decltype(whole)::value || at < g.k;
-            pw[i] = *reinterpret_cast<const u32x4 *>(w + (in ? at : 0));
-            if (!in) pw[i] = none;
+            constexpr bool W = decltype(whole)::value;
+            if (W)
+                __builtin_memcpy(&pw[i], w + at, 16);
+            else
+                pw[i] = row16(w, at, g.k);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-                px[i][t] = *reinterpret_cast<const u32x4 *>(x[t] + (in ? at : 0));
-                if (!in || !live[t]) px[i][t] = none;
+                if (W)
+                    __builtin_memcpy(&px[i][t], x[t] + at, 16);
+                else
+                    px[i][t] = row16(x[t], at, g.k);
+                if (!live[t]) px[i][t] = none;
             }
         }
 #pragma unroll
@@ -550,6 +571,137 @@ template <typename IO> __global__ __launch_bounds__(256) void k_bwd_prep(PrepArg
     }
 }
 
+// The whole gradient of up to 8 rows in one pass over the weight: bound by its
+// bytes, read for dx and written for dW.  A workgroup owns 16 bytes a lane of
+// `run` weight rows; its waves take rows in turn.  e is worked out in LDS in
+// fp32 (and stays fp32); dx goes out in one part per run, in fp32.
+constexpr int kFewBwdRows = 8, kFewRun = 128;  // rows of x; weight rows of a workgroup at most
+
+template <typename IO, int M>
+__global__ __launch_bounds__(256) void k_few_bwd(PrepArgs g, GemmArgs gx, IO *dw, float *db) {
+    constexpr int V = 16 / (int)sizeof(IO);
+    __shared__ float es[kFewRun][M];
+    __shared__ float red[4][64 * V];
+    const int lane = threadIdx.x & 63, wv = wave_id();
+    const uint32_t cols = (uint32_t)((g.k + 64 * V - 1) / (64 * V));
+    const int64_t run = blockIdx.x / cols, c = (int64_t)(blockIdx.x % cols * 64 + lane) * V;
+    const int64_t n0 = run * g.run, n1 = n0 + g.run < g.n ? n0 + g.run : g.n;
+    const int rows = (int)(n1 - n0);
+    const IO *dy = static_cast<const IO *>(g.dy), *pre = static_cast<const IO *>(g.pre);
+    for (int i = threadIdx.x; i < rows * M; i += 256) {
+        const int m = i / rows, r = i % rows;
+        float e = 0.f;
+        if (m < g.m) {
+            e = to_f32(dy[m * g.n + n0 + r]);
+            if (pre) e *= act_grad(to_f32(pre[m * g.n + n0 + r]), g.act);
+        }
+        es[r][m] = e;
+    }
+    float x[M][V], dx[M][V];
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        u32x4 v = {0, 0, 0, 0};
+        if (dw && m < g.m) v = row16(static_cast<const IO *>(g.x) + m * g.k, c, g.k);
+        IO e[V];
+        __builtin_memcpy(e, &v, 16);
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[m][i] = to_f32(e[i]), dx[m][i] = 0.f;
+    }
+    __syncthreads();
+    if (db && blockIdx.x % cols == 0)
+        for (int r = threadIdx.x; r < rows; r += 256) {
+            float t = 0.f;
+#pragma unroll
+            for (int m = 0; m < M; ++m) t += es[r][m];
+            db[n0 + r] = t;
+        }
+    constexpr int U = 4;  // weight rows in flight a wave
+    for (int r = wv; r < rows; r += 4 * U) {
+        u32x4 pw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int q = r + 4 * u < rows ? r + 4 * u : r;
+            pw[u] = u32x4{0, 0, 0, 0};
+            if (gx.tm) pw[u] = row16(static_cast<const IO *>(g.w) + (n0 + q) * g.k, c, g.k);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int q = r + 4 * u;
+            if (q >= rows) break;
+            IO we[V], o[V];
+            __builtin_memcpy(we, &pw[u], 16);
+            float s[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] = 0.f;
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const float e = es[q][m];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    s[i] = fmaf(e, x[m][i], s[i]);
+                    dx[m][i] = fmaf(e, to_f32(we[i]), dx[m][i]);
+                }
+            }
+            if (!dw || c >= g.k) continue;
+            IO *to = dw + (n0 + q) * g.k + c;
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[i] = (IO)s[i];
+            if (c + V <= g.k)
+                __builtin_memcpy(to, o, 16);
+            else
+                for (int i = 0; i < V; ++i)
+                    if (c + i < g.k) to[i] = o[i];
+        }
+    }
+    if (!gx.tm) return;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+        if (m >= g.m) break;
+#pragma unroll
+        for (int i = 0; i < V; ++i) red[wv][i * 64 + lane] = dx[m][i];
+        __syncthreads();
+        for (int k = threadIdx.x; k < 64 * V; k += 256) {
+            const int64_t col = (int64_t)(blockIdx.x % cols) * 64 * V + (k & 63) * V + (k >> 6);
+            if (col < g.k)
+                gx.parts[(run * g.m + m) * g.k + col] =
+                    (red[0][k] + red[1][k]) + (red[2][k] + red[3][k]);
+        }
+        __syncthreads();
+    }
+}
+
+// dx of few rows from its runs' parts: a workgroup takes 128 columns of a row,
+// 8 runs at a time with four loads in flight, added in a fixed order.
+template <typename IO> __global__ __launch_bounds__(256) void k_few_sum(GemmArgs g) {
+    __shared__ f32x4 s[8][32];
+    const int c = threadIdx.x & 31, q = threadIdx.x >> 5;
+    const int64_t row = blockIdx.y, col = ((int64_t)blockIdx.x * 32 + c) * 4;
+    auto part = [&](int64_t r) {
+        const float *p = g.parts + (r * g.m + row) * g.n + col;
+        f32x4 v = zero4();
+        if (col + 4 <= g.n)
+            v = ldu4(p);
+        else
+            for (int i = 0; col + i < g.n; ++i) v[i] = p[i];
+        return v;
+    };
+    f32x4 t = zero4();
+    int64_t r = q;
+    for (; r + 24 < g.split; r += 32) {
+        f32x4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = part(r + 8 * i);
+        t += (v[0] + v[1]) + (v[2] + v[3]);
+    }
+    for (; r < g.split; r += 8) t += part(r);
+    s[q][c] = t;
+    __syncthreads();
+    if (q != 0 || col >= g.n) return;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) t += s[k][c];
+    finish4<IO>(g.ep, row, col, g.n, t);
+}
+
 // Everything after them in one launch: the sums of products in parts, and the
 // bias gradient from its runs' sums (a workgroup: 32 columns by 8 runs at a
 // time, four loads in flight, added in a fixed order).
@@ -609,6 +761,7 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int64_t kCus = 256;       // compute units of the part this is written for
 constexpr int64_t kFewRows = 32;    // rows up to which k_few runs
+constexpr int64_t kFewOdd = 4;      // and reads rows of odd widths where they are
 
 enum Tile { kT64, kT128, kT192, kTiles };
 struct Shape {
@@ -698,11 +851,19 @@ bool linear_sizes(int64_t m, int64_t n, int64_t k) {
     return m * cdiv(n, 4) < big && m * cdiv(k, 4) < big && n * cdiv(k, 4) < big;
 }
 
-size_t fwd_bytes(int64_t m, int64_t n, int64_t k, int io, size_t *copies) {
-    *copies = odd_rows(k, io) ? up(m * pad(k) * esz(io)) + up(n * pad(k) * esz(io)) : 0;
-    if (m <= kFewRows) return *copies;
-    return *copies + parts_bytes(plan(nullptr, 0, nullptr, 0, m, n, k, choose_fwd(m, n, k, io), 0,
-                                      Epi{}, nullptr, io));
+// Whether a forward call lays its operands out again first.  k_few reads odd
+// rows where they are; bf16 accesses off 4 bytes are slow enough that more than
+// kFewOdd rows of x against a large weight repay the copies (10576 x 2561, 16
+// rows: 48 against 34 us; 1000 x 333: 4.4 against 7.0).
+bool pads(int64_t m, int64_t n, int64_t k, int io) {
+    return odd_rows(k, io) && (m > kFewRows || (io == SSD_BF16 && m > kFewOdd && n * k > (1 << 21)));
+}
+
+size_t fwd_bytes(int64_t m, int64_t n, int64_t k, int io) {
+    const size_t copies = pads(m, n, k, io) ? up(m * pad(k) * esz(io)) + up(n * pad(k) * esz(io)) : 0;
+    if (m <= kFewRows) return copies;
+    return copies + parts_bytes(plan(nullptr, 0, nullptr, 0, m, n, k, choose_fwd(m, n, k, io), 0,
+                                     Epi{}, nullptr, io));
 }
 
 template <typename IO>
@@ -710,7 +871,7 @@ int32_t run_linear(const void *x, const void *w, const Epi &ep, int64_t m, int64
                    char *ws, hipStream_t s) {
     const int io = sizeof(IO) == 2 ? SSD_BF16 : SSD_F32;
     int64_t ld = k;
-    if (odd_rows(k, io)) {
+    if (pads(m, n, k, io)) {
         PrepArgs p{};
         ld = pad(k);
         p.x = x, p.w = w, p.px = ws, p.pw = ws + up(m * ld * sizeof(IO));
@@ -722,7 +883,7 @@ int32_t run_linear(const void *x, const void *w, const Epi &ep, int64_t m, int64
     }
     if (m <= kFewRows) {
         GemmArgs g{};
-        g.A = x, g.B = w, g.lda = g.ldb = ld, g.m = m, g.n = n, g.k = ld, g.ep = ep;
+        g.A = x, g.B = w, g.lda = g.ldb = ld, g.m = m, g.n = n, g.k = k, g.ep = ep;
         const dim3 grid((unsigned)cdiv(n, 16)), block(kFewWaves * 64);
         if (m <= 16)
             hipLaunchKernelGGL((k_few<IO, 1>), grid, block, 0, s, g);
@@ -746,6 +907,14 @@ int32_t run_linear(const void *x, const void *w, const Epi &ep, int64_t m, int64
     return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
+// Whether the gradient takes the one-pass kernel of few rows: for weights of 8 MB
+// or more, where the bytes count (3 rows, 5712 x 4761 fp32: 53 against 110 us by
+// the tiles); a smaller one is done sooner by the tiles (2 rows, 1000 x 1000
+// bf16: 13 against 8 us).
+bool few_bwd(int64_t m, int64_t n, int64_t k, int io) {
+    return m <= kFewBwdRows && n * k * esz(io) >= (8 << 20);
+}
+
 // Parts of the gradient's workspace.
 struct BwdWs {
     bool own_e;
@@ -754,6 +923,14 @@ struct BwdWs {
     size_t e, w, x, part, px, pw, total;
     BwdWs(int64_t m, int64_t n, int64_t k, int act, int io) {
         const int64_t es = esz(io);
+        if (few_bwd(m, n, k, io)) {
+            // about four workgroups a compute unit, 64 to kFewRun weight rows each
+            run = n * cdiv(k, 1024 / es) / (4 * kCus) / 16 * 16;
+            run = run < 64 ? 64 : run > kFewRun ? kFewRun : run;
+            runs = cdiv(n, run);
+            px = 0, total = up(runs * m * k * 4);
+            return;
+        }
         own_e = act != SSD_ACT_NONE || odd_rows(n, io);
         ln = own_e ? pad(n) : n, lk = odd_rows(k, io) ? pad(k) : k;
         // 64 rows a workgroup, or 16 where that leaves compute units without one
@@ -772,11 +949,37 @@ struct BwdWs {
 };
 
 template <typename IO>
+int32_t run_few_bwd(const void *dy, const void *x, const void *w, const void *pre, int act, void *dx,
+                    void *dw, float *db, int64_t m, int64_t n, int64_t k, const BwdWs &L, char *ws,
+                    hipStream_t s) {
+    PrepArgs p{};
+    p.dy = dy, p.pre = act != SSD_ACT_NONE ? pre : nullptr, p.x = x, p.w = w, p.act = act;
+    p.m = m, p.n = n, p.k = k, p.run = (int)L.run;
+    GemmArgs gx{};
+    gx.m = m, gx.n = k, gx.split = L.runs, gx.parts = reinterpret_cast<float *>(ws + L.px);
+    gx.tm = dx != nullptr, gx.ep.out = dx;
+    const dim3 grid((unsigned)(L.runs * cdiv(k, 1024 / (int64_t)sizeof(IO)))), block(256);
+#define SSD_FEW(M)                                                                               \
+    hipLaunchKernelGGL((k_few_bwd<IO, M>), grid, block, 0, s, p, gx, static_cast<IO *>(dw), db)
+    if (m <= 1) SSD_FEW(1);
+    else if (m <= 2) SSD_FEW(2);
+    else if (m <= 4) SSD_FEW(4);
+    else SSD_FEW(8);
+#undef SSD_FEW
+    if (dx)
+        hipLaunchKernelGGL((k_few_sum<IO>), dim3((unsigned)cdiv(k, 128), (unsigned)m), dim3(256), 0, s,
+                           gx);
+    return hipGetLastError() == hipSuccess ? SSD_OK : SSD_ERR_HIP;
+}
+
+template <typename IO>
 int32_t run_linear_bwd(const void *dy, const void *x, const void *w, const void *pre, int act,
                        void *dx, void *dw, float *db, int64_t m, int64_t n, int64_t k, char *ws,
                        hipStream_t s) {
     const int io = sizeof(IO) == 2 ? SSD_BF16 : SSD_F32;
     const BwdWs L(m, n, k, act, io);
+    if (few_bwd(m, n, k, io))
+        return run_few_bwd<IO>(dy, x, w, pre, act, dx, dw, db, m, n, k, L, ws, s);
     PrepArgs p{};
     p.dy = dy, p.pre = act != SSD_ACT_NONE ? pre : nullptr, p.x = x, p.w = w, p.act = act;
     p.m = m, p.n = n, p.k = k, p.ln = L.ln, p.lk = L.lk, p.run = (int)L.run;
@@ -831,8 +1034,7 @@ size_t ssd_linear_workspace_bytes(int64_t rows, int64_t in_dim, int64_t out_dim,
     if ((io_dtype != SSD_F32 && io_dtype != SSD_BF16) || rows <= 0 || in_dim <= 0 || out_dim <= 0 ||
         !linear_sizes(rows, out_dim, in_dim))
         return 0;
-    size_t copies;
-    return fwd_bytes(rows, out_dim, in_dim, io_dtype, &copies);
+    return fwd_bytes(rows, out_dim, in_dim, io_dtype);
 }
 
 size_t ssd_linear_bwd_workspace_bytes(int64_t rows, int64_t in_dim, int64_t out_dim,

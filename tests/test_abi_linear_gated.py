@@ -68,8 +68,8 @@ def test_linear_refusals(lib, L):
     assert lin(k=65, ws=FAKE + 16) == L.SSD_ERR_ALIGN
     assert lin(m=0, x=None) == L.SSD_OK
     ws = lib.ssd_linear_workspace_bytes
-    assert ws(0, 64, 64, 1) == 0 and ws(4, 0, 64, 1) == 0 and ws(4, 65, 64, 5) == 0
-    assert ws(4, 65, 64, 1) == ws(4, 65, 64, 1) > 0
+    assert ws(0, 64, 64, 1) == 0 and ws(40, 0, 64, 1) == 0 and ws(40, 65, 64, 5) == 0
+    assert ws(40, 65, 64, 1) == ws(40, 65, 64, 1) > 0
 
 
 def test_linear_bwd_refusals(lib, L):

@@ -145,7 +145,9 @@ def test_linear_nan_rows_stay_in_their_row():
 
 BWD = [(1, 64, 16), (1, 33, 7), (3, 1, 5), (5, 100, 130), (64, 128, 64), (65, 72, 80),
        (200, 770, 39), (128, 256, 128), (300, 264, 520), (1025, 96, 257), (2047, 130, 71),
-       (4099, 64, 48), (1, 2560, 768), (17, 8, 4)]
+       (4099, 64, 48), (1, 2560, 768), (17, 8, 4),
+       (2, 4761, 300), (7, 80, 1000), (8, 513, 260), (4, 1024, 2047), (9, 72, 40), (8, 520, 9000),
+       (1, 2561, 2000), (2, 8200, 555), (3, 4761, 1111), (6, 1031, 4444)]
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
