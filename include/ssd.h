@@ -494,8 +494,9 @@ size_t ssd_linear_workspace_bytes(int64_t rows, int64_t in_dim, int64_t out_dim,
  *   workspace   ssd_linear_bwd_workspace_bytes(...) bytes, 256-byte aligned
  *
  * Alignment as for ssd_linear.  bf16 io: with an activation, e is rounded
- * to bf16 as the products' operand (their accumulation is fp32); dbias sums
- * the fp32 values of e.  rows == 0 writes zeros to dweight and dbias.
+ * to bf16 as the products' operand (their accumulation is fp32), except for
+ * a few rows against a large weight, whose e stays fp32; dbias sums the fp32
+ * values of e.  rows == 0 writes zeros to dweight and dbias.
  */
 int32_t ssd_linear_bwd(const void *dy, const void *x, const void *weight, const void *pre,
                        int32_t activation, void *dx, void *dweight, float *dbias, int64_t rows,

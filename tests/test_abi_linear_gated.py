@@ -49,6 +49,7 @@ def test_linear_refusals(lib, L):
     assert lin(n=-4) == L.SSD_ERR_SHAPE
     assert lin(k=(1 << 20) + 1) == L.SSD_ERR_UNSUPPORTED
     assert lin(m=1 << 31) == L.SSD_ERR_UNSUPPORTED
+    assert lin(m=1 << 30, k=1, n=1) == L.SSD_ERR_UNSUPPORTED    # rows of one element, padded
     for name in ("x", "w", "o"):
         assert lin(**{name: None}) == L.SSD_ERR_NULL
     # each tensor as its rows are among themselves: 64 and 40 bf16 values are
@@ -125,6 +126,7 @@ def test_gated_refusals(lib, L):
         assert f(scale=math.inf) == L.SSD_ERR_SHAPE
         assert f(scale=math.nan) == L.SSD_ERR_SHAPE
         assert f(b=70000) == L.SSD_ERR_UNSUPPORTED
+        assert f(b=64, l=1 << 20, d=1 << 16) == L.SSD_ERR_UNSUPPORTED   # 2^42 elements
         assert f(x=None) == L.SSD_ERR_NULL
         assert f(g=None) == L.SSD_ERR_NULL
         assert f(lam=None) == L.SSD_ERR_NULL
@@ -160,6 +162,7 @@ def test_gated_refusals(lib, L):
     for name in ("s", "x", "g", "lam", "y"):
         assert step(**{name: None}) == L.SSD_ERR_NULL
         assert step(**{name: FAKE + 1}) == L.SSD_ERR_ALIGN
+    assert step(b=1 << 20, d=1 << 14) == L.SSD_ERR_UNSUPPORTED
     assert step(b=0) == L.SSD_OK
 
 
