@@ -104,6 +104,9 @@ __device__ __forceinline__ void stu4(bf16 *p, f32x4 v) {
     __builtin_memcpy(p, &o, 8);
 }
 
+template <typename IO> struct Four { typedef f32x4 type; };
+template <> struct Four<bf16> { typedef bf16x4 type; };
+
 // Four consecutive n of one row m.
 template <typename IO>
 __device__ __forceinline__ void finish4(const Epi &ep, int64_t m, int64_t n, int64_t N, f32x4 v) {
@@ -309,24 +312,61 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint32_t item, char
         if (k + 1 < steps) step(k + 1, std::integral_constant<int, 1>{});
     }
     // element r of a lane: row m of lane & 15, column 4 (lane >> 4) + r
+    const int64_t mw = m0 + wm + (lane & 15), nw = n0 + wn + 4 * (lane >> 4);
+    if (g.split > 1) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int64_t m = m0 + wm + 16 * i + (lane & 15);
-        if (m >= g.m) continue;
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < NI; ++j) {
-            const int64_t n = n0 + wn + 16 * j + 4 * (lane >> 4);
-            if (n >= g.n) continue;
-            if (g.split > 1) {
+            for (int j = 0; j < NI; ++j) {
+                const int64_t m = mw + 16 * i, n = nw + 16 * j;
+                if (m >= g.m || n >= g.n) continue;
                 float *p = g.parts + (part * g.m + m) * g.n + n;
                 if (n + 4 <= g.n)
                     stu4(p, acc[i][j]);
                 else
-                    for (int r = 0; r < 4 && n + r < g.n; ++r) p[r] = acc[i][j][r];
-            } else {
-                finish4<IO>(g.ep, m, n, g.n, acc[i][j]);
+                    for (int r = 0; n + r < g.n; ++r) p[r] = acc[i][j][r];
             }
+    } else if (m0 + wm + BM / WM <= g.m && n0 + wn + BN / WN <= g.n) {
+        // the wave's part is whole: every residual and bias is requested before
+        // any is used (one after the other, each element waited for its own)
+        const int64_t at = mw * g.n + nw;
+        typedef typename Four<IO>::type R;
+        R res[MI][NI];
+        f32x4 bias[NI];
+#pragma unroll
+        for (int j = 0; j < NI; ++j) bias[j] = g.ep.bias ? ldu4(g.ep.bias + nw + 16 * j) : zero4();
+        if (g.ep.res) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NI; ++j)
+                    __builtin_memcpy(&res[i][j],
+                                     static_cast<const IO *>(g.ep.res) + at + 16 * i * g.n + 16 * j,
+                                     sizeof(R));
         }
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                const int64_t to = at + 16 * i * g.n + 16 * j;
+                f32x4 v = acc[i][j] + bias[j];
+                if (g.ep.pre) stu4(static_cast<IO *>(g.ep.pre) + to, v);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = act_f(v[r], g.ep.act);
+                if (g.ep.res) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] += (float)res[i][j][r];
+                }
+                stu4(static_cast<IO *>(g.ep.out) + to, v);
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j) {
+                const int64_t m = mw + 16 * i, n = nw + 16 * j;
+                if (m < g.m && n < g.n) finish4<IO>(g.ep, m, n, g.n, acc[i][j]);
+            }
     }
 }
 
