@@ -16,6 +16,7 @@ x [b, l, h, p], dt [b, l, h], B and C [b, l, g, n], states [b, h, n, p]
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from typing import Optional, Tuple
 
@@ -525,6 +526,12 @@ def _launch(name, dev, *args) -> None:
         raise SsdError(name, rc)
 
 
+@functools.lru_cache(maxsize=1024)
+def _query(name, *sizes) -> int:
+    """A workspace query of the library: a pure function of the sizes."""
+    return int(getattr(load(), name)(*sizes))
+
+
 def _scratch(workspace, nbytes, dev):
     """The caller's workspace, or one of nbytes from torch's allocator."""
     torch = _torch()
@@ -557,7 +564,6 @@ def linear(x, weight, bias=None, activation: str = "none", residual=None,
     and with return_pre also the pre-activation in the io dtype, which
     linear_bwd takes.  `out` may be the residual."""
     torch = _torch()
-    lib = load()
     dev = x.device
     if dev.type != "cuda":
         raise ValueError("x must be a GPU tensor")
@@ -579,7 +585,7 @@ def linear(x, weight, bias=None, activation: str = "none", residual=None,
         pre = torch.empty(shape, dtype=io, device=dev) if pre_out is None else pre_out
         _fit("pre_out", pre, io, shape, dev)
     m = x.numel() // k if k else 0
-    wsb = int(lib.ssd_linear_workspace_bytes(m, k, n, code))
+    wsb = _query("ssd_linear_workspace_bytes", m, k, n, code)
     ws = _scratch(workspace, wsb, dev) if wsb or workspace is not None else None
     _launch("ssd_linear", dev, _ptr(x), _ptr(weight), _ptr(bias), _ptr(residual), _ptr(o),
             _ptr(pre), act, m, k, n, code, _ptr(ws), 0 if ws is None else ws.numel())
@@ -594,7 +600,6 @@ def linear_bwd(dy, x, weight, pre=None, activation: str = "none", bias: bool = F
     Returns a dict: dx, dweight (io dtype), dbias (fp32); the residual's
     gradient is dy."""
     torch = _torch()
-    lib = load()
     dev = dy.device
     if dev.type != "cuda":
         raise ValueError("dy must be a GPU tensor")
@@ -615,7 +620,7 @@ def linear_bwd(dy, x, weight, pre=None, activation: str = "none", bias: bool = F
     if bias:
         res["dbias"] = torch.empty((n,), dtype=torch.float32, device=dev)
     m = dy.numel() // n if n else 0
-    ws = _scratch(workspace, int(lib.ssd_linear_bwd_workspace_bytes(m, k, n, act, code)), dev)
+    ws = _scratch(workspace, _query("ssd_linear_bwd_workspace_bytes", m, k, n, act, code), dev)
     _launch("ssd_linear_bwd", dev, _ptr(dy), _ptr(x), _ptr(weight), _ptr(pre), act,
             _ptr(res["dx"]), _ptr(res["dweight"]), _ptr(res.get("dbias")), m, k, n, code,
             _ptr(ws), ws.numel())
@@ -645,7 +650,6 @@ def gated_scan(x, gates, lam, scale: float = 8.0, initial_state=None, seq_idx=No
     after every 64 tokens [b, ceil(l / 64), d] (fp32, for gated_scan_bwd) when
     asked for.  final_out may be initial_state."""
     torch = _torch()
-    lib = load()
     if x.dim() != 3:
         raise ValueError("x must be [batch, seqlen, dim]")
     b, l, d = x.shape
@@ -671,7 +675,7 @@ def gated_scan(x, gates, lam, scale: float = 8.0, initial_state=None, seq_idx=No
         states = torch.empty((b, ns, d), dtype=torch.float32, device=dev) \
             if states_out is None else states_out
         _fit("states_out", states, torch.float32, (b, ns, d), dev)
-    ws = _scratch(workspace, int(lib.ssd_gated_scan_workspace_bytes(b, l, d)), dev)
+    ws = _scratch(workspace, _query("ssd_gated_scan_workspace_bytes", b, l, d), dev)
     _launch("ssd_gated_scan", dev, _ptr(x), _ptr(gates), _ptr(lam), float(scale),
             _ptr(initial_state), _ptr(seq_idx), _ptr(y), _ptr(fin), _ptr(states), b, l, d,
             code, _ptr(ws), ws.numel())
@@ -688,7 +692,6 @@ def gated_scan_bwd(x, gates, lam, dy, scale: float = 8.0, initial_state=None, d_
     Returns a dict: dx, dgates (io dtype), dlam, and d_init (fp32) if
     initial_state was given."""
     torch = _torch()
-    lib = load()
     if x.dim() != 3:
         raise ValueError("x must be [batch, seqlen, dim]")
     b, l, d = x.shape
@@ -708,7 +711,7 @@ def gated_scan_bwd(x, gates, lam, dy, scale: float = 8.0, initial_state=None, d_
     res = dict(dx=torch.empty_like(x), dgates=torch.empty_like(gates), dlam=torch.empty_like(lam))
     if initial_state is not None:
         res["d_init"] = torch.empty_like(initial_state)
-    ws = _scratch(workspace, int(lib.ssd_gated_scan_bwd_workspace_bytes(b, l, d)), dev)
+    ws = _scratch(workspace, _query("ssd_gated_scan_bwd_workspace_bytes", b, l, d), dev)
     _launch("ssd_gated_scan_bwd", dev, _ptr(x), _ptr(gates), _ptr(lam), float(scale),
             _ptr(initial_state), _ptr(seq_idx), _ptr(states), _ptr(dy), _ptr(d_final),
             _ptr(res["dx"]), _ptr(res["dgates"]), _ptr(res["dlam"]),
@@ -720,7 +723,6 @@ def gated_step(state, x, gates, lam, scale: float = 8.0, out=None):
     """One token of gated_scan (ssd_gated_step): updates `state` [b, d] (fp32)
     in place, returns y [b, d].  x [b, d], gates [b, 2d] in the io dtype."""
     torch = _torch()
-    lib = load()
     if x.dim() != 2:
         raise ValueError("x must be [batch, dim]")
     b, d = x.shape

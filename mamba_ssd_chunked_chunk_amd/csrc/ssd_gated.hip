@@ -66,25 +66,28 @@ __device__ __forceinline__ void decay(float u2, float &a, float &om) {
 
 // How the tiles of one column (64 V channels of one sequence) hand states
 // along in one pass.  A tile publishes its own map as soon as its rows are
-// read; a tile then needs the maps of the earlier tiles of its group
-// and the state after the group before, which the last tile of that
-// group publishes.  So a state crosses a group per hand-over, and each
-// sum has one order whatever runs first.  Tiles are numbered as their
-// workgroups start (a ticket per column): every tile waits only for lower
-// tickets of its own column, which are running and wait for lower ones in
-// turn, so every wait ends.  The words are written and read at agent scope
-// (the XCDs' L2 caches are not coherent inside a kernel), a flag after its
-// data has reached memory.
-constexpr int kMostGroup = 32;  // tiles of a group: 8 to 32, see group_of
+// read; a tile then needs the maps of the earlier tiles of its group and the
+// state after the group before, which the last tile of that group publishes.
+// So a state crosses a group per hand-over, and each sum has one order whatever
+// runs first.  Tiles are numbered as their workgroups start (a ticket per
+// column): every tile waits only for lower tickets of its own column, which are
+// running and wait for lower ones in turn, so every wait ends.
+//
+// A channel's map is one 64-bit word (its A with the sign bit set, which A
+// never has, and its S), a state one with a mark beside it: a word that is not
+// zero is whole, so nothing has to be ordered against anything and a reader
+// waits on the data itself (with a flag behind the data the writer waited for
+// its stores and the reader made two trips: 65536 tokens of 64 channels 58
+// against 49 us, the gradient of 3 x 1001 x 771 40 against 33).  Words are written and read at agent scope, as the XCDs' L2 caches are not
+// coherent inside a kernel, and cleared before every call.
+constexpr int kMostGroup = 32;    // tiles of a group: 8 to 32, see group_of
 constexpr int kTicketWords = 32;  // a 128-byte line per column's ticket
 
 struct Chain {
-    uint32_t *ticket;   // [cols][kTicketWords]
-    uint32_t *flag;     // [cols][tiles]   the tile's map is there
-    uint32_t *gflag;    // [cols][groups]  the state after the group is there
-    uint64_t *map;      // [cols][tiles][64 V]  (A, S) of a channel
-    uint32_t *after;    // [cols][groups][64 V] the state after the group
-    float *rate;        // [d] scale softplus(lam) in binary orders (NULL without a chain)
+    uint32_t *ticket;  // [cols][kTicketWords]
+    uint64_t *map;     // [cols][tiles][64 V]
+    uint64_t *after;   // [cols][groups][64 V] the state after the group
+    float *rate;       // [d] scale softplus(lam) in binary orders (NULL without a chain)
 };
 
 struct GArgs {
@@ -106,20 +109,35 @@ struct GArgs {
     int group;  // tiles of a group
 };
 
-__device__ __forceinline__ uint32_t get32(const uint32_t *p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+template <int V> struct Words { uint64_t e[V]; };
+
+__device__ __forceinline__ void put_word(uint64_t *p, uint32_t lo, float hi) {
+    __hip_atomic_store(p, ((uint64_t)__builtin_bit_cast(uint32_t, hi) << 32) | lo, __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void put32(uint32_t *p, uint32_t v) {
-    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ float word_value(uint64_t w) {
+    return __builtin_bit_cast(float, (uint32_t)(w >> 32));
 }
-// Waits until *p is set.  The bound (many seconds) only turns a broken
-// promise of the scheduler into NaN results instead of a hang.
-__device__ __forceinline__ bool wait_flag(const uint32_t *p) {
+__device__ __forceinline__ float word_decay(uint64_t w) {
+    return __builtin_bit_cast(float, (uint32_t)w & 0x7fffffffu);
+}
+// Waits until the V words at every lane's p are there.  The bound (many seconds)
+// only turns a broken promise of the scheduler into NaN results instead of a hang.
+template <int V> __device__ __forceinline__ Words<V> wait_words(const uint64_t *p) {
+    Words<V> w;
     for (uint32_t n = 0; n < (1u << 25); ++n) {
-        if (get32(p)) return true;
+        bool there = true;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            w.e[e] = __hip_atomic_load(p + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            there = there && w.e[e] != 0;
+        }
+        if (__all(there)) return w;
         __builtin_amdgcn_s_sleep(1);
     }
-    return false;
+#pragma unroll
+    for (int e = 0; e < V; ++e) w.e[e] = 0x7fc000007fc00000ull;
+    return w;
 }
 
 // What one tile's loads need: this lane's channels and its rows.
@@ -278,35 +296,24 @@ __device__ __forceinline__ void enter_tile(const GArgs &g, Lds<V, NW> &lds, int6
             uint64_t *m = g.ch.map + (col * g.tiles + j) * W + lane * V;
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                __hip_atomic_store(m + e,
-                                   ((uint64_t)__builtin_bit_cast(uint32_t, tS.e[e]) << 32) |
-                                       __builtin_bit_cast(uint32_t, tA.e[e]),
-                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            vm_wait<0>();
-            if (lane == 0) put32(g.ch.flag + col * g.tiles + j, 1);
+                put_word(m + e, __builtin_bit_cast(uint32_t, tA.e[e]) | 0x80000000u, tS.e[e]);
         }
     }
     // the earlier tiles of the group, a wave each; the group before by the last wave
     for (int k = wv; k < in; k += NW) {
         const int64_t t = (int64_t)grp * g.group + k;
-        const bool ok = wait_flag(g.ch.flag + col * g.tiles + t);
-        const uint64_t *m = g.ch.map + (col * g.tiles + t) * W + lane * V;
+        const Words<V> m = wait_words<V>(g.ch.map + (col * g.tiles + t) * W + lane * V);
         VecF<V> A, S;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const uint64_t w = __hip_atomic_load(m + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            A.e[e] = ok ? __builtin_bit_cast(float, (uint32_t)w) : NAN;
-            S.e[e] = __builtin_bit_cast(float, (uint32_t)(w >> 32));
-        }
+        for (int e = 0; e < V; ++e) A.e[e] = word_decay(m.e[e]), S.e[e] = word_value(m.e[e]);
         lds.pA[k][lane] = A;
         lds.pS[k][lane] = S;
     }
     if (wv == NW - 1 && grp > 0) {
-        const bool ok = wait_flag(g.ch.gflag + col * groups + grp - 1);
-        const uint32_t *m = g.ch.after + (col * groups + grp - 1) * W + lane * V;
+        const Words<V> m = wait_words<V>(g.ch.after + (col * groups + grp - 1) * W + lane * V);
         VecF<V> p;
 #pragma unroll
-        for (int e = 0; e < V; ++e) p.e[e] = ok ? __builtin_bit_cast(float, get32(m + e)) : NAN;
+        for (int e = 0; e < V; ++e) p.e[e] = word_value(m.e[e]);
         lds.before[lane] = p;
     }
     __syncthreads();
@@ -319,12 +326,9 @@ __device__ __forceinline__ void enter_tile(const GArgs &g, Lds<V, NW> &lds, int6
         for (int e = 0; e < V; ++e) h[e] = fmaf(A.e[e], h[e], S.e[e]);
     }
     if (wv == 0 && last) {
-        uint32_t *m = g.ch.after + (col * groups + grp) * W + lane * V;
+        uint64_t *m = g.ch.after + (col * groups + grp) * W + lane * V;
 #pragma unroll
-        for (int e = 0; e < V; ++e)
-            put32(m + e, __builtin_bit_cast(uint32_t, fmaf(tA.e[e], h[e], tS.e[e])));
-        vm_wait<0>();
-        if (lane == 0) put32(g.ch.gflag + col * groups + grp, 1);
+        for (int e = 0; e < V; ++e) put_word(m + e, 1, fmaf(tA.e[e], h[e], tS.e[e]));
     }
     // the waves before this one
 #pragma unroll
@@ -338,13 +342,16 @@ __device__ __forceinline__ void enter_tile(const GArgs &g, Lds<V, NW> &lds, int6
     }
 }
 
-// Clears the tickets and flags, and works out the channels' rates once (a
-// softplus is as much work as a token's decay).
-__global__ __launch_bounds__(256) void k_gated_setup(uint32_t *p, int64_t n, const float *lam,
-                                                     float scale, float *rate, int64_t d) {
-    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k < n) p[k] = 0;
-    if (k < d) rate[k] = scale * softplus_f(lam[k]) * kLog2e;
+// Clears the words of one or two chains (counts of 16 bytes), and works out the
+// channels' rates once (a softplus is as much work as a token's decay).
+__global__ __launch_bounds__(256) void k_gated_setup(u32x4 *p, int64_t n, u32x4 *p2, int64_t n2,
+                                                     const float *lam, float scale, float *rate,
+                                                     int64_t d) {
+    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x, all = (int64_t)gridDim.x * 256;
+    const u32x4 zero = {0, 0, 0, 0};
+    for (int64_t i = k; i < n; i += all) p[i] = zero;
+    for (int64_t i = k; i < n2; i += all) p2[i] = zero;
+    for (int64_t i = k; i < d; i += all) rate[i] = scale * softplus_f(lam[i]) * kLog2e;
 }
 
 // ------------------------------------------------------------- forward ----
@@ -624,21 +631,20 @@ bool al(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 constexpr int kLeastTile = 64;  // tokens of the shortest tile
 
-// Workspace: the tickets and flags of every column, the columns' maps and the
-// states after their groups, for any lane width; the backward pass also the
-// states it starts from and the sums behind dlam.
+// Workspace: a chain's tickets, maps and states after groups for any lane width
+// (the gradient may need a second one, to run the forward pass), the rates, and
+// for the gradient the states it starts from and the sums behind dlam.
 struct GatedWs {
-    int64_t words;  // tickets and flags
-    size_t map, after, rate, kept, part, total;
+    size_t chain, chain2, rate, kept, part, total;
     GatedWs(int64_t b, int64_t l, int64_t d, bool bwd) {
         auto up = [](size_t v) { return (v + 255) & ~(size_t)255; };
         const int64_t tiles = (l + kLeastTile - 1) / kLeastTile, groups = (tiles + 7) / 8;
         const int64_t cols = b * ((d + 63) / 64), wide = b * ((d + 255) / 256 * 256);
         const bool one = tiles == 1;
-        words = one ? 0 : cols * (kTicketWords + tiles + groups);
-        size_t o = up(words * 4);
-        map = o, o += one ? 0 : up((size_t)wide * tiles * 8);
-        after = o, o += one ? 0 : up((size_t)wide * groups * 4);
+        const size_t words = one ? 0 : up(cols * kTicketWords * 4 + wide * (tiles + groups) * 8);
+        size_t o = 0;
+        chain = o, o += words;
+        chain2 = o, o += bwd ? words : 0;
         rate = o, o += one ? 0 : up((size_t)d * 4);
         kept = o, o += bwd && !one ? up((size_t)b * ((l + SSD_GATED_CHUNK - 1) / SSD_GATED_CHUNK) * d * 4) : 0;
         part = o, o += bwd ? up((size_t)b * tiles * d * 4) : 0;
@@ -672,50 +678,73 @@ template <typename IO> struct FwdShape { static constexpr int SEG = sizeof(IO) =
 struct BwdShape { static constexpr int SEG = 8, NW = 8; };
 
 // Tiles of a group.  A column's states cross a group per hand-over (2-3 us),
-// and each tile reads the maps of half a group: with few columns the chain of
-// hand-overs is what a call waits for, with many the maps are traffic.
-int group_of(int64_t cols) { return cols <= 4 ? 32 : cols <= 12 ? 16 : 8; }
+// and each tile reads the maps of half a group: where few columns or few tiles
+// leave the chain of hand-overs to wait for, long groups are better (65536
+// tokens of 64 channels: 58 us with 32, 125 with 8), with many the maps are
+// traffic (2560 channels: 318 against 295).
+int group_of(int64_t cols, int64_t tiles) {
+    return cols <= 4 || cols * tiles <= 1024 ? 32 : cols <= 12 ? 16 : 8;
+}
 
-// The columns' layout at lane width v and `tokens` a tile, the cleared tickets
-// and flags and the rates.
-void set_chain(GArgs &g, const GatedWs &W, char *ws, int v, int tokens, hipStream_t s) {
+// The layout of a chain at lane width v and `tokens` a tile, in `words`; returns
+// the 16-byte pieces to clear.
+int64_t set_chain(GArgs &g, char *words, float *rate, int v, int tokens) {
     g.ncol = (g.d + 64 * v - 1) / (64 * v);
     g.tiles = (g.l + tokens - 1) / tokens;
     const int64_t cols = g.b * g.ncol;
-    g.group = group_of(cols);  // a call of one tile divides by it too
-    if (g.tiles == 1) return;
+    g.group = group_of(cols, g.tiles);  // a call of one tile divides by it too
+    if (g.tiles == 1) return 0;
     const int64_t groups = (g.tiles + g.group - 1) / g.group;
-    g.ch.ticket = reinterpret_cast<uint32_t *>(ws);
-    g.ch.flag = g.ch.ticket + cols * kTicketWords;
-    g.ch.gflag = g.ch.flag + cols * g.tiles;
-    g.ch.map = reinterpret_cast<uint64_t *>(ws + W.map);
-    g.ch.after = reinterpret_cast<uint32_t *>(ws + W.after);
-    g.ch.rate = reinterpret_cast<float *>(ws + W.rate);
-    const int64_t n = cols * (kTicketWords + g.tiles + groups), most = n > g.d ? n : g.d;
-    hipLaunchKernelGGL(k_gated_setup, dim3((unsigned)((most + 255) / 256)), dim3(256), 0, s,
-                       g.ch.ticket, n, g.lam, g.scale, g.ch.rate, g.d);
+    g.ch.ticket = reinterpret_cast<uint32_t *>(words);
+    g.ch.map = reinterpret_cast<uint64_t *>(words + cols * kTicketWords * 4);
+    g.ch.after = g.ch.map + cols * g.tiles * 64 * v;
+    g.ch.rate = rate;
+    return cols * (kTicketWords * 4 + (g.tiles + groups) * 64 * v * 8) / 16;
+}
+
+void setup(const GArgs &g, char *words, int64_t n, char *words2, int64_t n2, float *rate,
+           hipStream_t s) {
+    if (n + n2 == 0) return;
+    int64_t blocks = ((n > g.d ? n : g.d) + 255) / 256;
+    if (blocks > 4096) blocks = 4096;
+    hipLaunchKernelGGL(k_gated_setup, dim3((unsigned)blocks), dim3(256), 0, s,
+                       reinterpret_cast<u32x4 *>(words), n, reinterpret_cast<u32x4 *>(words2), n2,
+                       g.lam, g.scale, rate, g.d);
+}
+
+template <typename IO, int V> void run_fwd(const GArgs &g, hipStream_t s) {
+    typedef FwdShape<IO> F;
+    hipLaunchKernelGGL((k_gated_fwd<IO, V, F::SEG, F::NW>),
+                       dim3((unsigned)(g.b * g.ncol * g.tiles)), dim3(F::NW * 64), 0, s, g);
 }
 
 template <typename IO, int V>
 hipError_t fwd(GArgs g, const GatedWs &W, char *ws, hipStream_t s) {
     typedef FwdShape<IO> F;
-    set_chain(g, W, ws, V, F::SEG * F::NW, s);
-    hipLaunchKernelGGL((k_gated_fwd<IO, V, F::SEG, F::NW>),
-                       dim3((unsigned)(g.b * g.ncol * g.tiles)), dim3(F::NW * 64), 0, s, g);
+    float *rate = reinterpret_cast<float *>(ws + W.rate);
+    const int64_t n = set_chain(g, ws + W.chain, rate, V, F::SEG * F::NW);
+    setup(g, ws + W.chain, n, nullptr, 0, rate, s);
+    run_fwd<IO, V>(g, s);
     return hipGetLastError();
 }
 
 template <typename IO, int V>
 hipError_t bwd(GArgs g, const GatedWs &W, char *ws, float *dlam, hipStream_t s) {
     typedef BwdShape B;
-    if (!g.kept && g.l > B::SEG * B::NW) {
+    typedef FwdShape<IO> F;
+    float *rate = reinterpret_cast<float *>(ws + W.rate);
+    const int64_t n = set_chain(g, ws + W.chain, rate, V, B::SEG * B::NW);
+    if (!g.kept && g.tiles > 1) {  // the states that the tiles start from
         GArgs f = g;
+        f.ch = Chain{};
         f.y = nullptr, f.fin = nullptr, f.states = reinterpret_cast<float *>(ws + W.kept);
-        const hipError_t e = fwd<IO, V>(f, W, ws, s);
-        if (e != hipSuccess) return e;
+        const int64_t n2 = set_chain(f, ws + W.chain2, rate, V, F::SEG * F::NW);
+        setup(g, ws + W.chain, n, ws + W.chain2, n2, rate, s);
+        run_fwd<IO, V>(f, s);
         g.kept = f.states;
+    } else {
+        setup(g, ws + W.chain, n, nullptr, 0, rate, s);
     }
-    set_chain(g, W, ws, V, B::SEG * B::NW, s);
     hipLaunchKernelGGL((k_gated_bwd<IO, V, B::SEG, B::NW>),
                        dim3((unsigned)(g.b * g.ncol * g.tiles)), dim3(B::NW * 64), 0, s, g);
     hipLaunchKernelGGL(k_gated_lam, dim3((unsigned)((g.d + 31) / 32)), dim3(1024), 0, s, g.part,
