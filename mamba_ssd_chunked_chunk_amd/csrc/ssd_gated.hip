@@ -566,7 +566,7 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
 }
 
 // dlam: the tiles' sums, added in a fixed order in fp64.  One workgroup: 32
-// channels by 32 runs of tiles, four loads in flight a thread.
+// channels by 32 runs of tiles, sixteen loads in flight a thread.
 __global__ __launch_bounds__(1024) void k_gated_lam(const float *part, const float *lam,
                                                     float *dlam, int64_t rows, int64_t d) {
     __shared__ double s[32][33];
@@ -575,6 +575,13 @@ __global__ __launch_bounds__(1024) void k_gated_lam(const float *part, const flo
     double t = 0;
     if (ch < d) {
         int64_t j = k;
+        for (; j + 32 * 15 < rows; j += 512) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = part[(j + 32 * i) * d + ch];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) t += v[i];
+        }
         for (; j + 96 < rows; j += 128) {
             float v[4];
 #pragma unroll
@@ -600,10 +607,9 @@ template <typename IO, int V>
 __global__ __launch_bounds__(256) void k_gated_step(float *state, const IO *x, const IO *gates,
                                                     const float *lam, float scale, IO *y,
                                                     int64_t b, int64_t d) {
-    const int64_t n = b * (d / V);
-    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k >= n) return;
-    const int64_t bi = k / (d / V), c = (k % (d / V)) * V, at = bi * d + c;
+    const uint32_t q = (uint32_t)d / V, k = blockIdx.x * 256 + threadIdx.x;  // fewer than 2^32
+    if (k >= b * q) return;
+    const int64_t bi = k / q, c = (int64_t)(k % q) * V, at = bi * d + c;
     VecF<V> h = *reinterpret_cast<const VecF<V> *>(state + at);
     const VecF<V> lm = *reinterpret_cast<const VecF<V> *>(lam + c);
     const VecIO<IO, V> xv = ldv<IO, V>(x, at), r = ldv<IO, V>(gates, at + bi * d),

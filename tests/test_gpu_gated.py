@@ -251,3 +251,75 @@ def test_tensors_at_odd_offsets(io):
             assert torch.equal(u, v)
         for k in ga:
             assert torch.equal(ga[k], gb[k]), k
+
+
+def test_every_token_its_own_document():
+    """With a new document at every token the state is what the token adds, and
+    no gradient crosses."""
+    import mamba_ssd_chunked_chunk_amd as ssd
+    from oracle import gated as go
+    torch = torch_mod()
+    c = _case(5500, 2, 300, 40, io="f32")
+    seq = torch.arange(300, dtype=torch.int32, device="cuda").repeat(2, 1)
+    y, fin = ssd.gated_scan(c["x"], c["gates"], c["lam"], seq_idx=seq, return_final_state=True)
+    g = ssd.gated_scan_bwd(c["x"], c["gates"], c["lam"], c["dy"], seq_idx=seq)
+    torch.cuda.synchronize()
+    n = _np(c)
+    r = go.scan(n["x"], n["gates"], n["lam"], 8.0, None, seq.cpu().numpy(), delta=DELTA)
+    _close(y, r["y"], r["err"] + 1e-30, "y")
+    assert torch.equal(fin, y[:, -1])
+    k = go.grad(n["x"], n["gates"], n["lam"], 8.0, n["dy"], None, seq.cpu().numpy(), None,
+                delta=DELTA)
+    for key in ("dx", "dgates", "dlam"):
+        _close(g[key], k[key], k["err_" + key] + 1e-30, key)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with its own workspace, give what each gives alone."""
+    import mamba_ssd_chunked_chunk_amd as ssd
+    torch = torch_mod()
+    cs = [_case(5600 + k, 2, 3000, 512, io="bf16", docs=k == 1) for k in range(2)]
+
+    def run(c):
+        y, fin, st = ssd.gated_scan(c["x"], c["gates"], c["lam"], initial_state=c["init"],
+                                    seq_idx=c["seq"], return_final_state=True,
+                                    return_states=True)
+        g = ssd.gated_scan_bwd(c["x"], c["gates"], c["lam"], c["dy"], initial_state=c["init"],
+                               seq_idx=c["seq"], d_final=c["dfin"])
+        return [y, fin, st] + [g[k] for k in sorted(g)]
+    want = [run(c) for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(5):
+        for k, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[k] = run(cs[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        for a, b in zip(got[k], want[k]):
+            assert torch.equal(a, b)
+
+
+def test_offsets_beyond_32_bits():
+    """Gates of 2.4e9 values (4.9 GB): the last tokens equal a scan of the tail
+    from the state kept before it, up to the rounding of the states on the way
+    (a few 2^-24) and one bf16 step."""
+    import mamba_ssd_chunked_chunk_amd as ssd
+    torch = torch_mod()
+    b, l, d = 1, 300032, 4096
+    log("gated_scan", b, l, d)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn((b, l, d), generator=gen, device="cuda", dtype=torch.bfloat16)
+    gates = torch.randn((b, l, 2 * d), generator=gen, device="cuda", dtype=torch.bfloat16)
+    lam = torch.full((d,), -6.0, device="cuda")
+    y, fin, st = ssd.gated_scan(x, gates, lam, return_final_state=True, return_states=True)
+    at = l - 512
+    yt, ft = ssd.gated_scan(x[:, at:].clone(), gates[:, at:].clone(), lam,
+                            initial_state=st[:, at // 64 - 1].clone(), return_final_state=True)
+    torch.cuda.synchronize()
+    a, o = to_f64(y[:, at:]), to_f64(yt)
+    assert (np.abs(a - o) <= 2.0 ** -7 * np.abs(o) + 1e-5).all()
+    np.testing.assert_allclose(to_f64(fin), to_f64(ft), rtol=1e-5, atol=1e-5)

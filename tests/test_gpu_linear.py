@@ -246,3 +246,38 @@ def test_linear_of_row_slices(io):
         assert torch.equal(got, want)
         for key in gg:
             assert torch.equal(gg[key], gw[key]), key
+
+
+def test_offsets_beyond_32_bits():
+    """An output of 2.9e9 values: sampled rows, and the weight's gradient over all
+    of them, against fp64 (tolerances as above)."""
+    import mamba_ssd_chunked_chunk_amd as ssd
+    torch = torch_mod()
+    m, k, n = 700001, 24, 4096
+    log("linear", m, k, n)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((m, k), generator=gen, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn((n, k), generator=gen, device="cuda", dtype=torch.bfloat16)
+    y = ssd.linear(x, w)
+    g = ssd.linear_bwd(y, x, w, bias=True)
+    torch.cuda.synchronize()
+    rows = [0, 1, 127, 128, 350000, 524287, 524288, m - 130, m - 2, m - 1]
+    xo, wo = to_f64(x[rows]), to_f64(w)
+    o, mag = xo @ wo.T, np.abs(xo) @ np.abs(wo).T
+    _close(y[rows], o, 1.01 * (HALF["bf16"] * np.abs(o) + (k + 4) * 2.0 ** -24 * mag), "y")
+    e = to_f64(y[rows])
+    o, mag = e @ wo, np.abs(e) @ np.abs(wo)
+    _close(g["dx"][rows], o, 1.01 * (HALF["bf16"] * np.abs(o) + (n + 4) * 2.0 ** -24 * mag), "dx")
+    dw = torch.zeros((n, k), dtype=torch.float64, device="cuda")
+    ma, db, mb = torch.zeros_like(dw), torch.zeros(n, dtype=torch.float64, device="cuda"), 0
+    for i in range(0, m, 50000):
+        ec, xc = y[i:i + 50000].double().t().contiguous(), x[i:i + 50000].double()
+        dw += ec @ xc
+        ma += ec.abs() @ xc.abs()
+        db += ec.sum(1)
+        mb = mb + ec.abs().sum(1)
+    o = to_f64(g["dweight"])
+    tol = 1.01 * (HALF["bf16"] * dw.abs() + (m + 4) * 2.0 ** -24 * ma).cpu().numpy()
+    assert (np.abs(o - dw.cpu().numpy()) <= tol).all()
+    tol = 1.01 * ((m + 4) * 2.0 ** -24 * mb).cpu().numpy()
+    assert (np.abs(to_f64(g["dbias"]) - db.cpu().numpy()) <= tol).all()
