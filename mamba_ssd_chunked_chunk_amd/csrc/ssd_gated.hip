@@ -158,9 +158,7 @@ template <typename IO, int V, int SEG> struct Tile {
 
 // V elements at element `row` + `lane` of p.  With the row wave-uniform and the
 // lane's channel apart, the access is a scalar address plus a 32-bit offset
-// (the forward pass: 296 -> 291 us at 65536 x 2560); the gradient, short of
-// registers, is faster with whole addresses in them (174 -> 163 us at
-// 4 x 4096 x 2560), and adds the channel to the row.
+// (the forward pass at 65536 x 2560: 291 us, 296 with whole addresses).
 template <typename IO, int V>
 __device__ __forceinline__ VecIO<IO, V> ldv(const void *p, int64_t row, uint32_t lane = 0) {
     const char *q = reinterpret_cast<const char *>(static_cast<const IO *>(p) + row);
@@ -175,16 +173,15 @@ __device__ __forceinline__ void stv(void *p, int64_t row, uint32_t lane, const V
 // The wave's rows of x, r and i (rows past the end read the last row).
 template <typename IO, int V, int SEG> struct Rows {
     VecIO<IO, V> x[SEG], r[SEG], i[SEG];
-    template <bool WHOLE> __device__ void load(const GArgs &g, const Tile<IO, V, SEG> &w) {
+    __device__ void load(const GArgs &g, const Tile<IO, V, SEG> &w) {
 #pragma unroll
         for (int k = 0; k < SEG; ++k) {
             int64_t t = w.t0 + k;
             if (t >= g.l) t = g.l - 1;
-            const int64_t row = (w.row0 + t) * g.d, in = WHOLE ? w.c : 0;
-            const uint32_t lane = WHOLE ? 0 : w.c;
-            x[k] = ldv<IO, V>(g.x, row + in, lane);
-            r[k] = ldv<IO, V>(g.gates, 2 * row + in, lane);
-            i[k] = ldv<IO, V>(g.gates, 2 * row + g.d + in, lane);
+            const int64_t row = (w.row0 + t) * g.d;
+            x[k] = ldv<IO, V>(g.x, row, w.c);
+            r[k] = ldv<IO, V>(g.gates, 2 * row, w.c);
+            i[k] = ldv<IO, V>(g.gates, 2 * row + g.d, w.c);
         }
     }
 };
@@ -374,7 +371,7 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_fwd(GArgs g) {
     float m2[V];
     rates(g, w, m2);
     Rows<IO, V, SEG> rw;
-    rw.template load<false>(g, w);
+    rw.load(g, w);
     const float *first = g.init ? g.init + bi * g.d + w.c : nullptr;
     float a[SEG][V], v[SEG][V];
     terms(g, w, rw, m2, a, v);
@@ -429,10 +426,11 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_fwd(GArgs g) {
 //
 // The states come from the forward pass's (or one more run of it), the adjoint
 // is chained as the states are there.  14 bytes an element (bf16): 4 x 4096 x
-// 2560 in 163 us, 3.6 TB/s.  Its five kept values per element fill the 128
-// registers that two workgroups a compute unit leave (11 spill); 4 tokens a wave
-// (no spill, more composing) take 190 us, 128-token tiles 185, one workgroup a
-// unit 188.
+// 2560 in 144 us, 4.1 TB/s.  Two workgroups a compute unit leave 128 registers
+// a thread: four values an element are kept and 1 - a^2 is computed twice, which
+// is one exponential more and no spilled registers (fp32: 2; five values kept:
+// 12 and 169 us).  4 tokens a wave (more composing) take 187 us, 128-token tiles
+// of 16 waves 159, 16 tokens a wave with one workgroup a unit 172.
 template <typename IO, int V, int SEG, int NW>
 __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
     constexpr int T = SEG * NW;
@@ -449,12 +447,12 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
     float m2[V];
     rates(g, w, m2);
     Rows<IO, V, SEG> rw;
-    rw.template load<true>(g, w);
+    rw.load(g, w);
     VecIO<IO, V> dy[SEG];
 #pragma unroll
     for (int k = 0; k < SEG; ++k) {
         const int64_t t = w.t0 + k < g.l ? w.t0 + k : g.l - 1;
-        dy[k] = ldv<IO, V>(g.dy, (w.row0 + t) * g.d + w.c);
+        dy[k] = ldv<IO, V>(g.dy, (w.row0 + t) * g.d, w.c);
     }
     float h[V], q[V];
     const float *first = g.dfin ? g.dfin + bi * g.d + w.c : nullptr;
@@ -465,16 +463,17 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
         h[e] = tile > 0 ? g.kept[(bi * ns + tile * T / SSD_GATED_CHUNK - 1) * g.d + ch]
                         : (g.init ? g.init[bi * g.d + ch] : 0.f);
     }
-    // kept for the second half: the decay, both gates and 1 - a^2
-    float a[SEG][V], v[SEG][V], sr[SEG][V], si[SEG][V], om[SEG][V];
+    // kept for the second half: the decay and both gates
+    float a[SEG][V], v[SEG][V], sr[SEG][V], si[SEG][V];
 #pragma unroll
     for (int k = 0; k < SEG; ++k) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             sr[k][e] = sigmoid_f(to_f32(rw.r[k].e[e]));
             si[k][e] = sigmoid_f(to_f32(rw.i[k].e[e]));
-            decay(m2[e] * sr[k][e], a[k][e], om[k][e]);
-            v[k][e] = __builtin_amdgcn_sqrtf(om[k][e]) * si[k][e] * to_f32(rw.x[k].e[e]);
+            float om;
+            decay(m2[e] * sr[k][e], a[k][e], om);
+            v[k][e] = __builtin_amdgcn_sqrtf(om) * si[k][e] * to_f32(rw.x[k].e[e]);
         }
         __builtin_amdgcn_sched_barrier(0);  // as in terms()
     }
@@ -517,7 +516,7 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
         }
     VecF<V> acc;
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc.e[e] = 0.f, m2[e] *= kLn2;
+    for (int e = 0; e < V; ++e) acc.e[e] = 0.f;
 #pragma unroll
     for (int k = SEG - 1; k >= 0; --k) {
         const int64_t t = w.t0 + k;
@@ -526,14 +525,20 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const float x = to_f32(rw.x[k].e[e]), gt = to_f32(dy[k].e[e]) + q[e];
+            // 1 - a^2 once more from the gate: the compiler, which would keep
+            // the first one and spill, is not to see that they are the same
+            asm volatile("" : "+v"(sr[k][e]));
+            const float u2 = m2[e] * sr[k][e];
+            float raw, om;  // raw: the decay before mask()
+            decay(u2, raw, om);
             // 1 / beta; a shut gate (om = 0) has beta = om rb = 0 and a finite
             // stand-in for the inverse, which u = 0 then cancels
-            const float rb = __builtin_amdgcn_rsqf(fmaxf(om[k][e], 1e-30f));
-            const float gx = gt * si[k][e], gb = gx * (om[k][e] * rb), gbx = gb * x;
+            const float rb = __builtin_amdgcn_rsqf(fmaxf(om, 1e-30f));
+            const float gx = gt * si[k][e], gb = gx * (om * rb), gbx = gb * x;
             q[e] = a[k][e] * gt;
             // a^2 = 1 - om also where a token starts a document (a = 0 there)
-            const float p = m2[e] * sr[k][e] *
-                            fmaf((1.f - om[k][e]) * rb, gx * x, -q[e] * v[k][e]);
+            const float p = kLn2 * u2 *
+                            fmaf((1.f - om) * rb, gx * x, -q[e] * v[k][e]);
             ox.e[e] = (IO)gb;
             oi.e[e] = (IO)fmaf(-gbx, si[k][e], gbx);
             orr.e[e] = (IO)fmaf(-p, sr[k][e], p);
@@ -542,9 +547,9 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
         __builtin_amdgcn_sched_barrier(0);
         if (w.live) {
             const int64_t row = (w.row0 + t) * g.d;
-            stv<IO, V>(g.y, row + w.c, 0, ox);
-            stv<IO, V>(g.dgates, 2 * row + w.c, 0, orr);
-            stv<IO, V>(g.dgates, 2 * row + g.d + w.c, 0, oi);
+            stv<IO, V>(g.y, row, w.c, ox);
+            stv<IO, V>(g.dgates, 2 * row, w.c, orr);
+            stv<IO, V>(g.dgates, 2 * row + g.d, w.c, oi);
         }
     }
     sS[wv][lane] = acc;
