@@ -522,7 +522,9 @@ size_t ssd_linear_bwd_workspace_bytes(int64_t rows, int64_t in_dim, int64_t out_
  *   init_state   [batch, dim] fp32 or NULL (zeros)
  *   seq_idx      [batch, seqlen] int32 or NULL, as for ssd_chunk_scan_ex: the
  *                state is zero before a token whose index differs from the
- *                token's before it; init_state belongs to the first document
+ *                token's before it; init_state belongs to the first document.
+ *                Nothing of one document reaches another, infinities and NaN
+ *                included, here and in the gradient of x and the gates
  *   y            [batch, seqlen, dim] io dtype, written
  *   final_state  [batch, dim] fp32 or NULL, written; may equal init_state
  *   states       [batch, ceil(seqlen / SSD_GATED_CHUNK), dim] fp32 or NULL:

@@ -186,25 +186,53 @@ template <typename IO, int V, int SEG> struct Rows {
     }
 };
 
-// Whether token t takes the state of the token before it (the first token
-// takes the initial state).
-__device__ __forceinline__ bool same_document(const GArgs &g, int64_t row0, int64_t t) {
-    if (!g.seq || t <= 0 || t >= g.l) return true;
-    return g.seq[row0 + t] == g.seq[row0 + t - 1];
+// PACKED calls hold several documents a sequence.  A run that holds a document's
+// first token keeps nothing of the state entering it, whatever that is: another
+// document's infinity or NaN times zero would not be zero.  Its A is infinite,
+// which no product of decays is, and says so (a zero would not do: decays that
+// underflow are to pass a NaN of their document).  The selects of these two and of
+// the tokens cost 1 to 8% of a call (65536 tokens of 64 channels 52 against 48
+// us), so calls without documents are kernels without them.
+constexpr float kCut = __builtin_inff();
+// The state behind a run that h enters.
+template <bool PACKED> __device__ __forceinline__ float through(float A, float S, float h) {
+    return PACKED && A == kCut ? S : fmaf(A, h, S);
+}
+// A of two runs.
+template <bool PACKED> __device__ __forceinline__ float join(float A, float B) {
+    return PACKED && (A == kCut || B == kCut) ? kCut : A * B;
 }
 
-// Zero decay into a document's first token, and the identity past the end.
+// Which of the wave's tokens (a bit each) start a document inside the sequence.
+// Lane k reads token k's document and the one before it ahead of the rows, so
+// that nothing waits for them later.
+template <bool PACKED, int SEG> struct Starts {
+    int here, before;
+    template <typename W> __device__ __forceinline__ void load(const GArgs &g, const W &w) {
+        here = before = 0;
+        if (!PACKED) return;
+        const int lane = threadIdx.x & 63;
+        const int64_t t = w.t0 + lane;
+        if (lane >= SEG || t <= 0 || t >= g.l) return;
+        here = g.seq[w.row0 + t];
+        before = g.seq[w.row0 + t - 1];
+    }
+    __device__ __forceinline__ uint32_t bits() const {
+        return PACKED ? (uint32_t)__ballot(here != before) : 0;
+    }
+};
+
+// The identity past the end.
 template <typename IO, int V, int SEG>
 __device__ __forceinline__ void mask(const GArgs &g, const Tile<IO, V, SEG> &w,
                                      float (&a)[SEG][V], float (&v)[SEG][V]) {
-    if (w.t0 + SEG <= g.l && !g.seq) return;
+    if (w.t0 + SEG <= g.l) return;
 #pragma unroll
     for (int k = 0; k < SEG; ++k) {
-        const int64_t t = w.t0 + k;
-        const bool in = t < g.l, same = same_document(g, w.row0, t);
+        const bool in = w.t0 + k < g.l;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            a[k][e] = in ? (same ? a[k][e] : 0.f) : 1.f;
+            a[k][e] = in ? a[k][e] : 1.f;
             v[k][e] = in ? v[k][e] : 0.f;
         }
     }
@@ -229,6 +257,29 @@ __device__ __forceinline__ void terms(const GArgs &g, const Tile<IO, V, SEG> &w,
         __builtin_amdgcn_sched_barrier(0);
     }
     mask(g, w, a, v);
+}
+
+// The map of the wave's tokens.
+template <int V, int SEG>
+__device__ __forceinline__ void run_map(const float (&a)[SEG][V], const float (&v)[SEG][V],
+                                        uint32_t cut, VecF<V> &A, VecF<V> &S) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        float p = 1.f, s = 0.f;
+        if (cut) {
+            p = kCut;
+#pragma unroll
+            for (int k = 0; k < SEG; ++k) s = fmaf(a[k][e], cut >> k & 1 ? 0.f : s, v[k][e]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < SEG; ++k) {
+                p *= a[k][e];
+                s = fmaf(a[k][e], s, v[k][e]);
+            }
+        }
+        A.e[e] = p;
+        S.e[e] = s;
+    }
 }
 
 template <typename IO, int V, int SEG>
@@ -260,7 +311,7 @@ template <int V, int NW> struct Lds {
 // zero); the tiles that take it have read it before they publish anything, so
 // the chain's end may overwrite it.  Every wave of the workgroup
 // calls it; the waves' maps are in lds.A, lds.S already.
-template <int V, int NW, bool BACK>
+template <int V, int NW, bool BACK, bool PACKED>
 __device__ __forceinline__ void enter_tile(const GArgs &g, Lds<V, NW> &lds, int64_t col, int64_t j,
                                            const float *first, float (&h)[V]) {
     const int lane = threadIdx.x & 63, wv = wave_id();
@@ -285,8 +336,8 @@ __device__ __forceinline__ void enter_tile(const GArgs &g, Lds<V, NW> &lds, int6
             const VecF<V> S = lds.S[BACK ? NW - 1 - k : k][lane];
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                tA.e[e] *= A.e[e];
-                tS.e[e] = fmaf(A.e[e], tS.e[e], S.e[e]);
+                tA.e[e] = join<PACKED>(tA.e[e], A.e[e]);
+                tS.e[e] = through<PACKED>(A.e[e], S.e[e], tS.e[e]);
             }
         }
         if (!last) {
@@ -320,12 +371,12 @@ __device__ __forceinline__ void enter_tile(const GArgs &g, Lds<V, NW> &lds, int6
     for (int k = 0; k < in; ++k) {
         const VecF<V> A = lds.pA[k][lane], S = lds.pS[k][lane];
 #pragma unroll
-        for (int e = 0; e < V; ++e) h[e] = fmaf(A.e[e], h[e], S.e[e]);
+        for (int e = 0; e < V; ++e) h[e] = through<PACKED>(A.e[e], S.e[e], h[e]);
     }
     if (wv == 0 && last) {
         uint64_t *m = g.ch.after + (col * groups + grp) * W + lane * V;
 #pragma unroll
-        for (int e = 0; e < V; ++e) put_word(m + e, 1, fmaf(tA.e[e], h[e], tS.e[e]));
+        for (int e = 0; e < V; ++e) put_word(m + e, 1, through<PACKED>(tA.e[e], tS.e[e], h[e]));
     }
     // the waves before this one
 #pragma unroll
@@ -334,7 +385,7 @@ __device__ __forceinline__ void enter_tile(const GArgs &g, Lds<V, NW> &lds, int6
         if (BACK ? w > wv : w < wv) {
             const VecF<V> A = lds.A[w][lane], S = lds.S[w][lane];
 #pragma unroll
-            for (int e = 0; e < V; ++e) h[e] = fmaf(A.e[e], h[e], S.e[e]);
+            for (int e = 0; e < V; ++e) h[e] = through<PACKED>(A.e[e], S.e[e], h[e]);
         }
     }
 }
@@ -357,7 +408,7 @@ __global__ __launch_bounds__(256) void k_gated_setup(u32x4 *p, int64_t n, u32x4 
 // left is the hand-over.  Reading everything twice (maps, chain, states) took
 // 857.  A wave takes 16 tokens of 128 channels in bf16: with 8 of 256 the tiles'
 // maps are twice the traffic (350 us).
-template <typename IO, int V, int SEG, int NW>
+template <typename IO, int V, int SEG, int NW, bool PACKED>
 __global__ __launch_bounds__(NW * 64, 4) void k_gated_fwd(GArgs g) {
     constexpr int T = SEG * NW;
     static_assert(T % SSD_GATED_CHUNK == 0 && SSD_GATED_CHUNK % SEG == 0, "where states are kept");
@@ -368,29 +419,22 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_fwd(GArgs g) {
     const int64_t tile = g.tiles > 1 ? take_ticket(g, col, &lds.slot) : 0;
     const Tile<IO, V, SEG> w(g, col, tile, T);
     const int64_t bi = (uint32_t)col / (uint32_t)g.ncol;
+    Starts<PACKED, SEG> st;
+    st.load(g, w);
     float m2[V];
     rates(g, w, m2);
     Rows<IO, V, SEG> rw;
     rw.load(g, w);
     const float *first = g.init ? g.init + bi * g.d + w.c : nullptr;
     float a[SEG][V], v[SEG][V];
+    const uint32_t cut = st.bits();
     terms(g, w, rw, m2, a, v);
     VecF<V> A, S;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        float p = 1.f, s = 0.f;
-#pragma unroll
-        for (int k = 0; k < SEG; ++k) {
-            p *= a[k][e];
-            s = fmaf(a[k][e], s, v[k][e]);
-        }
-        A.e[e] = p;
-        S.e[e] = s;
-    }
+    run_map(a, v, cut, A, S);
     lds.A[wv][lane] = A;
     lds.S[wv][lane] = S;
     float h[V];
-    enter_tile<V, NW, false>(g, lds, col, tile, first, h);
+    enter_tile<V, NW, false, PACKED>(g, lds, col, tile, first, h);
     if (!w.live || w.t0 >= g.l) return;
 #pragma unroll
     for (int k = 0; k < SEG; ++k) {
@@ -398,6 +442,7 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_fwd(GArgs g) {
         VecIO<IO, V> o;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
+            if (cut >> k & 1) h[e] = 0.f;
             h[e] = fmaf(a[k][e], h[e], v[k][e]);
             o.e[e] = (IO)h[e];
         }
@@ -431,7 +476,7 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_fwd(GArgs g) {
 // is one exponential more and no spilled registers (fp32: 2; five values kept:
 // 12 and 169 us).  4 tokens a wave (more composing) take 187 us, 128-token tiles
 // of 16 waves 159, 16 tokens a wave with one workgroup a unit 172.
-template <typename IO, int V, int SEG, int NW>
+template <typename IO, int V, int SEG, int NW, bool PACKED>
 __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
     constexpr int T = SEG * NW;
     static_assert(T % SSD_GATED_CHUNK == 0 && SSD_GATED_CHUNK % SEG == 0, "where states are kept");
@@ -444,6 +489,8 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
     const int64_t turn = g.tiles > 1 ? take_ticket(g, col, &lds.slot) : 0;
     const int64_t tile = g.tiles - 1 - turn;
     const Tile<IO, V, SEG> w(g, col, tile, T);
+    Starts<PACKED, SEG> st;
+    st.load(g, w);
     float m2[V];
     rates(g, w, m2);
     Rows<IO, V, SEG> rw;
@@ -477,32 +524,30 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
         }
         __builtin_amdgcn_sched_barrier(0);  // as in terms()
     }
+    const uint32_t cut = st.bits();
     mask(g, w, a, v);
     VecF<V> A, S, R;
+    run_map(a, v, cut, A, S);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        float p = 1.f, s = 0.f, r = 0.f;
+        float r = 0.f;
 #pragma unroll
-        for (int k = 0; k < SEG; ++k) {
-            p *= a[k][e];
-            s = fmaf(a[k][e], s, v[k][e]);
-        }
-#pragma unroll
-        for (int k = SEG - 1; k >= 0; --k)
+        for (int k = SEG - 1; k >= 0; --k) {
             if (w.t0 + k < g.l) r = a[k][e] * (to_f32(dy[k].e[e]) + r);
-        A.e[e] = p;
-        S.e[e] = s;
+            if (cut >> k & 1) r = 0.f;
+        }
         R.e[e] = r;
     }
     lds.A[wv][lane] = A;
     lds.S[wv][lane] = R;
     sS[wv][lane] = S;
-    enter_tile<V, NW, true>(g, lds, col, turn, first, q);
+    enter_tile<V, NW, true, PACKED>(g, lds, col, turn, first, q);
 #pragma unroll
     for (int j = 0; j < NW; ++j)
         if (j < wv) {
 #pragma unroll
-            for (int e = 0; e < V; ++e) h[e] = fmaf(lds.A[j][lane].e[e], h[e], sS[j][lane].e[e]);
+            for (int e = 0; e < V; ++e)
+                h[e] = through<PACKED>(lds.A[j][lane].e[e], sS[j][lane].e[e], h[e]);
         }
     __syncthreads();
     // the states before every token, in place of the added values
@@ -510,6 +555,7 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
     for (int k = 0; k < SEG; ++k)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
+            if (cut >> k & 1) h[e] = 0.f;
             const float hn = fmaf(a[k][e], h[e], v[k][e]);
             v[k][e] = h[e];
             h[e] = hn;
@@ -529,14 +575,13 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
             // the first one and spill, is not to see that they are the same
             asm volatile("" : "+v"(sr[k][e]));
             const float u2 = m2[e] * sr[k][e];
-            float raw, om;  // raw: the decay before mask()
-            decay(u2, raw, om);
+            float at, om;  // at: a[k][e]
+            decay(u2, at, om);
             // 1 / beta; a shut gate (om = 0) has beta = om rb = 0 and a finite
             // stand-in for the inverse, which u = 0 then cancels
             const float rb = __builtin_amdgcn_rsqf(fmaxf(om, 1e-30f));
             const float gx = gt * si[k][e], gb = gx * (om * rb), gbx = gb * x;
-            q[e] = a[k][e] * gt;
-            // a^2 = 1 - om also where a token starts a document (a = 0 there)
+            q[e] = cut >> k & 1 ? 0.f : a[k][e] * gt;
             const float p = kLn2 * u2 *
                             fmaf((1.f - om) * rb, gx * x, -q[e] * v[k][e]);
             ox.e[e] = (IO)gb;
@@ -725,8 +770,11 @@ void setup(const GArgs &g, char *words, int64_t n, char *words2, int64_t n2, flo
 
 template <typename IO, int V> void run_fwd(const GArgs &g, hipStream_t s) {
     typedef FwdShape<IO> F;
-    hipLaunchKernelGGL((k_gated_fwd<IO, V, F::SEG, F::NW>),
-                       dim3((unsigned)(g.b * g.ncol * g.tiles)), dim3(F::NW * 64), 0, s, g);
+    const dim3 grid((unsigned)(g.b * g.ncol * g.tiles)), block(F::NW * 64);
+    if (g.seq)
+        hipLaunchKernelGGL((k_gated_fwd<IO, V, F::SEG, F::NW, true>), grid, block, 0, s, g);
+    else
+        hipLaunchKernelGGL((k_gated_fwd<IO, V, F::SEG, F::NW, false>), grid, block, 0, s, g);
 }
 
 template <typename IO, int V>
@@ -756,8 +804,11 @@ hipError_t bwd(GArgs g, const GatedWs &W, char *ws, float *dlam, hipStream_t s) 
     } else {
         setup(g, ws + W.chain, n, nullptr, 0, rate, s);
     }
-    hipLaunchKernelGGL((k_gated_bwd<IO, V, B::SEG, B::NW>),
-                       dim3((unsigned)(g.b * g.ncol * g.tiles)), dim3(B::NW * 64), 0, s, g);
+    const dim3 grid((unsigned)(g.b * g.ncol * g.tiles)), block(B::NW * 64);
+    if (g.seq)
+        hipLaunchKernelGGL((k_gated_bwd<IO, V, B::SEG, B::NW, true>), grid, block, 0, s, g);
+    else
+        hipLaunchKernelGGL((k_gated_bwd<IO, V, B::SEG, B::NW, false>), grid, block, 0, s, g);
     hipLaunchKernelGGL(k_gated_lam, dim3((unsigned)((g.d + 31) / 32)), dim3(1024), 0, s, g.part,
                        g.lam, dlam, g.b * g.tiles, g.d);
     return hipGetLastError();

@@ -323,3 +323,50 @@ def test_offsets_beyond_32_bits():
     a, o = to_f64(y[:, at:]), to_f64(yt)
     assert (np.abs(a - o) <= 2.0 ** -7 * np.abs(o) + 1e-5).all()
     np.testing.assert_allclose(to_f64(fin), to_f64(ft), rtol=1e-5, atol=1e-5)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [33, 128])
+def test_documents_do_not_reach_each_other(d, io):
+    """Infinities and NaN in some documents (and in the state that the first one
+    starts from) leave the bits of the others as they are, and every later token
+    of their own document not finite."""
+    import mamba_ssd_chunked_chunk_amd as ssd
+    torch = torch_mod()
+    b, l = 2, 2300
+    c = _case(29, b, l, d, io)
+    # starts at the edges of waves, tiles and groups, inside them, and alone
+    starts = [0, 1, 63, 64, 65, 128, 250, 256, 263, 511, 512, 1024, 1025, 1536, 1700, 2048, 2299]
+    seq = torch.zeros(l, dtype=torch.int32)
+    for k, t in enumerate(starts):
+        seq[t:] = k
+    seq = seq.repeat(b, 1).cuda()
+
+    def run(c):
+        y, fin, st = ssd.gated_scan(c["x"], c["gates"], c["lam"], initial_state=c["init"], seq_idx=seq,
+                                    return_final_state=True, return_states=True)
+        for s in (st, None):
+            g = ssd.gated_scan_bwd(c["x"], c["gates"], c["lam"], c["dy"], initial_state=c["init"],
+                                   seq_idx=seq, d_final=c["dfin"], states=s)
+            yield y, fin, g["dx"], g["dgates"]
+
+    clean = list(run(c))
+    for odd in (0, 1):
+        bad = (seq[0] % 2 == odd)
+        p = {k: v.clone() if torch.is_tensor(v) else v for k, v in c.items()}
+        first = [t for k, t in enumerate(starts) if k % 2 == odd]
+        last = [t - 1 for k, t in enumerate(starts) if k and (k - 1) % 2 == odd]
+        p["x"][:, first] = float("nan")
+        p["x"][:, last] = float("inf")
+        p["dy"][:, last] = float("nan")
+        p["gates"][:, first[1:], :d // 2] = float("nan")
+        if odd == 0:
+            p["init"][:] = float("inf")  # the first document's; the last is even too
+            p["dfin"][:] = float("nan")
+        for (y, fin, dx, dg), (y0, fin0, dx0, dg0) in zip(run(p), clean):
+            for g, w in ((y, y0), (dx, dx0), (dg, dg0)):
+                assert torch.equal(g[:, ~bad], w[:, ~bad])
+            assert not torch.isfinite(y[:, bad]).any()
+            assert not torch.isfinite(fin).any() if odd == 0 else torch.equal(fin, fin0)
+            starting = torch.tensor(first)
+            assert torch.isnan(dx[:, starting]).all()
