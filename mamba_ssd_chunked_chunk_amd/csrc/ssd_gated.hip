@@ -37,9 +37,10 @@ __device__ __forceinline__ float sigmoid_f(float z) {
 
 // softplus(v) = max(v, 0) + log1p(y), y = e^-|v|: the exponential with the
 // rounding of its argument put back, and log1p(y) = 2 atanh(z), z = y / (2 + y)
-// <= 1/3, from seven terms (the eighth is below 2^-26 of the sum).
+// <= 1/3, from seven terms (the eighth is below 2^-26 of the sum).  Beyond 200 y
+// is zero in fp32 whatever v, also for an infinite one (a NaN stays one).
 __device__ __forceinline__ float softplus_f(float v) {
-    const float w = -fabsf(v), p = w * kLog2e;
+    const float w = v > 200.f || v < -200.f ? -200.f : -fabsf(v), p = w * kLog2e;
     // log2(e) = kLog2e + 1.9e-8
     const float lo = fmaf(w, kLog2e, -p) + w * 1.925963033e-8f;
     const float y = exp2_fast(p) * fmaf(lo, kLn2, 1.f);

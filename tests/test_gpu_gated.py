@@ -370,3 +370,29 @@ def test_documents_do_not_reach_each_other(d, io):
             assert not torch.isfinite(fin).any() if odd == 0 else torch.equal(fin, fin0)
             starting = torch.tensor(first)
             assert torch.isnan(dx[:, starting]).all()
+
+
+@pytest.mark.parametrize("l", [1, 40, 300])
+def test_rates_at_their_ends(l):
+    """A rate of exactly zero (lam = -inf, or far below) keeps the state and shuts
+    the input, one without bound (lam = inf) keeps nothing; a NaN stays in its
+    channel."""
+    import mamba_ssd_chunked_chunk_amd as ssd
+    torch = torch_mod()
+    c = _case(31, 2, l, 6, "f32")
+    lam = torch.tensor([-float("inf"), -1e4, float("inf"), 1e4, float("nan"), -3.0], device="cuda")
+    kw = dict(initial_state=c["init"])
+    y, fin, st = ssd.gated_scan(c["x"], c["gates"], lam, return_final_state=True,
+                                return_states=True, **kw)
+    g = ssd.gated_scan_bwd(c["x"], c["gates"], lam, c["dy"], states=st, **kw)
+    state = c["init"].clone()
+    y1 = ssd.gated_step(state, c["x"][:, 0].contiguous(), c["gates"][:, 0].contiguous(), lam)
+    for t in (y, y1[:, None]):
+        assert torch.equal(t[..., :2], c["init"][:, None, :2].expand_as(t[..., :2]))
+        assert torch.isnan(t[..., 4]).all() and torch.isfinite(t[..., 5]).all()
+    assert torch.equal(g["dgates"][..., :2], torch.zeros_like(g["dgates"][..., :2]))
+    assert torch.equal(g["dx"][..., :2], torch.zeros_like(g["dx"][..., :2]))
+    # a = 0, beta = 1: sigmoid(i) x, off by at most 14 2^-24 and a rounding
+    want = torch.sigmoid(c["gates"][..., 8:10].double()) * c["x"][..., 2:4].double()
+    assert ((y[..., 2:4] - want).abs() <= 2.0 ** -20 * want.abs()).all()
+    assert torch.isnan(g["dx"][..., 4]).all() and torch.isfinite(g["dx"][..., 5]).all()
