@@ -13,6 +13,7 @@
 #include <type_traits>
 
 #include "../../include/ssd.h"
+#include "ssd_copies.hpp"
 #include "ssd_device.hpp"
 
 namespace ssd {
@@ -153,80 +154,38 @@ __device__ __forceinline__ void finish4(const Epi &ep, int64_t m, int64_t n, int
 }
 
 // ------------------------------------------------------------ LDS tiles ----
-// An operand's tile is ROWS stored rows of 16-byte chunks, CH chunks a row,
-// chunk c of row r kept at slot c ^ f(r).
-//   contraction contiguous: ROWS = tile rows m, a row is 128 bytes of k
-//   contraction outermost:  ROWS = 128 / sizeof(IO) values of k, a row is the tile's m
-template <typename IO, bool TR, int BM> struct OpTile {
-    static constexpr int EPC = 16 / (int)sizeof(IO);
-    static constexpr int BK = 128 / (int)sizeof(IO);
-    static constexpr int ROWS = TR ? BK : BM;
-    static constexpr int CH = TR ? BM / EPC : 8;
-    static constexpr int BYTES = ROWS * CH * 16;
-    static_assert(!TR || (sizeof(IO) == 2 ? CH % 8 : CH % 16) == 0, "f stays inside a row");
-    static __device__ __forceinline__ int f(int r) {
-        if (!TR) return r & 7;
-        // The transposing loads of 32 lanes take 32 bytes of rows 0-3 and 8-11
-        // (4-7 and 12-15): f moves them to eight different eighths of the banks.
-        // Rows of an odd number of 128 bytes alternate halves by themselves.
-        if (sizeof(IO) == 2)
-            return CH % 16 == 0 ? ((r & 3) | ((r >> 1) & 4)) << 1 : (r & 2) | ((r >> 1) & 4);
-        return ((r >> 2) & 3) << 2;  // fp32: 64 bytes of rows 4 apart
-    }
-};
+template <typename IO, bool TR, int BM> using OpTile = TileGeometry<(int)sizeof(IO), TR, BM>;
 
 // A wave's share of an operand's copies into LDS, a step of the contraction at
 // a time: byte offsets from the step's first element, the same in every step,
 // and the resource that the step reads through, moved on by one scalar
-// addition.  What lies past the operand's rows or its contraction is read as
-// zeros: contraction contiguous, the resource ends with the rows (the pieces
-// of a row past its end are masked in the last step); contraction outermost,
-// it ends with the contraction, which only the last step can reach.  Offsets
-// inside a tile stay below 2^30, so where nothing ends kOpen is far enough.
-constexpr int64_t kOpen = 0x7fffffff;
-
+// addition.
 template <typename IO, bool TR, int BM, int NT> struct Copies {
     typedef OpTile<IO, TR, BM> T;
     static constexpr int N = T::BYTES / 16 / NT;
     static_assert(T::BYTES % (16 * NT) == 0, "every wave copies as much");
+    const CopySteps<(int)sizeof(IO), TR, BM> plan;
     uint32_t off[N];
     const char *base;
-    int64_t stride;   // bytes from step to step
-    int bytes, last;  // reach of the resource in a step, and in the last one
-    int tail;         // contraction elements in the last step
-    static __device__ __forceinline__ int chunk(int slot) {
-        return slot % T::CH ^ T::f(slot / T::CH);
-    }
-    // Rows m0 .. of the operand (it has mEnd), `steps` steps from k0 to kEnd.
     __device__ __forceinline__ Copies(const void *src, int64_t ld, int64_t m0, int64_t mEnd,
-                                      int64_t k0, int64_t kEnd, int steps) {
-        constexpr int64_t ES = sizeof(IO);
-        const int64_t kLast = k0 + (int64_t)(steps - 1) * T::BK;
-        base = static_cast<const char *>(src) + (TR ? k0 * ld + m0 : m0 * ld + k0) * ES;
-        stride = TR ? T::BK * ld * ES : T::BK * ES;
-        const int64_t end = (TR ? (kEnd - kLast) * ld - m0 : (mEnd - m0) * ld) * ES;
-        last = (int)(end < kOpen ? end : kOpen);
-        bytes = TR ? (int)kOpen : last;
-        tail = (int)(kEnd - kLast);
+                                      int64_t k0, int64_t kEnd, int steps)
+        : plan(ld, m0, mEnd, k0, kEnd, steps), base(static_cast<const char *>(src) + plan.first) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int slot = i * NT + (int)threadIdx.x;
-            off[i] = (uint32_t)(slot / T::CH * ld + chunk(slot) * T::EPC) * (uint32_t)ES;
-        }
+        for (int i = 0; i < N; ++i) off[i] = T::offset(i * NT + (int)threadIdx.x, ld);
     }
     __device__ __forceinline__ void next(char *lds, bool final) {
-        const RsrcW r = make_rsrc_w(base, final ? last : bytes);
+        const RsrcW r = make_rsrc_w(base, final ? plan.last : plan.bytes);
         char *dst = lds + wave_id() * 1024;
-        if (!TR && final && tail < T::BK) {
+        if (!TR && final && plan.tail < T::BK) {
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 lds_dma16(r, (lds_void *)(dst + i * NT * 16),
-                          chunk(i * NT + (int)threadIdx.x) * T::EPC < tail ? off[i] : 0xffffff00u);
+                          plan.masked(i * NT + (int)threadIdx.x) ? 0xffffff00u : off[i]);
         } else {
 #pragma unroll
             for (int i = 0; i < N; ++i) lds_dma16(r, (lds_void *)(dst + i * NT * 16), off[i]);
         }
-        base += stride;
+        base += plan.stride;
     }
 };
 
