@@ -576,15 +576,17 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
             // the first one and spill, is not to see that they are the same
             asm volatile("" : "+v"(sr[k][e]));
             const float u2 = m2[e] * sr[k][e];
-            float at, om;  // at: a[k][e]
+            // at: a[k][e].  The gradient takes a^2 from it: 1 - om, om being
+            // rounded near one, is off by 2e-3 of itself at u = 5.5 and has
+            // nothing left from u = 9
+            float at, om;
             decay(u2, at, om);
             // 1 / beta; a shut gate (om = 0) has beta = om rb = 0 and a finite
             // stand-in for the inverse, which u = 0 then cancels
             const float rb = __builtin_amdgcn_rsqf(fmaxf(om, 1e-30f));
             const float gx = gt * si[k][e], gb = gx * (om * rb), gbx = gb * x;
             q[e] = cut >> k & 1 ? 0.f : a[k][e] * gt;
-            const float p = kLn2 * u2 *
-                            fmaf((1.f - om) * rb, gx * x, -q[e] * v[k][e]);
+            const float p = kLn2 * u2 * fmaf(at * at * rb, gx * x, -q[e] * v[k][e]);
             ox.e[e] = (IO)gb;
             oi.e[e] = (IO)fmaf(-gbx, si[k][e], gbx);
             orr.e[e] = (IO)fmaf(-p, sr[k][e], p);

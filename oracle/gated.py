@@ -25,8 +25,9 @@ def _parts(x, gates, lam, scale, seq):
 
 def scan(x, gates, lam, scale, init=None, seq=None, delta=0.0):
     """dict y (= every state) [b, l, d], final [b, d], states; with `delta`, a
-    relative error of every decay and added value, also err [b, l, d]: the
-    error they bring to y."""
+    relative error of every added value and (times max(1, u), as a relative
+    error of u is u times as large in e^-u) of every decay, also err [b, l, d]:
+    the error they bring to y."""
     x, lam, sp, sr, si, u, a, beta, kept = _parts(x, gates, lam, scale, seq)
     b, l, d = x.shape
     v = beta * si * x
@@ -34,8 +35,9 @@ def scan(x, gates, lam, scale, init=None, seq=None, delta=0.0):
     first = h.copy()
     big, e = np.abs(h), np.zeros((b, d))
     y, err = np.empty((b, l, d)), np.empty((b, l, d))
+    du = delta * np.maximum(1.0, u)
     for t in range(l):
-        e = kept[:, t] * e + delta * (kept[:, t] * big + np.abs(v[:, t]))
+        e = kept[:, t] * e + du[:, t] * kept[:, t] * big + delta * np.abs(v[:, t])
         big = kept[:, t] * big + np.abs(v[:, t])
         h = kept[:, t] * h + v[:, t]
         y[:, t], err[:, t] = h, e
@@ -55,18 +57,19 @@ def grad(x, gates, lam, scale, dy, init=None, seq=None, d_final=None, delta=0.0)
     q = np.zeros((b, d)) if d_final is None else np.asarray(d_final, np.float64).copy()
     big, e = np.abs(q), np.zeros((b, d))
     g, G, E = np.empty((b, l, d)), np.empty((b, l, d)), np.empty((b, l, d))
+    du = delta * np.maximum(1.0, u)
     for t in range(l - 1, -1, -1):
         g[:, t] = dy[:, t] + q
         G[:, t] = np.abs(dy[:, t]) + big
         E[:, t] = e + delta * G[:, t]
         q = kept[:, t] * g[:, t]
         big = kept[:, t] * G[:, t]
-        e = kept[:, t] * E[:, t] + delta * big
+        e = kept[:, t] * E[:, t] + du[:, t] * big
     ratio = np.where(u > 0, u / np.where(beta > 0, beta, 1.0), 0.0)
     w1, w2 = a * a * ratio * si * x, u * kept * before
     p = g * (w1 - w2)
     ep = E * (np.abs(w1) + np.abs(w2)) + np.abs(g) * u * kept * ebefore \
-        + 4 * delta * np.abs(g) * (np.abs(w1) + np.abs(w2))
+        + 4 * du * np.abs(g) * (np.abs(w1) + np.abs(w2))
     gi = g * beta * x * si * (1 - si)
     sig = np.where(lam < -30, 1.0, expit(lam) / sp)
     return dict(

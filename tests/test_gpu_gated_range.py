@@ -1,0 +1,108 @@
+"""The gated recurrence away from decays near one: strong decays (rates up to
+90), rates near the bottom of fp32 and rates without bound, against the fp64
+oracle in oracle/gated.py.
+
+Tolerances, per element, in units of 2^-24.  Gates are cut at +-8, so a
+sigmoid is off by 14 (its exponential's argument 8 x 1.5, the exponential, the
+sum and the reciprocal), the rate u by 24 (softplus and two products 10 more)
+and a decay e^-u by 24 u + 4.  1 - a^2 takes 24 from u (2u / (e^2u - 1) <= 1)
+and at most 40 from the subtraction, which starts at 2u = 1/8; its square root
+half of that, so an added value is off by at most 50.  a^2 u / beta is off by
+48 u + 80.  delta = 2^-18 is 64 units: it covers a decay with max(1, u) delta, an
+added value with delta, and the gradient's terms with 4 max(1, u) delta, which is
+how the oracle takes it through the recurrence and the gradient to first
+order.  An output in bf16 adds half a step, 2^-8 of its value.  1e-30 stands for
+what underflows.
+"""
+import numpy as np
+import pytest
+
+from gpu_util import log, to_f64, torch_mod
+
+pytestmark = pytest.mark.gpu
+
+DELTA = 2.0 ** -18
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+TINY = 1e-30
+
+
+def _case(seed, b, l, d, io, lam, docs=False, init=True):
+    torch = torch_mod()
+    rng = np.random.default_rng(seed)
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+
+    def t(a):
+        return torch.from_numpy(a.astype(np.float32)).to("cuda")
+    seq = None
+    if docs:
+        seq = torch.from_numpy(np.cumsum(rng.random((b, l)) < 0.1, 1).astype(np.int32)).to("cuda")
+    return dict(x=t(rng.normal(size=(b, l, d))).to(dt),
+                gates=t(np.clip(3 * rng.normal(size=(b, l, 2 * d)), -8, 8)).to(dt),
+                lam=t(np.linspace(*lam, d)), init=t(rng.normal(size=(b, d))) if init else None,
+                seq=seq, dy=t(rng.normal(size=(b, l, d))).to(dt), dfin=t(rng.normal(size=(b, d))))
+
+
+def _np(c):
+    return {k: None if v is None else (v.cpu().numpy() if k == "seq" else to_f64(v))
+            for k, v in c.items()}
+
+
+def _close(g, o, tol, what):
+    g = to_f64(g)
+    assert g.shape == o.shape, (what, g.shape, o.shape)
+    assert np.isfinite(g).all(), what
+    err = np.abs(g - o) - tol
+    assert (err <= 0).all(), "%s: %d of %d outside, worst excess %.3g at %s (got %r, want %r)" % (
+        what, int((err > 0).sum()), err.size, err.max(), np.unravel_index(err.argmax(), err.shape),
+        g.flat[err.argmax()], o.flat[err.argmax()])
+
+
+def _compare(c, io, scale, with_final=True):
+    """Forward, gradient (from kept states and without) and decode steps."""
+    import mamba_ssd_chunked_chunk_amd as ssd
+    from oracle import gated as go
+    torch = torch_mod()
+    n, half = _np(c), HALF[io]
+    kw = dict(scale=scale, initial_state=c["init"], seq_idx=c["seq"])
+    y, fin, st = ssd.gated_scan(c["x"], c["gates"], c["lam"], return_final_state=True,
+                                return_states=True, **kw)
+    dfin = c["dfin"] if with_final else None
+    grads = [ssd.gated_scan_bwd(c["x"], c["gates"], c["lam"], c["dy"], d_final=dfin, states=s, **kw)
+             for s in (None, st)]
+    torch.cuda.synchronize()
+    r = go.scan(n["x"], n["gates"], n["lam"], scale, n["init"], n["seq"], delta=DELTA)
+    _close(y, r["y"], r["err"] + half * 1.01 * np.abs(r["y"]) + TINY, "y")
+    _close(fin, r["final"], r["err"][:, -1] + 2.0 ** -24 * np.abs(r["final"]) + TINY, "final")
+    k = go.grad(n["x"], n["gates"], n["lam"], scale, n["dy"], n["init"], n["seq"],
+                n["dfin"] if with_final else None, delta=DELTA)
+    d = c["lam"].shape[0]
+    for g in grads:
+        _close(g["dx"], k["dx"], k["err_dx"] + half * 1.01 * np.abs(k["dx"]) + TINY, "dx")
+        for what, s in (("dr", slice(0, d)), ("di", slice(d, None))):
+            o = k["dgates"][..., s]
+            _close(g["dgates"][..., s], o,
+                   k["err_dgates"][..., s] + half * 1.01 * np.abs(o) + TINY, what)
+        _close(g["dlam"], k["dlam"], k["err_dlam"] + TINY, "dlam")
+        if "d_init" in g:
+            _close(g["d_init"], k["d_init"],
+                   k["err_d_init"] + 2.0 ** -23 * np.abs(k["d_init"]) + TINY, "d_init")
+    if c["seq"] is None:
+        state = torch.zeros_like(c["dfin"]) if c["init"] is None else c["init"].clone()
+        for t in range(min(3, c["x"].shape[1])):
+            ys = ssd.gated_step(state, c["x"][:, t].contiguous(), c["gates"][:, t].contiguous(),
+                                c["lam"], scale=scale)
+            torch.cuda.synchronize()
+            o, e = r["y"][:, t], r["err"][:, t]
+            _close(ys, o, e + half * 1.01 * np.abs(o) + TINY, "step")
+            _close(state, o, e + 2.0 ** -24 * np.abs(o) + TINY, "step's state")
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("docs,init", [(False, True), (False, False), (True, True), (True, False)])
+@pytest.mark.parametrize("shape,scale", [((2, 1, 64), 8.0), ((3, 70, 33), 8.0), ((1, 300, 128), 8.0),
+                                         ((2, 200, 66), 1.5), ((2, 130, 40), 30.0)], ids=str)
+def test_strong_decays(shape, scale, docs, init, io):
+    """Rates from scale softplus(-8) to scale softplus(3)."""
+    log("strong decays", shape, scale, docs, init, io)
+    c = _case(6000 + shape[1], *shape, io=io, lam=(-8.0, 3.0), docs=docs, init=init)
+    _compare(c, io, scale, with_final=shape[1] != 70)
