@@ -581,10 +581,10 @@ __global__ __launch_bounds__(NW * 64, 4) void k_gated_bwd(GArgs g) {
             // nothing left from u = 9
             float at, om;
             decay(u2, at, om);
-            // 1 / beta; a shut gate (om = 0) has beta = om rb = 0 and a finite
-            // stand-in for the inverse, which u = 0 then cancels
-            const float rb = __builtin_amdgcn_rsqf(fmaxf(om, 1e-30f));
-            const float gx = gt * si[k][e], gb = gx * (om * rb), gbx = gb * x;
+            // 1 / beta; a shut gate (om = 0) has a finite stand-in for it, which
+            // u = 0 then cancels
+            const float rb = __builtin_amdgcn_rsqf(fmaxf(om, 0x1p-126f));
+            const float gx = gt * si[k][e], gb = gx * __builtin_amdgcn_sqrtf(om), gbx = gb * x;
             q[e] = cut >> k & 1 ? 0.f : a[k][e] * gt;
             const float p = kLn2 * u2 * fmaf(at * at * rb, gx * x, -q[e] * v[k][e]);
             ox.e[e] = (IO)gb;

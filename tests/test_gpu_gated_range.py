@@ -57,7 +57,7 @@ def _close(g, o, tol, what):
         g.flat[err.argmax()], o.flat[err.argmax()])
 
 
-def _compare(c, io, scale, with_final=True):
+def _compare(c, io, scale, with_final=True, tiny=TINY):
     """Forward, gradient (from kept states and without) and decode steps."""
     import mamba_ssd_chunked_chunk_amd as ssd
     from oracle import gated as go
@@ -71,21 +71,21 @@ def _compare(c, io, scale, with_final=True):
              for s in (None, st)]
     torch.cuda.synchronize()
     r = go.scan(n["x"], n["gates"], n["lam"], scale, n["init"], n["seq"], delta=DELTA)
-    _close(y, r["y"], r["err"] + half * 1.01 * np.abs(r["y"]) + TINY, "y")
-    _close(fin, r["final"], r["err"][:, -1] + 2.0 ** -24 * np.abs(r["final"]) + TINY, "final")
+    _close(y, r["y"], r["err"] + half * 1.01 * np.abs(r["y"]) + tiny, "y")
+    _close(fin, r["final"], r["err"][:, -1] + 2.0 ** -24 * np.abs(r["final"]) + tiny, "final")
     k = go.grad(n["x"], n["gates"], n["lam"], scale, n["dy"], n["init"], n["seq"],
                 n["dfin"] if with_final else None, delta=DELTA)
     d = c["lam"].shape[0]
     for g in grads:
-        _close(g["dx"], k["dx"], k["err_dx"] + half * 1.01 * np.abs(k["dx"]) + TINY, "dx")
+        _close(g["dx"], k["dx"], k["err_dx"] + half * 1.01 * np.abs(k["dx"]) + tiny, "dx")
         for what, s in (("dr", slice(0, d)), ("di", slice(d, None))):
             o = k["dgates"][..., s]
             _close(g["dgates"][..., s], o,
-                   k["err_dgates"][..., s] + half * 1.01 * np.abs(o) + TINY, what)
-        _close(g["dlam"], k["dlam"], k["err_dlam"] + TINY, "dlam")
+                   k["err_dgates"][..., s] + half * 1.01 * np.abs(o) + tiny, what)
+        _close(g["dlam"], k["dlam"], k["err_dlam"] + tiny, "dlam")
         if "d_init" in g:
             _close(g["d_init"], k["d_init"],
-                   k["err_d_init"] + 2.0 ** -23 * np.abs(k["d_init"]) + TINY, "d_init")
+                   k["err_d_init"] + 2.0 ** -23 * np.abs(k["d_init"]) + tiny, "d_init")
     if c["seq"] is None:
         state = torch.zeros_like(c["dfin"]) if c["init"] is None else c["init"].clone()
         for t in range(min(3, c["x"].shape[1])):
@@ -93,8 +93,8 @@ def _compare(c, io, scale, with_final=True):
                                 c["lam"], scale=scale)
             torch.cuda.synchronize()
             o, e = r["y"][:, t], r["err"][:, t]
-            _close(ys, o, e + half * 1.01 * np.abs(o) + TINY, "step")
-            _close(state, o, e + 2.0 ** -24 * np.abs(o) + TINY, "step's state")
+            _close(ys, o, e + half * 1.01 * np.abs(o) + tiny, "step")
+            _close(state, o, e + 2.0 ** -24 * np.abs(o) + tiny, "step's state")
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
@@ -106,3 +106,15 @@ def test_strong_decays(shape, scale, docs, init, io):
     log("strong decays", shape, scale, docs, init, io)
     c = _case(6000 + shape[1], *shape, io=io, lam=(-8.0, 3.0), docs=docs, init=init)
     _compare(c, io, scale, with_final=shape[1] != 70)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("init", [False, True])
+def test_rates_near_the_bottom(init, io):
+    """Rates from 8 e^-82 to 8 e^-60: 1 - a^2 down to 1e-36, its square root, which
+    the gradient divides by, down to 1e-18; nothing but fp32's smallest normal
+    value is taken for zero.  Gates from -2, so that every product stays normal."""
+    log("rates near the bottom", init, io)
+    c = _case(6100, 2, 70, 46, io, lam=(-82.0, -60.0), init=init)
+    c["gates"] = c["gates"].clamp(min=-2)
+    _compare(c, io, 8.0, tiny=2.0 ** -126)
