@@ -53,6 +53,15 @@ __device__ __forceinline__ float softplus_f(float v) {
     return fmaxf(v, 0.f) + 2.f * fmaf(z * q, s, z);
 }
 
+// scale softplus(lam) in binary orders.  A rate without bound (an infinite lam,
+// or an overflow) is the largest finite value: its decay is zero all the same,
+// and its products with a zero are zero and not NaN (a NaN stays one).
+__device__ __forceinline__ float rate_of(float lam, float scale) {
+    constexpr float kMost = 0x1.fffffep127f;
+    const float s = softplus_f(lam), m = scale * (s > kMost ? kMost : s) * kLog2e;
+    return m > kMost ? kMost : m;
+}
+
 // a = e^-u and 1 - a^2 = -expm1(-2u) for u = u2 ln 2 >= 0.  Where the
 // subtraction would cancel (2u < 1/8) the difference is u2 times the cubic of
 // least largest relative error (1.6e-8 there, before rounding); above, the
@@ -287,7 +296,7 @@ template <typename IO, int V, int SEG>
 __device__ __forceinline__ void rates(const GArgs &g, const Tile<IO, V, SEG> &w, float (&m2)[V]) {
 #pragma unroll
     for (int e = 0; e < V; ++e)
-        m2[e] = g.ch.rate ? g.ch.rate[w.c + e] : g.scale * softplus_f(g.lam[w.c + e]) * kLog2e;
+        m2[e] = g.ch.rate ? g.ch.rate[w.c + e] : rate_of(g.lam[w.c + e], g.scale);
 }
 
 // This workgroup's tile of its column, in the order of the chain.
@@ -400,7 +409,7 @@ __global__ __launch_bounds__(256) void k_gated_setup(u32x4 *p, int64_t n, u32x4 
     const u32x4 zero = {0, 0, 0, 0};
     for (int64_t i = k; i < n; i += all) p[i] = zero;
     for (int64_t i = k; i < n2; i += all) p2[i] = zero;
-    for (int64_t i = k; i < d; i += all) rate[i] = scale * softplus_f(lam[i]) * kLog2e;
+    for (int64_t i = k; i < d; i += all) rate[i] = rate_of(lam[i], scale);
 }
 
 // ------------------------------------------------------------- forward ----
@@ -671,7 +680,7 @@ __global__ __launch_bounds__(256) void k_gated_step(float *state, const IO *x, c
 #pragma unroll
     for (int e = 0; e < V; ++e) {
         float a, om;
-        decay(scale * softplus_f(lm.e[e]) * kLog2e * sigmoid_f(to_f32(r.e[e])), a, om);
+        decay(rate_of(lm.e[e], scale) * sigmoid_f(to_f32(r.e[e])), a, om);
         h.e[e] = fmaf(a, h.e[e], __builtin_amdgcn_sqrtf(om) * sigmoid_f(to_f32(i.e[e])) *
                                      to_f32(xv.e[e]));
         o.e[e] = (IO)h.e[e];

@@ -118,3 +118,56 @@ def test_rates_near_the_bottom(init, io):
     c = _case(6100, 2, 70, 46, io, lam=(-82.0, -60.0), init=init)
     c["gates"] = c["gates"].clamp(min=-2)
     _compare(c, io, 8.0, tiny=2.0 ** -126)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("l", [1, 40, 300])
+@pytest.mark.parametrize("docs", [False, True])
+def test_gradient_of_rates_without_bound(docs, l, io):
+    """lam = inf, lam so far out that scale softplus(lam) overflows, and a rate that
+    overflows only in binary orders: the decay is zero and stays zero, so the
+    decay gate, lam and the initial state have zero gradients and x and the
+    other gate those of y = sigmoid(i) x; a NaN stays in its channel.  With
+    scale = 0 nothing decays, whatever lam."""
+    import mamba_ssd_chunked_chunk_amd as ssd
+    torch = torch_mod()
+    log("rates without bound", docs, l, io)
+    for scale, ends in ((8.0, [np.inf, 1e38, 3e37]), (1e30, [np.inf, 1e9, 5.0])):
+        c = _case(6200 + l, 2, l, 6, io, lam=(-3.0, -2.0), docs=docs)
+        lam = c["lam"]
+        lam[:3] = torch.tensor(ends)
+        lam[3] = float("nan")
+        c["lam"] = lam
+        kw = dict(scale=scale, initial_state=c["init"], seq_idx=c["seq"])
+        y, st = ssd.gated_scan(c["x"], c["gates"], lam, return_states=True, **kw)
+        grads = [ssd.gated_scan_bwd(c["x"], c["gates"], lam, c["dy"], d_final=c["dfin"], states=s,
+                                    **kw) for s in (st, None)]
+        torch.cuda.synchronize()
+        n = _np(c)
+        x, i, dy = n["x"][..., :3], n["gates"][..., 6:9], n["dy"][..., :3].copy()
+        s = 1 / (1 + np.exp(-i))
+        # a sigmoid off by 14 of 2^-24, one minus it by as much absolutely
+        _close(y[..., :3], s * x, (2.0 ** -19 + HALF[io]) * np.abs(s * x) + TINY, "y")
+        dy[:, -1] += n["dfin"][:, :3]
+        for g in grads:
+            assert not bool(g["dgates"][..., :3].any()), "dr"
+            assert not bool(g["dlam"][:3].any()) and not bool(g["d_init"][:, :3].any())
+            o = dy * s
+            _close(g["dx"][..., :3], o, (2.0 ** -19 + HALF[io]) * np.abs(o) + TINY, "dx")
+            o = dy * s * (1 - s) * x
+            _close(g["dgates"][..., 6:9], o, 2.0 ** -19 * np.abs(dy * s * x) + HALF[io] * np.abs(o)
+                   + TINY, "di")
+            assert bool(torch.isnan(g["dx"][..., 3]).all()) and bool(torch.isnan(g["dlam"][3]))
+            if scale == 8.0:
+                for v in (g["dx"], g["dgates"][..., :6], g["dgates"][..., 6:], g["d_init"], g["dlam"]):
+                    assert bool(torch.isfinite(v[..., 4:]).all())
+    c = _case(6300, 2, l, 4, io, lam=(-3.0, 0.0))
+    c["lam"] = torch.tensor([-3.0, 0.0, 1e38, np.inf], device="cuda")
+    kw = dict(scale=0.0, initial_state=c["init"])
+    y, fin = ssd.gated_scan(c["x"], c["gates"], c["lam"], return_final_state=True, **kw)
+    g = ssd.gated_scan_bwd(c["x"], c["gates"], c["lam"], c["dy"], **kw)
+    state = c["init"].clone()
+    ssd.gated_step(state, c["x"][:, 0].contiguous(), c["gates"][:, 0].contiguous(), c["lam"], scale=0.0)
+    torch.cuda.synchronize()
+    assert torch.equal(fin, c["init"]) and torch.equal(state, c["init"])
+    assert not bool(g["dx"].any()) and not bool(g["dgates"].any())
