@@ -1,5 +1,5 @@
-"""The linear layer's larger tiles, and its few-row kernel on rows laid out
-again, against fp64.
+"""The linear layer's larger tiles, its few-row kernel on rows laid out again,
+and the tails of GELU, against fp64.
 
 The sizes are ones for which the choice of tile and parts takes, bf16 and fp32:
 128 x 192 and 128 x 128 forward, and in the gradient both with and without
@@ -77,3 +77,28 @@ def test_large_tiles_gradient(shape, io):
         _close(g[key], o, 1.01 * (by_e + (terms + 4) * 2.0 ** -24 * mag + HALF[io] * np.abs(o)), key)
     _close(g["dbias"], r["dbias"],
            (ev.sum(0) + (m + 4) * 2.0 ** -24 * ea.sum(0)) * 1.01 + 1e-30, "dbias")
+
+
+def test_gelu_tail():
+    """GELU and its gradient in fp32 from -3 to -8, relative to their terms.
+    Phi's polynomial is off by at most 1.12e-5 of Phi there; the exponential's
+    argument, up to 46 binary orders, is rounded three times: 46 ln 2 x 2.5 x
+    2^-24 = 4.8e-6; everything else a few 2^-24.  Below 2^-15 = 3.05e-5."""
+    import mamba_ssd_chunked_chunk_amd as ssd
+    from scipy.special import ndtr
+    torch = torch_mod()
+    v = np.linspace(-8, -3, 20001).astype(np.float32)
+    x = torch.zeros((v.size, 4), device="cuda")
+    x[:, 0] = torch.from_numpy(v).cuda()
+    w = torch.zeros((4, 4), device="cuda")
+    w[:, 0] = 1
+    y, pre = ssd.linear(x, w, activation="gelu", return_pre=True)
+    dy = torch.zeros_like(y)
+    dy[:, 0] = 1
+    g = ssd.linear_bwd(dy, x, w, pre=pre, activation="gelu")
+    torch.cuda.synchronize()
+    z = v.astype(np.float64)
+    phi, dens = ndtr(z), np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
+    assert np.array_equal(to_f64(pre)[:, 0], z)
+    _close(y[:, 0], z * phi, 2.0 ** -15 * np.abs(z * phi), "gelu")
+    _close(g["dx"][:, 0], phi + z * dens, 2.0 ** -15 * (phi + np.abs(z) * dens), "its gradient")
