@@ -457,13 +457,15 @@ size_t ssd_chunk_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t
  *
  * Alignment: each tensor to the largest power of two up to 16 bytes that
  * divides one of its rows (so that any run of a tensor's rows qualifies),
- * bias to 4.  Any row count (one decoded token upwards) and any widths up to
- * 2^20; operands whose rows are not multiples of 16 bytes are first laid out
- * again in the workspace.  Matrix-core products with fp32
- * accumulation in a fixed order (bf16 io: bf16 operands exactly as given;
- * fp32 io: fp32 operands); bias, activation and residual in fp32; one
- * rounding to nearest even at each output.  out and pre must not overlap
- * anything else (out may be the residual).
+ * bias to 4.  Any row count below 2^31 (one decoded token upwards) and any
+ * widths up to 2^20, with x, weight and out below 2^34 values each when their
+ * rows are rounded up to 64 values; beyond that SSD_ERR_UNSUPPORTED, and 0 from
+ * the queries.  Operands whose rows are not multiples of 16 bytes are first
+ * laid out again in the workspace (but for a few rows of x).  Matrix-core
+ * products with fp32 accumulation in a fixed order (bf16 io: bf16 operands
+ * exactly as given; fp32 io: fp32 operands); bias, activation and residual in
+ * fp32; one rounding to nearest even at each output.  out and pre must not
+ * overlap anything else (out may be the residual).
  */
 enum ssd_activation {
     SSD_ACT_NONE = 0, SSD_ACT_SILU = 1, SSD_ACT_GELU = 2, SSD_ACT_SIGMOID = 3
@@ -493,7 +495,7 @@ size_t ssd_linear_workspace_bytes(int64_t rows, int64_t in_dim, int64_t out_dim,
  *   dbias       [out_dim] fp32 or NULL
  *   workspace   ssd_linear_bwd_workspace_bytes(...) bytes, 256-byte aligned
  *
- * Alignment as for ssd_linear.  bf16 io: with an activation, e is rounded
+ * Alignment and sizes as for ssd_linear.  bf16 io: with an activation, e is rounded
  * to bf16 as the products' operand (their accumulation is fp32), except for
  * a few rows against a large weight, whose e stays fp32; dbias sums the fp32
  * values of e.  rows == 0 writes zeros to dweight and dbias.

@@ -882,14 +882,14 @@ Choice choose_bwd(int64_t m, int64_t n, int64_t k, int io) {
     return choose(p, 2, io);
 }
 
-// Widths up to 2^20 elements and tensors up to 2^34: a tile's byte offsets stay
-// below 2^30, and pieces of four elements (of eight in padded rows), threads and
-// workgroups are counted in 32 bits.
+// Widths up to 2^20 elements, and tensors below 2^34 with their rows rounded up to
+// 64: a tile's byte offsets stay below 2^30, pieces of four elements are counted
+// in 32 bits, and so are the threads that lay two operands out again in one
+// launch, a piece of eight each (the launch takes no more than 2^32).
 bool linear_sizes(int64_t m, int64_t n, int64_t k) {
-    const int64_t w = (int64_t)1 << 20, big = (int64_t)1 << 32;
+    const int64_t w = (int64_t)1 << 20, most = (int64_t)1 << 34;
     if (n > w || k > w || m >= ((int64_t)1 << 31)) return false;
-    return m * cdiv(n, 4) < big && m * cdiv(k, 4) < big && n * cdiv(k, 4) < big &&
-           m * (pad(n) / 8) < big && m * (pad(k) / 8) < big && n * (pad(k) / 8) < big;
+    return m * pad(n) < most && m * pad(k) < most && n * pad(k) < most;
 }
 
 // Whether a forward call lays its operands out again first.  k_few reads odd
