@@ -66,8 +66,9 @@ enum ssd_status {
     SSD_ERR_NULL = -1,        /* a required pointer is NULL */
     SSD_ERR_SHAPE = -2,       /* a size < 0 (or <= 0 where a size of 0 is meaningless),
                                  heads % groups != 0, chunk <= 0 */
-    SSD_ERR_UNSUPPORTED = -3, /* head_dim / state_dim outside the compiled set, or
-                                 an io dtype other than SSD_F32 / SSD_BF16 */
+    SSD_ERR_UNSUPPORTED = -3, /* head_dim / state_dim outside the compiled set, an
+                                 io dtype other than SSD_F32 / SSD_BF16, or sizes
+                                 beyond the limits that a call names */
     SSD_ERR_WORKSPACE = -4,   /* workspace NULL or smaller than the query returns */
     SSD_ERR_ALIGN = -5,       /* a pointer is not aligned as documented */
     SSD_ERR_HIP = -6,         /* the HIP runtime reported an error at launch */
@@ -534,9 +535,13 @@ size_t ssd_linear_bwd_workspace_bytes(int64_t rows, int64_t in_dim, int64_t out_
  *                seqlen) - 1, what ssd_gated_scan_bwd can start from
  *   workspace    ssd_gated_scan_workspace_bytes(...) bytes, 256-byte aligned
  *
- * Tensors aligned to their element.  Any dim; 4 (or 2) channels move at once
- * where dim is a multiple and the tensors are aligned to as many elements.  fp32 arithmetic and states, y rounded to nearest even;
- * 1 - a^2 is taken without cancellation as a goes to 1.  Deterministic.
+ * Tensors aligned to their element.  dim up to 2^24, seqlen up to 2^28, batch up
+ * to 65535 and batch ceil(dim / 64) ceil(seqlen / 64) below 2^23; beyond that
+ * SSD_ERR_UNSUPPORTED, and 0 from the queries.  Two channels move at once where
+ * dim is even and x, gates, y, final_state and states are aligned to two
+ * elements, one otherwise, with the same results.  fp32 arithmetic and states,
+ * y rounded to nearest even; 1 - a^2 is taken without cancellation as a goes to
+ * 1.  A rate u without bound (lam infinite) has a = 0.  Deterministic.
  * seqlen == 0 gives final_state = init_state or zeros.
  */
 #define SSD_GATED_CHUNK 64
@@ -560,7 +565,8 @@ size_t ssd_gated_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim
  *   dlam = sum p sigmoid(lam) / softplus(lam),  d_init = a_0 g_0
  *
  * with s_r, s_i the gates' sigmoids and beta = sqrt(1 - a^2); u / beta goes
- * to zero with u, so a gate that closes fully has a zero gradient.
+ * to zero with u, so a gate that closes fully has a zero gradient, as has one
+ * whose rate is without bound (u a and u a^2 go to zero).
  *
  *   states    the forward's states output for the same inputs, or NULL (they
  *             are then computed again)
@@ -569,7 +575,8 @@ size_t ssd_gated_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t dim
  *             io dtype;  dlam [dim] fp32;  d_init [batch, dim] fp32 or NULL
  *   workspace ssd_gated_scan_bwd_workspace_bytes(...) bytes, 256-byte aligned
  *
- * batch and seqlen >= 1; tensors aligned to their element.
+ * batch and seqlen >= 1, limits as for ssd_gated_scan; tensors aligned to their
+ * element (two channels at once as there, with dy, dx, dgates and d_init).
  */
 int32_t ssd_gated_scan_bwd(const void *x, const void *gates, const float *lam, float scale,
                            const float *init_state, const int32_t *seq_idx, const float *states,
@@ -584,7 +591,10 @@ size_t ssd_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t
 /*
  * ssd_gated_step -- one token of ssd_gated_scan: state [batch, dim] fp32 read
  * and overwritten, x [batch, dim], gates [batch, 2 dim], y [batch, dim] io
- * dtype; tensors aligned to their element.
+ * dtype; tensors aligned to their element.  Four or two channels move at once
+ * where dim is a multiple and every tensor is aligned to as many elements.  dim
+ * up to 2^24, batch up to 2^31, and batch * dim up to 2^32 - 256 times the
+ * channels that move at once, else SSD_ERR_UNSUPPORTED.
  */
 int32_t ssd_gated_step(float *state, const void *x, const void *gates, const float *lam,
                        float scale, void *y, int64_t batch, int64_t dim, int32_t io_dtype,
