@@ -408,7 +408,7 @@ template <typename IO> __global__ __launch_bounds__(256) void k_gemm_sum(GemmArg
 // widths are read where they are); the waves' sums meet in LDS and are added
 // in order.  One row, 2560 -> 10576 bf16: 11.9 us, 4.5 TB/s of weight (4 waves;
 // 8 leave 21 of the 661 workgroups to a second round, 15.0 us, 16 waves 22 us).
-// 32 rows: 22 us.
+// 32 rows of 768 -> 3352: 4.8 us (see few_fwd for what the tiles take).
 constexpr int kFewWaves = 4;
 constexpr int kFewUnroll = 4;  // weight pieces in flight a wave
 
@@ -797,8 +797,8 @@ int64_t esz(int io) { return io == SSD_BF16 ? 2 : 4; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int64_t kCus = 256;       // compute units of the part this is written for
-constexpr int64_t kFewRows = 32;    // rows up to which k_few runs
-constexpr int64_t kFewOdd = 4;      // and reads rows of odd widths where they are
+constexpr int64_t kFewRows = 32;    // rows that k_few can take
+constexpr int64_t kFewOdd = 4;      // rows up to which it reads odd widths where they are
 
 enum Tile { kT64, kT128, kT192, kTiles };
 struct Shape {
@@ -892,17 +892,36 @@ bool linear_sizes(int64_t m, int64_t n, int64_t k) {
     return m * pad(n) < most && m * pad(k) < most && n * pad(k) < most;
 }
 
+// Whether k_few takes a forward product of up to kFewRows rows, rather than the
+// tiles.  A workgroup of it walks a whole contraction for 16 columns, with all rows
+// of x for each: long contractions, and weights of more columns than one round of
+// workgroups (256 x 16), take in proportion to their length and rows, more than
+// 16 rows twice the matrix work; the tiles split a long contraction and read x
+// once.  fp32 tiles are slower, and odd rows have to be laid out for them.  Of 732
+// timed products of 1 to 32 rows this rule takes 0.5% (fp32 0.6%) more than the
+// better of both on average, 28% at most, against 20% and three times with a
+// rule on the rows alone.  bf16, k_few against tiles: 32 rows, 2560 -> 10576 23.1
+// and 14.4 us, 16 rows 16.0 and 14.6, 5 rows 12.7 and 14.2; 32 rows, 768 -> 1536 5.0
+// and 7.7; one row, 16384 -> 256 19.1 and 12.7.
+bool few_fwd(int64_t m, int64_t n, int64_t k, int io) {
+    if (m > kFewRows) return false;
+    if (io == SSD_BF16) return k * (n > 4096 ? n : 4096) * (8 + (m > 16 ? 40 : m)) <= 600000000;
+    if (odd_rows(k, io)) return true;
+    return m <= 16 ? k <= 4096 || n > 2048 : k < 4096 && n * k <= ((int64_t)1 << 24);
+}
+
 // Whether a forward call lays its operands out again first.  k_few reads odd
 // rows where they are; bf16 accesses off 4 bytes are slow enough that more than
-// kFewOdd rows of x against a large weight repay the copies (10576 x 2561, 16
-// rows: 48 against 34 us; 1000 x 333: 4.4 against 7.0).
+// kFewOdd rows of x against a large weight repay the copies (2561 -> 10576, 16
+// rows: 48 against 34 us; 333 -> 1000: 4.4 against 7.0).
 bool pads(int64_t m, int64_t n, int64_t k, int io) {
-    return odd_rows(k, io) && (m > kFewRows || (io == SSD_BF16 && m > kFewOdd && n * k > (1 << 21)));
+    return odd_rows(k, io) &&
+           (!few_fwd(m, n, k, io) || (io == SSD_BF16 && m > kFewOdd && n * k > (1 << 21)));
 }
 
 size_t fwd_bytes(int64_t m, int64_t n, int64_t k, int io) {
     const size_t copies = pads(m, n, k, io) ? up(m * pad(k) * esz(io)) + up(n * pad(k) * esz(io)) : 0;
-    if (m <= kFewRows) return copies;
+    if (few_fwd(m, n, k, io)) return copies;
     return copies + parts_bytes(plan(nullptr, 0, nullptr, 0, m, n, k, choose_fwd(m, n, k, io), 0,
                                      Epi{}, nullptr, io));
 }
@@ -922,7 +941,7 @@ int32_t run_linear(const void *x, const void *w, const Epi &ep, int64_t m, int64
         x = p.px, w = p.pw;
         ws = static_cast<char *>(p.pw) + up(n * ld * sizeof(IO));
     }
-    if (m <= kFewRows) {
+    if (few_fwd(m, n, k, io)) {
         GemmArgs g{};
         g.A = x, g.B = w, g.lda = g.ldb = ld, g.m = m, g.n = n, g.k = k, g.ep = ep;
         const dim3 grid((unsigned)cdiv(n, 16)), block(kFewWaves * 64);

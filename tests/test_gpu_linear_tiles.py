@@ -1,4 +1,4 @@
-"""The linear layer's larger tiles, its few-row kernel on rows laid out again,
+"""The linear layer's larger tiles, its few rows on both sides of the choice,
 and the tails of GELU, against fp64.
 
 The sizes are ones for which the choice of tile and parts takes, bf16 and fp32:
@@ -102,3 +102,16 @@ def test_gelu_tail():
     assert np.array_equal(to_f64(pre)[:, 0], z)
     _close(y[:, 0], z * phi, 2.0 ** -15 * np.abs(z * phi), "gelu")
     _close(g["dx"][:, 0], phi + z * dens, 2.0 ** -15 * (phi + np.abs(z) * dens), "its gradient")
+
+
+# few rows by the tiles: long contractions and large weights, rows of odd width
+# among them, and one size on each side of the choice; bf16, then fp32 sizes
+@pytest.mark.parametrize("shape,io", [
+    ((1, 16384, 256), "bf16"), ((3, 16385, 250), "bf16"), ((16, 8192, 520), "bf16"),
+    ((17, 2560, 4900), "bf16"), ((17, 2560, 4800), "bf16"), ((32, 2561, 10576), "bf16"),
+    ((31, 768, 16400), "bf16"), ((2, 20000, 1), "bf16"),
+    ((1, 4100, 2048), "f32"), ((1, 4096, 2048), "f32"), ((5, 16384, 130), "f32"),
+    ((17, 4096, 36), "f32"), ((20, 4092, 4100), "f32"), ((24, 2560, 7001), "f32"),
+    ((19, 4101, 300), "f32")], ids=str)
+def test_few_rows_by_the_tiles(shape, io):
+    _linear(*shape, io=io, act="gelu", bias=True, residual=True, pre=True, seed=3800)
