@@ -232,11 +232,12 @@ constexpr uint32_t kBand = 8;
 // compute unit, not a deeper pipeline: at 16384 x 5120 -> 2560 (bf16) a
 // 256 x 256 tile (one workgroup a unit, 8 waves) took 470 us, 256 x 320 440,
 // 128 x 128 422 with 4 waves and 398 with 8, and 128 x 192 with 8 waves, whose
-// two workgroups fill the 160 KB of LDS, 376 (1140 TFLOP/s; 362 in 4 full
-// rounds of a later box).  Three or four steps in flight changed nothing, nor
-// did reading operand pieces ahead.  L2 gives 17 TB/s (a 128-byte request each
-// 2 clocks and channel), 1320 TFLOP/s for this tile's 77 operations a byte:
-// that and the last, partly filled round are what it is bound by.
+// two workgroups fill the 160 KB of LDS, 376 (as first measured, side by side;
+// as it stands 385, 1117 TFLOP/s, and 397 to 426 with the residual, by the box).
+// Three or four steps in flight changed nothing, nor did reading operand pieces
+// ahead.  L2 gives 17 TB/s (a 128-byte request each 2 clocks and channel), 1320
+// TFLOP/s for this tile's 77 operations a byte: that and the last, partly filled
+// round are what it is bound by.
 template <typename IO, bool TA, bool TB, int BM, int BN, int WM, int WN>
 __device__ __forceinline__ void gemm_tile(const GemmArgs &g, uint32_t item, char *lds) {
     constexpr int NT = WM * WN * 64;
@@ -495,6 +496,14 @@ __global__ __launch_bounds__(kFewWaves * 64) void k_few(GemmArgs g) {
 // accesses there too): e = dy act'(pre), with its fp32 column sums over runs
 // of `run` rows, and x and W laid out again with padded rows.  Bound by memory:
 // 8192 x 5120 bf16 with GELU in 52-56 us, 4.6 TB/s.
+//
+// With bf16 io e is rounded to bf16, as dy and x are: it is an operand of both
+// products, whose other operand is bf16, and the matrix cores take both in one
+// type.  In fp32 the two products would run at a ninth of the rate and e would
+// be twice the bytes; as a sum of two bf16 values they would be twice the work.  So dx and
+// dweight carry two roundings instead of one, independent of each other: against
+// fp64 they are off by 0.00235 of their norm (2^-8.7), and by 0.00166 where e is kept
+// in fp32.  dbias takes e before the rounding.
 struct PrepArgs {
     const void *dy, *pre, *x, *w;
     void *e, *px, *pw;        // NULL: not wanted
