@@ -541,17 +541,22 @@ def _scratch(workspace, nbytes, dev):
     return workspace
 
 
+def _io_name(io) -> int:
+    try:
+        return {"f32": _lib.SSD_F32, "bf16": _lib.SSD_BF16}[io]
+    except KeyError:
+        raise ValueError("io must be f32 or bf16, got %r" % (io,)) from None
+
+
 def linear_workspace_bytes(rows, in_dim, out_dim, io="bf16") -> int:
     """Workspace bytes of one linear call (ssd_linear_workspace_bytes)."""
-    code = _lib.SSD_BF16 if io == "bf16" else _lib.SSD_F32
-    return int(load().ssd_linear_workspace_bytes(rows, in_dim, out_dim, code))
+    return int(load().ssd_linear_workspace_bytes(rows, in_dim, out_dim, _io_name(io)))
 
 
 def linear_bwd_workspace_bytes(rows, in_dim, out_dim, activation="none", io="bf16") -> int:
     """Workspace bytes of one linear_bwd call (ssd_linear_bwd_workspace_bytes)."""
-    code = _lib.SSD_BF16 if io == "bf16" else _lib.SSD_F32
     return int(load().ssd_linear_bwd_workspace_bytes(rows, in_dim, out_dim,
-                                                     _activation(activation), code))
+                                                     _activation(activation), _io_name(io)))
 
 
 def linear(x, weight, bias=None, activation: str = "none", residual=None,

@@ -79,3 +79,20 @@ def test_gated_step_limits(lib, L, b, d, ok):
         else:  # the count of threads is checked behind the pointers; one channel a lane
             off = FAKE + (4 if io == 0 else 2)
             assert lib.ssd_gated_step(FAKE + 4, off, off, FAKE + 4, 8.0, off, b, d, io, None) == want
+
+
+def test_workspace_queries_know_their_types(lib):
+    """The binding's queries take the names "f32" and "bf16" as state_chunks does,
+    and no other for one of them."""
+    import mamba_ssd_chunked_chunk_amd as ssd
+    assert ssd.linear_workspace_bytes(300, 65, 40, io="bf16") == \
+        lib.ssd_linear_workspace_bytes(300, 65, 40, 1)
+    assert ssd.linear_workspace_bytes(300, 65, 40, io="f32") == \
+        lib.ssd_linear_workspace_bytes(300, 65, 40, 0)
+    assert ssd.linear_bwd_workspace_bytes(300, 65, 40, "silu", io="f32") == \
+        lib.ssd_linear_bwd_workspace_bytes(300, 65, 40, 1, 0)
+    for name in ("bfloat16", "f16", None):
+        with pytest.raises(ValueError, match="io"):
+            ssd.linear_workspace_bytes(300, 65, 40, io=name)
+        with pytest.raises(ValueError, match="io"):
+            ssd.linear_bwd_workspace_bytes(300, 65, 40, io=name)
