@@ -11,7 +11,9 @@
  * (ssd_chunk_scan_bwd), the products around a mixer (ssd_linear and its
  * gradient ssd_linear_bwd), a gated linear recurrence per channel
  * (ssd_gated_scan, its gradient ssd_gated_scan_bwd, and its decode step
- * ssd_gated_step), and the pieces of a sequence split into segments
+ * ssd_gated_step), the gated delta rule (ssd_delta_scan, its gradient
+ * ssd_delta_scan_bwd, and its decode step ssd_delta_step), the layer norm in
+ * front of a mixer (ssd_layer_norm, ssd_layer_norm_bwd), and the pieces of a sequence split into segments
  * (ssd_segment_log_decay, ssd_combine_segments); plus workspace queries
  * and status strings.
  *
@@ -56,7 +58,7 @@
 extern "C" {
 #endif
 
-#define SSD_ABI_VERSION 7
+#define SSD_ABI_VERSION 8
 
 /* io dtype of x, dt, B, C and y */
 enum ssd_dtype { SSD_F32 = 0, SSD_BF16 = 1 };
@@ -599,6 +601,178 @@ size_t ssd_gated_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t
 int32_t ssd_gated_step(float *state, const void *x, const void *gates, const float *lam,
                        float scale, void *y, int64_t batch, int64_t dim, int32_t io_dtype,
                        void *hip_stream);
+
+/*
+ * ssd_layer_norm -- layer norm of every row of x [rows, dim], with the residual
+ * in front of it:
+ *
+ *   s = x + residual (rounded to the io dtype; x without a residual)
+ *   mean = sum s / dim,  rstd = 1 / sqrt(sum (s - mean)^2 / dim + eps)
+ *   y = (s - mean) rstd weight + bias
+ *
+ *   x, residual  [rows, dim] io dtype; residual may be NULL
+ *   weight, bias [dim] fp32 or NULL (ones, zeros)
+ *   eps          >= 0
+ *   y            [rows, dim] io dtype, written
+ *   sum          [rows, dim] io dtype, s written, or NULL; NULL without a residual
+ *   stats        [2, rows] fp32 (mean, then rstd), written, or NULL
+ *
+ * y may be x or residual, and sum may be x or residual, y and sum different
+ * buffers.  Tensors aligned to their element; 16 bytes move at once where dim
+ * and every tensor allow it.  dim up to 2^24, rows * dim up to 2^40, else
+ * SSD_ERR_UNSUPPORTED.  The mean and the squares about it are fp32 sums, each
+ * output is rounded once.  Deterministic.  rows == 0 is valid.
+ */
+int32_t ssd_layer_norm(const void *x, const void *residual, const float *weight,
+                       const float *bias, float eps, void *y, void *sum, float *stats,
+                       int64_t rows, int64_t dim, int32_t io_dtype, void *hip_stream);
+
+/*
+ * ssd_layer_norm_bwd -- gradients of ssd_layer_norm's y (cotangent dy),
+ * deterministic: with hat = (s - mean) rstd and g = dy weight,
+ *
+ *   dx = rstd (g - mean(g) - hat mean(g hat)) + d_sum
+ *   dweight = sum over rows of dy hat,  dbias = sum over rows of dy
+ *
+ *   dy, x      [rows, dim] io dtype; x is what was normalised (s)
+ *   stats      [2, rows] fp32, the forward's
+ *   weight     [dim] fp32 or NULL, the forward's
+ *   d_sum      [rows, dim] io dtype or NULL: the gradient that reaches s from
+ *              elsewhere (the residual stream)
+ *   dx         [rows, dim] io dtype or NULL; also the residual's gradient.  May
+ *              be dy or d_sum
+ *   dweight, dbias  [dim] fp32 or NULL
+ *   workspace  ssd_layer_norm_bwd_workspace_bytes(...) bytes, 256-byte aligned
+ *              (not used without dweight and dbias; may be 0 bytes)
+ *
+ * Alignment and sizes as for ssd_layer_norm.  rows == 0 writes zeros to dweight
+ * and dbias.
+ */
+int32_t ssd_layer_norm_bwd(const void *dy, const void *x, const float *stats, const float *weight,
+                           const void *d_sum, void *dx, float *dweight, float *dbias,
+                           int64_t rows, int64_t dim, int32_t io_dtype, void *workspace,
+                           size_t workspace_bytes, void *hip_stream);
+
+/* Bytes of workspace ssd_layer_norm_bwd needs (may be 0; 0 for invalid sizes). */
+size_t ssd_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
+
+/*
+ * ssd_delta_scan -- the gated delta rule over a whole sequence.  Per head, with
+ * a state S [key_dim, value_dim] and the time step of ssd_chunk_scan,
+ * d_t = clamp(softplus(dt_t + dt_bias), dt_min, dt_max):
+ *
+ *   P_t = exp(A d_t) S_{t-1}
+ *   u_t = beta_t (v_t - P_t^T k_t)
+ *   S_t = P_t + k_t u_t^T,   y_t = scale S_t^T q_t
+ *
+ * The heads of a group share q and k; head hh uses group hh / (heads / groups).
+ *
+ *   q, k         [batch, seqlen, groups, key_dim] io dtype; 16-byte aligned
+ *   v            [batch, seqlen, heads, value_dim] io dtype; 16-byte aligned
+ *   dt, beta     [batch, seqlen, heads] io dtype (dt raw, before dt_bias; beta
+ *                as it is used)
+ *   A            [heads] fp32;  dt_bias [heads] fp32 or NULL (zeros)
+ *   dt_softplus, dt_min, dt_max   as for ssd_chunk_scan
+ *   scale        factor of y
+ *   normalize    nonzero: q and k are divided by sqrt(|.|^2 + norm_eps) first
+ *                (norm_eps >= 0, finite; a row of zeros stays zeros)
+ *   init_state   [batch, heads, key_dim, value_dim] fp32 or NULL (zeros);
+ *                16-byte aligned
+ *   seq_idx      [batch, seqlen] int32 or NULL, as for ssd_chunk_scan_ex
+ *   y            [batch, seqlen, heads, value_dim] io dtype, written; 16-byte
+ *                aligned
+ *   final_state  [batch, heads, key_dim, value_dim] fp32 or NULL, written; may
+ *                equal init_state; 16-byte aligned
+ *   states       [batch, ceil(seqlen / SSD_DELTA_CHUNK), heads, key_dim,
+ *                value_dim] fp32 or NULL: entry c is the state after token
+ *                min(SSD_DELTA_CHUNK (c + 1), seqlen) - 1, what
+ *                ssd_delta_scan_bwd can start from; 16-byte aligned
+ *   workspace    ssd_delta_scan_workspace_bytes(...) bytes, 256-byte aligned
+ *
+ * value_dim in {16, 32, 64, 128}, key_dim in {32, 64, 128}; batch up to 65535,
+ * heads up to 16384, seqlen up to 2^28 and batch heads ceil(seqlen / 64) below
+ * 2^23; beyond that SSD_ERR_UNSUPPORTED, and 0 from the queries.
+ *
+ * Preconditions not checked on the device: A <= 0, inputs finite, y overlaps no
+ * input, and the step does not expand: 0 <= beta_t |k_t|^2 <= 2 (k after its
+ * normalisation).  Inside 64 tokens beta_i |k_i| |k_j| has to stay below 2^15.
+ *
+ * Precision: operands of the matrix products formed inside the call are split
+ * into two fp16 terms with a power of two per row or column, 22 significant
+ * bits (fp32 io: q and k too); with bf16 io the read-out takes the first term,
+ * 11 bits, of the state, of u and of the masked q k products.  States, sums,
+ * decays and the triangular inverse are fp32 (log decays are summed in fp64);
+ * y is rounded to nearest even.  Deterministic.  seqlen == 0 gives final_state =
+ * init_state or zeros.
+ */
+#define SSD_DELTA_CHUNK 64
+int32_t ssd_delta_scan(const void *q, const void *k, const void *v, const void *dt,
+                       const float *A, const float *dt_bias, int32_t dt_softplus, float dt_min,
+                       float dt_max, const void *beta, float scale, int32_t normalize,
+                       float norm_eps, const float *init_state, const int32_t *seq_idx, void *y,
+                       float *final_state, float *states, int64_t batch, int64_t seqlen,
+                       int64_t heads, int64_t value_dim, int64_t key_dim, int64_t groups,
+                       int32_t io_dtype, void *workspace, size_t workspace_bytes,
+                       void *hip_stream);
+
+/* Bytes of workspace ssd_delta_scan needs (0 for invalid or empty sizes). */
+size_t ssd_delta_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
+                                      int64_t value_dim, int64_t key_dim, int64_t groups,
+                                      int32_t io_dtype);
+
+/*
+ * ssd_delta_scan_bwd -- gradients of ssd_delta_scan's y (cotangent dy) and
+ * final state (d_final) with respect to every input, deterministic.
+ *
+ *   states    the forward's states output for the same inputs, or NULL (they
+ *             are then computed again)
+ *   dy        [batch, seqlen, heads, value_dim] io dtype; 16-byte aligned
+ *   d_final   [batch, heads, key_dim, value_dim] fp32 or NULL; 16-byte aligned
+ *   dq, dk    [batch, seqlen, groups, key_dim] io dtype, summed over the heads
+ *             that share them; 16-byte aligned
+ *   dv        like v, 16-byte aligned;  ddt, dbeta like dt
+ *   dA        [heads] fp32;  ddt_bias [heads] fp32 or NULL
+ *   d_init    [batch, heads, key_dim, value_dim] fp32 or NULL; 16-byte aligned
+ *   workspace ssd_delta_scan_bwd_workspace_bytes(...) bytes, 256-byte aligned
+ *
+ * A time step beyond a limit of the clamp has no gradient, nor has the decay in
+ * front of a document's first token or of a zero initial state.  batch and
+ * seqlen >= 1, limits and preconditions as for ssd_delta_scan.  bf16 io: dq, dk
+ * and dbeta are products of bf16 operands (the states, N = v - P^T k and the
+ * cotangents behind them rounded once) with fp32 accumulation; everything that
+ * the other outputs and the adjoint recurrence need keeps 22 bits.  A decay's
+ * gradient is a difference of sums of dy . y and dv . v over up to 64 tokens and
+ * off by about 2^-21 of them; where a decay is below 2^-21 it is zero.
+ */
+int32_t ssd_delta_scan_bwd(const void *q, const void *k, const void *v, const void *dt,
+                           const float *A, const float *dt_bias, int32_t dt_softplus,
+                           float dt_min, float dt_max, const void *beta, float scale,
+                           int32_t normalize, float norm_eps, const float *init_state,
+                           const int32_t *seq_idx, const float *states, const void *dy,
+                           const float *d_final, void *dq, void *dk, void *dv, void *ddt,
+                           void *dbeta, float *dA, float *ddt_bias, float *d_init, int64_t batch,
+                           int64_t seqlen, int64_t heads, int64_t value_dim, int64_t key_dim,
+                           int64_t groups, int32_t io_dtype, void *workspace,
+                           size_t workspace_bytes, void *hip_stream);
+
+/* Bytes of workspace ssd_delta_scan_bwd needs, with or without the forward's
+ * states (0 for invalid sizes). */
+size_t ssd_delta_scan_bwd_workspace_bytes(int64_t batch, int64_t seqlen, int64_t heads,
+                                          int64_t value_dim, int64_t key_dim, int64_t groups,
+                                          int32_t io_dtype, int32_t with_states);
+
+/*
+ * ssd_delta_step -- one token of ssd_delta_scan: state [batch, heads, key_dim,
+ * value_dim] fp32 read and overwritten (16-byte aligned), q and k [batch,
+ * groups, key_dim], v and y [batch, heads, value_dim] (aligned to 4 elements),
+ * dt and beta [batch, heads] io dtype.  fp32 arithmetic.  heads up to 16384 and
+ * batch * heads up to 2^23, else SSD_ERR_UNSUPPORTED.
+ */
+int32_t ssd_delta_step(float *state, const void *q, const void *k, const void *v, const void *dt,
+                       const float *A, const float *dt_bias, int32_t dt_softplus, float dt_min,
+                       float dt_max, const void *beta, float scale, int32_t normalize,
+                       float norm_eps, void *y, int64_t batch, int64_t heads, int64_t value_dim,
+                       int64_t key_dim, int64_t groups, int32_t io_dtype, void *hip_stream);
 
 /*
  * Sequence segments (one per GPU for contexts beyond one GPU).  The state

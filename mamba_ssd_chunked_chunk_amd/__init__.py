@@ -29,6 +29,9 @@ __all__ = ["chunk_scan", "chunk_scan_noalloc", "chunk_scan_bwd", "step", "conv1d
            "linear", "linear_bwd", "linear_workspace_bytes", "linear_bwd_workspace_bytes",
            "gated_scan", "gated_scan_bwd", "gated_step", "gated_scan_workspace_bytes",
            "gated_scan_bwd_workspace_bytes",
+           "layer_norm", "layer_norm_bwd", "layer_norm_bwd_workspace_bytes",
+           "delta_scan", "delta_scan_bwd", "delta_step", "delta_scan_workspace_bytes",
+           "delta_scan_bwd_workspace_bytes",
            "workspace_bytes", "state_chunks", "abi_version",
            "LibraryMissing", "SsdError"]
 
@@ -744,4 +747,239 @@ def gated_step(state, x, gates, lam, scale: float = 8.0, out=None):
     _fit("out", y, io, (b, d), dev)
     _launch("ssd_gated_step", dev, _ptr(state), _ptr(x), _ptr(gates), _ptr(lam), float(scale),
             _ptr(y), b, d, code)
+    return y
+
+
+def layer_norm_bwd_workspace_bytes(rows, dim) -> int:
+    """Workspace bytes of one layer_norm_bwd call (ssd_layer_norm_bwd_workspace_bytes)."""
+    return int(load().ssd_layer_norm_bwd_workspace_bytes(rows, dim))
+
+
+def layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5,
+               return_stats: bool = False, out=None, sum_out=None):
+    """Layer norm over the last axis (ssd_layer_norm): (x - mean) rstd weight
+    + bias, with `residual` of x + residual, rounded to the io dtype.
+
+    x [..., dim] and residual in the io dtype, weight and bias [dim] fp32.
+    Returns y, followed by the sum (with `residual`) and by the row statistics
+    [2, rows] fp32 (mean, 1 / deviation; return_stats), which layer_norm_bwd
+    takes.  `sum_out` may be x or residual, `out` either where the sum is
+    another tensor."""
+    torch = _torch()
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("x must be a GPU tensor")
+    io = x.dtype
+    code = _io_code(io)
+    if x.dim() < 1:
+        raise ValueError("x must be [..., dim]")
+    dim, shape = x.shape[-1], x.shape
+    _check("x", x, io)
+    _fit("residual", residual, io, shape, dev)
+    _fit("weight", weight, torch.float32, (dim,), dev)
+    _fit("bias", bias, torch.float32, (dim,), dev)
+    y = torch.empty_like(x) if out is None else out
+    _fit("out", y, io, shape, dev)
+    total = None
+    if residual is not None:
+        total = torch.empty_like(x) if sum_out is None else sum_out
+        _fit("sum_out", total, io, shape, dev)
+    elif sum_out is not None:
+        raise ValueError("sum_out is the output of x + residual, and there is no residual")
+    rows = x.numel() // dim if dim else 0
+    stats = torch.empty((2, rows), dtype=torch.float32, device=dev) if return_stats else None
+    _launch("ssd_layer_norm", dev, _ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), float(eps),
+            _ptr(y), _ptr(total), _ptr(stats), rows, dim, code)
+    if total is None and stats is None:
+        return y
+    return (y,) + (() if total is None else (total,)) + (() if stats is None else (stats,))
+
+
+def layer_norm_bwd(dy, x, stats, weight=None, bias: bool = False, d_sum=None, out=None,
+                   workspace=None):
+    """Gradients of layer_norm's y (cotangent dy) with respect to its input,
+    weight and, with `bias`, the bias (ssd_layer_norm_bwd), deterministic.
+
+    x: what was normalised (the sum, where there was a residual); stats: what
+    layer_norm returned; d_sum: the gradient that reaches the sum from
+    elsewhere, added to dx.  Returns a dict: dx (io dtype; also the residual's
+    gradient), dweight (fp32, with `weight`) and dbias (fp32).  `out` (for dx)
+    may be dy or d_sum."""
+    torch = _torch()
+    dev = dy.device
+    if dev.type != "cuda":
+        raise ValueError("dy must be a GPU tensor")
+    io = dy.dtype
+    code = _io_code(io)
+    if dy.dim() < 1:
+        raise ValueError("dy must be [..., dim]")
+    dim, shape = dy.shape[-1], dy.shape
+    rows = dy.numel() // dim if dim else 0
+    _check("dy", dy, io)
+    _fit("x", x, io, shape, dev)
+    _fit("stats", stats, torch.float32, (2, rows), dev)
+    _fit("weight", weight, torch.float32, (dim,), dev)
+    _fit("d_sum", d_sum, io, shape, dev)
+    dx = torch.empty_like(dy) if out is None else out
+    _fit("out", dx, io, shape, dev)
+    res = dict(dx=dx)
+    if weight is not None:
+        res["dweight"] = torch.empty((dim,), dtype=torch.float32, device=dev)
+    if bias:
+        res["dbias"] = torch.empty((dim,), dtype=torch.float32, device=dev)
+    need = _query("ssd_layer_norm_bwd_workspace_bytes", rows, dim) if len(res) > 1 else 0
+    ws = _scratch(workspace, need, dev) if need or workspace is not None else None
+    _launch("ssd_layer_norm_bwd", dev, _ptr(dy), _ptr(x), _ptr(stats), _ptr(weight), _ptr(d_sum),
+            _ptr(dx), _ptr(res.get("dweight")), _ptr(res.get("dbias")), rows, dim, code, _ptr(ws),
+            0 if ws is None else ws.numel())
+    return res
+
+
+def delta_scan_workspace_bytes(batch, seqlen, heads, value_dim, key_dim, groups, io="bf16") -> int:
+    """Workspace bytes of one delta_scan call (ssd_delta_scan_workspace_bytes)."""
+    return int(load().ssd_delta_scan_workspace_bytes(batch, seqlen, heads, value_dim, key_dim,
+                                                     groups, _io_name(io)))
+
+
+def delta_scan_bwd_workspace_bytes(batch, seqlen, heads, value_dim, key_dim, groups, io="bf16",
+                                   with_states: bool = True) -> int:
+    """Workspace bytes of one delta_scan_bwd call (ssd_delta_scan_bwd_workspace_bytes)."""
+    return int(load().ssd_delta_scan_bwd_workspace_bytes(batch, seqlen, heads, value_dim, key_dim,
+                                                         groups, _io_name(io),
+                                                         int(bool(with_states))))
+
+
+def _delta_inputs(lead, q, k, v, dt, A, beta, dt_bias):
+    """The checks that delta_scan, its gradient and its step share; lead is the
+    number of axes in front of the heads.  Returns io dtype, code, device, the
+    leading sizes and heads, value_dim, key_dim, groups."""
+    torch = _torch()
+    names = "[batch, seqlen, " if lead == 2 else "[batch, "
+    if v.dim() != lead + 2:
+        raise ValueError("v must be %sheads, value_dim]" % names)
+    if k.dim() != lead + 2:
+        raise ValueError("k must be %sgroups, key_dim]" % names)
+    dev = v.device
+    if dev.type != "cuda":
+        raise ValueError("v must be a GPU tensor")
+    io = v.dtype
+    code = _io_code(io)
+    lead = tuple(v.shape[:lead])
+    h, p = v.shape[-2:]
+    g, n = k.shape[-2:]
+    _check("v", v, io)
+    _fit("k", k, io, lead + (g, n), dev)
+    _fit("q", q, io, lead + (g, n), dev)
+    _fit("dt", dt, io, lead + (h,), dev)
+    _fit("beta", beta, io, lead + (h,), dev)
+    _fit("A", A, torch.float32, (h,), dev)
+    _fit("dt_bias", dt_bias, torch.float32, (h,), dev)
+    return io, code, dev, lead, h, p, n, g
+
+
+def _delta_rule(q, k, v, dt, A, beta, dt_bias, dt_softplus, dt_limit, scale, normalize, norm_eps, n):
+    """The arguments from q to norm_eps of the library's calls."""
+    return (_ptr(q), _ptr(k), _ptr(v), _ptr(dt), _ptr(A), _ptr(dt_bias), int(bool(dt_softplus)),
+            float(dt_limit[0]), float(dt_limit[1]), _ptr(beta),
+            float(n) ** -0.5 if scale is None else float(scale), int(bool(normalize)),
+            float(norm_eps))
+
+
+def delta_scan(q, k, v, dt, A, beta, dt_bias=None, dt_softplus: bool = True,
+               dt_limit: Tuple[float, float] = (0.0, math.inf), scale: Optional[float] = None,
+               normalize: bool = False, norm_eps: float = 1e-6, initial_state=None, seq_idx=None,
+               return_final_state: bool = False, return_states: bool = False, out=None,
+               final_out=None, states_out=None, workspace=None):
+    """The gated delta rule over a whole sequence (ssd_delta_scan): per head,
+    with a state S [n, p] and d = clamp(softplus(dt + dt_bias)),
+
+        P_t = exp(A d_t) S_{t-1},  u_t = beta_t (v_t - P_t^T k_t)
+        S_t = P_t + k_t u_t^T,     y_t = scale S_t^T q_t
+
+    v [b, l, h, p], q and k [b, l, g, n], dt and beta [b, l, h] in the io
+    dtype, A and dt_bias [h] fp32, initial_state [b, h, n, p] fp32, seq_idx
+    [b, l] int32.  scale: 1 / sqrt(n) by default.  normalize: q and k are
+    divided by sqrt(|.|^2 + norm_eps) first.  Returns y [b, l, h, p], followed
+    by the final state [b, h, n, p] and by the states after every 64 tokens
+    [b, ceil(l / 64), h, n, p] (fp32, for delta_scan_bwd) when asked for.
+    final_out may be initial_state."""
+    torch = _torch()
+    io, code, dev, (b, l), h, p, n, g = _delta_inputs(2, q, k, v, dt, A, beta, dt_bias)
+    _fit("initial_state", initial_state, torch.float32, (b, h, n, p), dev)
+    _fit("seq_idx", seq_idx, torch.int32, (b, l), dev)
+    y = torch.empty_like(v) if out is None else out
+    _fit("out", y, io, (b, l, h, p), dev)
+    fin = states = None
+    if return_final_state:
+        fin = torch.empty((b, h, n, p), dtype=torch.float32, device=dev) \
+            if final_out is None else final_out
+        _fit("final_out", fin, torch.float32, (b, h, n, p), dev)
+    if return_states:
+        shape = (b, -(-l // _lib.SSD_DELTA_CHUNK), h, n, p)
+        states = torch.empty(shape, dtype=torch.float32, device=dev) \
+            if states_out is None else states_out
+        _fit("states_out", states, torch.float32, shape, dev)
+    ws = _scratch(workspace, _query("ssd_delta_scan_workspace_bytes", b, l, h, p, n, g, code), dev)
+    _launch("ssd_delta_scan", dev,
+            *_delta_rule(q, k, v, dt, A, beta, dt_bias, dt_softplus, dt_limit, scale, normalize,
+                         norm_eps, n),
+            _ptr(initial_state), _ptr(seq_idx), _ptr(y), _ptr(fin), _ptr(states), b, l, h, p, n, g,
+            code, _ptr(ws), ws.numel())
+    if not return_final_state and not return_states:
+        return y
+    return (y,) + ((fin,) if return_final_state else ()) + ((states,) if return_states else ())
+
+
+def delta_scan_bwd(q, k, v, dt, A, beta, dy, dt_bias=None, dt_softplus: bool = True,
+                   dt_limit: Tuple[float, float] = (0.0, math.inf),
+                   scale: Optional[float] = None, normalize: bool = False,
+                   norm_eps: float = 1e-6, initial_state=None, d_final=None, seq_idx=None,
+                   states=None, workspace=None):
+    """Gradients of delta_scan's y (cotangent dy) and final state (d_final)
+    with respect to every input (ssd_delta_scan_bwd), deterministic.  states:
+    what delta_scan returned for these inputs (None: computed again).
+    Returns a dict: dq, dk, dv, ddt, dbeta (io dtype), dA, ddt_bias (with
+    dt_bias) and d_init (with initial_state) in fp32."""
+    torch = _torch()
+    io, code, dev, (b, l), h, p, n, g = _delta_inputs(2, q, k, v, dt, A, beta, dt_bias)
+    _fit("dy", dy, io, (b, l, h, p), dev)
+    _fit("initial_state", initial_state, torch.float32, (b, h, n, p), dev)
+    _fit("d_final", d_final, torch.float32, (b, h, n, p), dev)
+    _fit("seq_idx", seq_idx, torch.int32, (b, l), dev)
+    _fit("states", states, torch.float32, (b, -(-l // _lib.SSD_DELTA_CHUNK), h, n, p), dev)
+    res = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+               ddt=torch.empty_like(dt), dbeta=torch.empty_like(beta), dA=torch.empty_like(A))
+    if dt_bias is not None:
+        res["ddt_bias"] = torch.empty_like(dt_bias)
+    if initial_state is not None:
+        res["d_init"] = torch.empty_like(initial_state)
+    ws = _scratch(workspace, _query("ssd_delta_scan_bwd_workspace_bytes", b, l, h, p, n, g, code,
+                                    int(states is not None)), dev)
+    _launch("ssd_delta_scan_bwd", dev,
+            *_delta_rule(q, k, v, dt, A, beta, dt_bias, dt_softplus, dt_limit, scale, normalize,
+                         norm_eps, n),
+            _ptr(initial_state), _ptr(seq_idx), _ptr(states), _ptr(dy), _ptr(d_final),
+            _ptr(res["dq"]), _ptr(res["dk"]), _ptr(res["dv"]), _ptr(res["ddt"]),
+            _ptr(res["dbeta"]), _ptr(res["dA"]), _ptr(res.get("ddt_bias")),
+            _ptr(res.get("d_init")), b, l, h, p, n, g, code, _ptr(ws), ws.numel())
+    return res
+
+
+def delta_step(state, q, k, v, dt, A, beta, dt_bias=None, dt_softplus: bool = True,
+               dt_limit: Tuple[float, float] = (0.0, math.inf), scale: Optional[float] = None,
+               normalize: bool = False, norm_eps: float = 1e-6, out=None):
+    """One token of delta_scan (ssd_delta_step): updates `state` [b, h, n, p]
+    (fp32) in place, returns y [b, h, p].  v [b, h, p], q and k [b, g, n], dt
+    and beta [b, h] in the io dtype."""
+    torch = _torch()
+    io, code, dev, (b,), h, p, n, g = _delta_inputs(1, q, k, v, dt, A, beta, dt_bias)
+    _fit("state", state, torch.float32, (b, h, n, p), dev)
+    if state is None:
+        raise ValueError("state is needed")
+    y = torch.empty_like(v) if out is None else out
+    _fit("out", y, io, (b, h, p), dev)
+    _launch("ssd_delta_step", dev, _ptr(state),
+            *_delta_rule(q, k, v, dt, A, beta, dt_bias, dt_softplus, dt_limit, scale, normalize,
+                         norm_eps, n),
+            _ptr(y), b, h, p, n, g, code)
     return y

@@ -34,12 +34,17 @@ EXPORTS = ("ssd_chunk_scan", "ssd_chunk_scan_ex", "ssd_chunk_scan_noalloc",
            "ssd_linear_bwd_workspace_bytes", "ssd_gated_scan",
            "ssd_gated_scan_workspace_bytes", "ssd_gated_scan_bwd",
            "ssd_gated_scan_bwd_workspace_bytes", "ssd_gated_step",
+           "ssd_layer_norm", "ssd_layer_norm_bwd", "ssd_layer_norm_bwd_workspace_bytes",
+           "ssd_delta_scan", "ssd_delta_scan_workspace_bytes", "ssd_delta_scan_bwd",
+           "ssd_delta_scan_bwd_workspace_bytes", "ssd_delta_step",
            "ssd_status_string", "ssd_abi_version")
 
 # ssd_linear's activations by name
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "sigmoid": 3}
 # tokens between the states that ssd_gated_scan keeps for its gradient
 SSD_GATED_CHUNK = 64
+# tokens between the states that ssd_delta_scan keeps for its gradient
+SSD_DELTA_CHUNK = 64
 
 _lib = None
 
@@ -119,6 +124,24 @@ def load() -> ctypes.CDLL:
     lib.ssd_gated_scan_bwd_workspace_bytes.argtypes = [I64, I64, I64]
     lib.ssd_gated_step.restype = I32
     lib.ssd_gated_step.argtypes = [P, P, P, P, F, P, I64, I64, I32, P]
+    lib.ssd_layer_norm.restype = I32
+    lib.ssd_layer_norm.argtypes = [P, P, P, P, F, P, P, P, I64, I64, I32, P]
+    lib.ssd_layer_norm_bwd.restype = I32
+    lib.ssd_layer_norm_bwd.argtypes = [P, P, P, P, P, P, P, P, I64, I64, I32, P, Z, P]
+    lib.ssd_layer_norm_bwd_workspace_bytes.restype = Z
+    lib.ssd_layer_norm_bwd_workspace_bytes.argtypes = [I64, I64]
+    rule = [P, P, P, P, P, P, I32, F, F, P, F, I32, F]  # q .. norm_eps
+    lib.ssd_delta_scan.restype = I32
+    lib.ssd_delta_scan.argtypes = rule + [P, P, P, P, P, I64, I64, I64, I64, I64, I64, I32, P, Z, P]
+    lib.ssd_delta_scan_workspace_bytes.restype = Z
+    lib.ssd_delta_scan_workspace_bytes.argtypes = [I64] * 6 + [I32]
+    lib.ssd_delta_scan_bwd.restype = I32
+    lib.ssd_delta_scan_bwd.argtypes = rule + [P] * 5 + [P] * 8 + \
+        [I64, I64, I64, I64, I64, I64, I32, P, Z, P]
+    lib.ssd_delta_scan_bwd_workspace_bytes.restype = Z
+    lib.ssd_delta_scan_bwd_workspace_bytes.argtypes = [I64] * 6 + [I32, I32]
+    lib.ssd_delta_step.restype = I32
+    lib.ssd_delta_step.argtypes = [P] + rule + [P, I64, I64, I64, I64, I64, I32, P]
     lib.ssd_status_string.restype = ctypes.c_char_p
     lib.ssd_status_string.argtypes = [I32]
     lib.ssd_abi_version.restype = I32

@@ -1,0 +1,276 @@
+// The gated delta rule: what its kernels share (the mathematics, the layout of
+// the workspace, operand images).  Per head, with a state S [key_dim, value_dim]:
+//
+//   P_t = e^{g_t} S_{t-1},  u_t = beta_t (v_t - P_t^T k_t),  S_t = P_t + k_t u_t^T
+//   y_t = scale S_t^T q_t,  g_t = A d_t,  d_t = clamp(softplus(dt_t + dt_bias))
+//
+// In chunks of C = 64 tokens, with G_i the sum of g over the chunk up to token i,
+// D_ij = e^{G_i - G_j} (j <= i, same document), S the state in front and
+// N_i = v_i - P_i^T k_i (so u = beta N):
+//
+//   kk = tril(K K^T . D, -1)         T = (I + kk diag(beta))^-1
+//   N  = T (V - e^G K S)             U = diag(beta) N
+//   Y  = scale (e^G Q S + tril(Q K^T . D) U)
+//   S' = e^{G_C} S + K^T (e^{G_C - G} U)
+//
+// and backwards, with S the state in front, dS that of the state behind:
+//
+//   dU = scale tril(Q K^T . D)^T dY + e^{G_C - G} K dS
+//   Z  = (I + diag(beta) kk)^-T dU,  dV = diag(beta) Z,  dbeta_i = Z_i . N_i
+//   dS <- e^{G_C} dS + scale Q^T (e^G dY) - K^T (e^G dV)
+//   dQ_i = scale e^{G_i} S dY_i + scale sum_{j<=i} D_ij (dY_i . U_j) k_j
+//   dK_j = scale sum_{i>=j} D_ij (dY_i . U_j) q_i - e^{G_j} S dV_j
+//          + e^{G_C-G_j} dS U_j - (X + X^T) K,  X_ij = D_ij (dV_i . U_j), j < i
+//   dG_i = dY_i . Y_i - dV_i . V_i,  and e^{G_C} S', dS' behind the last token:
+//   dg_t = sum_{i>=t} dG_i + <S', dS>
+//
+// A token that starts a document has nothing in front: e^{G} is zero from it
+// on, D across it, and e^{G_C - G} in front of the last such token.
+//
+// Precision.  The products run on fp16 matrix instructions with fp32
+// accumulation.  Every operand is an fp32 value times a power of two (per row
+// of q and k, per column of a state or of a chunk's rows, so that the largest
+// magnitude fits), written as two fp16 terms hi + lo, 22 significant bits, and
+// multiplied as hi hi + hi lo + lo hi; q and k of bf16 io are exact in one.
+// With bf16 io the read-out (Y) takes hi terms alone: its 2^-11 is an eighth
+// of y's own rounding.  States, sums, decays and the triangular inverse are fp32
+// (the log decays' sums fp64).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "ssd_device.hpp"
+
+namespace ssd {
+
+constexpr int kDC = 64;       // tokens of a chunk
+constexpr int kPieces = 6;    // 16 x 32 pieces of a lower triangular 64 x 64 matrix
+constexpr int kRows = 8;      // row arrays of the scans: see RowOf
+constexpr int kRowsGrad = 8;  // row arrays of the gradient's last pass
+
+// Per token of a chunk and head, fp32 [array][64].  fk and fq undo the powers
+// of two that k and q are stored with (times 1 / norm where the call normalises).
+enum RowOf {
+    kReadK,   // e^G fk
+    kFk,      // fk
+    kWriteK,  // e^{G_C - G} fk
+    kReadQ,   // scale e^G fq
+    kFq,      // scale fq
+    kBeta,    // beta
+    kCarry,   // [0]: e^{G_C}
+    kSpare
+};
+enum RowOfGrad {
+    kGhi,    // log2 of e^G, as two floats
+    kGlo,
+    kDoc,    // documents started in the chunk up to the token
+    kRead,   // e^G
+    kWrite,  // e^{G_C - G}
+    kRk,     // 1 / |k| where the call normalises, else 1
+    kRq,
+    kStep    // d_t
+};
+
+struct DeltaArgs {
+    const void *q, *k, *v, *dt, *beta;
+    const float *A, *bias, *init;
+    const int32_t *seq;
+    void *y;
+    float *fin, *states;       // written by the forward pass
+    const float *kept;         // states of an earlier forward pass
+    const void *dy;
+    const float *dfin;
+    void *dq, *dk, *dv, *ddt, *dbeta;
+    float *dA, *dbias, *dinit;
+    // workspace
+    f16 *kimg, *qimg, *timg, *mimg, *pimg;
+    float *rows, *rows2;
+    void *nimg, *nlow, *zimg, *simg, *dsimg;
+    float *doo, *dvv, *dzn, *eend;
+    double *part;
+    int64_t b, l, h, g, nc;
+    int p, softplus, norm;
+    float scale, eps, lo, hi;
+};
+
+// Operand images.  A matrix M[t][x] (t in tiles of 16, x in blocks of 32) is
+// kept as pieces of 64 lanes x 8 elements, piece (t >> 4) * XB + (x >> 5): lane
+// (t & 15) + 16 ((x >> 2) & 3) holds, at 4 ((x >> 4) & 1) + (x & 3), element
+// (t, x).  So a piece is one operand fragment whose free index is t and whose
+// contraction index is x (one 16-byte read per lane, no bank conflicts), four
+// consecutive x are contiguous for the transposing read that gives the
+// fragment with x free and t contracted, and a copy into LDS is linear.
+template <typename T> struct Frag8;
+template <> struct Frag8<f16> { typedef f16x8 type; };
+template <> struct Frag8<bf16> { typedef __bf16 type __attribute__((ext_vector_type(8))); };
+template <> struct Frag8<float> { typedef float type __attribute__((ext_vector_type(8))); };
+
+template <typename T>
+__device__ __forceinline__ typename Frag8<T>::type img_rows(const T *img, int piece, int lane) {
+    return *reinterpret_cast<const typename Frag8<T>::type *>(img + piece * 512 + lane * 8);
+}
+
+// Element offset inside an image of XB blocks a row.
+__device__ __forceinline__ int img_at(int t, int x, int XB) {
+    return ((t >> 4) * XB + (x >> 5)) * 512 + ((t & 15) + 16 * ((x >> 2) & 3)) * 8 +
+           4 * ((x >> 4) & 1) + (x & 3);
+}
+
+// Fragment with x free (tile x16) and the 32 contraction indices of pieces p0
+// (t = 0..15) and p1 (t = 16..31); x16 & 1 picks the half inside the pieces.
+template <typename T>
+__device__ __forceinline__ typename Frag8<T>::type img_cols(const T *img, int p0, int p1, int x16,
+                                                            int lane) {
+    const int g = lane >> 4, j = lane & 15;
+    if constexpr (sizeof(T) == 2) {
+        const int o = (4 * g + (j >> 2) + 16 * (j & 3)) * 8 + 4 * (x16 & 1);
+        const T *a = img + p0 * 512 + o, *b = img + p1 * 512 + o;
+        const f16x4 u = __builtin_bit_cast(
+            f16x4, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4 *)a));
+        const f16x4 w = __builtin_bit_cast(
+            f16x4, __builtin_amdgcn_ds_read_tr16_b64_v4f16((lds_fp16x4 *)b));
+        return __builtin_bit_cast(typename Frag8<T>::type,
+                                  f16x8{u[0], u[1], u[2], u[3], w[0], w[1], w[2], w[3]});
+    } else {
+        typename Frag8<T>::type r;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            r[e] = img[(e < 4 ? p0 : p1) * 512 + (4 * g + (e & 3) + 16 * (j >> 2)) * 8 +
+                       4 * (x16 & 1) + (j & 3)];
+        return r;
+    }
+}
+
+// Piece of a lower triangular matrix's row tile rt and 32-block kb <= rt / 2.
+__device__ __forceinline__ constexpr int tri_piece(int rt, int kb) {
+    return rt < 2 ? rt : 2 * rt - 2 + kb;
+}
+
+__device__ __forceinline__ f32x4 mma16(f16x8 a, f16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Power of two that brings magnitudes up to mx into [2^13, 2^14), and its inverse.
+struct Pow2 {
+    float sc, inv;
+    __device__ explicit Pow2(float mx) {
+        const int e = (int)(__builtin_bit_cast(uint32_t, mx) >> 23) & 255;
+        int f = 267 - e;
+        f = f > 253 ? 253 : f;
+        sc = __builtin_bit_cast(float, (uint32_t)f << 23);
+        inv = __builtin_bit_cast(float, (uint32_t)(254 - f) << 23);
+    }
+};
+
+// hi + lo of two accumulator tiles times sc, as one fragment each (contraction
+// over the tiles' rows).
+struct Split {
+    f16x8 hi, lo;
+};
+__device__ __forceinline__ Split split8(const f32x4 &a, const f32x4 &b, float sc) {
+    Split s;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float x = (i < 4 ? a[i & 3] : b[i & 3]), y = (i < 4 ? a[(i & 3) + 1] : b[(i & 3) + 1]);
+        const f16x2 h = __builtin_convertvector(f32x2{x * sc, y * sc}, f16x2);
+        s.hi[i] = h[0], s.hi[i + 1] = h[1];
+        s.lo[i] = (f16)fmaf(x, sc, -(float)h[0]);
+        s.lo[i + 1] = (f16)fmaf(y, sc, -(float)h[1]);
+    }
+    return s;
+}
+
+// Largest value over the four lane groups that share a column.  (The swaps'
+// results go through scalars: the compiler takes a bit cast of a vector's
+// element as one of its first element.)
+__device__ __forceinline__ float col_max(float v) {
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    const uint32_t a = __builtin_bit_cast(uint32_t, v);
+    const u2 r = __builtin_amdgcn_permlane32_swap(a, a, false, false);
+    const uint32_t r0 = r[0], r1 = r[1];
+    const uint32_t b = __builtin_bit_cast(
+        uint32_t, fmaxf(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1)));
+    const u2 s = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    const uint32_t s0 = s[0], s1 = s[1];
+    return fmaxf(__builtin_bit_cast(float, s0), __builtin_bit_cast(float, s1));
+}
+__device__ __forceinline__ float abs_max(float m, const f32x4 &v) {
+    return fmaxf(fmaxf(fmaxf(m, fabsf(v[0])), fmaxf(fabsf(v[1]), fabsf(v[2]))), fabsf(v[3]));
+}
+
+// Sum over the 16 lanes of a row of lanes (every lane gets it).
+template <int CTRL> __device__ __forceinline__ float dpp_add(float v) {
+    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                             0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float sum16(float v) {
+    v = dpp_add<0x128>(v);  // row_ror 8, 4, 2, 1
+    v = dpp_add<0x124>(v);
+    v = dpp_add<0x122>(v);
+    return dpp_add<0x121>(v);
+}
+
+// lds_dma16 of ssd_device.hpp with the LDS address as a number.
+__device__ __forceinline__ void lds_dma16_at(RsrcW r, uint32_t dst, uint32_t voff) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff),
+                 "s"(r), "s"(__builtin_amdgcn_readfirstlane(dst))
+                 : "memory", "m0");
+#else
+    (void)r, (void)dst, (void)voff;
+#endif
+}
+__device__ __forceinline__ uint32_t lds_address(char *p) { return (uint32_t)(uintptr_t)(lds_void *)p; }
+
+// `bytes` of contiguous memory into LDS by `nw` waves, and zeros up to `all` (a
+// multiple of 1024).
+__device__ __forceinline__ void copy_lds(const void *src, int bytes, int all, uint32_t dst, int wave,
+                                         int nw, int lane) {
+    const RsrcW r = make_rsrc_w(src, bytes);
+    for (int i = wave; i < all >> 10; i += nw)
+        lds_dma16_at(r, dst + (i << 10), (uint32_t)((i << 10) + lane * 16));
+}
+
+// 64 rows of `rb` bytes (a multiple of 32), `pitch` bytes apart in memory, into
+// LDS without gaps; rows from `len` on as zeros.
+__device__ __forceinline__ void copy_rows(const void *src, int64_t pitch, int rb, int len,
+                                          uint32_t dst, int wave, int nw, int lane) {
+    const RsrcW r = make_rsrc_w(src, (len - 1) * pitch + rb);
+    const int per = rb >> 4;  // 16-byte parts of a row
+    for (int i = wave; i < (64 * rb) >> 10; i += nw) {
+        const int part = i * 64 + lane, row = part / per;
+        const uint32_t off = row < len ? (uint32_t)(row * pitch + (part - row * per) * 16) : 0xf0000000u;
+        lds_dma16_at(r, dst + (i << 10), off);
+    }
+}
+
+// Rows 16 rt + 4 g + r of column col0 + (lane & 15) of 64 rows in LDS.
+__device__ __forceinline__ f32x4 lds_tile(const bf16 *M, int ld, int rt, int col0, int lane) {
+    const f16x4 v = lds_tr4(reinterpret_cast<const f16 *>(M), ld, 16 * rt, col0, lane);
+    const u32x2 w = __builtin_bit_cast(u32x2, v);
+    return f32x4{__builtin_bit_cast(float, w[0] << 16), __builtin_bit_cast(float, w[0] & 0xffff0000u),
+                 __builtin_bit_cast(float, w[1] << 16), __builtin_bit_cast(float, w[1] & 0xffff0000u)};
+}
+__device__ __forceinline__ f32x4 lds_tile(const float *M, int ld, int rt, int col0, int lane) {
+    const float *p = M + (16 * rt + 4 * (lane >> 4)) * ld + col0 + (lane & 15);
+    return f32x4{p[0], p[ld], p[2 * ld], p[3 * ld]};
+}
+__device__ __forceinline__ f32x4 row4(const float *rows, int array, int rt, int lane) {
+    return *reinterpret_cast<const f32x4 *>(rows + array * kDC + 16 * rt + 4 * (lane >> 4));
+}
+
+__device__ __forceinline__ void buf_put(Rsrc r, uint32_t off, float v, bf16) {
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(short, (bf16)v), r, off, 0, 0);
+}
+__device__ __forceinline__ void buf_put(Rsrc r, uint32_t off, float v, float) {
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, off, 0, 0);
+}
+
+// Launches (ssd_delta_scan.hip, ssd_delta_bwd.hip).
+hipError_t delta_prep(const DeltaArgs &a, int io, int n, bool grad, hipStream_t s);
+// forward: y, final state and states; grad: states (where none are kept), N and dY . Y
+hipError_t delta_forward(const DeltaArgs &a, int io, int n, bool grad, hipStream_t s);
+hipError_t delta_backward(const DeltaArgs &a, int io, int n, hipStream_t s);
+
+}  // namespace ssd
