@@ -147,6 +147,12 @@ __device__ __forceinline__ constexpr int tri_piece(int rt, int kb) {
     return rt < 2 ? rt : 2 * rt - 2 + kb;
 }
 
+// The same of an inverse, kept transposed (t the column j, x the row i): column
+// tile jt and 32-block ib >= jt / 2 of rows.
+__device__ __forceinline__ constexpr int tri_piece_t(int jt, int ib) {
+    return jt < 2 ? 2 * jt + ib : jt + 2;
+}
+
 __device__ __forceinline__ f32x4 mma16(f16x8 a, f16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }

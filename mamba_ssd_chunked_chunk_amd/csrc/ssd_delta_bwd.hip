@@ -79,6 +79,19 @@ __device__ __forceinline__ float state_dot(const float *st, int p, const f32x4 (
     return s + __shfl_xor(s, 32);
 }
 
+// The same of an inverse, which is kept transposed.
+__device__ __forceinline__ f32x4 inv_t(const f16 *M, int jt, const Split *f, int lane) {
+    f32x4 t = zero4();
+#pragma unroll
+    for (int ib = jt >> 1; ib < 2; ++ib) {
+        const f16x8 h = img_rows(M, tri_piece_t(jt, ib), lane);
+        t = mma16(h, f[ib].hi, t);
+        t = mma16(h, f[ib].lo, t);
+        t = mma16(img_rows(M + kPieces * 512, tri_piece_t(jt, ib), lane), f[ib].hi, t);
+    }
+    return t;
+}
+
 template <typename IO, int N, int NB>
 __global__ __launch_bounds__(256, 2) void k_delta_rev(DeltaArgs a) {
     typedef RevBuf<IO, N> B;
@@ -195,7 +208,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_rev(DeltaArgs a) {
         float *dvv = a.dvv + (hi * cts + ct) * kDC;
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
-            const f32x4 t = tri_t(M, rt, uf, lane);
+            const f32x4 t = inv_t(M, rt, uf, lane);
             const f32x4 be = row4(rows, kBeta, rt, lane), rk = row4(rows, kReadK, rt, lane);
             f32x4 d = lds_tile(V, cols, rt, 16 * wave, lane);
 #pragma unroll

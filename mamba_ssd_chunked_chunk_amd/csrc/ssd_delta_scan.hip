@@ -3,9 +3,9 @@
 // k_delta_prep, all chunks in parallel: everything of a chunk that does not
 // depend on the state -- k and q as operand images, the row factors, the
 // masked Q K^T and the inverse of the unit triangle.  The inverse is taken in
-// 16 x 16 blocks: the four on the diagonal by substitution (a lane per column),
-// the others by distance from it, T_ij = -T_ii sum_k (kk beta)_ik T_kj, on fp32
-// matrix instructions whose results feed the next product from registers.
+// 16 x 16 blocks: the four on the diagonal by substitution (a lane per block and
+// column), the others by distance from it, T_ij = -T_ii sum_k (kk beta)_ik T_kj,
+// on fp32 matrix instructions whose results feed the next product from registers.
 //
 // k_delta_fwd, chunk after chunk: a wave owns 16 value columns of one head's
 // state in registers (an accumulator tile per 16 keys).  Columns do not meet
@@ -26,244 +26,308 @@ int device_cus();
 namespace {
 
 // ------------------------------------------------------------------ prep ---
-constexpr int kTP = kDC + 4;  // pitch of the fp32 triangles in LDS
+// Keeps a wave's own LDS stores and loads in program order (the hardware does;
+// no barrier is needed as no other wave reads them).
+__device__ __forceinline__ void wave_fence() { asm volatile("" ::: "memory"); }
 
-template <typename IO, int N, bool GRAD>
-__global__ __launch_bounds__(256) void k_delta_prep(DeltaArgs a) {
+constexpr int kDP = 20;  // pitch of the 16 x 16 blocks in LDS: 16-byte rows, spread over the banks
+
+struct alignas(16) PrepLds {
+    float A[4][16 * kDP], X[4][16 * kDP];  // the triangle's diagonal blocks, and their inverses
+    float fac[2][kDC], rn[2][kDC];         // row factors of k and q
+    float ghi[kDC], glo[kDC], doc[kDC], bet[kDC];
+};
+
+// A 16-row tile of k or q as operand fragments (contraction over x in the order
+// of memory, lane group g the eight from 8 g on): brings each row's largest
+// value into [1/2, 1) by a power of two, leaves the row's factors in LDS and, if
+// asked, the fragments in the image.
+template <typename IO, int N>
+__device__ __forceinline__ void load_tile(const DeltaArgs &a, const IO *src, int64_t pitch, int rt,
+                                          int len, float *fac, float *rn, f16 *img, f16x8 (&hi)[N / 32],
+                                          f16x8 (&lo)[N / 32], int lane) {
     constexpr bool F32 = sizeof(IO) == 4;
-    constexpr int PL = F32 ? 2 : 1, XB = N / 32, Q4 = N / 4;
-    constexpr int IMG = kDC * N;                   // elements of an image
-    constexpr int NT = GRAD ? 2 : 1;               // triangles: T, and (I + beta kk)^-1
-    constexpr int PPL = F32 || GRAD ? 2 : 1;       // terms of tril(Q K^T)
-    __shared__ __align__(16) f16 kq[2][PL * IMG];  // k, q
-    __shared__ __align__(16) float tri[1 + NT][kDC * kTP];  // kk, then its inverses
-    __shared__ __align__(16) f16 pst[PPL][kPieces * 512];
-    __shared__ float fac[2][kDC], rn[2][kDC], ghi[kDC], glo[kDC], bet[kDC], rd[kDC], wr[kDC];
-    __shared__ int doc[kDC];
-
-    const int tid = threadIdx.x, lane = tid & 63, wave = wave_id(), g = lane >> 4, j16 = lane & 15;
-    const int64_t item = xcd_item(blockIdx.x, gridDim.x);
-    const int64_t hh = item % a.h, ci = item / a.h, c = ci % a.nc, bb = ci / a.nc;
-    const int ratio = (int)(a.h / a.g);
-    const int64_t gg = hh / ratio, t0 = c * kDC;
-    const int len = (int)(a.l - t0 < kDC ? a.l - t0 : kDC);
-
-    // rows of k and q: a quarter row per thread
-    {
-        const int row = tid >> 2, part = tid & 3;
+    constexpr int XB = N / 32, IMG = kDC * N;
+    const int g = lane >> 4, row = 16 * rt + (lane & 15);
+    float v[XB][8];
+    float mx = 0.f, ss = 0.f;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            const IO *src = static_cast<const IO *>(m ? a.q : a.k) +
-                            ((bb * a.l + t0 + row) * a.g + gg) * N + part * Q4;
-            float v[Q4];
+    for (int kb = 0; kb < XB; ++kb) {
+        const IO *p = src + row * pitch + 32 * kb + 8 * g;
+        const f32x4 u = row < len ? ld4<IO>(p) : zero4(), w = row < len ? ld4<IO>(p + 4) : zero4();
 #pragma unroll
-            for (int i = 0; i < Q4; i += 4) {
-                const f32x4 w = row < len ? ld4<IO>(src + i) : zero4();
+        for (int e = 0; e < 4; ++e) v[kb][e] = u[e], v[kb][4 + e] = w[e];
+    }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[i + e] = w[e];
-            }
-            float mx = 0.f;
+    for (int kb = 0; kb < XB; ++kb)
 #pragma unroll
-            for (int i = 0; i < Q4; ++i) mx = fmaxf(mx, fabsf(v[i]));
-            mx = fmaxf(mx, __shfl_xor(mx, 1));
-            mx = fmaxf(mx, __shfl_xor(mx, 2));
-            // a power of two that brings the row's largest value into [1/2, 1)
-            const int e = (int)(__builtin_bit_cast(uint32_t, mx) >> 23) & 255;
-            const int f = mx == 0.f ? 127 : 253 - e < 1 ? 1 : 253 - e;
-            const float sc = __builtin_bit_cast(float, (uint32_t)f << 23);
-            const float back = __builtin_bit_cast(float, (uint32_t)(254 - f) << 23);
-            float ss = 0.f;
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[kb][e]));
+    mx = col_max(mx);
+    const int e = (int)(__builtin_bit_cast(uint32_t, mx) >> 23) & 255;
+    const int f = mx == 0.f ? 127 : 253 - e < 1 ? 1 : 253 - e;
+    const float sc = __builtin_bit_cast(float, (uint32_t)f << 23);
+    const float back = __builtin_bit_cast(float, (uint32_t)(254 - f) << 23);
 #pragma unroll
-            for (int i = 0; i < Q4; ++i) v[i] *= sc, ss = fmaf(v[i], v[i], ss);
-            ss += __shfl_xor(ss, 1);
-            ss += __shfl_xor(ss, 2);
-            // |row|^2 = ss / sc^2: the norm without leaving fp32's range
-            const float unit = ss > 0.f ? 1.f / sqrtf(fmaf(a.eps * sc, sc, ss)) : 0.f;
-            if (part == 0) {
-                fac[m][row] = a.norm ? unit : back;
-                rn[m][row] = a.norm ? unit * sc : 1.f;
-            }
+    for (int kb = 0; kb < XB; ++kb) {
 #pragma unroll
-            for (int i = 0; i < Q4; i += 4) {
-                const f16x2 h0 = __builtin_convertvector(f32x2{v[i], v[i + 1]}, f16x2);
-                const f16x2 h1 = __builtin_convertvector(f32x2{v[i + 2], v[i + 3]}, f16x2);
-                const int at = img_at(row, part * Q4 + i, XB);
-                *reinterpret_cast<f16x4 *>(&kq[m][at]) = f16x4{h0[0], h0[1], h1[0], h1[1]};
-                if constexpr (F32)
-                    *reinterpret_cast<f16x4 *>(&kq[m][IMG + at]) =
-                        f16x4{(f16)(v[i] - (float)h0[0]), (f16)(v[i + 1] - (float)h0[1]),
-                              (f16)(v[i + 2] - (float)h1[0]), (f16)(v[i + 3] - (float)h1[1])};
+        for (int i = 0; i < 8; ++i) v[kb][i] *= sc;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const f16x2 h = __builtin_convertvector(f32x2{v[kb][i], v[kb][i + 1]}, f16x2);
+            hi[kb][i] = h[0], hi[kb][i + 1] = h[1];
+            if constexpr (F32) {
+                lo[kb][i] = (f16)(v[kb][i] - (float)h[0]);
+                lo[kb][i + 1] = (f16)(v[kb][i + 1] - (float)h[1]);
             }
         }
     }
-    for (int i = tid; i < PPL * kPieces * 64; i += 256)
-        reinterpret_cast<u32x4 *>(&pst[0][0])[i] = u32x4{0, 0, 0, 0};
-    float step = 0.f;
-    if (wave == 0) {  // decays: a lane per token
-        const int64_t at = (bb * a.l + t0 + lane) * a.h + hh;
-        const bool in = lane < len;
-        double s = 0.0;
-        float be = 0.f;
-        if (in) {
-            step = time_step(to_f32(static_cast<const IO *>(a.dt)[at]), a.bias ? a.bias[hh] : 0.f,
-                             a.softplus, a.lo, a.hi);
-            // below -1e4 e^g is zero all the same, and sums of such steps stay finite
-            s = fmax((double)a.A[hh] * (double)step, -1e4) * 1.4426950408889634;
-            be = to_f32(static_cast<const IO *>(a.beta)[at]);
-        }
+    float factor = back, norm = 1.f;
+    if (a.norm) {
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const double u = __shfl_up(s, o);
-            if (lane >= o) s += u;
-        }
-        const double end = __shfl(s, 63);
-        bool cut = false;
-        if (a.seq && in && t0 + lane > 0) {
-            const int32_t *q = a.seq + bb * a.l + t0 + lane;
-            cut = q[0] != q[-1];
-        }
-        const uint64_t cuts = __ballot(cut);
-        const uint64_t upto = cuts & (~0ull >> (63 - lane));
-        ghi[lane] = (float)s;
-        glo[lane] = (float)(s - (double)(float)s);
-        doc[lane] = __popcll(upto);
-        bet[lane] = be;
-        rd[lane] = upto ? 0.f : exp2f((float)s);
-        wr[lane] = upto == cuts ? exp2f((float)(end - s)) : 0.f;
-        if (lane == 0)
-            a.rows[((ci * a.h + hh) * kRows + kCarry) * kDC] = cuts ? 0.f : exp2f((float)end);
-    }
-    __syncthreads();
-
-    if (hh % ratio == 0) {
-        f16 *dst[2] = {a.kimg + (ci * a.g + gg) * (PL * IMG), a.qimg + (ci * a.g + gg) * (PL * IMG)};
-        for (int i = tid; i < PL * IMG / 8; i += 256)
+        for (int kb = 0; kb < XB; ++kb)
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
-                reinterpret_cast<u32x4 *>(dst[m])[i] = reinterpret_cast<const u32x4 *>(kq[m])[i];
+            for (int i = 0; i < 8; ++i) ss = fmaf(v[kb][i], v[kb][i], ss);
+        ss += __shfl_xor(ss, 16);
+        ss += __shfl_xor(ss, 32);
+        // |row|^2 = ss / sc^2: the norm without leaving fp32's range
+        factor = ss > 0.f ? 1.f / sqrtf(fmaf(a.eps * sc, sc, ss)) : 0.f;
+        norm = factor * sc;
     }
-    if (tid < kDC) {
-        float *r = a.rows + (ci * a.h + hh) * kRows * kDC + tid;
-        r[kReadK * kDC] = rd[tid] * fac[0][tid];
-        r[kFk * kDC] = fac[0][tid];
-        r[kWriteK * kDC] = wr[tid] * fac[0][tid];
-        r[kReadQ * kDC] = a.scale * rd[tid] * fac[1][tid];
-        r[kFq * kDC] = a.scale * fac[1][tid];
-        r[kBeta * kDC] = bet[tid];
-        if constexpr (GRAD) {
-            float *e = a.rows2 + (ci * a.h + hh) * kRowsGrad * kDC + tid;
-            e[kGhi * kDC] = ghi[tid];
-            e[kGlo * kDC] = glo[tid];
-            e[kDoc * kDC] = (float)doc[tid];
-            e[kRead * kDC] = rd[tid];
-            e[kWrite * kDC] = wr[tid];
-            e[kRk * kDC] = rn[0][tid];
-            e[kRq * kDC] = rn[1][tid];
-            e[kStep * kDC] = step;
-        }
-    }
-
-    // row tile `wave` of K K^T and Q K^T, decayed and masked
-    for (int jt = 0; jt <= wave; ++jt) {
-        f32x4 kk = zero4(), qk = zero4();
+    if (g == 0) fac[row] = factor, rn[row] = norm;
+    if (img) {
+        // x = 8 g .. 8 g + 7 are two groups of four of the image's order
+        f16 *dst = img + (rt * XB * 64 + (lane & 15) + 16 * ((2 * g) & 3)) * 8 + 4 * (g >> 1);
 #pragma unroll
         for (int kb = 0; kb < XB; ++kb) {
-            const f16x8 kj = img_rows(kq[0], jt * XB + kb, lane);
-            const f16x8 ki = img_rows(kq[0], wave * XB + kb, lane);
-            const f16x8 qi = img_rows(kq[1], wave * XB + kb, lane);
-            kk = mma16(ki, kj, kk);
-            qk = mma16(qi, kj, qk);
+            const u32x4 w = __builtin_bit_cast(u32x4, hi[kb]);
+            *reinterpret_cast<u32x2 *>(dst + kb * 512) = u32x2{w[0], w[1]};
+            *reinterpret_cast<u32x2 *>(dst + kb * 512 + 128) = u32x2{w[2], w[3]};
             if constexpr (F32) {
-                const f16x8 lj = img_rows(kq[0] + IMG, jt * XB + kb, lane);
-                kk = mma16(ki, lj, kk);
-                qk = mma16(qi, lj, qk);
-                kk = mma16(img_rows(kq[0] + IMG, wave * XB + kb, lane), kj, kk);
-                qk = mma16(img_rows(kq[1] + IMG, wave * XB + kb, lane), kj, qk);
+                const u32x4 z = __builtin_bit_cast(u32x4, lo[kb]);
+                *reinterpret_cast<u32x2 *>(dst + IMG + kb * 512) = u32x2{z[0], z[1]};
+                *reinterpret_cast<u32x2 *>(dst + IMG + kb * 512 + 128) = u32x2{z[2], z[3]};
             }
         }
-        const int j = 16 * jt + j16;
-        const float hj = ghi[j], lj = glo[j], fj = fac[0][j];
-        const int dj = doc[j];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int i = 16 * wave + 4 * g + r;
-            const bool in = j <= i && doc[i] == dj;
-            const float d = in ? exp2f((ghi[i] - hj) + (glo[i] - lj)) : 0.f;
-            tri[0][i * kTP + j] = j < i ? kk[r] * d * (fac[0][i] * fj) : 0.f;
-            const float p = qk[r] * d;
-            const f16 h = (f16)p;
-            const int at = tri_piece(wave, jt >> 1) * 512 + (4 * g + r + 16 * (j16 >> 2)) * 8 +
-                           4 * (jt & 1) + (j16 & 3);
-            pst[0][at] = h;
-            if constexpr (PPL == 2) pst[1][at] = (f16)(p - (float)h);
-        }
     }
-    __syncthreads();
+}
 
-    // the inverses' diagonal blocks: column j16, lane group 0 of T, group 1 of
-    // (I + beta kk)^-1
-    if (g < NT) {
-        float x[16];
-        const float *K = tri[0] + 16 * wave * kTP + 16 * wave;
-        const float *be = bet + 16 * wave;
+__device__ __forceinline__ constexpr int tri_tile(int i, int j) { return i * (i + 1) / 2 + j; }
+
+// exp2 of a double, by its value in two floats.
+__device__ __forceinline__ float exp2_d(double x) {
+    const float h = (float)x, e = exp2f(h);
+    return fmaf(e, (float)(x - (double)h) * 0.69314718f, e);
+}
+
+// A wave takes one chunk and `hs` heads of one group, without a barrier: the
+// group's K K^T and Q K^T stay in its registers, transposed (lane: token i = lane
+// & 15 of a tile, four consecutive j), which is the form of the triangle's rows
+// both as an operand of the inverse's products and in the image.
+template <typename IO, int N, bool GRAD>
+__global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
+    constexpr bool F32 = sizeof(IO) == 4;
+    constexpr int PL = F32 ? 2 : 1, XB = N / 32, IMG = kDC * N;
+    constexpr int NT = GRAD ? 2 : 1;          // inverses: T, and (I + beta kk)^-1
+    constexpr int PPL = F32 || GRAD ? 2 : 1;  // terms of tril(Q K^T)
+    __shared__ PrepLds all[4];
+    const int lane = threadIdx.x & 63, wave = wave_id(), g = lane >> 4, j16 = lane & 15;
+    PrepLds &L = all[wave];
+    const int ratio = (int)(a.h / a.g), parts = ratio / hs;
+    int64_t item = xcd_item(blockIdx.x, gridDim.x) * 4 + wave;
+    if (item >= a.b * a.nc * a.g * parts) return;
+    const int part = (int)(item % parts);
+    item /= parts;
+    const int64_t gg = item % a.g, ci = item / a.g, c = ci % a.nc, bb = ci / a.nc, t0 = c * kDC;
+    const int len = (int)(a.l - t0 < kDC ? a.l - t0 : kDC);
+    const int64_t row0 = ((bb * a.l + t0) * a.g + gg) * N, pitch = a.g * N;
+
+    f32x4 kk[10], qk[10];
+    {
+        f16x8 kh[4][XB], kl[4][XB], qh[XB], ql[XB];
+        f16 *kimg = part ? nullptr : a.kimg + item * (PL * IMG);
+        f16 *qimg = part ? nullptr : a.qimg + item * (PL * IMG);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            float s = 0.f;
+        for (int rt = 0; rt < 4; ++rt)
+            load_tile<IO, N>(a, static_cast<const IO *>(a.k) + row0, pitch, rt, len, L.fac[0], L.rn[0],
+                             kimg, kh[rt], kl[rt], lane);
 #pragma unroll
-            for (int k = 0; k < i; ++k) s = fmaf(K[i * kTP + k], g == 0 ? be[k] * x[k] : x[k], s);
-            x[i] = (i == j16 ? 1.f : 0.f) - (g == 0 ? s : be[i] * s);
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int jt = 0; jt <= it; ++jt) {
+                f32x4 t = zero4();
+#pragma unroll
+                for (int kb = 0; kb < XB; ++kb) {
+                    t = mma16(kh[jt][kb], kh[it][kb], t);
+                    if constexpr (F32) {
+                        t = mma16(kh[jt][kb], kl[it][kb], t);
+                        t = mma16(kl[jt][kb], kh[it][kb], t);
+                    }
+                }
+                kk[tri_tile(it, jt)] = t;
+            }
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            load_tile<IO, N>(a, static_cast<const IO *>(a.q) + row0, pitch, it, len, L.fac[1], L.rn[1],
+                             qimg, qh, ql, lane);
+#pragma unroll
+            for (int jt = 0; jt <= it; ++jt) {
+                f32x4 t = zero4();
+#pragma unroll
+                for (int kb = 0; kb < XB; ++kb) {
+                    t = mma16(kh[jt][kb], qh[kb], t);
+                    if constexpr (F32) {
+                        t = mma16(kh[jt][kb], ql[kb], t);
+                        t = mma16(kl[jt][kb], qh[kb], t);
+                    }
+                }
+                qk[tri_tile(it, jt)] = t;
+            }
         }
-        float *o = (NT == 1 || g == 0 ? tri[1] : tri[NT]) + 16 * wave * kTP + 16 * wave + j16;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[i * kTP] = x[i];
     }
-    __syncthreads();
-    for (int d = 1; d < 4; ++d) {
-        for (int task = wave; task < NT * (4 - d); task += 4) {
-            const int m = task / (4 - d), j = task % (4 - d), i = j + d;
-            float *T = tri[1 + m];
-            f32x4 x = zero4();
-            for (int k = j; k < i; ++k) {
-                const f32x4 ka =
-                    *reinterpret_cast<const f32x4 *>(tri[0] + (16 * i + j16) * kTP + 16 * k + 4 * g);
+    for (int64_t hh = gg * ratio + part * hs; hh < gg * ratio + (part + 1) * hs; ++hh) {
+        const int64_t hi = ci * a.h + hh;
+        // decays: a lane per token
+        {
+            const int64_t at = (bb * a.l + t0 + lane) * a.h + hh;
+            const bool in = lane < len;
+            double s = 0.0;
+            float be = 0.f, step = 0.f;
+            if (in) {
+                step = time_step(to_f32(static_cast<const IO *>(a.dt)[at]), a.bias ? a.bias[hh] : 0.f,
+                                 a.softplus, a.lo, a.hi);
+                // below -1e4 e^g is zero all the same, and sums of such steps stay finite
+                s = fmax((double)a.A[hh] * (double)step, -1e4) * 1.4426950408889634;
+                be = to_f32(static_cast<const IO *>(a.beta)[at]);
+            }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int kr = 16 * k + 4 * g + q;
-                    const float t = T[kr * kTP + 16 * j + j16];
-                    x = Mfma<float>::mma(ka[q], m == 0 ? bet[kr] * t : t, x);
+            for (int o = 1; o < 64; o <<= 1) {
+                const double u = __shfl_up(s, o);
+                if (lane >= o) s += u;
+            }
+            const double end = __shfl(s, 63);
+            bool cut = false;
+            if (a.seq && in && t0 + lane > 0) {
+                const int32_t *q = a.seq + bb * a.l + t0 + lane;
+                cut = q[0] != q[-1];
+            }
+            const uint64_t cuts = __ballot(cut);
+            const uint64_t upto = cuts & (~0ull >> (63 - lane));
+            const float gh = (float)s, gl = (float)(s - (double)gh), doc = (float)__popcll(upto);
+            const float rd = upto ? 0.f : exp2_d(s), wr = upto == cuts ? exp2_d(end - s) : 0.f;
+            wave_fence();
+            L.ghi[lane] = gh, L.glo[lane] = gl, L.doc[lane] = doc, L.bet[lane] = be;
+            const float fk = L.fac[0][lane], fq = L.fac[1][lane];
+            float *r = a.rows + hi * (kRows * kDC) + lane;
+            r[kReadK * kDC] = rd * fk;
+            r[kFk * kDC] = fk;
+            r[kWriteK * kDC] = wr * fk;
+            r[kReadQ * kDC] = a.scale * rd * fq;
+            r[kFq * kDC] = a.scale * fq;
+            r[kBeta * kDC] = be;
+            if (lane == 0) r[kCarry * kDC] = cuts ? 0.f : exp2_d(end);
+            if constexpr (GRAD) {
+                float *e = a.rows2 + hi * (kRowsGrad * kDC) + lane;
+                e[kGhi * kDC] = gh;
+                e[kGlo * kDC] = gl;
+                e[kDoc * kDC] = doc;
+                e[kRead * kDC] = rd;
+                e[kWrite * kDC] = wr;
+                e[kRk * kDC] = L.rn[0][lane];
+                e[kRq * kDC] = L.rn[1][lane];
+                e[kStep * kDC] = step;
+            }
+            wave_fence();
+        }
+        // decays and masks on both triangles
+        f32x4 A[10];
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int i = 16 * it + j16;
+            const float gi = L.ghi[i], li = L.glo[i], di = L.doc[i], fi = L.fac[0][i];
+            f32x4 pq[4];
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt) {
+                pq[jt] = zero4();
+                if (jt > it) continue;
+                const f32x4 gj = row4(L.ghi, 0, jt, lane), lj = row4(L.glo, 0, jt, lane),
+                            dj = row4(L.doc, 0, jt, lane), fj = row4(L.fac[0], 0, jt, lane);
+                f32x4 d;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bool in = dj[r] == di && (jt < it || 4 * g + r <= j16);
+                    d[r] = in ? exp2f((gi - gj[r]) + (li - lj[r])) : 0.f;
+                    const float k = kk[tri_tile(it, jt)][r] * d[r] * (fi * fj[r]);
+                    A[tri_tile(it, jt)][r] = jt < it || 4 * g + r < j16 ? k : 0.f;
+                    pq[jt][r] = qk[tri_tile(it, jt)][r] * d[r];
                 }
             }
-            if (m == 1)
+            f16 *dst = a.pimg + hi * (PPL * kPieces * 512) + lane * 8;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] *= bet[16 * i + 4 * g + r];
-            const f32x4 ti =
-                *reinterpret_cast<const f32x4 *>(T + (16 * i + j16) * kTP + 16 * i + 4 * g);
-            f32x4 o = zero4();
-#pragma unroll
-            for (int q = 0; q < 4; ++q) o = Mfma<float>::mma(ti[q], x[q], o);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) T[(16 * i + 4 * g + r) * kTP + 16 * j + j16] = -o[r];
+            for (int kb = 0; kb <= it / 2; ++kb) {
+                const Split s = split8(pq[2 * kb], pq[2 * kb + 1], 1.f);
+                *reinterpret_cast<f16x8 *>(dst + tri_piece(it, kb) * 512) = s.hi;
+                if constexpr (PPL == 2)
+                    *reinterpret_cast<f16x8 *>(dst + (kPieces + tri_piece(it, kb)) * 512) = s.lo;
+            }
+            *reinterpret_cast<f32x4 *>(&L.A[it][j16 * kDP + 4 * g]) = A[tri_tile(it, it)];
         }
-        __syncthreads();
+        f32x4 be[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) be[t] = row4(L.bet, 0, t, lane);
+#pragma unroll
+        for (int m = 0; m < NT; ++m) {
+            // diagonal blocks: block g, column j16
+            wave_fence();
+            float x[16];
+            const float *K = L.A[g], *bt = L.bet + 16 * g;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float s = 0.f;
+#pragma unroll
+                for (int k = 0; k < i; ++k) s = fmaf(K[i * kDP + k], m == 0 ? bt[k] * x[k] : x[k], s);
+                x[i] = (i == j16 ? 1.f : 0.f) - (m == 0 ? s : bt[i] * s);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) L.X[g][i * kDP + j16] = x[i];
+            wave_fence();
+            // the others by their distance from it
+            f32x4 T[10], ti[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                ti[t] = *reinterpret_cast<const f32x4 *>(&L.X[t][j16 * kDP + 4 * g]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) T[tri_tile(t, t)][r] = L.X[t][(4 * g + r) * kDP + j16];
+            }
+#pragma unroll
+            for (int d = 1; d < 4; ++d)
+#pragma unroll
+                for (int j = 0; j < 4 - d; ++j) {
+                    const int i = j + d;
+                    f32x4 y = zero4(), o = zero4();
+#pragma unroll
+                    for (int k = j; k < i; ++k)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float t = T[tri_tile(k, j)][q];
+                            y = Mfma<float>::mma(A[tri_tile(i, k)][q], m == 0 ? be[k][q] * t : t, y);
+                        }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        o = Mfma<float>::mma(ti[i][q], m == 0 ? -y[q] : -be[i][q] * y[q], o);
+                    T[tri_tile(i, j)] = o;
+                }
+            f16 *dst = (m ? a.mimg : a.timg) + hi * (2 * kPieces * 512) + lane * 8;
+#pragma unroll
+            for (int jt = 0; jt < 4; ++jt)
+#pragma unroll
+                for (int ib = jt / 2; ib < 2; ++ib) {
+                    const f32x4 up = jt > 2 * ib ? zero4() : T[tri_tile(2 * ib, jt > 2 * ib ? 0 : jt)];
+                    const Split s = split8(up, T[tri_tile(2 * ib + 1, jt)], 1.f);
+                    *reinterpret_cast<f16x8 *>(dst + tri_piece_t(jt, ib) * 512) = s.hi;
+                    *reinterpret_cast<f16x8 *>(dst + (kPieces + tri_piece_t(jt, ib)) * 512) = s.lo;
+                }
+        }
     }
-
-    // images of the triangles
-    f16 *tdst = a.timg + (ci * a.h + hh) * (2 * kPieces * 512);
-    f16 *mdst = GRAD ? a.mimg + (ci * a.h + hh) * (2 * kPieces * 512) : nullptr;
-    for (int i = tid; i < NT * kPieces * 64; i += 256) {
-        const int m = i / (kPieces * 64), piece = (i >> 6) % kPieces, ln = i & 63;
-        const int rt = piece < 2 ? piece : 2 + ((piece - 2) >> 1), kb = piece < 2 ? 0 : (piece & 1);
-        const float *src = tri[1 + m] + (16 * rt + (ln & 15)) * kTP + 32 * kb + 4 * (ln >> 4);
-        const f32x4 u = *reinterpret_cast<const f32x4 *>(src);
-        const f32x4 w = 2 * kb + 1 <= rt ? *reinterpret_cast<const f32x4 *>(src + 16) : zero4();
-        const Split s = split8(u, w, 1.f);
-        f16 *dst = (m ? mdst : tdst) + piece * 512 + ln * 8;
-        *reinterpret_cast<f16x8 *>(dst) = s.hi;
-        *reinterpret_cast<f16x8 *>(dst + kPieces * 512) = s.lo;
-    }
-    f16 *pdst = a.pimg + (ci * a.h + hh) * (PPL * kPieces * 512);
-    for (int i = tid; i < PPL * kPieces * 64; i += 256)
-        reinterpret_cast<u32x4 *>(pdst)[i] = reinterpret_cast<const u32x4 *>(&pst[0][0])[i];
 }
 
 // --------------------------------------------------------------- forward ---
@@ -412,10 +476,11 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
             f32x4 t = zero4();
 #pragma unroll
             for (int tb = 0; tb <= rt / 2; ++tb) {
-                const f16x8 th = img_rows(T, tri_piece(rt, tb), lane);
+                const int p0 = tri_piece_t(2 * tb, rt >> 1), p1 = tri_piece_t(2 * tb + 1, rt >> 1);
+                const f16x8 th = img_cols(T, p0, p1, rt, lane);
                 t = mma16(th, rf[tb].hi, t);
                 t = mma16(th, rf[tb].lo, t);
-                t = mma16(img_rows(T + kPieces * 512, tri_piece(rt, tb), lane), rf[tb].hi, t);
+                t = mma16(img_cols(T + kPieces * 512, p0, p1, rt, lane), rf[tb].hi, t);
             }
             const f32x4 be = row4(rows, kBeta, rt, lane), fk = row4(rows, kFk, rt, lane),
                         wk = row4(rows, kWriteK, rt, lane);
@@ -568,11 +633,15 @@ hipError_t run_fwd(const DeltaArgs &a, hipStream_t s) {
 }
 
 template <typename IO, int N> hipError_t prep_n(const DeltaArgs &a, bool grad, hipStream_t s) {
-    const dim3 grid((unsigned)(a.b * a.nc * a.h)), block(256);
+    // heads of a wave: as many of a group as leave eight waves to a compute unit
+    const int64_t groups = a.b * a.nc * a.g, ratio = a.h / a.g;
+    int64_t hs = ratio;
+    while (hs > 1 && (ratio % hs || groups * (ratio / hs) < 8 * device_cus())) --hs;
+    const dim3 grid((unsigned)((groups * (ratio / hs) + 3) / 4)), block(256);
     if (grad)
-        hipLaunchKernelGGL((k_delta_prep<IO, N, true>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((k_delta_prep<IO, N, true>), grid, block, 0, s, a, (int)hs);
     else
-        hipLaunchKernelGGL((k_delta_prep<IO, N, false>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((k_delta_prep<IO, N, false>), grid, block, 0, s, a, (int)hs);
     return hipGetLastError();
 }
 
