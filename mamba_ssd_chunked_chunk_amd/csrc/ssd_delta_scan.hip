@@ -38,26 +38,58 @@ struct alignas(16) PrepLds {
     float ghi[kDC], glo[kDC], doc[kDC], bet[kDC];
 };
 
-// A 16-row tile of k or q as operand fragments (contraction over x in the order
-// of memory, lane group g the eight from 8 g on): brings each row's largest
-// value into [1/2, 1) by a power of two, leaves the row's factors in LDS and, if
-// asked, the fragments in the image.
+// A 16-row tile of k or q as it is in memory, a fragment (contraction over x in
+// the order of memory, lane group g the eight from 8 g on) per 32 columns.
+template <typename IO, int N> struct RawTile { u32x4 e[N / 32][sizeof(IO) / 2]; };
+
 template <typename IO, int N>
-__device__ __forceinline__ void load_tile(const DeltaArgs &a, const IO *src, int64_t pitch, int rt,
-                                          int len, float *fac, float *rn, f16 *img, f16x8 (&hi)[N / 32],
-                                          f16x8 (&lo)[N / 32], int lane) {
+__device__ __forceinline__ void fetch_tile(RawTile<IO, N> &t, const IO *src, int64_t pitch, int rt,
+                                           int len, int lane) {
+    const int row = 16 * rt + (lane & 15);
+    const IO *p = src + row * pitch + 8 * (lane >> 4);
+#pragma unroll
+    for (int kb = 0; kb < N / 32; ++kb)
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(IO) / 2; ++i) {
+            t.e[kb][i] = u32x4{0, 0, 0, 0};
+            if (row < len)
+                t.e[kb][i] = *reinterpret_cast<const u32x4 *>(p + 32 * kb + i * (16 / sizeof(IO)));
+        }
+}
+template <int N>
+__device__ __forceinline__ void widen(const RawTile<bf16, N> &t, float (&v)[N / 32][8]) {
+#pragma unroll
+    for (int kb = 0; kb < N / 32; ++kb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = t.e[kb][0][i];
+            v[kb][2 * i] = __builtin_bit_cast(float, w << 16);
+            v[kb][2 * i + 1] = __builtin_bit_cast(float, w & 0xffff0000u);
+        }
+}
+template <int N>
+__device__ __forceinline__ void widen(const RawTile<float, N> &t, float (&v)[N / 32][8]) {
+#pragma unroll
+    for (int kb = 0; kb < N / 32; ++kb)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w = t.e[kb][i >> 2][i & 3];
+            v[kb][i] = __builtin_bit_cast(float, w);
+        }
+}
+
+// Brings each row's largest value into [1/2, 1) by a power of two, leaves the
+// row's factors in LDS and, if asked, the fragments in the image.
+template <typename IO, int N>
+__device__ __forceinline__ void use_tile(const DeltaArgs &a, const RawTile<IO, N> &raw, int rt,
+                                         float *fac, float *rn, f16 *img, f16x8 (&hi)[N / 32],
+                                         f16x8 (&lo)[N / 32], int lane) {
     constexpr bool F32 = sizeof(IO) == 4;
     constexpr int XB = N / 32, IMG = kDC * N;
     const int g = lane >> 4, row = 16 * rt + (lane & 15);
     float v[XB][8];
+    widen<N>(raw, v);
     float mx = 0.f, ss = 0.f;
-#pragma unroll
-    for (int kb = 0; kb < XB; ++kb) {
-        const IO *p = src + row * pitch + 32 * kb + 8 * g;
-        const f32x4 u = row < len ? ld4<IO>(p) : zero4(), w = row < len ? ld4<IO>(p + 4) : zero4();
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[kb][e] = u[e], v[kb][4 + e] = w[e];
-    }
 #pragma unroll
     for (int kb = 0; kb < XB; ++kb)
 #pragma unroll
@@ -146,10 +178,17 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
         f16x8 kh[4][XB], kl[4][XB], qh[XB], ql[XB];
         f16 *kimg = part ? nullptr : a.kimg + item * (PL * IMG);
         f16 *qimg = part ? nullptr : a.qimg + item * (PL * IMG);
+        const IO *ks = static_cast<const IO *>(a.k) + row0, *qs = static_cast<const IO *>(a.q) + row0;
+        // all of k in flight at once, and of q what the registers hold beside it
+        RawTile<IO, N> kr[4], qr[4];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) fetch_tile<IO, N>(kr[rt], ks, pitch, rt, len, lane);
+#pragma unroll
+        for (int rt = 0; rt < (F32 ? 1 : 4); ++rt) fetch_tile<IO, N>(qr[rt], qs, pitch, rt, len, lane);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
-            load_tile<IO, N>(a, static_cast<const IO *>(a.k) + row0, pitch, rt, len, L.fac[0], L.rn[0],
-                             kimg, kh[rt], kl[rt], lane);
+            use_tile<IO, N>(a, kr[rt], rt, L.fac[0], L.rn[0], kimg, kh[rt], kl[rt], lane);
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
@@ -167,8 +206,8 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
             }
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-            load_tile<IO, N>(a, static_cast<const IO *>(a.q) + row0, pitch, it, len, L.fac[1], L.rn[1],
-                             qimg, qh, ql, lane);
+            if (F32 && it < 3) fetch_tile<IO, N>(qr[it + 1], qs, pitch, it + 1, len, lane);
+            use_tile<IO, N>(a, qr[it], it, L.fac[1], L.rn[1], qimg, qh, ql, lane);
 #pragma unroll
             for (int jt = 0; jt <= it; ++jt) {
                 f32x4 t = zero4();
@@ -255,7 +294,8 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const bool in = dj[r] == di && (jt < it || 4 * g + r <= j16);
-                    d[r] = in ? exp2f((gi - gj[r]) + (li - lj[r])) : 0.f;
+                    const float e = exp2_fast((gi - gj[r]) + (li - lj[r]));
+                    d[r] = in ? e : 0.f;
                     const float k = kk[tri_tile(it, jt)][r] * d[r] * (fi * fj[r]);
                     A[tri_tile(it, jt)][r] = jt < it || 4 * g + r < j16 ? k : 0.f;
                     pq[jt][r] = qk[tri_tile(it, jt)][r] * d[r];
@@ -278,14 +318,16 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
         for (int m = 0; m < NT; ++m) {
             // diagonal blocks: block g, column j16
             wave_fence();
-            float x[16];
+            float x[16], bx[16];
             const float *K = L.A[g], *bt = L.bet + 16 * g;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                float s = 0.f;
+                float s[2] = {0.f, 0.f};  // two chains
 #pragma unroll
-                for (int k = 0; k < i; ++k) s = fmaf(K[i * kDP + k], m == 0 ? bt[k] * x[k] : x[k], s);
-                x[i] = (i == j16 ? 1.f : 0.f) - (m == 0 ? s : bt[i] * s);
+                for (int k = 0; k < i; ++k) s[k & 1] = fmaf(K[i * kDP + k], bx[k], s[k & 1]);
+                const float v = s[0] + s[1];
+                x[i] = (i == j16 ? 1.f : 0.f) - (m == 0 ? v : bt[i] * v);
+                bx[i] = m == 0 ? bt[i] * x[i] : x[i];
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) L.X[g][i * kDP + j16] = x[i];
