@@ -147,7 +147,7 @@ __global__ void k_delta_copy(float *dst, const float *src, int64_t n) {
 // ------------------------------------------------------------- workspace ---
 struct DeltaWs {
     size_t total = 0;
-    size_t kimg, qimg, timg, mimg, pimg, rows, rows2, nimg, nlow, zimg, simg, dsimg, doo, dvv, dzn,
+    size_t gimg, himg, rows2, nimg, nlow, zimg, simg, dsimg, doo, dvv, dzn,
         eend, part, states;
     size_t add(size_t bytes) {
         const size_t at = total;
@@ -158,14 +158,11 @@ struct DeltaWs {
             bool keep) {
         const size_t el = io == SSD_BF16 ? 2 : 4, planes = el / 2;
         const size_t nc = (size_t)((l + kDC - 1) / kDC), ch = b * nc * h, cg = b * nc * g;
-        kimg = add(cg * planes * kDC * n * 2);
-        qimg = add(cg * planes * kDC * n * 2);
-        timg = add(ch * 2 * kPieces * 1024);
-        pimg = add(ch * (grad ? 2 : planes) * kPieces * 1024);
-        rows = add(ch * kRows * kDC * 4);
-        mimg = rows2 = nimg = nlow = zimg = simg = dsimg = doo = dvv = dzn = eend = part = states = 0;
+        const size_t tri = kPieces * 1024;
+        gimg = add(cg * 2 * planes * kDC * n * 2);
+        himg = add(ch * (2 * tri + kRows * kDC * 4 + (grad ? 4 : planes) * tri));
+        rows2 = nimg = nlow = zimg = simg = dsimg = doo = dvv = dzn = eend = part = states = 0;
         if (!grad) return;
-        mimg = add(ch * 2 * kPieces * 1024);
         rows2 = add(ch * kRowsGrad * kDC * 4);
         nimg = add(ch * kDC * p * el);
         nlow = add(io == SSD_BF16 ? ch * kDC * p * el : 0);
@@ -180,13 +177,8 @@ struct DeltaWs {
         if (keep) states = add(ch * n * p * 4);
     }
     void set(DeltaArgs &a, char *ws, bool grad) const {
-        a.kimg = reinterpret_cast<f16 *>(ws + kimg);
-        a.qimg = reinterpret_cast<f16 *>(ws + qimg);
-        a.timg = reinterpret_cast<f16 *>(ws + timg);
-        a.pimg = reinterpret_cast<f16 *>(ws + pimg);
-        a.rows = reinterpret_cast<float *>(ws + rows);
+        a.gimg = ws + gimg, a.himg = ws + himg;
         if (!grad) return;
-        a.mimg = reinterpret_cast<f16 *>(ws + mimg);
         a.rows2 = reinterpret_cast<float *>(ws + rows2);
         a.nimg = ws + nimg, a.nlow = ws + nlow, a.zimg = ws + zimg, a.simg = ws + simg, a.dsimg = ws + dsimg;
         a.doo = reinterpret_cast<float *>(ws + doo);

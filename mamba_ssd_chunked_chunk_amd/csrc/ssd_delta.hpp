@@ -84,8 +84,8 @@ struct DeltaArgs {
     void *dq, *dk, *dv, *ddt, *dbeta;
     float *dA, *dbias, *dinit;
     // workspace
-    f16 *kimg, *qimg, *timg, *mimg, *pimg;
-    float *rows, *rows2;
+    char *gimg, *himg;  // GroupImg, HeadImg
+    float *rows2;
     void *nimg, *nlow, *zimg, *simg, *dsimg;
     float *doo, *dvv, *dzn, *eend;
     double *part;
@@ -187,6 +187,19 @@ __device__ __forceinline__ Split split8(const f32x4 &a, const f32x4 &b, float sc
     return s;
 }
 
+// One row tile's share of such fragments in LDS ([hi, lo][2 blocks of 32 rows][lane][8]).
+template <bool LO = true>
+__device__ __forceinline__ void put_half(f16 *dst, const f32x4 &v, float sc, int rt, int lane) {
+    const f16x2 h0 = __builtin_convertvector(f32x2{v[0] * sc, v[1] * sc}, f16x2);
+    const f16x2 h1 = __builtin_convertvector(f32x2{v[2] * sc, v[3] * sc}, f16x2);
+    f16 *p = dst + ((rt >> 1) * 64 + lane) * 8 + 4 * (rt & 1);
+    *reinterpret_cast<f16x4 *>(p) = f16x4{h0[0], h0[1], h1[0], h1[1]};
+    if constexpr (LO)
+        *reinterpret_cast<f16x4 *>(p + 1024) =
+            f16x4{(f16)fmaf(v[0], sc, -(float)h0[0]), (f16)fmaf(v[1], sc, -(float)h0[1]),
+                  (f16)fmaf(v[2], sc, -(float)h1[0]), (f16)fmaf(v[3], sc, -(float)h1[1])};
+}
+
 // Largest value over the four lane groups that share a column.  (The swaps'
 // results go through scalars: the compiler takes a bit cast of a vector's
 // element as one of its first element.)
@@ -217,17 +230,56 @@ __device__ __forceinline__ float sum16(float v) {
     return dpp_add<0x121>(v);
 }
 
-// lds_dma16 of ssd_device.hpp with the LDS address as a number.
-__device__ __forceinline__ void lds_dma16_at(RsrcW r, uint32_t dst, uint32_t voff) {
+// lds_dma16 of ssd_device.hpp with the LDS address as a number (uniform, as the
+// scalar offset is).
+__device__ __forceinline__ void lds_dma16_at(RsrcW r, uint32_t dst, uint32_t voff, uint32_t soff) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff),
-                 "s"(r), "s"(__builtin_amdgcn_readfirstlane(dst))
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds" ::"v"(
+                     voff),
+                 "s"(r), "s"(dst), "s"(soff)
                  : "memory", "m0");
 #else
-    (void)r, (void)dst, (void)voff;
+    (void)r, (void)dst, (void)voff, (void)soff;
 #endif
 }
 __device__ __forceinline__ uint32_t lds_address(char *p) { return (uint32_t)(uintptr_t)(lds_void *)p; }
+
+// What k_delta_prep leaves of a chunk and group (k and q, in PL terms each), and
+// of a chunk and head (T, the row arrays, tril(Q K^T) in PPL terms and, for the
+// gradient, (I + beta kk)^-1): the scans copy a range of the latter at once.
+template <typename IO, int N> struct GroupImg {
+    static constexpr int PL = sizeof(IO) / 2, Q = PL * kDC * N * 2, BYTES = 2 * Q;
+};
+template <typename IO, bool GRAD> struct HeadImg {
+    static constexpr int TRI = kPieces * 1024, PPL = sizeof(IO) == 4 || GRAD ? 2 : 1;
+    static constexpr int T = 0, R = 2 * TRI, P = R + kRows * kDC * 4, M = P + PPL * TRI;
+    static constexpr int BYTES = M + (GRAD ? 2 * TRI : 0);
+};
+
+// Values that are the same in every lane, told to the compiler once (what comes
+// out of a 64-bit division is in vector registers).
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const char *uni(const void *p) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a);
+    const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+    return reinterpret_cast<const char *>(hi << 32 | lo);
+}
+
+__device__ __forceinline__ RsrcW uniform_rsrc(const void *base, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    return RsrcW{(uint32_t)a, (uint32_t)(a >> 32) & 0xffffu, bytes, (uint32_t)kRsrcWord3};
+}
+
+// BYTES (a multiple of 1024) of contiguous memory into LDS, a run of them by each
+// of `nw` waves.
+template <int BYTES>
+__device__ __forceinline__ void copy_image(const char *src, uint32_t dst, int wave, int nw, int lane) {
+    constexpr int CNT = BYTES >> 10;
+    const RsrcW r = uniform_rsrc(src, BYTES);
+    for (int i = wave * CNT / nw; i < (wave + 1) * CNT / nw; ++i)
+        lds_dma16_at(r, dst + (i << 10), (uint32_t)(lane * 16), (uint32_t)(i << 10));
+}
 
 // `bytes` of contiguous memory into LDS by `nw` waves, and zeros up to `all` (a
 // multiple of 1024).
@@ -235,19 +287,19 @@ __device__ __forceinline__ void copy_lds(const void *src, int bytes, int all, ui
                                          int nw, int lane) {
     const RsrcW r = make_rsrc_w(src, bytes);
     for (int i = wave; i < all >> 10; i += nw)
-        lds_dma16_at(r, dst + (i << 10), (uint32_t)((i << 10) + lane * 16));
+        lds_dma16_at(r, dst + (i << 10), (uint32_t)((i << 10) + lane * 16), 0);
 }
 
-// 64 rows of `rb` bytes (a multiple of 32), `pitch` bytes apart in memory, into
-// LDS without gaps; rows from `len` on as zeros.
-__device__ __forceinline__ void copy_rows(const void *src, int64_t pitch, int rb, int len,
+// 64 rows of `rb` bytes (a power of two from 32 on), `pitch` bytes apart in
+// memory, into LDS without gaps.  Rows from `len` on lie beyond the resource and
+// come as zeros.
+__device__ __forceinline__ void copy_rows(const char *src, uint32_t pitch, int rb, int len,
                                           uint32_t dst, int wave, int nw, int lane) {
-    const RsrcW r = make_rsrc_w(src, (len - 1) * pitch + rb);
-    const int per = rb >> 4;  // 16-byte parts of a row
-    for (int i = wave; i < (64 * rb) >> 10; i += nw) {
-        const int part = i * 64 + lane, row = part / per;
-        const uint32_t off = row < len ? (uint32_t)(row * pitch + (part - row * per) * 16) : 0xf0000000u;
-        lds_dma16_at(r, dst + (i << 10), off);
+    const RsrcW r = uniform_rsrc(src, (uint32_t)(len - 1) * pitch + rb);
+    const int sh = 27 - __builtin_clz(rb);  // log2 of the 16-byte parts of a row
+    for (int i = wave; i < rb >> 4; i += nw) {
+        const int part = i * 64 + lane;
+        lds_dma16_at(r, dst + (i << 10), (part >> sh) * pitch + (part & ((1 << sh) - 1)) * 16, 0);
     }
 }
 

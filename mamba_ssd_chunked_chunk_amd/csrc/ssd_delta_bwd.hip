@@ -25,31 +25,40 @@ namespace {
 constexpr int kLdsMost = 160 * 1024;
 
 template <typename IO, int N> struct RevBuf {
-    static constexpr int PL = sizeof(IO) == 4 ? 2 : 1;
-    static constexpr int K = 0, Q = PL * kDC * N * 2, M = 2 * Q, P = M + 2 * kPieces * 1024;
-    static constexpr int R = P + 2 * kPieces * 1024, V = R + kRows * kDC * 4;
+    typedef GroupImg<IO, N> G;
+    typedef HeadImg<IO, true> H;
+    static constexpr int K = 0, Q = G::Q, HEAD = H::BYTES - H::R;  // from the row arrays on
+    static constexpr int R = G::BYTES, P = R + H::P - H::R, M = R + H::M - H::R, V = R + HEAD;
     static __host__ __device__ int bytes(int cols) { return V + 2 * kDC * cols * (int)sizeof(IO); }
 };
 
-template <typename IO, int N>
-__device__ __forceinline__ void rev_copy(const DeltaArgs &a, uint32_t buf, int64_t bb, int64_t c,
-                                         int64_t hh, int col0, int cols, int wave, int nw, int lane) {
+// Where a chunk's operands of one head and `cols` columns are; back() moves to
+// the chunk in front.
+template <typename IO, int N> struct RevSrc {
     typedef RevBuf<IO, N> B;
-    const int64_t ci = bb * a.nc + c, gi = ci * a.g + hh / (a.h / a.g), hi = ci * a.h + hh;
-    const int64_t t0 = c * kDC;
-    const int len = (int)(a.l - t0 < kDC ? a.l - t0 : kDC);
-    copy_lds(a.kimg + gi * (B::PL * kDC * N), B::Q, B::Q, buf + B::K, wave, nw, lane);
-    copy_lds(a.qimg + gi * (B::PL * kDC * N), B::Q, B::Q, buf + B::Q, wave, nw, lane);
-    copy_lds(a.mimg + hi * (2 * kPieces * 512), 2 * kPieces * 1024, 2 * kPieces * 1024, buf + B::M, wave, nw, lane);
-    copy_lds(a.pimg + hi * (2 * kPieces * 512), 2 * kPieces * 1024, 2 * kPieces * 1024, buf + B::P, wave, nw, lane);
-    copy_lds(a.rows + hi * (kRows * kDC), kRows * kDC * 4, kRows * kDC * 4, buf + B::R, wave, nw, lane);
-    const int64_t at = ((bb * a.l + t0) * a.h + hh) * a.p + col0;
-    const int64_t pitch = a.h * a.p * (int64_t)sizeof(IO);
-    copy_rows(static_cast<const IO *>(a.v) + at, pitch, cols * (int)sizeof(IO), len, buf + B::V, wave,
-              nw, lane);
-    copy_rows(static_cast<const IO *>(a.dy) + at, pitch, cols * (int)sizeof(IO), len,
-              buf + B::V + kDC * cols * (int)sizeof(IO), wave, nw, lane);
-}
+    const char *grp, *head, *v, *dy;
+    int64_t sg, sh, sv;
+    uint32_t pitch;
+    int rb, len;
+    __device__ RevSrc(const DeltaArgs &a, int64_t bb, int64_t hh, int col0, int cols) {
+        const int64_t ci = bb * a.nc + a.nc - 1, t0 = (a.nc - 1) * kDC;
+        grp = uni(a.gimg + (ci * a.g + hh / (a.h / a.g)) * B::G::BYTES);
+        head = uni(a.himg + (ci * a.h + hh) * B::H::BYTES + B::H::R);
+        const int64_t at = (((bb * a.l + t0) * a.h + hh) * a.p + col0) * (int64_t)sizeof(IO);
+        v = uni(static_cast<const char *>(a.v) + at);
+        dy = uni(static_cast<const char *>(a.dy) + at);
+        pitch = (uint32_t)(a.h * a.p * sizeof(IO));
+        sg = a.g * B::G::BYTES, sh = a.h * B::H::BYTES, sv = (int64_t)kDC * pitch;
+        rb = cols * (int)sizeof(IO), len = uni((int)(a.l - t0));
+    }
+    __device__ void back() { grp -= sg, head -= sh, v -= sv, dy -= sv, len = kDC; }
+    __device__ void copy(uint32_t buf, int wave, int nw, int lane) const {
+        copy_image<B::G::BYTES>(grp, buf, wave, nw, lane);
+        copy_image<B::HEAD>(head, buf + B::R, wave, nw, lane);
+        copy_rows(v, pitch, rb, len, buf + B::V, wave, nw, lane);
+        copy_rows(dy, pitch, rb, len, buf + B::V + kDC * rb, wave, nw, lane);
+    }
+};
 
 // The transposed product of a lower triangle (its hi and lo images at M) with
 // the rows in f: row tile jt.
@@ -111,8 +120,8 @@ __global__ __launch_bounds__(256, 2) void k_delta_rev(DeltaArgs a) {
     const uint32_t base = lds_address(lds);
     const uint32_t pitch = (uint32_t)(a.h * a.p * sizeof(IO));
 
-    rev_copy<IO, N>(a, base + (NB == 2 ? ((a.nc - 1) & 1) * bufbytes : 0), bb, a.nc - 1, hh, col0,
-                    cols, wave, nw, lane);
+    RevSrc<IO, N> src(a, bb, hh, col0, cols);
+    src.copy(base + (NB == 2 ? ((a.nc - 1) & 1) * bufbytes : 0), wave, nw, lane);
     f32x4 dS[NT];
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
@@ -132,9 +141,10 @@ __global__ __launch_bounds__(256, 2) void k_delta_rev(DeltaArgs a) {
         lds_barrier();
         const int64_t hi = (bb * a.nc + c) * a.h + hh, t0 = c * kDC;
         const int len = (int)(a.l - t0 < kDC ? a.l - t0 : kDC);
-        if (NB == 2 && c > 0)
-            rev_copy<IO, N>(a, base + ((c - 1) & 1) * bufbytes, bb, c - 1, hh, col0, cols, wave, nw,
-                            lane);
+        if (NB == 2 && c > 0) {
+            src.back();
+            src.copy(base + ((c - 1) & 1) * bufbytes, wave, nw, lane);
+        }
         const f16 *K = reinterpret_cast<const f16 *>(buf + B::K);
         const f16 *Q = reinterpret_cast<const f16 *>(buf + B::Q);
         const f16 *M = reinterpret_cast<const f16 *>(buf + B::M);
@@ -283,7 +293,8 @@ __global__ __launch_bounds__(256, 2) void k_delta_rev(DeltaArgs a) {
         }
         if (NB == 1 && c > 0) {
             lds_barrier();  // everyone is done with the buffer
-            rev_copy<IO, N>(a, base, bb, c - 1, hh, col0, cols, wave, nw, lane);
+            src.back();
+            src.copy(base, wave, nw, lane);
         }
     }
     if (a.init) {
@@ -355,7 +366,7 @@ __device__ __forceinline__ void copy_nat(const IO *src, int64_t pitch, int W, in
         const int x = 32 * (piece % XB) + 8 * (ln >> 4) + (PER == 2 ? 4 * (part & 1) : 0);
         const uint32_t off =
             row < len && x < W ? (uint32_t)((row * pitch + x) * (int64_t)sizeof(IO)) : 0xf0000000u;
-        lds_dma16_at(r, dst + (i << 10), off);
+        lds_dma16_at(r, dst + (i << 10), off, 0);
     }
 }
 // Fragment with x free (tile x16) and the 32 rows of the pieces' row tiles r0,
@@ -431,6 +442,7 @@ template <typename IO, int N>
 __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
     typedef typename Frag8<IO>::type F;
     typedef GradBuf<IO, N> B;
+    typedef HeadImg<IO, true> H;
     constexpr int XB = N / 32, NT = N / 16;
     __shared__ __align__(1024) char lds[2 * B::BYTES];
 
@@ -468,7 +480,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
                          buf + B::K, w, lane);
             copy_nat<XB>(static_cast<const IO *>(a.q) + kq, a.g * N, N, len,
                          buf + B::Q, w, lane);
-            copy_lds(a.rows + hi * (kRows * kDC), kRows * kDC * 4, kRows * kDC * 4, buf + B::R, w, 4, lane);
+            copy_image<kRows * kDC * 4>(uni(a.himg + hi * H::BYTES + H::R), buf + B::R, w, 4, lane);
             copy_lds(a.rows2 + hi * (kRowsGrad * kDC), kRowsGrad * kDC * 4, kRowsGrad * kDC * 4,
                       buf + B::R2, w, 4, lane);
         }
@@ -491,7 +503,8 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
         const char *buf = lds + (q & 1) * B::BYTES;
         if (st == 0) {
             const float *r2 = a.rows2 + hi * (kRowsGrad * kDC) + m;
-            const float be = a.rows[(hi * kRows + kBeta) * kDC + m];
+            const float be =
+                reinterpret_cast<const float *>(a.himg + hi * H::BYTES + H::R)[kBeta * kDC + m];
             fq = a.scale * r2[kRead * kDC], fz = -r2[kRead * kDC] * be, fn = r2[kWrite * kDC] * be;
         }
         vm_wait<0>();

@@ -16,6 +16,7 @@
 #include "ssd_delta.hpp"
 
 #include <math.h>
+#include <stdlib.h>
 
 #include "../../include/ssd.h"
 
@@ -145,6 +146,12 @@ __device__ __forceinline__ void use_tile(const DeltaArgs &a, const RawTile<IO, N
 
 __device__ __forceinline__ constexpr int tri_tile(int i, int j) { return i * (i + 1) / 2 + j; }
 
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
+    return v;
+}
+
 // exp2 of a double, by its value in two floats.
 __device__ __forceinline__ float exp2_d(double x) {
     const float h = (float)x, e = exp2f(h);
@@ -176,8 +183,9 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
     f32x4 kk[10], qk[10];
     {
         f16x8 kh[4][XB], kl[4][XB], qh[XB], ql[XB];
-        f16 *kimg = part ? nullptr : a.kimg + item * (PL * IMG);
-        f16 *qimg = part ? nullptr : a.qimg + item * (PL * IMG);
+        typedef GroupImg<IO, N> G;
+        f16 *kimg = part ? nullptr : reinterpret_cast<f16 *>(a.gimg + item * G::BYTES);
+        f16 *qimg = part ? nullptr : reinterpret_cast<f16 *>(a.gimg + item * G::BYTES + G::Q);
         const IO *ks = static_cast<const IO *>(a.k) + row0, *qs = static_cast<const IO *>(a.q) + row0;
         // all of k in flight at once, and of q what the registers hold beside it
         RawTile<IO, N> kr[4], qr[4];
@@ -224,8 +232,12 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
         }
     }
     for (int64_t hh = gg * ratio + part * hs; hh < gg * ratio + (part + 1) * hs; ++hh) {
+        typedef HeadImg<IO, GRAD> H;
         const int64_t hi = ci * a.h + hh;
+        char *himg = a.himg + hi * H::BYTES;
+        float *rows = reinterpret_cast<float *>(himg + H::R);
         // decays: a lane per token
+        float bound;
         {
             const int64_t at = (bb * a.l + t0 + lane) * a.h + hh;
             const bool in = lane < len;
@@ -256,14 +268,16 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
             wave_fence();
             L.ghi[lane] = gh, L.glo[lane] = gl, L.doc[lane] = doc, L.bet[lane] = be;
             const float fk = L.fac[0][lane], fq = L.fac[1][lane];
-            float *r = a.rows + hi * (kRows * kDC) + lane;
+            float *r = rows + lane;
             r[kReadK * kDC] = rd * fk;
             r[kFk * kDC] = fk;
             r[kWriteK * kDC] = wr * fk;
             r[kReadQ * kDC] = a.scale * rd * fq;
             r[kFq * kDC] = a.scale * fq;
             r[kBeta * kDC] = be;
-            if (lane == 0) r[kCarry * kDC] = cuts ? 0.f : exp2_d(end);
+            const float most = wave_max(rd * fabsf(fk)), load = wave_max(fabsf(be * fk));
+            if (lane == 0) r[kCarry * kDC] = cuts ? 0.f : exp2_d(end), r[kCarry * kDC + 1] = most;
+            bound = 64.f * load;
             if constexpr (GRAD) {
                 float *e = a.rows2 + hi * (kRowsGrad * kDC) + lane;
                 e[kGhi * kDC] = gh;
@@ -301,7 +315,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
                     pq[jt][r] = qk[tri_tile(it, jt)][r] * d[r];
                 }
             }
-            f16 *dst = a.pimg + hi * (PPL * kPieces * 512) + lane * 8;
+            f16 *dst = reinterpret_cast<f16 *>(himg + H::P) + lane * 8;
 #pragma unroll
             for (int kb = 0; kb <= it / 2; ++kb) {
                 const Split s = split8(pq[2 * kb], pq[2 * kb + 1], 1.f);
@@ -358,7 +372,14 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
                         o = Mfma<float>::mma(ti[i][q], m == 0 ? -y[q] : -be[i][q] * y[q], o);
                     T[tri_tile(i, j)] = o;
                 }
-            f16 *dst = (m ? a.mimg : a.timg) + hi * (2 * kPieces * 512) + lane * 8;
+            if (m == 0) {
+                float most = 0.f;
+#pragma unroll
+                for (int t = 0; t < 10; ++t) most = abs_max(most, T[t]);
+                most = wave_max(most);
+                if (lane == 0) rows[kCarry * kDC + 2] = bound * most;
+            }
+            f16 *dst = reinterpret_cast<f16 *>(himg + (m ? H::M : H::T)) + lane * 8;
 #pragma unroll
             for (int jt = 0; jt < 4; ++jt)
 #pragma unroll
@@ -376,35 +397,45 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
 // One buffer of LDS: images of k and q, T, tril(Q K^T), the row arrays, then
 // the 64 rows of v (and of dy) of the workgroup's columns.
 template <typename IO, int N, bool GRAD> struct FwdBuf {
-    static constexpr int PL = sizeof(IO) == 4 ? 2 : 1;
-    static constexpr int PPL = sizeof(IO) == 4 || GRAD ? 2 : 1;
-    static constexpr int K = 0, Q = PL * kDC * N * 2, T = 2 * Q, P = T + 2 * kPieces * 1024;
-    static constexpr int R = P + PPL * kPieces * 1024, V = R + kRows * kDC * 4;
+    typedef GroupImg<IO, N> G;
+    typedef HeadImg<IO, GRAD> H;
+    static constexpr int K = 0, Q = G::Q, HEAD = H::M;  // what the scan copies of a head's image
+    static constexpr int T = G::BYTES + H::T, R = G::BYTES + H::R, P = G::BYTES + H::P;
+    static constexpr int V = G::BYTES + HEAD;
     static __host__ __device__ int bytes(int cols) {
         return V + (GRAD ? 2 : 1) * kDC * cols * (int)sizeof(IO);
     }
 };
 
-template <typename IO, int N, bool GRAD>
-__device__ __forceinline__ void fwd_copy(const DeltaArgs &a, uint32_t buf, int64_t bb, int64_t c,
-                                         int64_t hh, int col0, int cols, int wave, int nw, int lane) {
+// Where a chunk's operands of one head and `cols` columns are; next() moves on by
+// one chunk.
+template <typename IO, int N, bool GRAD> struct FwdSrc {
     typedef FwdBuf<IO, N, GRAD> B;
-    const int64_t ci = bb * a.nc + c, gi = ci * a.g + hh / (a.h / a.g), hi = ci * a.h + hh;
-    const int64_t t0 = c * kDC;
-    const int len = (int)(a.l - t0 < kDC ? a.l - t0 : kDC);
-    copy_lds(a.kimg + gi * (B::PL * kDC * N), B::Q, B::Q, buf + B::K, wave, nw, lane);
-    copy_lds(a.qimg + gi * (B::PL * kDC * N), B::Q, B::Q, buf + B::Q, wave, nw, lane);
-    copy_lds(a.timg + hi * (2 * kPieces * 512), 2 * kPieces * 1024, 2 * kPieces * 1024, buf + B::T, wave, nw, lane);
-    copy_lds(a.pimg + hi * (B::PPL * kPieces * 512), B::PPL * kPieces * 1024, B::PPL * kPieces * 1024, buf + B::P, wave, nw, lane);
-    copy_lds(a.rows + hi * (kRows * kDC), kRows * kDC * 4, kRows * kDC * 4, buf + B::R, wave, nw, lane);
-    const int64_t at = ((bb * a.l + t0) * a.h + hh) * a.p + col0;
-    const int64_t pitch = a.h * a.p * (int64_t)sizeof(IO);
-    copy_rows(static_cast<const IO *>(a.v) + at, pitch, cols * (int)sizeof(IO), len, buf + B::V, wave,
-              nw, lane);
-    if constexpr (GRAD)
-        copy_rows(static_cast<const IO *>(a.dy) + at, pitch, cols * (int)sizeof(IO), len,
-                  buf + B::V + kDC * cols * (int)sizeof(IO), wave, nw, lane);
-}
+    const char *grp, *head, *v, *dy;
+    int64_t sg, sh, sv;
+    uint32_t pitch;
+    int rb, left;  // bytes of a row, tokens from here on
+    __device__ FwdSrc(const DeltaArgs &a, int64_t bb, int64_t c, int64_t hh, int col0, int cols) {
+        const int64_t ci = bb * a.nc + c, t0 = c * kDC;
+        grp = uni(a.gimg + (ci * a.g + hh / (a.h / a.g)) * B::G::BYTES);
+        head = uni(a.himg + (ci * a.h + hh) * B::H::BYTES);
+        const int64_t at = (((bb * a.l + t0) * a.h + hh) * a.p + col0) * (int64_t)sizeof(IO);
+        v = uni(static_cast<const char *>(a.v) + at);
+        dy = GRAD ? uni(static_cast<const char *>(a.dy) + at) : nullptr;
+        pitch = (uint32_t)(a.h * a.p * sizeof(IO));
+        sg = a.g * B::G::BYTES, sh = a.h * B::H::BYTES, sv = (int64_t)kDC * pitch;
+        rb = cols * (int)sizeof(IO);
+        left = uni((int)(a.l - t0));
+    }
+    __device__ void next() { grp += sg, head += sh, v += sv, dy += sv, left -= kDC; }
+    __device__ void copy(uint32_t buf, int wave, int nw, int lane) const {
+        copy_image<B::G::BYTES>(grp, buf, wave, nw, lane);
+        copy_image<B::HEAD>(head, buf + B::G::BYTES, wave, nw, lane);
+        const int len = left < kDC ? left : kDC;
+        copy_rows(v, pitch, rb, len, buf + B::V, wave, nw, lane);
+        if constexpr (GRAD) copy_rows(dy, pitch, rb, len, buf + B::V + kDC * rb, wave, nw, lane);
+    }
+};
 
 // SERIAL: a workgroup walks all chunks of a head's columns; otherwise each
 // chunk has a workgroup of its own, started from the kept states (gradient).
@@ -428,7 +459,8 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
     const int bufbytes = B::bytes(cols);
     const uint32_t base = lds_address(lds);
 
-    fwd_copy<IO, N, GRAD>(a, base, bb, c0, hh, col0, cols, wave, nw, lane);
+    FwdSrc<IO, N, GRAD> src(a, bb, c0, hh, col0, cols);
+    src.copy(base, wave, nw, lane);
     f32x4 S[NT];
     {
         const float *src = nullptr;
@@ -446,7 +478,7 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
         }
     }
     for (int64_t c = c0; c < c1; ++c) {
-        const char *buf = lds + (NB == 2 ? (c & 1) * bufbytes : 0);
+        const char *buf = lds + (NB == 2 ? ((c - c0) & 1) * bufbytes : 0);
         // the copies of this chunk are older than the last chunk's stores
         if (c == c0)
             vm_wait<0>();
@@ -457,9 +489,10 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
         else
             vm_wait<(F32 ? 2 * XB : XB) + 4 + 4 + 4 * NT>();
         lds_barrier();
-        if (NB == 2 && c + 1 < c1)
-            fwd_copy<IO, N, GRAD>(a, base + ((c + 1) & 1) * bufbytes, bb, c + 1, hh, col0, cols, wave,
-                                  nw, lane);
+        if (NB == 2 && c + 1 < c1) {
+            src.next();
+            src.copy(base + ((c + 1 - c0) & 1) * bufbytes, wave, nw, lane);
+        }
         const f16 *K = reinterpret_cast<const f16 *>(buf + B::K);
         const f16 *Q = reinterpret_cast<const f16 *>(buf + B::Q);
         const f16 *T = reinterpret_cast<const f16 *>(buf + B::T);
@@ -633,7 +666,8 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
         }
         if (NB == 1 && c + 1 < c1) {
             lds_barrier();  // everyone is done with the buffer
-            fwd_copy<IO, N, GRAD>(a, base, bb, c + 1, hh, col0, cols, wave, nw, lane);
+            src.next();
+            src.copy(base, wave, nw, lane);
         }
     }
     if (SERIAL && a.fin) {
@@ -642,6 +676,251 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
         for (int x = 0; x < NT; ++x)
 #pragma unroll
             for (int r = 0; r < 4; ++r) dst[(16 * x + 4 * g + r) * a.p] = S[x][r];
+    }
+}
+
+// The same walk by four waves to 16 columns, for calls with few of them (the
+// chain of chunks is then all there is to wait for, and a wave alone issues one
+// instruction in four cycles).  A wave owns a quarter of the keys' rows of the
+// state and the rows of one of the four row tiles; what it has of K S and Q S
+// goes to the rows' owners, and R, u and e^{G_C - G} u, split, to everyone, through
+// LDS, with a barrier after each.  The powers of two that the waves have to
+// share come from bounds that they exchange with the values before.
+template <typename IO> struct CoopBuf {
+    static constexpr int UL = sizeof(IO) == 4 ? 2 : 1;  // terms of u in the read-out
+    static constexpr int P = 0, R = P + 12 * 1024, W = R + 4 * 1024, U = W + 4 * 1024;
+    static constexpr int M = U + UL * 2 * 1024, BYTES = M + 3 * 4 * 64;
+};
+
+template <typename IO, int N, int NB>
+__global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
+    typedef FwdBuf<IO, N, false> B;
+    typedef CoopBuf<IO> X;
+    constexpr bool F32 = sizeof(IO) == 4;
+    constexpr int PL = F32 ? 2 : 1, XB = N / 32, NT = N / 16, IMG = kDC * N;
+    constexpr int TPW = NT / 4 > 0 ? NT / 4 : 1;  // key tiles of a wave
+    extern __shared__ __align__(1024) char lds[];
+    const int lane = threadIdx.x & 63, w = wave_id(), g = lane >> 4, j16 = lane & 15;
+    int64_t item = xcd_item(blockIdx.x, gridDim.x);
+    const int cts = a.p >> 4, col = (int)(item % cts) * 16;
+    item /= cts;
+    const int64_t hh = item % a.h, bb = item / a.h;
+    const int bufbytes = B::bytes(16);
+    const uint32_t base = lds_address(lds);
+    char *ex = lds + NB * bufbytes;
+    f32x4 *part = reinterpret_cast<f32x4 *>(ex + X::P);        // [to wave][3 others][lane]
+    f16 *rfr = reinterpret_cast<f16 *>(ex + X::R);              // [hi, lo][32 tokens][lane][8]
+    f16 *wfr = reinterpret_cast<f16 *>(ex + X::W);
+    f16 *ufr = reinterpret_cast<f16 *>(ex + X::U);
+    float *mxs = reinterpret_cast<float *>(ex + X::M);          // [S, V, R][wave][column]
+    const bool owner = TPW * w < NT;                            // key_dim 32 has two tiles
+    const int x0 = TPW * w, kb = x0 >> 1;
+    const uint32_t pitch = (uint32_t)(a.h * a.p * sizeof(IO));
+
+    FwdSrc<IO, N, false> src(a, bb, 0, hh, col, 16);
+    src.copy(base, w, 4, lane);
+    f32x4 S[TPW];
+#pragma unroll
+    for (int x = 0; x < TPW; ++x) {
+        S[x] = zero4();
+        if (a.init && owner)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                S[x][r] = a.init[((bb * a.h + hh) * N + 16 * (x0 + x) + 4 * g + r) * a.p + col + j16];
+    }
+    vm_wait<0>();
+    lds_barrier();
+    for (int64_t c = 0; c < a.nc; ++c) {
+        const char *buf = lds + (NB == 2 ? (c & 1) * bufbytes : 0);
+        if (NB == 2 && c + 1 < a.nc) {
+            src.next();
+            src.copy(base + ((c + 1) & 1) * bufbytes, w, 4, lane);
+        }
+        const f16 *K = reinterpret_cast<const f16 *>(buf + B::K);
+        const f16 *Q = reinterpret_cast<const f16 *>(buf + B::Q);
+        const f16 *T = reinterpret_cast<const f16 *>(buf + B::T);
+        const f16 *P = reinterpret_cast<const f16 *>(buf + B::P);
+        const float *rows = reinterpret_cast<const float *>(buf + B::R);
+        const IO *V = reinterpret_cast<const IO *>(buf + B::V);
+        const int64_t t0 = c * kDC, hi = (bb * a.nc + c) * a.h + hh;
+        const int len = (int)(a.l - t0 < kDC ? a.l - t0 : kDC);
+
+        // all of the chunk's operands into registers
+        f16x8 kf[PL][4], qf[PL][4], kc[PL][TPW][2], tf[2][2], pf[PL][2];
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                kf[i][rt] = img_rows(K + i * IMG, rt * XB + kb, lane);
+                qf[i][rt] = img_rows(Q + i * IMG, rt * XB + kb, lane);
+            }
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+            const int b = tb <= w >> 1 ? tb : 0;  // blocks beyond the diagonal are not used
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                tf[i][tb] = img_cols(T + i * kPieces * 512, tri_piece_t(2 * b, w >> 1),
+                                     tri_piece_t(2 * b + 1, w >> 1), w, lane);
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+                pf[i][tb] = img_rows(P + i * kPieces * 512, tri_piece(w, b), lane);
+#pragma unroll
+            for (int i = 0; i < PL; ++i)
+#pragma unroll
+                for (int x = 0; x < TPW; ++x) {
+                    const int t = owner ? x0 + x : 0;
+                    kc[i][x][tb] = img_cols(K + i * IMG, 2 * tb * XB + (t >> 1),
+                                            (2 * tb + 1) * XB + (t >> 1), t, lane);
+                }
+        }
+        const f32x4 v = lds_tile(V, 16, w, 0, lane);
+        const f32x4 fr = row4(rows, kReadK, w, lane), fk = row4(rows, kFk, w, lane),
+                    wk = row4(rows, kWriteK, w, lane), be = row4(rows, kBeta, w, lane),
+                    yr = row4(rows, kReadQ, w, lane), yp = row4(rows, kFq, w, lane);
+        const float carry = rows[kCarry * kDC], mostf = rows[kCarry * kDC + 1],
+                    mostu = rows[kCarry * kDC + 2];
+
+        // this wave's part of K S and Q S
+        float mx = 0.f;
+#pragma unroll
+        for (int x = 0; x < TPW; ++x) mx = abs_max(mx, S[x]);
+        mx = col_max(mx);
+        const Pow2 ps(mx);
+        // half a block where a wave has one tile
+        const Split sf = TPW == 2 ? split8(S[0], S[TPW - 1], ps.sc)
+                                  : split8(x0 & 1 ? zero4() : S[0], x0 & 1 ? S[0] : zero4(), ps.sc);
+        const float mv = col_max(abs_max(0.f, v));
+        if (g == 0) mxs[w * 16 + j16] = mx, mxs[64 + w * 16 + j16] = mv;
+        f32x4 ks[4], qs[4];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            ks[rt] = mma16(kf[0][rt], sf.hi, zero4());
+            qs[rt] = mma16(qf[0][rt], sf.hi, zero4());
+        }
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            ks[rt] = mma16(kf[0][rt], sf.lo, ks[rt]);
+            if constexpr (F32) {
+                qs[rt] = mma16(qf[0][rt], sf.lo, qs[rt]);
+                ks[rt] = mma16(kf[PL - 1][rt], sf.hi, ks[rt]);
+                qs[rt] = mma16(qf[PL - 1][rt], sf.hi, qs[rt]);
+            }
+        }
+        f32x4 mine = zero4(), myq = zero4();
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) ks[rt][r] *= ps.inv, qs[rt][r] *= ps.inv;
+            if (rt == w)
+                mine = ks[rt], myq = qs[rt];
+            else
+                part[(rt * 3 + (w < rt ? w : w - 1)) * 64 + lane] = ks[rt];
+        }
+        lds_barrier();
+        if (NB == 1 && c + 1 < a.nc) {
+            src.next();
+            src.copy(base, w, 4, lane);
+        }
+        // R of this wave's rows
+        f32x4 R;
+        {
+            const f32x4 p0 = part[(w * 3) * 64 + lane], p1 = part[(w * 3 + 1) * 64 + lane],
+                        p2 = part[(w * 3 + 2) * 64 + lane];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                R[r] = fmaf(-fr[r], (p0[r] + p1[r]) + (p2[r] + mine[r]), v[r]);
+        }
+        // |R| <= max |v| + kReadK sum over the keys of |k| |S|, with |k| < 1 here
+        float top = 0.f, sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, mxs[64 + i * 16 + j16]), sum += mxs[i * 16 + j16];
+        const Pow2 pr(fmaf(mostf * (16.f * TPW), sum, top));
+        const float mr = col_max(abs_max(0.f, R));
+        if (g == 0) mxs[128 + w * 16 + j16] = mr;
+        put_half(rfr, R, pr.sc, w, lane);
+        lds_barrier();
+        // N = T R, and u
+        f32x4 n = zero4();
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+            if (tb <= w >> 1) {
+                const f16x8 rh = img_rows(rfr, tb, lane), rl = img_rows(rfr + 1024, tb, lane);
+                n = mma16(tf[0][tb], rh, n);
+                n = mma16(tf[0][tb], rl, n);
+                n = mma16(tf[1][tb], rh, n);
+            }
+        f32x4 U, W;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float u = n[r] * pr.inv * be[r];
+            U[r] = u * fk[r];
+            W[r] = u * wk[r];
+        }
+        top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, mxs[128 + i * 16 + j16]);
+        const Pow2 pu(mostu * top);
+        put_half(wfr, W, pu.sc, w, lane);
+        put_half<F32>(ufr, U, pu.sc, w, lane);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+            if (rt != w) part[(rt * 3 + (w < rt ? w : w - 1)) * 64 + lane] = qs[rt];
+        vm_wait<0>();
+        lds_barrier();
+        // this wave's rows of the state
+        f32x4 t[TPW];
+#pragma unroll
+        for (int x = 0; x < TPW; ++x) t[x] = zero4();
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+            const f16x8 wh = img_rows(wfr, tb, lane), wl = img_rows(wfr + 1024, tb, lane);
+#pragma unroll
+            for (int x = 0; x < TPW; ++x) {
+                t[x] = mma16(kc[0][x][tb], wh, t[x]);
+                t[x] = mma16(kc[0][x][tb], wl, t[x]);
+                if constexpr (F32) t[x] = mma16(kc[PL - 1][x][tb], wh, t[x]);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < TPW; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[x][r] = owner ? fmaf(t[x][r], pu.inv, carry * S[x][r]) : 0.f;
+        if (a.states && owner) {
+            float *st = a.states + hi * N * a.p + col + j16;
+#pragma unroll
+            for (int x = 0; x < TPW; ++x)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) st[(16 * (x0 + x) + 4 * g + r) * a.p] = S[x][r];
+        }
+        // and of Y
+        if (a.y) {
+            f32x4 y = zero4();
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb)
+                if (tb <= w >> 1) {
+                    const f16x8 uh = img_rows(ufr, tb, lane);
+                    y = mma16(pf[0][tb], uh, y);
+                    if constexpr (F32) {
+                        y = mma16(pf[0][tb], img_rows(ufr + 1024, tb, lane), y);
+                        y = mma16(pf[PL - 1][tb], uh, y);
+                    }
+                }
+            const f32x4 p0 = part[(w * 3) * 64 + lane], p1 = part[(w * 3 + 1) * 64 + lane],
+                        p2 = part[(w * 3 + 2) * 64 + lane];
+            const Rsrc ry = make_rsrc(static_cast<IO *>(a.y) + ((bb * a.l + t0) * a.h + hh) * a.p + col,
+                                      (int64_t)(len - 1) * pitch + 16 * sizeof(IO));
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                buf_put(ry, (16 * w + 4 * g + r) * pitch + j16 * sizeof(IO),
+                        fmaf(yr[r], (p0[r] + p1[r]) + (p2[r] + myq[r]), yp[r] * pu.inv * y[r]), IO{});
+        }
+    }
+    if (a.fin && owner) {
+        float *dst = a.fin + (bb * a.h + hh) * N * a.p + col + j16;
+#pragma unroll
+        for (int x = 0; x < TPW; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dst[(16 * (x0 + x) + 4 * g + r) * a.p] = S[x][r];
     }
 }
 
@@ -687,7 +966,20 @@ template <typename IO, int N> hipError_t prep_n(const DeltaArgs &a, bool grad, h
     return hipGetLastError();
 }
 
+template <typename IO, int N> hipError_t run_coop(const DeltaArgs &a, hipStream_t s) {
+    const int one = FwdBuf<IO, N, false>::bytes(16), ex = CoopBuf<IO>::BYTES;
+    const int64_t items = a.b * a.h * (a.p / 16);
+    const bool two = items <= device_cus() && 2 * one + ex <= kLdsMost;
+    auto *k = two ? &k_delta_coop<IO, N, 2> : &k_delta_coop<IO, N, 1>;
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kLdsMost);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k, dim3((unsigned)items), dim3(256), (two ? 2 : 1) * one + ex, s, a);
+    return hipGetLastError();
+}
+
 template <typename IO, int N> hipError_t fwd_n(const DeltaArgs &a, bool grad, hipStream_t s) {
+    if (!grad && (getenv("XCOOP") ? atoi(getenv("XCOOP")) : a.b * a.h * (a.p / 16) <= 4 * device_cus())) return run_coop<IO, N>(a, s);
     if (!grad) return run_fwd<IO, N, false, true>(a, s);
     return a.kept ? run_fwd<IO, N, true, false>(a, s) : run_fwd<IO, N, true, true>(a, s);
 }
