@@ -146,9 +146,8 @@ __global__ void k_delta_copy(float *dst, const float *src, int64_t n) {
 
 // ------------------------------------------------------------- workspace ---
 struct DeltaWs {
-    size_t total = 0;
-    size_t gimg, himg, rows2, nimg, nlow, zimg, simg, dsimg, doo, dvv, dzn,
-        eend, part, states;
+    size_t total = 0, hbytes;
+    size_t gimg, himg, rows2, nimg, zimg, simg, dsimg, yimg, scales, g0, x0, toks, eend, cells, part, states;
     size_t add(size_t bytes) {
         const size_t at = total;
         total += (bytes + 255) & ~(size_t)255;
@@ -160,31 +159,38 @@ struct DeltaWs {
         const size_t nc = (size_t)((l + kDC - 1) / kDC), ch = b * nc * h, cg = b * nc * g;
         const size_t tri = kPieces * 1024;
         gimg = add(cg * 2 * planes * kDC * n * 2);
-        himg = add(ch * (2 * tri + kRows * kDC * 4 + (grad ? 4 : planes) * tri));
-        rows2 = nimg = nlow = zimg = simg = dsimg = doo = dvv = dzn = eend = part = states = 0;
+        hbytes = 2 * tri + kRows * kDC * 4 + (grad ? 4 : planes) * tri;
+        himg = add(ch * hbytes);
+        rows2 = nimg = zimg = simg = dsimg = yimg = scales = g0 = x0 = toks = eend = cells = part = states = 0;
         if (!grad) return;
         rows2 = add(ch * kRowsGrad * kDC * 4);
-        nimg = add(ch * kDC * p * el);
-        nlow = add(io == SSD_BF16 ? ch * kDC * p * el : 0);
-        zimg = add(ch * kDC * p * el);
+        nimg = add(ch * kDC * p * 4);  // two fp16 terms or one fp32
+        zimg = add(ch * kDC * p * 4);
         simg = add(ch * n * p * el);
         dsimg = add(ch * n * p * el);
-        doo = add(ch * (p / 16) * kDC * 4);
-        dvv = add(ch * (p / 16) * kDC * 4);
-        dzn = add(ch * (p / 16) * kDC * 4);
-        eend = add((ch + b * h) * (p / 16) * 4);  // and in front of the first chunk
+        yimg = add(ch * kDC * p * el);
+        scales = add(ch * (p / 16) * kScales * 4);
+        g0 = add(ch * kDC * p * 4);
+        x0 = add(ch * kDC * p * 4);
+        toks = add(ch * (p / 16) * kSums * kDC * 4);
+        eend = add(ch * (p / 16) * 4);
+        cells = add(ch * 5 * kDC * 8);
         part = add(ch * 2 * 8);
         if (keep) states = add(ch * n * p * 4);
     }
     void set(DeltaArgs &a, char *ws, bool grad) const {
         a.gimg = ws + gimg, a.himg = ws + himg;
+        a.hstride = hbytes;
         if (!grad) return;
         a.rows2 = reinterpret_cast<float *>(ws + rows2);
-        a.nimg = ws + nimg, a.nlow = ws + nlow, a.zimg = ws + zimg, a.simg = ws + simg, a.dsimg = ws + dsimg;
-        a.doo = reinterpret_cast<float *>(ws + doo);
-        a.dvv = reinterpret_cast<float *>(ws + dvv);
-        a.dzn = reinterpret_cast<float *>(ws + dzn);
+        a.nimg = ws + nimg, a.zimg = ws + zimg, a.simg = ws + simg, a.dsimg = ws + dsimg;
+        a.yimg = ws + yimg;
+        a.scales = reinterpret_cast<float *>(ws + scales);
+        a.g0 = reinterpret_cast<float *>(ws + g0);
+        a.x0 = reinterpret_cast<float *>(ws + x0);
+        a.toks = reinterpret_cast<float *>(ws + toks);
         a.eend = reinterpret_cast<float *>(ws + eend);
+        a.cells = reinterpret_cast<double *>(ws + cells);
         a.part = reinterpret_cast<double *>(ws + part);
     }
 };
@@ -268,7 +274,7 @@ int32_t ssd_delta_scan(const void *q, const void *k, const void *v, const void *
     a.scale = scale, a.eps = norm_eps, a.lo = dt_min, a.hi = dt_max;
     W.set(a, static_cast<char *>(workspace), false);
     hipError_t e = delta_prep(a, io_dtype, (int)key_dim, false, s);
-    if (e == hipSuccess) e = delta_forward(a, io_dtype, (int)key_dim, false, s);
+    if (e == hipSuccess) e = delta_forward(a, io_dtype, (int)key_dim, s);
     return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }
 
@@ -319,8 +325,11 @@ int32_t ssd_delta_scan_bwd(const void *q, const void *k, const void *v, const vo
     const int n = (int)key_dim;
     if (!states) a.states = reinterpret_cast<float *>(ws + W.states);
     hipError_t e = delta_prep(a, io_dtype, n, true, s);
-    if (e == hipSuccess) e = delta_forward(a, io_dtype, n, true, s);
-    if (!states) a.kept = a.states;
+    if (!states) {
+        a.y = a.nimg;  // not needed: to where N comes later
+        if (e == hipSuccess) e = delta_forward(a, io_dtype, n, s);
+        a.kept = a.states;
+    }
     if (e == hipSuccess) e = delta_backward(a, io_dtype, n, s);
     return e == hipSuccess ? SSD_OK : SSD_ERR_HIP;
 }

@@ -21,8 +21,10 @@
 //   dQ_i = scale e^{G_i} S dY_i + scale sum_{j<=i} D_ij (dY_i . U_j) k_j
 //   dK_j = scale sum_{i>=j} D_ij (dY_i . U_j) q_i - e^{G_j} S dV_j
 //          + e^{G_C-G_j} dS U_j - (X + X^T) K,  X_ij = D_ij (dV_i . U_j), j < i
-//   dG_i = dY_i . Y_i - dV_i . V_i,  and e^{G_C} S', dS' behind the last token:
-//   dg_t = sum_{i>=t} dG_i + <S', dS>
+//   dg_t, from the terms that cross token t:
+//   C_ij = scale D_ij (q_i . k_j) (dY_i . U_j) - kk_ij (dV_i . U_j),  j <= i
+//   dg_t = sum_{i>=t} (scale e^{G_i} dY_i . S^T q_i - e^{G_i} dV_i . S^T k_i)
+//          + sum_{i>=t>j} C_ij + sum_{j<t} e^{G_C-G_j} U_j . dS^T k_j + e^{G_C} <S, dS>
 //
 // A token that starts a document has nothing in front: e^{G} is zero from it
 // on, D across it, and e^{G_C - G} in front of the last such token.
@@ -59,7 +61,7 @@ enum RowOf {
     kFq,      // scale fq
     kBeta,    // beta
     kCarry,   // [0]: e^{G_C}
-    kSpare
+    kRawQ    // fq
 };
 enum RowOfGrad {
     kGhi,    // log2 of e^G, as two floats
@@ -71,6 +73,15 @@ enum RowOfGrad {
     kRq,
     kStep    // d_t
 };
+
+// k_delta_grad's operands: with bf16 io fp16 terms under one power of two for 16
+// value columns of a chunk (of N and Z both terms, in two planes), fp32 otherwise.
+template <typename IO> struct GradOp { typedef f16 type; static constexpr int PL = 2; };
+template <> struct GradOp<float> { typedef float type; static constexpr int PL = 1; };
+enum ScaleOf { kScS, kScD, kScN, kScZ, kScY, kScales = 8 };  // the powers' inverses
+// Per token, summed over 16 columns: dY . (scale e^G Q S), dV . (e^G K S),
+// U . (e^{G_C - G} K dS) and Z . N.
+enum SumOf { kSumQ, kSumK, kSumOut, kSumZ, kSums };
 
 struct DeltaArgs {
     const void *q, *k, *v, *dt, *beta;
@@ -86,9 +97,14 @@ struct DeltaArgs {
     // workspace
     char *gimg, *himg;  // GroupImg, HeadImg
     float *rows2;
-    void *nimg, *nlow, *zimg, *simg, *dsimg;
-    float *doo, *dvv, *dzn, *eend;
-    double *part;
+    void *nimg, *zimg, *simg, *dsimg, *yimg;  // operands of k_delta_grad, see GradOp
+    float *scales;                            // [chunk, head][16 columns][kScales]
+    // e^G K S and tril(Q K^T)^T dY of 16 columns, in accumulator order
+    float *g0, *x0;
+    float *toks;                              // [chunk, head][16 columns][kSums][64]
+    float *eend;
+    double *cells, *part;                     // [chunk, head][row sums, 4 column sums][64]
+    int64_t hstride;                          // bytes of a HeadImg
     int64_t b, l, h, g, nc;
     int p, softplus, norm;
     float scale, eps, lo, hi;
@@ -158,12 +174,15 @@ __device__ __forceinline__ f32x4 mma16(f16x8 a, f16x8 b, f32x4 c) {
 }
 
 // Power of two that brings magnitudes up to mx into [2^13, 2^14), and its inverse.
+// k_delta_grad's operands stop at 2^60 (kOperand), so that the product of two
+// inverses stays in fp32's range.
+constexpr int kOperand = 187;
 struct Pow2 {
     float sc, inv;
-    __device__ explicit Pow2(float mx) {
+    __device__ explicit Pow2(float mx, int most = 253) {
         const int e = (int)(__builtin_bit_cast(uint32_t, mx) >> 23) & 255;
         int f = 267 - e;
-        f = f > 253 ? 253 : f;
+        f = f > most ? most : f;
         sc = __builtin_bit_cast(float, (uint32_t)f << 23);
         inv = __builtin_bit_cast(float, (uint32_t)(254 - f) << 23);
     }
@@ -216,6 +235,25 @@ __device__ __forceinline__ float col_max(float v) {
 }
 __device__ __forceinline__ float abs_max(float m, const f32x4 &v) {
     return fmaxf(fmaxf(fmaxf(m, fabsf(v[0])), fmaxf(fabsf(v[1]), fabsf(v[2]))), fabsf(v[3]));
+}
+
+// Largest value of a wave's 16 columns, in every lane.
+template <int CTRL> __device__ __forceinline__ float dpp_max(float v) {
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                                  0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true)));
+}
+__device__ __forceinline__ float tile_max(float v) {
+    v = dpp_max<0x128>(col_max(v));  // row_ror 8, 4, 2, 1
+    v = dpp_max<0x124>(v);
+    v = dpp_max<0x122>(v);
+    return dpp_max<0x121>(v);
+}
+
+// Has the loads of a matrix waited for here, not at their first use: in a loop that
+// use would wait for the next chunk's copies too.
+template <typename V, int T> __device__ __forceinline__ void landed(V (&v)[T]) {
+#pragma unroll
+    for (int i = 0; i < T; ++i) asm volatile("" : "+v"(v[i]));
 }
 
 // Sum over the 16 lanes of a row of lanes (every lane gets it).
@@ -303,6 +341,49 @@ __device__ __forceinline__ void copy_rows(const char *src, uint32_t pitch, int r
     }
 }
 
+// One buffer of LDS: images of k and q, T, tril(Q K^T), the row arrays, then
+// the 64 rows of v (and of dy) of the workgroup's columns.
+template <typename IO, int N, bool GRAD> struct FwdBuf {
+    typedef GroupImg<IO, N> G;
+    typedef HeadImg<IO, GRAD> H;
+    static constexpr int K = 0, Q = G::Q, HEAD = H::M;
+    static constexpr int T = G::BYTES + H::T, R = G::BYTES + H::R, P = G::BYTES + H::P;
+    static constexpr int V = G::BYTES + HEAD;
+    static __host__ __device__ int bytes(int cols) {
+        return V + (GRAD ? 2 : 1) * kDC * cols * (int)sizeof(IO);
+    }
+};
+
+// Where a chunk's operands of one head and `cols` columns are; next() moves on by
+// one chunk.
+template <typename IO, int N, bool GRAD> struct FwdSrc {
+    typedef FwdBuf<IO, N, GRAD> B;
+    const char *grp, *head, *v, *dy;
+    int64_t sg, sh, sv;
+    uint32_t pitch;
+    int rb, left;  // bytes of a row, tokens from here on
+    __device__ FwdSrc(const DeltaArgs &a, int64_t bb, int64_t c, int64_t hh, int col0, int cols) {
+        const int64_t ci = bb * a.nc + c, t0 = c * kDC;
+        grp = uni(a.gimg + (ci * a.g + hh / (a.h / a.g)) * B::G::BYTES);
+        head = uni(a.himg + (ci * a.h + hh) * a.hstride);
+        const int64_t at = (((bb * a.l + t0) * a.h + hh) * a.p + col0) * (int64_t)sizeof(IO);
+        v = uni(static_cast<const char *>(a.v) + at);
+        dy = GRAD ? uni(static_cast<const char *>(a.dy) + at) : nullptr;
+        pitch = (uint32_t)(a.h * a.p * sizeof(IO));
+        sg = a.g * B::G::BYTES, sh = a.h * a.hstride, sv = (int64_t)kDC * pitch;
+        rb = cols * (int)sizeof(IO);
+        left = uni((int)(a.l - t0));
+    }
+    __device__ void next() { grp += sg, head += sh, v += sv, dy += sv, left -= kDC; }
+    __device__ void copy(uint32_t buf, int wave, int nw, int lane) const {
+        copy_image<B::G::BYTES>(grp, buf, wave, nw, lane);
+        copy_image<B::HEAD>(head, buf + B::G::BYTES, wave, nw, lane);
+        const int len = left < kDC ? left : kDC;
+        copy_rows(v, pitch, rb, len, buf + B::V, wave, nw, lane);
+        if constexpr (GRAD) copy_rows(dy, pitch, rb, len, buf + B::V + kDC * rb, wave, nw, lane);
+    }
+};
+
 // Rows 16 rt + 4 g + r of column col0 + (lane & 15) of 64 rows in LDS.
 __device__ __forceinline__ f32x4 lds_tile(const bf16 *M, int ld, int rt, int col0, int lane) {
     const f16x4 v = lds_tr4(reinterpret_cast<const f16 *>(M), ld, 16 * rt, col0, lane);
@@ -325,10 +406,22 @@ __device__ __forceinline__ void buf_put(Rsrc r, uint32_t off, float v, float) {
     __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v), r, off, 0, 0);
 }
 
+int device_cus();
+constexpr int kLdsMost = 160 * 1024;
+
+// A kernel with `bytes` of LDS, which may be more than the default's 64 KB.
+template <typename K> hipError_t launch(K *k, int64_t items, int threads, int bytes, const DeltaArgs &a,
+                                       hipStream_t s) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, kLdsMost);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k, dim3((unsigned)items), dim3(threads), bytes, s, a);
+    return hipGetLastError();
+}
+
 // Launches (ssd_delta_scan.hip, ssd_delta_bwd.hip).
 hipError_t delta_prep(const DeltaArgs &a, int io, int n, bool grad, hipStream_t s);
-// forward: y, final state and states; grad: states (where none are kept), N and dY . Y
-hipError_t delta_forward(const DeltaArgs &a, int io, int n, bool grad, hipStream_t s);
+hipError_t delta_forward(const DeltaArgs &a, int io, int n, hipStream_t s);  // y, states: where given
 hipError_t delta_backward(const DeltaArgs &a, int io, int n, hipStream_t s);
 
 }  // namespace ssd

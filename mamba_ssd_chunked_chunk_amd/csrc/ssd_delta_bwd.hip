@@ -1,17 +1,21 @@
-// The gated delta rule's gradient (formulas in ssd_delta.hpp), after the forward
-// kernels have left the states in front of the chunks, N and dY . Y:
+// The gated delta rule's gradient (formulas in ssd_delta.hpp), from the states
+// in front of the chunks:
+//
+// k_delta_mid, all chunks in parallel: N = v - P^T k of 16 value columns per
+// wave, and what of the gradient needs only the state in front.
 //
 // k_delta_rev, chunk after chunk from the end: the adjoint state of 16 value
 // columns in a wave's registers, as in the forward pass; leaves Z, dV, the
-// adjoint state behind every chunk, and per token dV . V and per chunk <S', dS>,
-// from which the decays' gradient follows without q, k or any further product.
+// adjoint state behind every chunk, and per token the terms of the decays'
+// gradient that reach into the chunk from outside.
 //
 // k_delta_grad, all chunks in parallel: dq and dk, which contract over the value
-// columns.  A wave owns 16 tokens, all keys of them in registers, transposed
-// ([key][token]), so that the masked products dY U^T and Z N^T are the next
-// product's operands as they stand; the heads that share q and k are walked in
-// order by one workgroup.  Its operands are the io type's (bf16, or fp32 on the
-// fp32 matrix instructions): nothing of it enters the recurrence.
+// columns, and the decays' terms inside the chunk.  A wave owns 16 tokens, all
+// keys of them in registers, transposed ([key][token]), so that the masked
+// products dY U^T and Z N^T are the next product's operands as they stand; the
+// heads that share q and k are walked in order by one workgroup.  With bf16 io
+// its operands are fp16 terms: one of each for dq and dk (2^-11, an eighth of
+// their own rounding), two of N and Z where the decays' gradient needs them.
 #include "ssd_delta.hpp"
 
 #include <math.h>
@@ -22,43 +26,20 @@ namespace ssd {
 
 namespace {
 
-constexpr int kLdsMost = 160 * 1024;
-
-template <typename IO, int N> struct RevBuf {
-    typedef GroupImg<IO, N> G;
-    typedef HeadImg<IO, true> H;
-    static constexpr int K = 0, Q = G::Q, HEAD = H::BYTES - H::R;  // from the row arrays on
-    static constexpr int R = G::BYTES, P = R + H::P - H::R, M = R + H::M - H::R, V = R + HEAD;
-    static __host__ __device__ int bytes(int cols) { return V + 2 * kDC * cols * (int)sizeof(IO); }
-};
-
-// Where a chunk's operands of one head and `cols` columns are; back() moves to
-// the chunk in front.
-template <typename IO, int N> struct RevSrc {
-    typedef RevBuf<IO, N> B;
-    const char *grp, *head, *v, *dy;
-    int64_t sg, sh, sv;
-    uint32_t pitch;
-    int rb, len;
-    __device__ RevSrc(const DeltaArgs &a, int64_t bb, int64_t hh, int col0, int cols) {
-        const int64_t ci = bb * a.nc + a.nc - 1, t0 = (a.nc - 1) * kDC;
-        grp = uni(a.gimg + (ci * a.g + hh / (a.h / a.g)) * B::G::BYTES);
-        head = uni(a.himg + (ci * a.h + hh) * B::H::BYTES + B::H::R);
-        const int64_t at = (((bb * a.l + t0) * a.h + hh) * a.p + col0) * (int64_t)sizeof(IO);
-        v = uni(static_cast<const char *>(a.v) + at);
-        dy = uni(static_cast<const char *>(a.dy) + at);
-        pitch = (uint32_t)(a.h * a.p * sizeof(IO));
-        sg = a.g * B::G::BYTES, sh = a.h * B::H::BYTES, sv = (int64_t)kDC * pitch;
-        rb = cols * (int)sizeof(IO), len = uni((int)(a.l - t0));
+// A matrix of 16 value columns as k_delta_grad's operand: fragment f of it.
+template <typename IO, int PL>
+__device__ __forceinline__ void put_operand(typename GradOp<IO>::type *dst, const f32x4 &a, const f32x4 &b,
+                                            const Split &s, int f, int plane, int lane) {
+    if constexpr (sizeof(IO) == 2) {
+        *reinterpret_cast<f16x8 *>(dst + f * 512 + lane * 8) = s.hi;
+        if constexpr (PL == 2) *reinterpret_cast<f16x8 *>(dst + plane + f * 512 + lane * 8) = s.lo;
+    } else {
+        *reinterpret_cast<f32x4 *>(dst + f * 512 + lane * 8) = a;
+        *reinterpret_cast<f32x4 *>(dst + f * 512 + lane * 8 + 4) = b;
     }
-    __device__ void back() { grp -= sg, head -= sh, v -= sv, dy -= sv, len = kDC; }
-    __device__ void copy(uint32_t buf, int wave, int nw, int lane) const {
-        copy_image<B::G::BYTES>(grp, buf, wave, nw, lane);
-        copy_image<B::HEAD>(head, buf + B::R, wave, nw, lane);
-        copy_rows(v, pitch, rb, len, buf + B::V, wave, nw, lane);
-        copy_rows(dy, pitch, rb, len, buf + B::V + kDC * rb, wave, nw, lane);
-    }
-};
+}
+// Elements of N or Z of 16 columns of a chunk.
+template <typename IO> constexpr int kOperandN = GradOp<IO>::PL * 2 * 512;
 
 // The transposed product of a lower triangle (its hi and lo images at M) with
 // the rows in f: row tile jt.
@@ -75,20 +56,184 @@ __device__ __forceinline__ f32x4 tri_t(const f16 *M, int jt, const Split *f, int
     return t;
 }
 
-// Sum over a wave's 16 columns of a state in memory times one in accumulators.
-template <int NT>
-__device__ __forceinline__ float state_dot(const float *st, int p, const f32x4 (&d)[NT], int lane) {
-    float s = 0.f;
+template <typename IO, int N>
+__global__ __launch_bounds__(256, 2) void k_delta_mid(DeltaArgs a) {
+    typedef FwdBuf<IO, N, true> B;
+    typedef typename GradOp<IO>::type OT;
+    constexpr bool F32 = sizeof(IO) == 4;
+    constexpr int XB = N / 32, NT = N / 16, IMG = kDC * N;
+    extern __shared__ __align__(1024) char lds[];
+    const int lane = threadIdx.x & 63, wave = wave_id(), nw = blockDim.x >> 6;
+    const int g = lane >> 4, j16 = lane & 15;
+    const int cols = 16 * nw, slices = a.p / cols, cts = a.p >> 4;
+    int64_t item = xcd_item(blockIdx.x, gridDim.x);
+    const int col0 = (int)(item % slices) * cols;
+    item /= slices;
+    const int64_t hh = item % a.h, ci = item / a.h, c = ci % a.nc, bb = ci / a.nc, hi = ci * a.h + hh;
+    const int col = col0 + 16 * wave, ct = col >> 4;
+
+    FwdSrc<IO, N, true> src(a, bb, c, hh, col0, cols);
+    src.copy(lds_address(lds), wave, nw, lane);
+    f32x4 S[NT];
+    {
+        const float *s0 = c ? a.kept + (hi - a.h) * N * a.p
+                            : a.init ? a.init + (bb * a.h + hh) * N * a.p : nullptr;
 #pragma unroll
-    for (int x = 0; x < NT; ++x)
+        for (int x = 0; x < NT; ++x) {
+            S[x] = zero4();
+            if (s0)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) s = fmaf(st[(16 * x + 4 * (lane >> 4) + r) * p], d[x][r], s);
-    s = sum16(s);
-    s += __shfl_xor(s, 16);
-    return s + __shfl_xor(s, 32);
+                for (int r = 0; r < 4; ++r) S[x][r] = s0[(16 * x + 4 * g + r) * a.p + col + j16];
+        }
+    }
+    vm_wait<0>();
+    lds_barrier();
+    const f16 *K = reinterpret_cast<const f16 *>(lds + B::K);
+    const f16 *Q = reinterpret_cast<const f16 *>(lds + B::Q);
+    const f16 *T = reinterpret_cast<const f16 *>(lds + B::T);
+    const f16 *P = reinterpret_cast<const f16 *>(lds + B::P);
+    const float *rows = reinterpret_cast<const float *>(lds + B::R);
+    const IO *V = reinterpret_cast<const IO *>(lds + B::V);
+    const IO *dY = V + kDC * cols;
+    float *scales = a.scales + (hi * cts + ct) * kScales;
+
+    float mx = 0.f;
+#pragma unroll
+    for (int x = 0; x < NT; ++x) mx = abs_max(mx, S[x]);
+    const Pow2 ps(tile_max(mx), kOperand);
+    Split sf[XB];
+    OT *simg = static_cast<OT *>(a.simg) + (hi * cts + ct) * (XB * 512);
+#pragma unroll
+    for (int kb = 0; kb < XB; ++kb) {
+        sf[kb] = split8(S[2 * kb], S[2 * kb + 1], ps.sc);
+        put_operand<IO, 1>(simg, S[2 * kb], S[2 * kb + 1], sf[kb], kb, 0, lane);
+    }
+    f32x4 R[4];
+    f32x4 *g0 = reinterpret_cast<f32x4 *>(a.g0 + (hi * cts + ct) * (16 * kDC)) + lane;
+    float *qs = a.toks + ((hi * cts + ct) * kSums + kSumQ) * kDC;
+    mx = 0.f;
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+        f32x4 t = zero4(), u = zero4();
+#pragma unroll
+        for (int kb = 0; kb < XB; ++kb) {
+            const f16x8 k = img_rows(K, rt * XB + kb, lane), q = img_rows(Q, rt * XB + kb, lane);
+            t = mma16(k, sf[kb].hi, t);
+            u = mma16(q, sf[kb].hi, u);
+            t = mma16(k, sf[kb].lo, t);
+            u = mma16(q, sf[kb].lo, u);
+            if constexpr (F32) {
+                t = mma16(img_rows(K + IMG, rt * XB + kb, lane), sf[kb].hi, t);
+                u = mma16(img_rows(Q + IMG, rt * XB + kb, lane), sf[kb].hi, u);
+            }
+        }
+        const f32x4 v = lds_tile(V, cols, rt, 16 * wave, lane), f = row4(rows, kReadK, rt, lane);
+        const f32x4 d = lds_tile(dY, cols, rt, 16 * wave, lane), fq = row4(rows, kReadQ, rt, lane);
+        f32x4 s;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            t[r] *= f[r] * ps.inv;
+            R[rt][r] = v[r] - t[r];
+            s[r] = sum16(d[r] * (fq[r] * ps.inv * u[r]));
+        }
+        g0[64 * rt] = t;
+        if (j16 == 0) *reinterpret_cast<f32x4 *>(qs + 16 * rt + 4 * g) = s;
+        mx = abs_max(mx, R[rt]);
+    }
+    const Pow2 pr(col_max(mx));
+    Split rf[2];
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb) rf[tb] = split8(R[2 * tb], R[2 * tb + 1], pr.sc);
+    mx = 0.f;
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+        f32x4 t = zero4();
+#pragma unroll
+        for (int tb = 0; tb <= rt / 2; ++tb) {
+            const int p0 = tri_piece_t(2 * tb, rt >> 1), p1 = tri_piece_t(2 * tb + 1, rt >> 1);
+            const f16x8 th = img_cols(T, p0, p1, rt, lane);
+            t = mma16(th, rf[tb].hi, t);
+            t = mma16(th, rf[tb].lo, t);
+            t = mma16(img_cols(T + kPieces * 512, p0, p1, rt, lane), rf[tb].hi, t);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) R[rt][r] = t[r] * pr.inv;
+        mx = abs_max(mx, R[rt]);
+    }
+    const Pow2 pn(tile_max(mx), kOperand);
+    OT *nimg = static_cast<OT *>(a.nimg) + (hi * cts + ct) * kOperandN<IO>;
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb)
+        put_operand<IO, 2>(nimg, R[2 * tb], R[2 * tb + 1], split8(R[2 * tb], R[2 * tb + 1], pn.sc), tb,
+                           1024, lane);
+    // dY as k_delta_grad's operand, and scale tril(Q K^T)^T dY
+    float my = 0.f;
+    mx = 0.f;
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+        const f32x4 d = lds_tile(dY, cols, rt, 16 * wave, lane), f = row4(rows, kFq, rt, lane);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) R[rt][r] = d[r] * f[r];
+        mx = abs_max(mx, R[rt]);
+        my = abs_max(my, d);
+    }
+    const Pow2 pe(col_max(mx)), py(tile_max(my), kOperand);
+    OT *yimg = static_cast<OT *>(a.yimg) + (hi * cts + ct) * 1024;
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb) {
+        rf[tb] = split8(R[2 * tb], R[2 * tb + 1], pe.sc);
+        const f32x4 d0 = lds_tile(dY, cols, 2 * tb, 16 * wave, lane),
+                    d1 = lds_tile(dY, cols, 2 * tb + 1, 16 * wave, lane);
+        put_operand<IO, 1>(yimg, d0, d1, split8(d0, d1, py.sc), tb, 0, lane);
+    }
+    f32x4 *x0 = reinterpret_cast<f32x4 *>(a.x0 + (hi * cts + ct) * (16 * kDC)) + lane;
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) {
+        f32x4 t = tri_t(P, rt, rf, lane);
+        const f32x4 fk = row4(rows, kFk, rt, lane);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) t[r] *= fk[r] * pe.inv;
+        x0[64 * rt] = t;
+    }
+    if (lane == 0) scales[kScS] = ps.inv, scales[kScN] = pn.inv, scales[kScY] = py.inv;
 }
 
-// The same of an inverse, which is kept transposed.
+template <typename IO, int N> struct RevBuf {
+    typedef GroupImg<IO, N> G;
+    typedef HeadImg<IO, true> H;
+    static constexpr int ROWS = H::P - H::R, INV = H::BYTES - H::M;
+    static constexpr int K = 0, Q = G::Q, R = G::BYTES, M = R + ROWS, DY = M + INV;
+    static __host__ __device__ int bytes(int cols) { return DY + kDC * cols * (int)sizeof(IO); }
+};
+
+// Where a chunk's operands of one head and `cols` columns are; back() moves to
+// the chunk in front.
+template <typename IO, int N> struct RevSrc {
+    typedef RevBuf<IO, N> B;
+    const char *grp, *head, *dy;
+    int64_t sg, sh, sy;
+    uint32_t pitch;
+    int rb, len;
+    __device__ RevSrc(const DeltaArgs &a, int64_t bb, int64_t hh, int col0, int cols) {
+        const int64_t ci = bb * a.nc + a.nc - 1, t0 = (a.nc - 1) * kDC;
+        grp = uni(a.gimg + (ci * a.g + hh / (a.h / a.g)) * B::G::BYTES);
+        head = uni(a.himg + (ci * a.h + hh) * a.hstride);
+        const int64_t at = (((bb * a.l + t0) * a.h + hh) * a.p + col0) * (int64_t)sizeof(IO);
+        dy = uni(static_cast<const char *>(a.dy) + at);
+        pitch = (uint32_t)(a.h * a.p * sizeof(IO));
+        sg = a.g * B::G::BYTES, sh = a.h * a.hstride, sy = (int64_t)kDC * pitch;
+        rb = cols * (int)sizeof(IO), len = uni((int)(a.l - t0));
+    }
+    __device__ void back() { grp -= sg, head -= sh, dy -= sy, len = kDC; }
+    __device__ void copy(uint32_t buf, int wave, int nw, int lane) const {
+        copy_image<B::G::BYTES>(grp, buf, wave, nw, lane);
+        copy_image<B::ROWS>(head + B::H::R, buf + B::R, wave, nw, lane);
+        copy_image<B::INV>(head + B::H::M, buf + B::M, wave, nw, lane);
+        copy_rows(dy, pitch, rb, len, buf + B::DY, wave, nw, lane);
+    }
+};
+
+// tri_t of an inverse, which is kept transposed.
 __device__ __forceinline__ f32x4 inv_t(const f16 *M, int jt, const Split *f, int lane) {
     f32x4 t = zero4();
 #pragma unroll
@@ -101,10 +246,78 @@ __device__ __forceinline__ f32x4 inv_t(const f16 *M, int jt, const Split *f, int
     return t;
 }
 
+// What k_delta_mid left of a chunk's 16 columns, and the state in front of it, in
+// registers a chunk ahead; each part is loaded where the one before was used.
+template <typename IO, int N> struct RevAhead {
+    typedef typename GradOp<IO>::type OT;
+    static constexpr bool F32 = sizeof(IO) == 4;
+    static constexpr int NT = N / 16;
+    f32x4 S[NT], g0[4], x0[4], n[F32 ? 4 : 1];
+    f16x8 nh[F32 ? 1 : 2], nl[F32 ? 1 : 2];
+    float ninv;
+    __device__ void load_state(const DeltaArgs &a, int64_t bb, int64_t hh, int64_t c, int col, int lane) {
+        const float *s0 = c ? a.kept + ((bb * a.nc + c - 1) * a.h + hh) * N * a.p
+                            : a.init ? a.init + (bb * a.h + hh) * N * a.p : nullptr;
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            S[x] = zero4();
+            if (s0)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    S[x][r] = s0[(16 * x + 4 * (lane >> 4) + r) * a.p + col + (lane & 15)];
+        }
+    }
+    __device__ void load_x(const DeltaArgs &a, int64_t at, int lane) {
+        const f32x4 *x = reinterpret_cast<const f32x4 *>(a.x0 + at * (16 * kDC)) + lane;
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) x0[rt] = x[64 * rt];
+    }
+    __device__ void load_n(const DeltaArgs &a, int64_t at, int lane) {
+        const f32x4 *k = reinterpret_cast<const f32x4 *>(a.g0 + at * (16 * kDC)) + lane;
+        const OT *v = static_cast<const OT *>(a.nimg) + at * kOperandN<IO> + lane * 8;
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) g0[rt] = k[64 * rt];
+        if constexpr (F32) {
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt)
+                n[rt] = *reinterpret_cast<const f32x4 *>(v + 512 * (rt >> 1) + 4 * (rt & 1));
+        } else {
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) {
+                nh[tb] = *reinterpret_cast<const f16x8 *>(v + 512 * tb);
+                nl[tb] = *reinterpret_cast<const f16x8 *>(v + 1024 + 512 * tb);
+            }
+            ninv = a.scales[at * kScales + kScN];
+        }
+    }
+    __device__ void wait() {
+        landed(S), landed(g0), landed(x0);
+        if constexpr (F32) {
+            landed(n);
+        } else {
+            landed(nh), landed(nl);
+            asm volatile("" : "+v"(ninv));
+        }
+    }
+    __device__ f32x4 rows_n(int rt) const {
+        if constexpr (F32) {
+            return n[rt];
+        } else {
+            f32x4 v;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const f16 h = nh[rt >> 1][4 * (rt & 1) + r], l = nl[rt >> 1][4 * (rt & 1) + r];
+                v[r] = ((float)h + (float)l) * ninv;
+            }
+            return v;
+        }
+    }
+};
+
 template <typename IO, int N, int NB>
-__global__ __launch_bounds__(256, 2) void k_delta_rev(DeltaArgs a) {
+__global__ __launch_bounds__(256, 1) void k_delta_rev(DeltaArgs a) {
     typedef RevBuf<IO, N> B;
-    typedef typename Frag8<IO>::type F;
+    typedef typename GradOp<IO>::type OT;
     constexpr bool F32 = sizeof(IO) == 4;
     constexpr int XB = N / 32, NT = N / 16, IMG = kDC * N;
     extern __shared__ __align__(1024) char lds[];
@@ -131,15 +344,27 @@ __global__ __launch_bounds__(256, 2) void k_delta_rev(DeltaArgs a) {
             for (int r = 0; r < 4; ++r)
                 dS[x][r] = a.dfin[((bb * a.h + hh) * N + 16 * x + 4 * g + r) * a.p + col + j16];
     }
+    landed(dS);
+    // tiles of the chunk in front are `step` further back
+    const int64_t step = a.h * cts;
+    RevAhead<IO, N> in;
+    {
+        const int64_t at = ((bb * a.nc + a.nc - 1) * a.h + hh) * cts + ct;
+        in.load_state(a, bb, hh, a.nc - 1, col, lane);
+        in.load_x(a, at, lane);
+        in.load_n(a, at, lane);
+    }
     for (int64_t c = a.nc - 1; c >= 0; --c) {
         const char *buf = lds + (NB == 2 ? (c & 1) * bufbytes : 0);
-        // the copies of this chunk are older than the last chunk's stores
+        // the copies of this chunk are older than the last chunk's stores (these at
+        // the least: dV, the operands and the tokens' sums)
         if (c == a.nc - 1 || NB == 1)
             vm_wait<0>();
         else
-            vm_wait<16 + (F32 ? 4 : 2) + 8 + 1 + (F32 ? NT : NT / 2)>();
+            vm_wait<16 + (F32 ? 2 * XB : XB) + 4 + 12>();
+        in.wait();
         lds_barrier();
-        const int64_t hi = (bb * a.nc + c) * a.h + hh, t0 = c * kDC;
+        const int64_t hi = (bb * a.nc + c) * a.h + hh, t0 = c * kDC, at = hi * cts + ct;
         const int len = (int)(a.l - t0 < kDC ? a.l - t0 : kDC);
         if (NB == 2 && c > 0) {
             src.back();
@@ -148,50 +373,54 @@ __global__ __launch_bounds__(256, 2) void k_delta_rev(DeltaArgs a) {
         const f16 *K = reinterpret_cast<const f16 *>(buf + B::K);
         const f16 *Q = reinterpret_cast<const f16 *>(buf + B::Q);
         const f16 *M = reinterpret_cast<const f16 *>(buf + B::M);
-        const f16 *P = reinterpret_cast<const f16 *>(buf + B::P);
         const float *rows = reinterpret_cast<const float *>(buf + B::R);
-        const IO *V = reinterpret_cast<const IO *>(buf + B::V);
-        const IO *dY = V + kDC * cols;
+        const IO *dY = reinterpret_cast<const IO *>(buf + B::DY);
+        const float carry = rows[kCarry * kDC];
 
+        // e^{G_C} <S, dS> of these columns
+        {
+            float s = 0.f;
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s = fmaf(in.S[x][r], dS[x][r], s);
+            s = sum16(s);
+            s += __shfl_xor(s, 16);
+            s += __shfl_xor(s, 32);
+            if (lane == 0) a.eend[at] = carry * s;
+            if (c > 0) in.load_state(a, bb, hh, c - 1, col, lane);
+        }
         // the adjoint state behind the chunk: split, and kept for k_delta_grad
         float mx = 0.f;
 #pragma unroll
         for (int x = 0; x < NT; ++x) mx = abs_max(mx, dS[x]);
-        const Pow2 ps(col_max(mx));
+        const Pow2 ps(tile_max(mx), kOperand);
         Split sf[XB];
-        F *ds = reinterpret_cast<F *>(static_cast<IO *>(a.dsimg) + (hi * cts + ct) * (XB * 512)) + lane;
+        OT *ds = static_cast<OT *>(a.dsimg) + at * (XB * 512);
 #pragma unroll
         for (int kb = 0; kb < XB; ++kb) {
             sf[kb] = split8(dS[2 * kb], dS[2 * kb + 1], ps.sc);
-            F f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = (IO)dS[2 * kb + (e >> 2)][e & 3];
-            ds[64 * kb] = f;
+            put_operand<IO, 1>(ds, dS[2 * kb], dS[2 * kb + 1], sf[kb], kb, 0, lane);
         }
-        // dY with scale fq, and with e^G too, under one power of two
-        f32x4 E[4], G[4];
+        // scale e^G dY
+        f32x4 G[4];
         mx = 0.f;
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
-            const f32x4 d = lds_tile(dY, cols, rt, 16 * wave, lane);
-            const f32x4 f = row4(rows, kFq, rt, lane), fr = row4(rows, kReadQ, rt, lane);
+            const f32x4 d = lds_tile(dY, cols, rt, 16 * wave, lane), f = row4(rows, kReadQ, rt, lane);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) E[rt][r] = d[r] * f[r], G[rt][r] = d[r] * fr[r];
-            mx = abs_max(mx, E[rt]);
+            for (int r = 0; r < 4; ++r) G[rt][r] = d[r] * f[r];
+            mx = abs_max(mx, G[rt]);
         }
         const Pow2 pe(col_max(mx));
-        Split ef[2], gf[2];
+        Split gf[2];
 #pragma unroll
-        for (int tb = 0; tb < 2; ++tb) {
-            ef[tb] = split8(E[2 * tb], E[2 * tb + 1], pe.sc);
-            gf[tb] = split8(G[2 * tb], G[2 * tb + 1], pe.sc);
-        }
+        for (int tb = 0; tb < 2; ++tb) gf[tb] = split8(G[2 * tb], G[2 * tb + 1], pe.sc);
         // dU = tril(Q K^T)^T dY + e^{G_C - G} K dS
-        f32x4 U[4];
+        f32x4 U[4], KD[4];
         mx = 0.f;
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
-            const f32x4 x = tri_t(P, rt, ef, lane);
             f32x4 t = zero4();
 #pragma unroll
             for (int kb = 0; kb < XB; ++kb) {
@@ -200,12 +429,15 @@ __global__ __launch_bounds__(256, 2) void k_delta_rev(DeltaArgs a) {
                 t = mma16(k, sf[kb].lo, t);
                 if constexpr (F32) t = mma16(img_rows(K + IMG, rt * XB + kb, lane), sf[kb].hi, t);
             }
-            const f32x4 fk = row4(rows, kFk, rt, lane), wk = row4(rows, kWriteK, rt, lane);
+            const f32x4 wk = row4(rows, kWriteK, rt, lane);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                U[rt][r] = fmaf(fk[r] * pe.inv, x[r], wk[r] * ps.inv * t[r]);
+            for (int r = 0; r < 4; ++r) {
+                KD[rt][r] = wk[r] * ps.inv * t[r];
+                U[rt][r] = in.x0[rt][r] + KD[rt][r];
+            }
             mx = abs_max(mx, U[rt]);
         }
+        if (c > 0) in.load_x(a, at - step, lane);
         // Z, dV = beta Z, and their rows' products
         const Pow2 pu(col_max(mx));
         Split uf[2];
@@ -213,64 +445,48 @@ __global__ __launch_bounds__(256, 2) void k_delta_rev(DeltaArgs a) {
         for (int tb = 0; tb < 2; ++tb) uf[tb] = split8(U[2 * tb], U[2 * tb + 1], pu.sc);
         f32x4 Z[4], W[4];
         mx = 0.f;
+        float mz = 0.f;
         const Rsrc rv = make_rsrc(static_cast<IO *>(a.dv) + ((bb * a.l + t0) * a.h + hh) * a.p + col,
                                   (int64_t)(len - 1) * pitch + 16 * sizeof(IO));
-        float *dvv = a.dvv + (hi * cts + ct) * kDC;
+        float *toks = a.toks + (at * kSums) * kDC;
+        float *scales = a.scales + at * kScales;
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
-            const f32x4 t = inv_t(M, rt, uf, lane);
-            const f32x4 be = row4(rows, kBeta, rt, lane), rk = row4(rows, kReadK, rt, lane);
-            f32x4 d = lds_tile(V, cols, rt, 16 * wave, lane);
+            const f32x4 t = inv_t(M, rt, uf, lane), be = row4(rows, kBeta, rt, lane),
+                        rk = row4(rows, kReadK, rt, lane), gk = in.g0[rt], n = in.rows_n(rt);
+            f32x4 sk, so, sz;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 Z[rt][r] = t[r] * pu.inv;
                 const float v = be[r] * Z[rt][r];
                 W[rt][r] = rk[r] * v;
                 buf_put(rv, (16 * rt + 4 * g + r) * pitch + j16 * sizeof(IO), v, IO{});
-                d[r] = sum16(d[r] * v);
+                sk[r] = sum16(v * gk[r]);
+                so[r] = sum16(be[r] * n[r] * KD[rt][r]);
+                sz[r] = sum16(Z[rt][r] * n[r]);
             }
             mx = abs_max(mx, W[rt]);
-            if (j16 == 0) *reinterpret_cast<f32x4 *>(dvv + 16 * rt + 4 * g) = d;
-        }
-        F *dz = reinterpret_cast<F *>(static_cast<IO *>(a.zimg) + (hi * cts + ct) * (2 * 512)) + lane;
-#pragma unroll
-        for (int tb = 0; tb < 2; ++tb) {
-            F f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = (IO)Z[2 * tb + (e >> 2)][e & 3];
-            dz[64 * tb] = f;
-        }
-        // dbeta's products Z . N
-        {
-            const int64_t at = (hi * cts + ct) * (2 * 512) + 8 * lane;
-            float *o = a.dzn + (hi * cts + ct) * kDC;
-#pragma unroll
-            for (int tb = 0; tb < 2; ++tb) {
-                const F f = *reinterpret_cast<const F *>(static_cast<const IO *>(a.nimg) + at + 512 * tb);
-                F low = f;
-                if constexpr (!F32)
-                    low = *reinterpret_cast<const F *>(static_cast<const IO *>(a.nlow) + at + 512 * tb);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    f32x4 d;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int e = 4 * i + r;
-                        d[r] = sum16(Z[2 * tb + i][r] * (F32 ? (float)f[e] : (float)f[e] + (float)low[e]));
-                    }
-                    if (j16 == 0) *reinterpret_cast<f32x4 *>(o + 16 * (2 * tb + i) + 4 * g) = d;
-                }
+            mz = abs_max(mz, Z[rt]);
+            if (j16 == 0) {
+                float *o = toks + 16 * rt + 4 * g;
+                *reinterpret_cast<f32x4 *>(o + kSumK * kDC) = sk;
+                *reinterpret_cast<f32x4 *>(o + kSumOut * kDC) = so;
+                *reinterpret_cast<f32x4 *>(o + kSumZ * kDC) = sz;
             }
         }
-        // <S', dS> of these columns
-        const float along = state_dot(a.kept + hi * N * a.p + col + j16, a.p, dS, lane);
-        if (lane == 0) a.eend[hi * cts + ct] = along;
+        if (c > 0) in.load_n(a, at - step, lane);
+        const Pow2 pz(tile_max(mz), kOperand);
+        OT *dz = static_cast<OT *>(a.zimg) + at * kOperandN<IO>;
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+            put_operand<IO, 2>(dz, Z[2 * tb], Z[2 * tb + 1], split8(Z[2 * tb], Z[2 * tb + 1], pz.sc), tb,
+                               1024, lane);
+        if (lane == 0) scales[kScD] = ps.inv, scales[kScZ] = pz.inv;
         // dS <- e^{G_C} dS + Q^T (scale e^G dY) - K^T (e^G dV)
         const Pow2 pw(col_max(mx));
         Split wf[2];
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) wf[tb] = split8(W[2 * tb], W[2 * tb + 1], pw.sc);
-        const float carry = rows[kCarry * kDC];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             f32x4 t = zero4(), u = zero4();
@@ -297,11 +513,6 @@ __global__ __launch_bounds__(256, 2) void k_delta_rev(DeltaArgs a) {
             src.copy(base, wave, nw, lane);
         }
     }
-    if (a.init) {
-        const int64_t bh = bb * a.h + hh;
-        const float along = state_dot(a.init + bh * N * a.p + col + j16, a.p, dS, lane);
-        if (lane == 0) a.eend[(a.b * a.nc * a.h + bh) * cts + ct] = along;
-    }
     if (a.dinit) {
         float *dst = a.dinit + (bb * a.h + hh) * N * a.p + col + j16;
 #pragma unroll
@@ -312,11 +523,8 @@ __global__ __launch_bounds__(256, 2) void k_delta_rev(DeltaArgs a) {
 }
 
 // ------------------------------------------------------------- dq and dk ---
-typedef Frag8<bf16>::type bf16x8;
 typedef Frag8<float>::type f32x8;
-__device__ __forceinline__ f32x4 mma8(bf16x8 a, bf16x8 b, f32x4 c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
+__device__ __forceinline__ f32x4 mma8(f16x8 a, f16x8 b, f32x4 c) { return mma16(a, b, c); }
 __device__ __forceinline__ f32x4 mma8(f32x8 a, f32x8 b, f32x4 c) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) c = Mfma<float>::mma(a[e], b[e], c);
@@ -399,26 +607,26 @@ __device__ __forceinline__ f32x4 nat4(const IO *img, int row, int x) {
                    ((row & 15) + 16 * ((x >> 3) & 3)) * 8 + (x & 4));
 }
 
-// A token's gradient through the normalisation (the rows as they were are the
-// image's, r is 1 / norm), and out: four keys per lane and tile.
-template <int NT, typename IO>
-__device__ __forceinline__ void put_rows(f32x4 (&d)[NT], const IO *img, IO *out, float r, int norm,
-                                         bool live, int m, int g) {
+// A token's gradient through the normalisation (k[x] of its rows as the call has
+// them, r is 1 / norm), and out: four keys per lane and tile.
+template <int NT, typename IO, typename F>
+__device__ __forceinline__ void put_rows(f32x4 (&d)[NT], F unit, IO *out, float r, int norm, bool live,
+                                         int g) {
     if (norm) {
         float s = 0.f;
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-            const f32x4 v = nat4<NT / 2>(img, m, 16 * x + 4 * g);
+            const f32x4 v = unit(x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s = fmaf(d[x][i], v[i] * r, s);
+            for (int i = 0; i < 4; ++i) s = fmaf(d[x][i], v[i], s);
         }
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-            const f32x4 v = nat4<NT / 2>(img, m, 16 * x + 4 * g);
+            const f32x4 v = unit(x);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) d[x][i] = r * fmaf(-s, v[i] * r, d[x][i]);
+            for (int i = 0; i < 4; ++i) d[x][i] = r * fmaf(-s, v[i], d[x][i]);
         }
     }
     if (live)
@@ -426,13 +634,44 @@ __device__ __forceinline__ void put_rows(f32x4 (&d)[NT], const IO *img, IO *out,
         for (int x = 0; x < NT; ++x) st4<IO>(out + 16 * x + 4 * g, d[x]);
 }
 
+// Sum over the 16 lanes of a row of lanes, in fp64.
+template <int CTRL> __device__ __forceinline__ double dpp_addd(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xf, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xf, 0xf, true);
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double sum16(double v) {
+    v = dpp_addd<0x128>(v);
+    v = dpp_addd<0x124>(v);
+    v = dpp_addd<0x122>(v);
+    return dpp_addd<0x121>(v);
+}
+
+// Two tiles' operands under powers of two of their own: the product's common
+// power (its inverse) and what a lane's elements of the second operand take to
+// come under it (lane groups 0, 1 hold the first tile's columns, 2, 3 the
+// second's).
+struct Pair {
+    float inv;
+    f16 part;
+    __device__ Pair(const float *s, int x, int y, bool two, int g) {
+        const float e0 = s[x] * s[y], e1 = two ? s[kScales + x] * s[kScales + y] : e0;
+        inv = fmaxf(e0, e1);
+        part = (f16)__builtin_bit_cast(
+            float, __builtin_bit_cast(uint32_t, g < 2 ? e0 : e1) - __builtin_bit_cast(uint32_t, inv) +
+                       0x3f800000u);
+    }
+};
+
 // One stage of k_delta_grad in LDS: 32 value columns of a head (states in front
-// and adjoint states behind as [column][key] images, N and Z as [column][token],
-// rows of dY), or its group's rows of k and q with the head's row arrays.
+// and adjoint states behind as [column][key] images, N, Z and dY as
+// [column][token]), or its group's k and q with the head's row arrays.
 template <typename IO, int N> struct GradBuf {
-    static constexpr int E = (int)sizeof(IO);
-    static constexpr int S = 0, D = S + N * 32 * E, NV = D + N * 32 * E, Z = NV + kDC * 32 * E;
-    static constexpr int DY = Z + kDC * 32 * E, END1 = DY + kDC * 32 * E;
+    typedef GradOp<IO> O;
+    static constexpr int E = (int)sizeof(typename O::type), TOK = kDC * 32 * E;
+    static constexpr int S = 0, D = S + N * 32 * E, NV = D + N * 32 * E, Z = NV + O::PL * TOK;
+    static constexpr int DY = Z + O::PL * TOK, END1 = DY + TOK;
     static constexpr int K = 0, Q = K + kDC * N * E, R = Q + kDC * N * E;
     static constexpr int R2 = R + kRows * kDC * 4, END2 = R2 + kRowsGrad * kDC * 4;
     static constexpr int BYTES = END1 > END2 ? END1 : END2;
@@ -440,10 +679,12 @@ template <typename IO, int N> struct GradBuf {
 
 template <typename IO, int N>
 __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
-    typedef typename Frag8<IO>::type F;
+    typedef typename GradOp<IO>::type OT;
+    typedef typename Frag8<OT>::type F;
     typedef GradBuf<IO, N> B;
     typedef HeadImg<IO, true> H;
-    constexpr int XB = N / 32, NT = N / 16;
+    constexpr bool F32 = sizeof(IO) == 4;
+    constexpr int XB = N / 32, NT = N / 16, PN = 2 * GradOp<IO>::PL;  // pieces of a tile of N or Z
     __shared__ __align__(1024) char lds[2 * B::BYTES];
 
     const int lane = threadIdx.x & 63, w = wave_id(), g = lane >> 4, j16 = lane & 15;
@@ -465,24 +706,28 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
         if (st < slices) {
             const int tiles = cts - 2 * st < 2 ? 1 : 2;
             const int64_t at = hi * cts + 2 * st;
-            copy_lds(static_cast<const IO *>(a.simg) + at * (XB * 512), tiles * XB * 512 * B::E,
-                      N * 32 * B::E, buf + B::S, w, 4, lane);
-            copy_lds(static_cast<const IO *>(a.dsimg) + at * (XB * 512), tiles * XB * 512 * B::E,
-                      N * 32 * B::E, buf + B::D, w, 4, lane);
-            copy_lds(static_cast<const IO *>(a.nimg) + at * 1024, tiles * 1024 * B::E, kDC * 32 * B::E,
-                      buf + B::NV, w, 4, lane);
-            copy_lds(static_cast<const IO *>(a.zimg) + at * 1024, tiles * 1024 * B::E, kDC * 32 * B::E,
-                      buf + B::Z, w, 4, lane);
-            copy_nat<1>(static_cast<const IO *>(a.dy) + ((bb * a.l + t0) * a.h + hh) * a.p + 32 * st,
-                        a.h * a.p, 16 * tiles, len, buf + B::DY, w, lane);
+            const int whole = tiles * XB * 512 * B::E, tok = tiles * 1024 * B::E;
+            copy_lds(static_cast<const OT *>(a.simg) + at * (XB * 512), whole, N * 32 * B::E, buf + B::S,
+                     w, 4, lane);
+            copy_lds(static_cast<const OT *>(a.dsimg) + at * (XB * 512), whole, N * 32 * B::E,
+                     buf + B::D, w, 4, lane);
+            copy_lds(static_cast<const OT *>(a.nimg) + at * kOperandN<IO>, tok * B::O::PL,
+                     B::TOK * B::O::PL, buf + B::NV, w, 4, lane);
+            copy_lds(static_cast<const OT *>(a.zimg) + at * kOperandN<IO>, tok * B::O::PL,
+                     B::TOK * B::O::PL, buf + B::Z, w, 4, lane);
+            copy_lds(static_cast<const OT *>(a.yimg) + at * 1024, tok, B::TOK, buf + B::DY, w, 4, lane);
         } else {
-            copy_nat<XB>(static_cast<const IO *>(a.k) + kq, a.g * N, N, len,
-                         buf + B::K, w, lane);
-            copy_nat<XB>(static_cast<const IO *>(a.q) + kq, a.g * N, N, len,
-                         buf + B::Q, w, lane);
-            copy_image<kRows * kDC * 4>(uni(a.himg + hi * H::BYTES + H::R), buf + B::R, w, 4, lane);
+            if constexpr (F32) {
+                copy_nat<XB>(static_cast<const IO *>(a.k) + kq, a.g * N, N, len, buf + B::K, w, lane);
+                copy_nat<XB>(static_cast<const IO *>(a.q) + kq, a.g * N, N, len, buf + B::Q, w, lane);
+            } else {
+                copy_lds(a.gimg + (ci * a.g + gg) * GroupImg<IO, N>::BYTES, GroupImg<IO, N>::BYTES,
+                         GroupImg<IO, N>::BYTES, buf + B::K, w, 4, lane);
+            }
+            copy_lds(a.himg + hi * a.hstride + H::R, kRows * kDC * 4, kRows * kDC * 4, buf + B::R, w, 4,
+                     lane);
             copy_lds(a.rows2 + hi * (kRowsGrad * kDC), kRowsGrad * kDC * 4, kRowsGrad * kDC * 4,
-                      buf + B::R2, w, 4, lane);
+                     buf + B::R2, w, 4, lane);
         }
     };
 
@@ -504,104 +749,266 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
         if (st == 0) {
             const float *r2 = a.rows2 + hi * (kRowsGrad * kDC) + m;
             const float be =
-                reinterpret_cast<const float *>(a.himg + hi * H::BYTES + H::R)[kBeta * kDC + m];
+                reinterpret_cast<const float *>(a.himg + hi * a.hstride + H::R)[kBeta * kDC + m];
             fq = a.scale * r2[kRead * kDC], fz = -r2[kRead * kDC] * be, fn = r2[kWrite * kDC] * be;
         }
         vm_wait<0>();
         lds_barrier();
         if (q + 1 < ratio * stages) fetch(q + 1);
         if (st < slices) {
-            const IO *S = reinterpret_cast<const IO *>(buf + B::S);
-            const IO *D = reinterpret_cast<const IO *>(buf + B::D);
-            const IO *NV = reinterpret_cast<const IO *>(buf + B::NV);
-            const IO *ZV = reinterpret_cast<const IO *>(buf + B::Z);
-            const IO *DY = reinterpret_cast<const IO *>(buf + B::DY);
-            const F dy = img_rows(DY, w, lane);
-            const F nv = cols_nat(NV, w >> 1, 2, w, lane);
-            const F zv = cols_nat(ZV, w >> 1, 2, w, lane);
+            const OT *S = reinterpret_cast<const OT *>(buf + B::S);
+            const OT *D = reinterpret_cast<const OT *>(buf + B::D);
+            const OT *NV = reinterpret_cast<const OT *>(buf + B::NV);
+            const OT *ZV = reinterpret_cast<const OT *>(buf + B::Z);
+            const OT *DY = reinterpret_cast<const OT *>(buf + B::DY);
+            const F dy = cols_nat(DY, w >> 1, 2, w, lane), nv = cols_nat(NV, w >> 1, PN, w, lane),
+                    zv = cols_nat(ZV, w >> 1, PN, w, lane);
+            const float *sc = a.scales + (hi * cts + 2 * st) * kScales;
+            const bool two = cts - 2 * st > 1;
+            float gq = fq, gz = fz, gn = fn;
+            F dys = dy, zvs = zv, nvd = nv;
+            if constexpr (!F32) {
+                const Pair sy(sc, kScS, kScY, two, g), sz(sc, kScS, kScZ, two, g),
+                    dn(sc, kScD, kScN, two, g);
+                dys = dy * sy.part, zvs = zv * sz.part, nvd = nv * dn.part;
+                gq *= sy.inv, gz *= sz.inv, gn *= dn.inv;
+            }
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
                 const F s = cols_nat(S, x >> 1, XB, x, lane);
                 const F d = cols_nat(D, x >> 1, XB, x, lane);
-                const f32x4 t = mma8(s, dy, zero4()), u = mma8(s, zv, zero4()),
-                            v = mma8(d, nv, zero4());
+                const f32x4 t = mma8(s, dys, zero4()), u = mma8(s, zvs, zero4()),
+                            v = mma8(d, nvd, zero4());
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    dQ[x][r] = fmaf(fq, t[r], dQ[x][r]);
-                    dK[x][r] = fmaf(fz, u[r], fmaf(fn, v[r], dK[x][r]));
+                    dQ[x][r] = fmaf(gq, t[r], dQ[x][r]);
+                    dK[x][r] = fmaf(gz, u[r], fmaf(gn, v[r], dK[x][r]));
                 }
                 if (x & 1) sched_fence();
             }
+            F dyn = dy, zvn = zv, zvl = zv, nvy = nv, nvz = nv;
+            float ny = 1.f, nz = 1.f;
+            if constexpr (!F32) {
+                const Pair py(sc, kScN, kScY, two, g), pz(sc, kScN, kScZ, two, g);
+                dyn = dy * py.part, zvn = zv * pz.part, nvy = nv * py.part, nvz = nv * pz.part;
+                zvl = cols_nat(ZV, 2 + (w >> 1), PN, w, lane) * pz.part;
+                ny = py.inv, nz = pz.inv;
+            }
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
-                if (rt <= w) {
-                    const F n = cols_nat(NV, rt >> 1, 2, rt, lane);
-                    X[rt] = mma8(n, dy, X[rt]);
-                    Y[rt] = mma8(n, zv, Y[rt]);
+                if (rt <= w) {  // the decays' gradient needs these: both terms
+                    const F n = cols_nat(NV, rt >> 1, PN, rt, lane);
+                    f32x4 t = mma8(n, dyn, zero4()), u = mma8(n, zvn, zero4());
+                    if constexpr (!F32) {
+                        const F l = cols_nat(NV, 2 + (rt >> 1), PN, rt, lane);
+                        t = mma8(l, dyn, t);
+                        u = mma8(n, zvl, u);
+                        u = mma8(l, zvn, u);
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        X[rt][r] = fmaf(ny, t[r], X[rt][r]), Y[rt][r] = fmaf(nz, u[r], Y[rt][r]);
                 }
                 if (rt >= w) {
-                    const F d = img_rows(DY, rt, lane);
-                    const F z = cols_nat(ZV, rt >> 1, 2, rt, lane);
-                    if (rt == w) {
-                        Xd = mma8(d, nv, Xd);
-                        Yd = mma8(z, nv, Yd);
-                    } else {
-                        X[rt] = mma8(d, nv, X[rt]);
-                        Y[rt] = mma8(z, nv, Y[rt]);
+                    const F d = cols_nat(DY, rt >> 1, 2, rt, lane);
+                    const F z = cols_nat(ZV, rt >> 1, PN, rt, lane);
+                    const f32x4 t = mma8(d, nvy, zero4()), u = mma8(z, nvz, zero4());
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        if (rt == w)
+                            Xd[r] = fmaf(ny, t[r], Xd[r]), Yd[r] = fmaf(nz, u[r], Yd[r]);
+                        else
+                            X[rt][r] = fmaf(ny, t[r], X[rt][r]), Y[rt][r] = fmaf(nz, u[r], Y[rt][r]);
                     }
                 }
+                sched_fence();
             }
             continue;
         }
         // decays, masks and factors; rows j in front of this token give dq, rows
         // behind it dk, both give (X + X^T) K
-        const IO *K = reinterpret_cast<const IO *>(buf + B::K);
-        const IO *Q = reinterpret_cast<const IO *>(buf + B::Q);
-        const float *bet = reinterpret_cast<const float *>(buf + B::R) + kBeta * kDC;
+        const OT *K = reinterpret_cast<const OT *>(buf + B::K);
+        const OT *Q = reinterpret_cast<const OT *>(buf + B::Q);
+        const float *rows = reinterpret_cast<const float *>(buf + B::R);
         const float *r2 = reinterpret_cast<const float *>(buf + B::R2);
-        F bq[2], bk[2], bs[2];
-        const float hm = r2[kGhi * kDC + m], lm = r2[kGlo * kDC + m], dm = r2[kDoc * kDC + m];
-        const float bm = bet[m];
+        // the rows of k and q are the image's times these
+        const auto of_k = [&](int rt) { return F32 ? row4(r2, kRk, rt, lane) : row4(rows, kFk, rt, lane); };
+        const auto of_q = [&](int rt) {  // and scale
+            f32x4 f = F32 ? row4(r2, kRq, rt, lane) : row4(rows, kFq, rt, lane);
+            if constexpr (F32)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) f[r] *= a.scale;
+            return f;
+        };
+        const float bm = rows[kBeta * kDC + m];
+        f32x4 Dj[4];
+        {
+            const float hm = r2[kGhi * kDC + m], lm = r2[kGlo * kDC + m], dm = r2[kDoc * kDC + m];
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                const f32x4 gh = row4(r2, kGhi, rt, lane), gl = row4(r2, kGlo, rt, lane),
+                            dj = row4(r2, kDoc, rt, lane);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float G = (gh[r] - hm) + (gl[r] - lm);
+                    const float e = exp2_fast(16 * rt + 4 * g + r > m ? G : -G);
+                    Dj[rt][r] = dj[r] == dm ? e : 0.f;
+                }
+            }
+        }
+        // the terms of the decays' gradient inside the chunk, C_mj for j < m
+        {
+            const float fkm = F32 ? r2[kRk * kDC + m] : rows[kFk * kDC + m];
+            const float fqm = F32 ? a.scale * r2[kRq * kDC + m] : rows[kFq * kDC + m];
+            double sum = 0.0;
+            double *cells = a.cells + hi * (5 * kDC);
+#pragma unroll
+            for (int rt = 0; rt < 4; ++rt) {
+                double col[4] = {0.0, 0.0, 0.0, 0.0};
+                if (rt <= w) {
+                    f32x4 kk = zero4(), qk = zero4();
+#pragma unroll
+                    for (int kb = 0; kb < XB; ++kb) {
+                        const F kj = img_rows(K, rt * XB + kb, lane);
+                        qk = mma8(kj, img_rows(Q, w * XB + kb, lane), qk);
+                        kk = mma8(kj, img_rows(K, w * XB + kb, lane), kk);
+                    }
+                    const f32x4 bj = row4(rows, kBeta, rt, lane), fk = of_k(rt);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int j = 16 * rt + 4 * g + r;
+                        // the rows' factors first: q k and X are as large as the
+                        // squares of the inputs
+                        const float cell = bj[r] * Dj[rt][r] *
+                                           (X[rt][r] * (fk[r] * (fqm * qk[r])) -
+                                            bm * Y[rt][r] * (fk[r] * (fkm * kk[r])));
+                        const double v = j < m ? (double)cell : 0.0;
+                        sum += v;
+                        col[r] = sum16(v);
+                    }
+                }
+                if (j16 == 0)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) cells[(1 + w) * kDC + 16 * rt + 4 * g + r] = col[r];
+                sched_fence();
+            }
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (g == 0) cells[m] = sum;
+        }
+        // the masked products as operands, each token's under a power of two
+        const auto put = [&](F (&f)[2], const f32x4 (&v)[4]) {
+            if constexpr (F32) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) f[e >> 3][e & 7] = v[e >> 2][e & 3];
+                return 1.f;
+            } else {
+                float mx = 0.f;
+#pragma unroll
+                for (int rt = 0; rt < 4; ++rt) mx = abs_max(mx, v[rt]);
+                const Pow2 p(col_max(mx));
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const f16x2 h = __builtin_convertvector(
+                        f32x2{v[e >> 2][e & 3] * p.sc, v[e >> 2][(e & 3) + 1] * p.sc}, f16x2);
+                    f[e >> 3][e & 7] = h[0], f[e >> 3][(e & 7) + 1] = h[1];
+                }
+                return p.inv;
+            }
+        };
+        const auto kcols = [&](const OT *img, int tb, int x) {
+            if constexpr (F32)
+                return nat_cols<XB>(img, 2 * tb, x, lane);
+            else
+                return img_cols(img, 2 * tb * XB + (x >> 1), (2 * tb + 1) * XB + (x >> 1), x, lane);
+        };
+        f32x4 v[4];
+        F f[2];
+        // dQ += K^T (rows j <= m of dY U^T)
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
-            const f32x4 gh = row4(r2, kGhi, rt, lane), gl = row4(r2, kGlo, rt, lane),
-                        dj = row4(r2, kDoc, rt, lane), rk = row4(r2, kRk, rt, lane),
-                        rq = row4(r2, kRq, rt, lane), bj = row4(bet, 0, rt, lane);
+            const f32x4 bj = row4(rows, kBeta, rt, lane), fk = of_k(rt);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                v[rt][r] = rt <= w && 16 * rt + 4 * g + r <= m
+                               ? a.scale * bj[r] * fk[r] * Dj[rt][r] * X[rt][r] : 0.f;
+        }
+        float inv = put(f, v);
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            f32x4 t = mma8(kcols(K, 0, x), f[0], zero4());
+            if (w >> 1) t = mma8(kcols(K, 1, x), f[1], t);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dQ[x][r] = fmaf(inv, t[r], dQ[x][r]);
+            if (x & 1) sched_fence();
+        }
+        // dK += Q^T (rows i >= m of it)
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            const f32x4 fqr = of_q(rt);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int j = 16 * rt + 4 * g + r, e = 4 * (rt & 1) + r;
-                const float G = (gh[r] - hm) + (gl[r] - lm);
-                const float D = dj[r] == dm ? exp2_fast(j > m ? G : -G) : 0.f;
-                const float up = rt > w ? 0.f : X[rt][r], lo = rt < w ? 0.f : rt == w ? Xd[r] : X[rt][r];
-                const float yu = rt > w ? 0.f : Y[rt][r], yl = rt < w ? 0.f : rt == w ? Yd[r] : Y[rt][r];
-                bq[rt >> 1][e] = (IO)(j <= m ? a.scale * bj[r] * rk[r] * D * up : 0.f);
-                bk[rt >> 1][e] = (IO)(j >= m ? a.scale * bm * rq[r] * D * lo : 0.f);
-                bs[rt >> 1][e] = (IO)(j == m ? 0.f : -bj[r] * bm * rk[r] * D * (j < m ? yu : yl));
+                const float xv = rt == w ? Xd[r] : X[rt][r];
+                v[rt][r] = rt >= w && 16 * rt + 4 * g + r >= m ? bm * fqr[r] * Dj[rt][r] * xv : 0.f;
             }
-            sched_fence();
+        }
+        inv = put(f, v);
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            f32x4 t = mma8(kcols(Q, 1, x), f[1], zero4());
+            if (!(w >> 1)) t = mma8(kcols(Q, 0, x), f[0], t);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dK[x][r] = fmaf(inv, t[r], dK[x][r]);
+            if (x & 1) sched_fence();
+        }
+        // dK -= K^T (dV U^T and its transpose)
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+            const f32x4 bj = row4(rows, kBeta, rt, lane), fk = of_k(rt);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int j = 16 * rt + 4 * g + r;
+                const float yv = rt == w && j > m ? Yd[r] : Y[rt][r];
+                v[rt][r] = j == m ? 0.f : -bj[r] * bm * fk[r] * Dj[rt][r] * yv;
+            }
+        }
+        inv = put(f, v);
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+            f32x4 t = mma8(kcols(K, 0, x), f[0], zero4());
+            t = mma8(kcols(K, 1, x), f[1], t);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dK[x][r] = fmaf(inv, t[r], dK[x][r]);
+            if (x & 1) sched_fence();
         }
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) X[rt] = Y[rt] = zero4();
         Xd = Yd = zero4();
-#pragma unroll
-        for (int x = 0; x < NT; ++x) {
-#pragma unroll
-            for (int tb = 0; tb < 2; ++tb) {
-                const F k = nat_cols<XB>(K, 2 * tb, x, lane);
-                if (tb <= w >> 1) dQ[x] = mma8(k, bq[tb], dQ[x]);
-                dK[x] = mma8(k, bs[tb], dK[x]);
-                if (tb >= w >> 1) dK[x] = mma8(nat_cols<XB>(Q, 2 * tb, x, lane), bk[tb], dK[x]);
-            }
-            if (x & 1) sched_fence();
-        }
     }
     const char *buf = lds + ((ratio * stages - 1) & 1) * B::BYTES;
+    const float *rows = reinterpret_cast<const float *>(buf + B::R);
     const float *r2 = reinterpret_cast<const float *>(buf + B::R2);
     const int64_t at = ((bb * a.l + t0 + m) * a.g + gg) * N;
-    put_rows<NT>(dK, reinterpret_cast<const IO *>(buf + B::K), static_cast<IO *>(a.dk) + at,
-                 r2[kRk * kDC + m], a.norm, live, m, g);
-    put_rows<NT>(dQ, reinterpret_cast<const IO *>(buf + B::Q), static_cast<IO *>(a.dq) + at,
-                 r2[kRq * kDC + m], a.norm, live, m, g);
+    const float rk = r2[kRk * kDC + m], rq = r2[kRq * kDC + m];
+    // k and q as the rule has them, from their images
+    const float fk = F32 ? rk : rows[kFk * kDC + m], fqr = F32 ? rq : rows[kRawQ * kDC + m];
+    const auto unit = [&](const OT *img, float f, int x) {
+        f32x4 v;
+        if constexpr (F32) {
+            v = nat4<XB>(img, m, 16 * x + 4 * g);
+        } else {
+            const f16x4 h = *reinterpret_cast<const f16x4 *>(img + img_at(m, 16 * x + 4 * g, XB));
+            v = f32x4{(float)h[0], (float)h[1], (float)h[2], (float)h[3]};
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] *= f;
+        return v;
+    };
+    const OT *K = reinterpret_cast<const OT *>(buf + B::K), *Q = reinterpret_cast<const OT *>(buf + B::Q);
+    put_rows<NT>(dK, [&](int x) { return unit(K, fk, x); }, static_cast<IO *>(a.dk) + at, rk, a.norm, live,
+                 g);
+    put_rows<NT>(dQ, [&](int x) { return unit(Q, fqr, x); }, static_cast<IO *>(a.dq) + at, rq, a.norm,
+                 live, g);
 }
 
 // The gradients of dt and beta, a wave per chunk and head, a lane per token.
@@ -611,43 +1018,31 @@ template <typename IO> __global__ __launch_bounds__(256) void k_delta_dt(DeltaAr
     if (hi >= a.b * a.nc * a.h) return;
     const int64_t hh = hi % a.h, ci = hi / a.h, c = ci % a.nc, bb = ci / a.nc, t0 = c * kDC;
     const int len = (int)(a.l - t0 < kDC ? a.l - t0 : kDC);
-    double s = 0.0, e = 0.0, zn = 0.0;
+    // tokens from this one on, and columns in front of it
+    double s = 0.0, out = 0.0, zn = 0.0, e = 0.0;
     for (int t = 0; t < cts; ++t) {
-        const int64_t at = hi * cts + t;
-        s += (double)a.doo[at * kDC + lane] - (double)a.dvv[at * kDC + lane];
-        zn += (double)a.dzn[at * kDC + lane];
-        e += (double)a.eend[at];
+        const float *k = a.toks + ((hi * cts + t) * kSums) * kDC + lane;
+        s += (double)k[kSumQ * kDC] - (double)k[kSumK * kDC];
+        out += (double)k[kSumOut * kDC];
+        zn += (double)k[kSumZ * kDC];
+        e += (double)a.eend[hi * cts + t];
     }
+    const double *cells = a.cells + hi * (5 * kDC) + lane;
+    s += cells[0] - ((cells[kDC] + cells[2 * kDC]) + (cells[3 * kDC] + cells[4 * kDC]));
+    const double own = out;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const double u = __shfl_down(s, o), v = __shfl_up(out, o);
+        if (lane + o < 64) s += u;
+        if (lane >= o) out += v;
+    }
+    s += (out - own) + e;
     const float *r2 = a.rows2 + hi * (kRowsGrad * kDC);
     const float doc = r2[kDoc * kDC + lane], front = lane ? r2[kDoc * kDC + lane - 1] : 0.f;
     const float step = r2[kStep * kDC + lane];
-    // Nothing decays in front of a document's first token or of a zero state, and
-    // what is left of a decay below 2^-21 is less than the sums' roundings: the
-    // gradient there is zero, and sums do not cross it.
     const bool in = lane < len;
-    const bool first = doc != front || (in && a.A[hh] * step < -14.6f);
-    const uint64_t cuts = __ballot(first);
-    const uint64_t upto = cuts & (~0ull >> (63 - lane)), beyond = lane < 63 ? cuts >> (lane + 1) : 0;
-    const int start = upto ? 63 - __clzll((long long)upto) : 0;
-    int stop = beyond ? lane + 1 + __ffsll((long long)beyond) - 1 : 64;
-    // what follows the token up to the next such one
-    if (lane == 63) s += e;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double u = __shfl_down(s, o);
-        if (lane + o < stop) s += u;
-    }
-    // In front of the first token of such a run the sum is known: zero, or <S, dS>
-    // in front of the chunk.  What it has instead is the roundings', which are
-    // spread over the run.
-    double known = 0.0;
-    if (c || a.init)
-        for (int t = 0; t < cts; ++t)
-            known += (double)a.eend[(c ? hi - a.h : a.b * a.nc * a.h + bb * a.h + hh) * cts + t];
-    stop = stop < len ? stop : len;
-    const double off = __shfl(s, start) - (upto ? 0.0 : known);
-    if (in) s -= off * (double)(stop - lane) / (double)(stop - start);
-    const bool none = first || (t0 + lane == 0 && !a.init);
+    // nothing decays in front of a document's first token or of a zero state
+    const bool none = doc != front || (t0 + lane == 0 && !a.init);
     const int64_t at = (bb * a.l + t0 + lane) * a.h + hh;
     const double dg = !in || none ? 0.0 : s;
     const float z = in ? to_f32(static_cast<const IO *>(a.dt)[at]) + (a.bias ? a.bias[hh] : 0.f) : 0.f;
@@ -681,15 +1076,19 @@ __global__ __launch_bounds__(64) void k_delta_sum(DeltaArgs a) {
 }
 
 template <typename IO, int N> hipError_t bwd_n(const DeltaArgs &a, hipStream_t s) {
-    typedef RevBuf<IO, N> B;
-    const int nw = a.p >= 64 ? 4 : a.p / 16, one = B::bytes(16 * nw);
-    const dim3 grid((unsigned)(a.b * a.h * (a.p / (16 * nw)))), block(64 * nw);
+    const int nw = a.p >= 64 ? 4 : a.p / 16;
+    const int64_t walks = a.b * a.h * (a.p / (16 * nw));
+    int rw = nw;
+    while (rw > 1 && a.b * a.h * (a.p / (16 * rw)) < device_cus()) rw >>= 1;
+    const int one = RevBuf<IO, N>::bytes(16 * rw);
     const bool two = 2 * one <= kLdsMost;
-    auto *k = two ? &k_delta_rev<IO, N, 2> : &k_delta_rev<IO, N, 1>;
-    hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k),
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, kLdsMost);
+    hipError_t e = launch(&k_delta_mid<IO, N>, walks * a.nc, 64 * nw,
+                          FwdBuf<IO, N, true>::bytes(16 * nw), a, s);
+    if (e == hipSuccess)
+        e = launch(two ? &k_delta_rev<IO, N, 2> : &k_delta_rev<IO, N, 1>,
+                   a.b * a.h * (a.p / (16 * rw)), 64 * rw,
+                   two ? 2 * one : one, a, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k, grid, block, two ? 2 * one : one, s, a);
     hipLaunchKernelGGL((k_delta_grad<IO, N>), dim3((unsigned)(a.b * a.nc * a.g)), dim3(256), 0, s, a);
     hipLaunchKernelGGL(k_delta_dt<IO>, dim3((unsigned)((a.b * a.nc * a.h + 3) / 4)), dim3(256), 0, s, a);
     hipLaunchKernelGGL(k_delta_sum, dim3((unsigned)a.h), dim3(64), 0, s, a);

@@ -16,13 +16,10 @@
 #include "ssd_delta.hpp"
 
 #include <math.h>
-#include <stdlib.h>
 
 #include "../../include/ssd.h"
 
 namespace ssd {
-
-int device_cus();
 
 namespace {
 
@@ -234,7 +231,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
     for (int64_t hh = gg * ratio + part * hs; hh < gg * ratio + (part + 1) * hs; ++hh) {
         typedef HeadImg<IO, GRAD> H;
         const int64_t hi = ci * a.h + hh;
-        char *himg = a.himg + hi * H::BYTES;
+        char *himg = a.himg + hi * a.hstride;
         float *rows = reinterpret_cast<float *>(himg + H::R);
         // decays: a lane per token
         float bound;
@@ -275,6 +272,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
             r[kReadQ * kDC] = a.scale * rd * fq;
             r[kFq * kDC] = a.scale * fq;
             r[kBeta * kDC] = be;
+            r[kRawQ * kDC] = fq;
             const float most = wave_max(rd * fabsf(fk)), load = wave_max(fabsf(be * fk));
             if (lane == 0) r[kCarry * kDC] = cuts ? 0.f : exp2_d(end), r[kCarry * kDC + 1] = most;
             bound = 64.f * load;
@@ -394,55 +392,11 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
 }
 
 // --------------------------------------------------------------- forward ---
-// One buffer of LDS: images of k and q, T, tril(Q K^T), the row arrays, then
-// the 64 rows of v (and of dy) of the workgroup's columns.
-template <typename IO, int N, bool GRAD> struct FwdBuf {
-    typedef GroupImg<IO, N> G;
-    typedef HeadImg<IO, GRAD> H;
-    static constexpr int K = 0, Q = G::Q, HEAD = H::M;  // what the scan copies of a head's image
-    static constexpr int T = G::BYTES + H::T, R = G::BYTES + H::R, P = G::BYTES + H::P;
-    static constexpr int V = G::BYTES + HEAD;
-    static __host__ __device__ int bytes(int cols) {
-        return V + (GRAD ? 2 : 1) * kDC * cols * (int)sizeof(IO);
-    }
-};
-
-// Where a chunk's operands of one head and `cols` columns are; next() moves on by
-// one chunk.
-template <typename IO, int N, bool GRAD> struct FwdSrc {
-    typedef FwdBuf<IO, N, GRAD> B;
-    const char *grp, *head, *v, *dy;
-    int64_t sg, sh, sv;
-    uint32_t pitch;
-    int rb, left;  // bytes of a row, tokens from here on
-    __device__ FwdSrc(const DeltaArgs &a, int64_t bb, int64_t c, int64_t hh, int col0, int cols) {
-        const int64_t ci = bb * a.nc + c, t0 = c * kDC;
-        grp = uni(a.gimg + (ci * a.g + hh / (a.h / a.g)) * B::G::BYTES);
-        head = uni(a.himg + (ci * a.h + hh) * B::H::BYTES);
-        const int64_t at = (((bb * a.l + t0) * a.h + hh) * a.p + col0) * (int64_t)sizeof(IO);
-        v = uni(static_cast<const char *>(a.v) + at);
-        dy = GRAD ? uni(static_cast<const char *>(a.dy) + at) : nullptr;
-        pitch = (uint32_t)(a.h * a.p * sizeof(IO));
-        sg = a.g * B::G::BYTES, sh = a.h * B::H::BYTES, sv = (int64_t)kDC * pitch;
-        rb = cols * (int)sizeof(IO);
-        left = uni((int)(a.l - t0));
-    }
-    __device__ void next() { grp += sg, head += sh, v += sv, dy += sv, left -= kDC; }
-    __device__ void copy(uint32_t buf, int wave, int nw, int lane) const {
-        copy_image<B::G::BYTES>(grp, buf, wave, nw, lane);
-        copy_image<B::HEAD>(head, buf + B::G::BYTES, wave, nw, lane);
-        const int len = left < kDC ? left : kDC;
-        copy_rows(v, pitch, rb, len, buf + B::V, wave, nw, lane);
-        if constexpr (GRAD) copy_rows(dy, pitch, rb, len, buf + B::V + kDC * rb, wave, nw, lane);
-    }
-};
-
-// SERIAL: a workgroup walks all chunks of a head's columns; otherwise each
-// chunk has a workgroup of its own, started from the kept states (gradient).
-template <typename IO, int N, bool GRAD, bool SERIAL, int NB>
+// A workgroup walks all chunks of a head's columns.
+template <typename IO, int N, int NB>
 __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
-    typedef FwdBuf<IO, N, GRAD> B;
-    constexpr bool F32 = sizeof(IO) == 4, FULL = F32 || GRAD;
+    typedef FwdBuf<IO, N, false> B;
+    constexpr bool F32 = sizeof(IO) == 4;
     constexpr int XB = N / 32, NT = N / 16, IMG = kDC * N;
     extern __shared__ __align__(1024) char lds[];
     const int lane = threadIdx.x & 63, wave = wave_id(), nw = blockDim.x >> 6;
@@ -451,47 +405,34 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
     int64_t item = xcd_item(blockIdx.x, gridDim.x);
     const int col0 = (int)(item % slices) * cols;
     item /= slices;
-    const int64_t hh = item % a.h;
-    item /= a.h;
-    const int64_t c0 = SERIAL ? 0 : item % a.nc, bb = SERIAL ? item : item / a.nc;
-    const int64_t c1 = SERIAL ? a.nc : c0 + 1;
-    const int col = col0 + 16 * wave, ct = col >> 4;
+    const int64_t hh = item % a.h, bb = item / a.h;
+    const int col = col0 + 16 * wave;
     const int bufbytes = B::bytes(cols);
     const uint32_t base = lds_address(lds);
 
-    FwdSrc<IO, N, GRAD> src(a, bb, c0, hh, col0, cols);
+    FwdSrc<IO, N, false> src(a, bb, 0, hh, col0, cols);
     src.copy(base, wave, nw, lane);
     f32x4 S[NT];
-    {
-        const float *src = nullptr;
-        if (SERIAL || c0 == 0) {
-            if (a.init) src = a.init + (bb * a.h + hh) * N * a.p;
-        } else {
-            src = a.kept + ((bb * a.nc + c0 - 1) * a.h + hh) * N * a.p;
-        }
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-            S[x] = zero4();
-            if (src)
+    for (int x = 0; x < NT; ++x) {
+        S[x] = zero4();
+        if (a.init)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[x][r] = src[(16 * x + 4 * g + r) * a.p + col + j16];
-        }
+            for (int r = 0; r < 4; ++r)
+                S[x][r] = a.init[((bb * a.h + hh) * N + 16 * x + 4 * g + r) * a.p + col + j16];
     }
-    for (int64_t c = c0; c < c1; ++c) {
-        const char *buf = lds + (NB == 2 ? ((c - c0) & 1) * bufbytes : 0);
+    landed(S);
+    for (int64_t c = 0; c < a.nc; ++c) {
+        const char *buf = lds + (NB == 2 ? (c & 1) * bufbytes : 0);
         // the copies of this chunk are older than the last chunk's stores
-        if (c == c0)
+        if (c == 0 || NB == 1)
             vm_wait<0>();
-        else if (NB == 1)
-            vm_wait<0>();
-        else if (!GRAD)
-            a.states ? vm_wait<16 + 4 * NT>() : vm_wait<16>();
         else
-            vm_wait<(F32 ? 2 * XB : XB) + 4 + 4 + 4 * NT>();
+            a.states ? vm_wait<16 + 4 * NT>() : vm_wait<16>();
         lds_barrier();
-        if (NB == 2 && c + 1 < c1) {
+        if (NB == 2 && c + 1 < a.nc) {
             src.next();
-            src.copy(base + ((c + 1 - c0) & 1) * bufbytes, wave, nw, lane);
+            src.copy(base + ((c + 1) & 1) * bufbytes, wave, nw, lane);
         }
         const f16 *K = reinterpret_cast<const f16 *>(buf + B::K);
         const f16 *Q = reinterpret_cast<const f16 *>(buf + B::Q);
@@ -511,14 +452,6 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
 #pragma unroll
         for (int kb = 0; kb < XB; ++kb) {
             sf[kb] = split8(S[2 * kb], S[2 * kb + 1], ps.sc);
-            if constexpr (GRAD) {  // the state in front, as the gradient's operand
-                typedef typename Frag8<IO>::type F;
-                F f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = (IO)S[2 * kb + (e >> 2)][e & 3];
-                reinterpret_cast<F *>(static_cast<IO *>(a.simg) +
-                                      (hi * (a.p >> 4) + ct) * (XB * 512))[64 * kb + lane] = f;
-            }
         }
         f32x4 R[4], Y[4];
 #pragma unroll
@@ -545,7 +478,6 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
         for (int tb = 0; tb < 2; ++tb) rf[tb] = split8(R[2 * tb], R[2 * tb + 1], pr.sc);
         f32x4 U[4], W[4];
         mx = 0.f;
-        f32x4 Nv[4];
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
             f32x4 t = zero4();
@@ -562,7 +494,6 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const float v = t[r] * pr.inv;
-                Nv[rt][r] = v;
                 U[rt][r] = v * be[r] * fk[r];
                 W[rt][r] = v * be[r] * wk[r];
             }
@@ -571,7 +502,7 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
         // e^{G_C - G} <= 1, so one power of two serves both
         const Pow2 pu(col_max(mx));
         const float carry = rows[kCarry * kDC];
-        if (SERIAL) {
+        {
             Split wf[2];
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) wf[tb] = split8(W[2 * tb], W[2 * tb + 1], pu.sc);
@@ -601,14 +532,14 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
             for (int kb = 0; kb < XB; ++kb) {
                 const f16x8 q = img_rows(Q, rt * XB + kb, lane);
                 t = mma16(q, sf[kb].hi, t);
-                if constexpr (FULL) t = mma16(q, sf[kb].lo, t);
+                if constexpr (F32) t = mma16(q, sf[kb].lo, t);
                 if constexpr (F32) t = mma16(img_rows(Q + IMG, rt * XB + kb, lane), sf[kb].hi, t);
             }
 #pragma unroll
             for (int tb = 0; tb <= rt / 2; ++tb) {
                 const f16x8 p = img_rows(P, tri_piece(rt, tb), lane);
                 u = mma16(p, uf[tb].hi, u);
-                if constexpr (FULL) {
+                if constexpr (F32) {
                     u = mma16(p, uf[tb].lo, u);
                     u = mma16(img_rows(P + kPieces * 512, tri_piece(rt, tb), lane), uf[tb].hi, u);
                 }
@@ -618,7 +549,7 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
             for (int r = 0; r < 4; ++r)
                 Y[rt][r] = fmaf(fr[r] * ps.inv, t[r], fp[r] * pu.inv * u[r]);
         }
-        if constexpr (!GRAD) {
+        {
             const uint32_t pitch = (uint32_t)(a.h * a.p * sizeof(IO));
             const Rsrc ry = make_rsrc(static_cast<IO *>(a.y) +
                                           ((bb * a.l + t0) * a.h + hh) * a.p + col,
@@ -628,34 +559,8 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     buf_put(ry, (16 * rt + 4 * g + r) * pitch + j16 * sizeof(IO), Y[rt][r], IO{});
-        } else {
-            // N, as the gradient's operand type, in fragment order; with bf16 the
-            // remainder too, for dbeta
-            typedef typename Frag8<IO>::type F;
-            const int64_t at = (hi * (a.p >> 4) + ct) * (2 * 512) + 8 * lane;
-#pragma unroll
-            for (int tb = 0; tb < 2; ++tb) {
-                F f, low;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float v = Nv[2 * tb + (e >> 2)][e & 3];
-                    f[e] = (IO)v;
-                    if constexpr (!F32) low[e] = (IO)(v - (float)f[e]);
-                }
-                *reinterpret_cast<F *>(static_cast<IO *>(a.nimg) + at + 512 * tb) = f;
-                if constexpr (!F32) *reinterpret_cast<F *>(static_cast<IO *>(a.nlow) + at + 512 * tb) = low;
-            }
-            const IO *dY = V + kDC * cols;
-            float *o = a.doo + (hi * (a.p >> 4) + ct) * kDC;
-#pragma unroll
-            for (int rt = 0; rt < 4; ++rt) {
-                f32x4 d = lds_tile(dY, cols, rt, 16 * wave, lane);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) d[r] = sum16(d[r] * Y[rt][r]);
-                if (j16 == 0) *reinterpret_cast<f32x4 *>(o + 16 * rt + 4 * g) = d;
-            }
         }
-        if (SERIAL && a.states) {
+        if (a.states) {
             float *st = a.states + hi * N * a.p + col;
             const Rsrc rs = make_rsrc(st, ((int64_t)(N - 1) * a.p + 16) * 4);
 #pragma unroll
@@ -664,13 +569,13 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
                 for (int r = 0; r < 4; ++r)
                     buf_put(rs, (uint32_t)(((16 * x + 4 * g + r) * a.p + j16) * 4), S[x][r], 0.f);
         }
-        if (NB == 1 && c + 1 < c1) {
+        if (NB == 1 && c + 1 < a.nc) {
             lds_barrier();  // everyone is done with the buffer
             src.next();
             src.copy(base, wave, nw, lane);
         }
     }
-    if (SERIAL && a.fin) {
+    if (a.fin) {
         float *dst = a.fin + (bb * a.h + hh) * N * a.p + col + j16;
 #pragma unroll
         for (int x = 0; x < NT; ++x)
@@ -728,6 +633,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
             for (int r = 0; r < 4; ++r)
                 S[x][r] = a.init[((bb * a.h + hh) * N + 16 * (x0 + x) + 4 * g + r) * a.p + col + j16];
     }
+    landed(S);
     vm_wait<0>();
     lds_barrier();
     for (int64_t c = 0; c < a.nc; ++c) {
@@ -893,7 +799,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
                 for (int r = 0; r < 4; ++r) st[(16 * (x0 + x) + 4 * g + r) * a.p] = S[x][r];
         }
         // and of Y
-        if (a.y) {
+        {
             f32x4 y = zero4();
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb)
@@ -924,33 +830,16 @@ __global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
     }
 }
 
-constexpr int kLdsMost = 160 * 1024;
-
-template <typename IO, int N, bool GRAD, bool SERIAL>
-hipError_t run_fwd(const DeltaArgs &a, hipStream_t s) {
-    typedef FwdBuf<IO, N, GRAD> B;
+template <typename IO, int N> hipError_t run_fwd(const DeltaArgs &a, hipStream_t s) {
     // columns of a workgroup: all of a head's where that still gives every
     // compute unit a workgroup (its images are then copied once), else 64
     int nw = a.p / 16;
-    if (nw > 4 && a.b * a.h * (SERIAL ? 1 : a.nc) < device_cus()) nw = 4;
-    if (!SERIAL && nw > 4) nw = 4;
-    const int one = B::bytes(16 * nw);
-    const int64_t items = a.b * a.h * (a.p / (16 * nw)) * (SERIAL ? 1 : a.nc);
-    const dim3 grid((unsigned)items), block(64 * nw);
-    if (SERIAL && 2 * one <= kLdsMost) {
-        auto *k = &k_delta_fwd<IO, N, GRAD, SERIAL, 2>;
-        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, kLdsMost);
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(k, grid, block, 2 * one, s, a);
-    } else {
-        auto *k = &k_delta_fwd<IO, N, GRAD, SERIAL, 1>;
-        hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, kLdsMost);
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(k, grid, block, one, s, a);
-    }
-    return hipGetLastError();
+    if (nw > 4 && a.b * a.h < device_cus()) nw = 4;
+    const int one = FwdBuf<IO, N, false>::bytes(16 * nw);
+    const int64_t items = a.b * a.h * (a.p / (16 * nw));
+    const bool two = 2 * one <= kLdsMost;
+    return launch(two ? &k_delta_fwd<IO, N, 2> : &k_delta_fwd<IO, N, 1>, items, 64 * nw,
+                  two ? 2 * one : one, a, s);
 }
 
 template <typename IO, int N> hipError_t prep_n(const DeltaArgs &a, bool grad, hipStream_t s) {
@@ -968,20 +857,17 @@ template <typename IO, int N> hipError_t prep_n(const DeltaArgs &a, bool grad, h
 
 template <typename IO, int N> hipError_t run_coop(const DeltaArgs &a, hipStream_t s) {
     const int one = FwdBuf<IO, N, false>::bytes(16), ex = CoopBuf<IO>::BYTES;
-    const int64_t items = a.b * a.h * (a.p / 16);
-    const bool two = items <= device_cus() && 2 * one + ex <= kLdsMost;
-    auto *k = two ? &k_delta_coop<IO, N, 2> : &k_delta_coop<IO, N, 1>;
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(k),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, kLdsMost);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k, dim3((unsigned)items), dim3(256), (two ? 2 : 1) * one + ex, s, a);
-    return hipGetLastError();
+    const bool two = 2 * one + ex <= kLdsMost;
+    return launch(two ? &k_delta_coop<IO, N, 2> : &k_delta_coop<IO, N, 1>, a.b * a.h * (a.p / 16), 256,
+                  (two ? 2 : 1) * one + ex, a, s);
 }
 
-template <typename IO, int N> hipError_t fwd_n(const DeltaArgs &a, bool grad, hipStream_t s) {
-    if (!grad && (getenv("XCOOP") ? atoi(getenv("XCOOP")) : a.b * a.h * (a.p / 16) <= 4 * device_cus())) return run_coop<IO, N>(a, s);
-    if (!grad) return run_fwd<IO, N, false, true>(a, s);
-    return a.kept ? run_fwd<IO, N, true, false>(a, s) : run_fwd<IO, N, true, true>(a, s);
+template <typename IO, int N> hipError_t fwd_n(const DeltaArgs &a, hipStream_t s) {
+    // Four waves to 16 columns where each such group can have a compute unit of
+    // its own (64 heads of 64 columns: 2459 against 3886 us for 65536 tokens);
+    // with more of them the chains hide each other's waits (8 x 24 heads of 64
+    // columns: 153 against 238 us).
+    return a.b * a.h * (a.p / 16) <= device_cus() ? run_coop<IO, N>(a, s) : run_fwd<IO, N>(a, s);
 }
 
 }  // namespace
@@ -994,12 +880,10 @@ hipError_t delta_prep(const DeltaArgs &a, int io, int n, bool grad, hipStream_t 
                    : n == 64 ? prep_n<float, 64>(a, grad, s) : prep_n<float, 128>(a, grad, s);
 }
 
-hipError_t delta_forward(const DeltaArgs &a, int io, int n, bool grad, hipStream_t s) {
+hipError_t delta_forward(const DeltaArgs &a, int io, int n, hipStream_t s) {
     if (io == SSD_BF16)
-        return n == 32 ? fwd_n<bf16, 32>(a, grad, s)
-                       : n == 64 ? fwd_n<bf16, 64>(a, grad, s) : fwd_n<bf16, 128>(a, grad, s);
-    return n == 32 ? fwd_n<float, 32>(a, grad, s)
-                   : n == 64 ? fwd_n<float, 64>(a, grad, s) : fwd_n<float, 128>(a, grad, s);
+        return n == 32 ? fwd_n<bf16, 32>(a, s) : n == 64 ? fwd_n<bf16, 64>(a, s) : fwd_n<bf16, 128>(a, s);
+    return n == 32 ? fwd_n<float, 32>(a, s) : n == 64 ? fwd_n<float, 64>(a, s) : fwd_n<float, 128>(a, s);
 }
 
 }  // namespace ssd
