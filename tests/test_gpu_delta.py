@@ -94,6 +94,31 @@ def test_every_value_width_and_key_width(io):
             check_bwd(c, io, "gradient %d %d" % (n, p), states=st)
 
 
+# So many heads that the compute units are full with one wave per 16 columns, in
+# workgroups of every size; the last two have more than one head of a group in a
+# wave of the preparation.
+MANY = [  # b, l, h, g, n, p
+    (2, 130, 132, 4, 32, 16),
+    (1, 65, 260, 130, 128, 16),
+    (2, 200, 66, 6, 64, 32),
+    (3, 70, 24, 8, 128, 64),
+    (1, 129, 36, 36, 32, 128),
+    (1, 66, 264, 88, 64, 128),
+    (1, 65, 258, 3, 128, 128),
+    (6, 130, 256, 128, 32, 16),
+    (9, 250, 180, 60, 32, 16),
+]
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("shape", MANY, ids=lambda s: "x".join(map(str, s)))
+def test_many_heads(shape, io):
+    c = delta_case(sum(shape), *shape, io, normalize=True, packed=True, init=True)
+    kw = dict(normalize=True)
+    st = check_scan(c, io, "scan", **kw)
+    check_bwd(c, io, "gradient", states=st, **kw)
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("n,p", [(32, 16), (64, 128), (128, 64), (128, 128)])
 def test_steps_continue_a_scan(io, n, p):
