@@ -32,7 +32,7 @@ namespace {
 constexpr int kNormThreads = 256;
 constexpr int kMostLane = 64;                          // elements of a row per lane
 constexpr int kMostRow = kNormThreads * kMostLane;     // longest row in registers
-constexpr int kMostBlocks = 1024;                      // workgroups of the gradient
+constexpr int kMostBlocks = 1024;                      // workgroups of the gradient, at most
 
 template <typename IO, int V>
 struct alignas(sizeof(IO) * V < 16 ? sizeof(IO) * V : 16) NVec { IO e[V]; };
@@ -160,10 +160,21 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm_bwd(NormArgs a) {
         const Vec *px = reinterpret_cast<const Vec *>(static_cast<const IO *>(a.x) + at);
         const Vec *pd = reinterpret_cast<const Vec *>(static_cast<const IO *>(a.dy) + at);
         // the row's values as they were read; widened where they are used
-        Vec xv[K], dv[K];
+        Vec xv[K], dv[K], more[K];
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (k * G + lane < nv) xv[k] = px[k * G + lane], dv[k] = pd[k * G + lane];
+        if (a.dsum) {
+            const Vec *ps = reinterpret_cast<const Vec *>(static_cast<const IO *>(a.dsum) + at);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (k * G + lane < nv) more[k] = ps[k * G + lane];
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int e = 0; e < V; ++e) more[k].e[e] = (IO)0.f;
+        }
         const float mean = a.stats_in[row], rstd = a.stats_in[a.rows + row];
         float c1 = 0.f, c2 = 0.f;
 #pragma unroll
@@ -187,22 +198,20 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm_bwd(NormArgs a) {
         c1 = row_sum<G>(c1, red, half) * inv;
         c2 = row_sum<G>(c2, red, half) * inv;
         Vec *po = reinterpret_cast<Vec *>(static_cast<IO *>(a.y) + at);
-        const Vec *ps = reinterpret_cast<const Vec *>(static_cast<const IO *>(a.dsum) + at);
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if (k * G + lane < nv) {
                 const int c = k * G + lane;
                 NVec<float, V> w;
-                Vec more, o;
+                Vec o;
 #pragma unroll
-                for (int e = 0; e < V; ++e) w.e[e] = 1.f, more.e[e] = (IO)0.f;
+                for (int e = 0; e < V; ++e) w.e[e] = 1.f;
                 if (a.weight) w = reinterpret_cast<const NVec<float, V> *>(a.weight)[c];
-                if (a.dsum) more = ps[c];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     const float hat = (to_f32(xv[k].e[e]) - mean) * rstd;
                     const float g = to_f32(dv[k].e[e]) * w.e[e];
-                    o.e[e] = (IO)fmaf(rstd, g - c1 - hat * c2, to_f32(more.e[e]));
+                    o.e[e] = (IO)fmaf(rstd, g - c1 - hat * c2, to_f32(more[k].e[e]));
                 }
                 po[c] = o;
             }
@@ -331,25 +340,40 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm_cols(NormArgs a) {
     if (a.db) a.db[blockIdx.y * a.stride + c] = sb;
 }
 
-// The workgroups' partial sums [blocks][2 dim], added in order by eight strips.
+// The workgroups' partial sums [blocks][2 dim]: V columns a thread, added in order
+// by 32 strips whose sums are added in order.
+template <int V>
 __global__ __launch_bounds__(256) void k_layer_norm_sum(const float *__restrict__ part, float *dw,
                                                         float *db, int blocks, int64_t dim) {
-    __shared__ float red[8][32];
-    const int col = threadIdx.x & 31, strip = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + col;
-    float t = 0.f;
-    if (c < 2 * dim)
-        for (int b = strip; b < blocks; b += 8) t += part[(int64_t)b * 2 * dim + c];
+    typedef NVec<float, V> Vec;
+    __shared__ Vec red[32][8];
+    const int col = threadIdx.x & 7, strip = threadIdx.x >> 3;
+    const int64_t c = ((int64_t)blockIdx.x * 8 + col) * V;
+    Vec t;
+#pragma unroll
+    for (int e = 0; e < V; ++e) t.e[e] = 0.f;
+    if (c < 2 * dim) {
+#pragma unroll 8
+        for (int b = strip; b < blocks; b += 32) {
+            const Vec v = *reinterpret_cast<const Vec *>(part + (int64_t)b * 2 * dim + c);
+#pragma unroll
+            for (int e = 0; e < V; ++e) t.e[e] += v.e[e];
+        }
+    }
     red[strip][col] = t;
     __syncthreads();
     if (strip == 0 && c < 2 * dim) {
-        t = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) t += red[i][col];
-        if (c < dim) {
-            if (dw) dw[c] = t;
-        } else if (db) {
-            db[c - dim] = t;
+        for (int i = 1; i < 32; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) t.e[e] += red[i][col].e[e];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (c + e < dim) {
+                if (dw) dw[c + e] = t.e[e];
+            } else if (db) {
+                db[c + e - dim] = t.e[e];
+            }
         }
     }
 }
@@ -387,7 +411,8 @@ struct NormShape {
         else if (dim <= 64 * kMostLane) {
             g = 64;
             const int per = (int)((dim + 63) / 64);
-            e = per <= 8 ? 8 : per <= 16 ? 16 : per <= 32 ? 32 : per <= 48 ? 48 : 64;
+            e = per <= 8 ? 8 : per <= 16 ? 16 : per <= 24 ? 24 : per <= 32 ? 32 : per <= 40 ? 40
+                : per <= 48 ? 48 : 64;
         } else {
             g = kNormThreads;
             e = dim <= kNormThreads * 32 ? 32 : 64;
@@ -416,7 +441,9 @@ hipError_t norm_shape(const NormArgs &a, bool bwd, const NormShape &n, int block
     switch (n.e) {
     case 8: return norm_go<IO, V, 64, 8>(a, bwd, blocks, s);
     case 16: return norm_go<IO, V, 64, 16>(a, bwd, blocks, s);
+    case 24: return norm_go<IO, V, 64, 24>(a, bwd, blocks, s);
     case 32: return norm_go<IO, V, 64, 32>(a, bwd, blocks, s);
+    case 40: return norm_go<IO, V, 64, 40>(a, bwd, blocks, s);
     case 48: return norm_go<IO, V, 64, 48>(a, bwd, blocks, s);
     default: return norm_go<IO, V, 64, 64>(a, bwd, blocks, s);
     }
@@ -435,14 +462,19 @@ bool norm_sizes(int64_t rows, int64_t dim) {
     return dim <= ((int64_t)1 << 24) && rows <= ((int64_t)1 << 40) / dim;
 }
 
-// Workgroups of the gradient: four passes over rows each where the rows allow
-// it, so that the partial sums stay small beside the rows.
+// Workgroups of the gradient: as many as run at once (a lane's 16 columns and
+// fewer leave room for four on a compute unit, up to 64 for two), so that none
+// waits for a place: 16384 rows of 2560 take 93 us in 512 workgroups, 114 in 768
+// or 1024.  Fewer rows than that go one to each of G lanes, though a row of
+// partial sums is then written for few of them: 1999 rows of 771 take 20 us so,
+// 27 us with four rows to each.
 int norm_blocks(int64_t rows, int64_t dim) {
-    const int rpb = dim <= kMostRow ? NormShape(dim).rows_per_block() : 1;
-    const int64_t b = (rows + 4 * rpb - 1) / (4 * rpb);
+    const NormShape n(dim);
+    const int64_t slots = n.e <= 16 ? kMostBlocks : kMostBlocks / 2;
+    const int64_t b = (rows + n.rows_per_block() - 1) / n.rows_per_block();
     // beyond 16 MB of partial sums fewer workgroups run
     const int64_t most = ((int64_t)1 << 24) / (8 * dim);
-    const int64_t cap = most < 1 ? 1 : most > kMostBlocks ? kMostBlocks : most;
+    const int64_t cap = most < 1 ? 1 : most > slots ? slots : most;
     return (int)(b < cap ? b : cap);
 }
 
@@ -489,8 +521,10 @@ hipError_t norm_bwd(NormArgs a, float *dw, float *db, float *part, hipStream_t s
         e = norm_vecs<IO>(a, true, v, NormShape(a.dim), blocks, s);
     }
     if (sums && blocks > 1 && e == hipSuccess) {
-        hipLaunchKernelGGL(k_layer_norm_sum, dim3((unsigned)((2 * a.dim + 31) / 32)), dim3(256), 0, s,
-                           part, dw, db, blocks, a.dim);
+        const int64_t per = a.dim % 2 ? 16 : 32;  // columns of a workgroup
+        const dim3 grid((unsigned)((2 * a.dim + per - 1) / per));
+        hipLaunchKernelGGL(a.dim % 2 ? &k_layer_norm_sum<2> : &k_layer_norm_sum<4>, grid, dim3(256), 0,
+                           s, part, dw, db, blocks, a.dim);
         e = hipGetLastError();
     }
     return e;
