@@ -671,10 +671,12 @@ template <typename IO, int N> struct GradBuf {
     typedef GradOp<IO> O;
     static constexpr int E = (int)sizeof(typename O::type), TOK = kDC * 32 * E;
     static constexpr int S = 0, D = S + N * 32 * E, NV = D + N * 32 * E, Z = NV + O::PL * TOK;
-    static constexpr int DY = Z + O::PL * TOK, END1 = DY + TOK;
+    static constexpr int DY = Z + O::PL * TOK, SC = DY + TOK, END1 = SC + (E == 2 ? 1024 : 0);
     static constexpr int K = 0, Q = K + kDC * N * E, R = Q + kDC * N * E;
     static constexpr int R2 = R + kRows * kDC * 4, END2 = R2 + kRowsGrad * kDC * 4;
     static constexpr int BYTES = END1 > END2 ? END1 : END2;
+    // behind both buffers: row arrays for all stages of a head
+    static constexpr int R0 = 2 * BYTES, BETA = R0 + kRowsGrad * kDC * 4, ALL = BETA + 1024;
 };
 
 template <typename IO, int N>
@@ -685,50 +687,56 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
     typedef HeadImg<IO, true> H;
     constexpr bool F32 = sizeof(IO) == 4;
     constexpr int XB = N / 32, NT = N / 16, PN = 2 * GradOp<IO>::PL;  // pieces of a tile of N or Z
-    __shared__ __align__(1024) char lds[2 * B::BYTES];
+    __shared__ __align__(1024) char lds[B::ALL];
 
-    const int lane = threadIdx.x & 63, w = wave_id(), g = lane >> 4, j16 = lane & 15;
+    const int w = wave_id(), own = threadIdx.x & 63;
     const int64_t item = xcd_item(blockIdx.x, gridDim.x);
     const int64_t gg = item % a.g, ci = item / a.g, c = ci % a.nc, bb = ci / a.nc;
     const int ratio = (int)(a.h / a.g);
     const int64_t t0 = c * kDC;
     const int len = (int)(a.l - t0 < kDC ? a.l - t0 : kDC);
-    const int cts = a.p >> 4, m = 16 * w + j16;  // this lane's token
-    const bool live = m < len;
+    const int cts = a.p >> 4;
     const uint32_t base = lds_address(lds);
-    const int slices = (a.p + 31) >> 5, stages = slices + 1;
+    const int slices = (a.p + 31) >> 5;
     const int64_t kq = ((bb * a.l + t0) * a.g + gg) * N;
 
-    const auto fetch = [&](int q) {
-        const uint32_t buf = base + (q & 1) * B::BYTES;
-        const int64_t hh = gg * ratio + q / stages, hi = ci * a.h + hh;
-        const int st = q % stages;
-        if (st < slices) {
-            const int tiles = cts - 2 * st < 2 ? 1 : 2;
-            const int64_t at = hi * cts + 2 * st;
-            const int whole = tiles * XB * 512 * B::E, tok = tiles * 1024 * B::E;
-            copy_lds(static_cast<const OT *>(a.simg) + at * (XB * 512), whole, N * 32 * B::E, buf + B::S,
-                     w, 4, lane);
-            copy_lds(static_cast<const OT *>(a.dsimg) + at * (XB * 512), whole, N * 32 * B::E,
-                     buf + B::D, w, 4, lane);
-            copy_lds(static_cast<const OT *>(a.nimg) + at * kOperandN<IO>, tok * B::O::PL,
-                     B::TOK * B::O::PL, buf + B::NV, w, 4, lane);
-            copy_lds(static_cast<const OT *>(a.zimg) + at * kOperandN<IO>, tok * B::O::PL,
-                     B::TOK * B::O::PL, buf + B::Z, w, 4, lane);
-            copy_lds(static_cast<const OT *>(a.yimg) + at * 1024, tok, B::TOK, buf + B::DY, w, 4, lane);
-        } else {
-            if constexpr (F32) {
-                copy_nat<XB>(static_cast<const IO *>(a.k) + kq, a.g * N, N, len, buf + B::K, w, lane);
-                copy_nat<XB>(static_cast<const IO *>(a.q) + kq, a.g * N, N, len, buf + B::Q, w, lane);
-            } else {
-                copy_lds(a.gimg + (ci * a.g + gg) * GroupImg<IO, N>::BYTES, GroupImg<IO, N>::BYTES,
-                         GroupImg<IO, N>::BYTES, buf + B::K, w, 4, lane);
-            }
-            copy_lds(a.himg + hi * a.hstride + H::R, kRows * kDC * 4, kRows * kDC * 4, buf + B::R, w, 4,
-                     lane);
+    int half = 0;  // the buffer to be read next
+    const auto fetch = [&](int64_t hi, int st, int lane) {
+        const uint32_t buf = base + half * B::BYTES;
+        const int tiles = cts - 2 * st < 2 ? 1 : 2;
+        const int64_t at = hi * cts + 2 * st;
+        const int whole = tiles * XB * 512 * B::E, tok = tiles * 1024 * B::E;
+        copy_lds(static_cast<const OT *>(a.simg) + at * (XB * 512), whole, N * 32 * B::E, buf + B::S, w,
+                 4, lane);
+        copy_lds(static_cast<const OT *>(a.dsimg) + at * (XB * 512), whole, N * 32 * B::E, buf + B::D, w,
+                 4, lane);
+        copy_lds(static_cast<const OT *>(a.nimg) + at * kOperandN<IO>, tok * B::O::PL,
+                 B::TOK * B::O::PL, buf + B::NV, w, 4, lane);
+        copy_lds(static_cast<const OT *>(a.zimg) + at * kOperandN<IO>, tok * B::O::PL,
+                 B::TOK * B::O::PL, buf + B::Z, w, 4, lane);
+        copy_lds(static_cast<const OT *>(a.yimg) + at * 1024, tok, B::TOK, buf + B::DY, w, 4, lane);
+        if constexpr (!F32)
+            copy_lds(a.scales + at * kScales, tiles * kScales * 4, 1024, buf + B::SC, w, 4, lane);
+        if (st == 0) {
             copy_lds(a.rows2 + hi * (kRowsGrad * kDC), kRowsGrad * kDC * 4, kRowsGrad * kDC * 4,
-                     buf + B::R2, w, 4, lane);
+                     base + B::R0, w, 4, lane);
+            copy_lds(a.himg + hi * a.hstride + H::R + kBeta * kDC * 4, kDC * 4, 1024, base + B::BETA, w,
+                     4, lane);
         }
+    };
+    const auto fetch_rows = [&](int64_t hi, int lane) {
+        const uint32_t buf = base + half * B::BYTES;
+        if constexpr (F32) {
+            copy_nat<XB>(static_cast<const IO *>(a.k) + kq, a.g * N, N, len, buf + B::K, w, lane);
+            copy_nat<XB>(static_cast<const IO *>(a.q) + kq, a.g * N, N, len, buf + B::Q, w, lane);
+        } else {
+            copy_lds(a.gimg + (ci * a.g + gg) * GroupImg<IO, N>::BYTES, GroupImg<IO, N>::BYTES,
+                     GroupImg<IO, N>::BYTES, buf + B::K, w, 4, lane);
+        }
+        copy_lds(a.himg + hi * a.hstride + H::R, kRows * kDC * 4, kRows * kDC * 4, buf + B::R, w, 4,
+                 lane);
+        copy_lds(a.rows2 + hi * (kRowsGrad * kDC), kRowsGrad * kDC * 4, kRowsGrad * kDC * 4, buf + B::R2,
+                 w, 4, lane);
     };
 
     f32x4 dQ[NT], dK[NT];
@@ -739,23 +747,36 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
     f32x4 X[4], Y[4], Xd = zero4(), Yd = zero4();
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) X[rt] = Y[rt] = zero4();
-    float fq = 0.f, fz = 0.f, fn = 0.f;
 
-    fetch(0);
-    for (int q = 0; q < ratio * stages; ++q) {
-        const int64_t hh = gg * ratio + q / stages, hi = ci * a.h + hh;
-        const int st = q % stages;
-        const char *buf = lds + (q & 1) * B::BYTES;
-        if (st == 0) {
-            const float *r2 = a.rows2 + hi * (kRowsGrad * kDC) + m;
-            const float be =
-                reinterpret_cast<const float *>(a.himg + hi * a.hstride + H::R)[kBeta * kDC + m];
-            fq = a.scale * r2[kRead * kDC], fz = -r2[kRead * kDC] * be, fn = r2[kWrite * kDC] * be;
-        }
+    // The next buffer's copies have landed for everyone; the other one is free.  The
+    // lane comes out as a value not known to be the same each time: addresses are
+    // then computed where they are used, of which there are more than registers.
+    const auto turn = [&]() {
         vm_wait<0>();
         lds_barrier();
-        if (q + 1 < ratio * stages) fetch(q + 1);
-        if (st < slices) {
+        const char *buf = lds + half * B::BYTES;
+        half ^= 1;
+        return buf;
+    };
+    const auto fresh = [&]() {
+        int lane = own;
+        asm volatile("" : "+v"(lane));
+        return lane;
+    };
+    const int64_t h0 = ci * a.h + gg * ratio;
+    const char *buf = nullptr;
+    fetch(h0, 0, own);
+    for (int64_t hi = h0; hi < h0 + ratio; ++hi) {
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) X[rt] = Y[rt] = zero4();
+        Xd = Yd = zero4();
+        for (int st = 0; st < slices; ++st) {
+            buf = turn();
+            const int lane = fresh(), g = lane >> 4;
+            if (st + 1 < slices)
+                fetch(hi, st + 1, lane);
+            else
+                fetch_rows(hi, lane);
             const OT *S = reinterpret_cast<const OT *>(buf + B::S);
             const OT *D = reinterpret_cast<const OT *>(buf + B::D);
             const OT *NV = reinterpret_cast<const OT *>(buf + B::NV);
@@ -763,28 +784,18 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
             const OT *DY = reinterpret_cast<const OT *>(buf + B::DY);
             const F dy = cols_nat(DY, w >> 1, 2, w, lane), nv = cols_nat(NV, w >> 1, PN, w, lane),
                     zv = cols_nat(ZV, w >> 1, PN, w, lane);
-            const float *sc = a.scales + (hi * cts + 2 * st) * kScales;
+            const float *sc = reinterpret_cast<const float *>(buf + B::SC);
             const bool two = cts - 2 * st > 1;
-            float gq = fq, gz = fz, gn = fn;
+            const float *rows = reinterpret_cast<const float *>(lds + B::R0) + 16 * w + (lane & 15);
+            const float be = reinterpret_cast<const float *>(lds + B::BETA)[16 * w + (lane & 15)];
+            float gq = a.scale * rows[kRead * kDC], gz = -rows[kRead * kDC] * be,
+                  gn = rows[kWrite * kDC] * be;
             F dys = dy, zvs = zv, nvd = nv;
             if constexpr (!F32) {
                 const Pair sy(sc, kScS, kScY, two, g), sz(sc, kScS, kScZ, two, g),
                     dn(sc, kScD, kScN, two, g);
                 dys = dy * sy.part, zvs = zv * sz.part, nvd = nv * dn.part;
                 gq *= sy.inv, gz *= sz.inv, gn *= dn.inv;
-            }
-#pragma unroll
-            for (int x = 0; x < NT; ++x) {
-                const F s = cols_nat(S, x >> 1, XB, x, lane);
-                const F d = cols_nat(D, x >> 1, XB, x, lane);
-                const f32x4 t = mma8(s, dys, zero4()), u = mma8(s, zvs, zero4()),
-                            v = mma8(d, nvd, zero4());
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    dQ[x][r] = fmaf(gq, t[r], dQ[x][r]);
-                    dK[x][r] = fmaf(gz, u[r], fmaf(gn, v[r], dK[x][r]));
-                }
-                if (x & 1) sched_fence();
             }
             F dyn = dy, zvn = zv, zvl = zv, nvy = nv, nvz = nv;
             float ny = 1.f, nz = 1.f;
@@ -823,8 +834,23 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
                 }
                 sched_fence();
             }
-            continue;
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+                const F s = cols_nat(S, x >> 1, XB, x, lane);
+                const F d = cols_nat(D, x >> 1, XB, x, lane);
+                const f32x4 t = mma8(s, dys, zero4()), u = mma8(s, zvs, zero4()),
+                            v = mma8(d, nvd, zero4());
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    dQ[x][r] = fmaf(gq, t[r], dQ[x][r]);
+                    dK[x][r] = fmaf(gz, u[r], fmaf(gn, v[r], dK[x][r]));
+                }
+                if (x & 1) sched_fence();
+            }
         }
+        buf = turn();
+        const int lane = fresh(), g = lane >> 4, j16 = lane & 15, m = 16 * w + j16;  // this lane's token
+        if (hi + 1 < h0 + ratio) fetch(hi + 1, 0, lane);
         // decays, masks and factors; rows j in front of this token give dq, rows
         // behind it dk, both give (X + X^T) K
         const OT *K = reinterpret_cast<const OT *>(buf + B::K);
@@ -981,11 +1007,9 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
             for (int r = 0; r < 4; ++r) dK[x][r] = fmaf(inv, t[r], dK[x][r]);
             if (x & 1) sched_fence();
         }
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) X[rt] = Y[rt] = zero4();
-        Xd = Yd = zero4();
     }
-    const char *buf = lds + ((ratio * stages - 1) & 1) * B::BYTES;
+    const int lane = own, g = lane >> 4, m = 16 * w + (lane & 15);
+    const bool live = m < len;
     const float *rows = reinterpret_cast<const float *>(buf + B::R);
     const float *r2 = reinterpret_cast<const float *>(buf + B::R2);
     const int64_t at = ((bb * a.l + t0 + m) * a.g + gg) * N;
