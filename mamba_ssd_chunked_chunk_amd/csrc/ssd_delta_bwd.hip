@@ -258,14 +258,15 @@ template <typename IO, int N> struct RevAhead {
     __device__ void load_state(const DeltaArgs &a, int64_t bb, int64_t hh, int64_t c, int col, int lane) {
         const float *s0 = c ? a.kept + ((bb * a.nc + c - 1) * a.h + hh) * N * a.p
                             : a.init ? a.init + (bb * a.h + hh) * N * a.p : nullptr;
+        // without a state in front all of it lies beyond the resource and comes as zeros
+        const Rsrc rs = make_rsrc(reinterpret_cast<const float *>(uni(s0)), s0 ? N * a.p * 4 : 0);
+        const int row = 4 * a.p, off = (4 * (lane >> 4) * a.p + col + (lane & 15)) * 4;
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-            S[x] = zero4();
-            if (s0)
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    S[x][r] = s0[(16 * x + 4 * (lane >> 4) + r) * a.p + col + (lane & 15)];
-        }
+            for (int r = 0; r < 4; ++r)
+                S[x][r] = __builtin_bit_cast(
+                    float, __builtin_amdgcn_raw_buffer_load_b32(rs, off, (16 * x + r) * row, 0));
     }
     __device__ void load_x(const DeltaArgs &a, int64_t at, int lane) {
         const f32x4 *x = reinterpret_cast<const f32x4 *>(a.x0 + at * (16 * kDC)) + lane;
@@ -365,6 +366,8 @@ __global__ __launch_bounds__(256, 1) void k_delta_rev(DeltaArgs a) {
         in.wait();
         lds_barrier();
         const int64_t hi = (bb * a.nc + c) * a.h + hh, t0 = c * kDC, at = hi * cts + ct;
+        // the chunk in front, or once more the first, whose values are not used then
+        const int64_t front = c ? c - 1 : 0, ahead = c ? at - step : at;
         const int len = (int)(a.l - t0 < kDC ? a.l - t0 : kDC);
         if (NB == 2 && c > 0) {
             src.back();
@@ -388,7 +391,7 @@ __global__ __launch_bounds__(256, 1) void k_delta_rev(DeltaArgs a) {
             s += __shfl_xor(s, 16);
             s += __shfl_xor(s, 32);
             if (lane == 0) a.eend[at] = carry * s;
-            if (c > 0) in.load_state(a, bb, hh, c - 1, col, lane);
+            in.load_state(a, bb, hh, front, col, lane);
         }
         // the adjoint state behind the chunk: split, and kept for k_delta_grad
         float mx = 0.f;
@@ -437,7 +440,7 @@ __global__ __launch_bounds__(256, 1) void k_delta_rev(DeltaArgs a) {
             }
             mx = abs_max(mx, U[rt]);
         }
-        if (c > 0) in.load_x(a, at - step, lane);
+        in.load_x(a, ahead, lane);
         // Z, dV = beta Z, and their rows' products
         const Pow2 pu(col_max(mx));
         Split uf[2];
@@ -474,7 +477,7 @@ __global__ __launch_bounds__(256, 1) void k_delta_rev(DeltaArgs a) {
                 *reinterpret_cast<f32x4 *>(o + kSumZ * kDC) = sz;
             }
         }
-        if (c > 0) in.load_n(a, at - step, lane);
+        in.load_n(a, ahead, lane);
         const Pow2 pz(tile_max(mz), kOperand);
         OT *dz = static_cast<OT *>(a.zimg) + at * kOperandN<IO>;
 #pragma unroll
