@@ -34,9 +34,10 @@
 // of q and k, per column of a state or of a chunk's rows, so that the largest
 // magnitude fits), written as two fp16 terms hi + lo, 22 significant bits, and
 // multiplied as hi hi + hi lo + lo hi; q and k of bf16 io are exact in one.
-// With bf16 io the read-out (Y) takes hi terms alone: its 2^-11 is an eighth
-// of y's own rounding.  States, sums, decays and the triangular inverse are fp32
-// (the log decays' sums fp64).
+// With bf16 io the read-out (Y) and the products of dQ and dK take hi terms alone:
+// their 2^-12 at most is a sixteenth of the result's own rounding.  States, sums,
+// decays and the triangular inverse are fp32, the log decays' sums fp64, and so
+// are the sums of C_ij, of which a row's and a column's share all but a few terms.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -60,8 +61,8 @@ enum RowOf {
     kReadQ,   // scale e^G fq
     kFq,      // scale fq
     kBeta,    // beta
-    kCarry,   // [0]: e^{G_C}
-    kRawQ    // fq
+    kCarry,   // [0]: e^{G_C}; [1], [2]: bounds of kReadK and of beta fk times an inverse's row
+    kRawQ     // fq
 };
 enum RowOfGrad {
     kGhi,    // log2 of e^G, as two floats

@@ -6,13 +6,21 @@
 // 16 x 16 blocks: the four on the diagonal by substitution (a lane per block and
 // column), the others by distance from it, T_ij = -T_ii sum_k (kk beta)_ik T_kj,
 // on fp32 matrix instructions whose results feed the next product from registers.
+// Bound by its instructions: 4800 for a wave's first head, 1600 for each further
+// one of the group; two waves fit a SIMD.  65536 tokens of 64 heads, eight to a
+// group, keys of 128: 390 us, with 1.3 GB written (275 us of a copy); 8 x 2048
+// tokens of 24 heads with a group each 106 us.  Three waves to a SIMD would leave
+// 168 registers and spill a hundred.
 //
 // k_delta_fwd, chunk after chunk: a wave owns 16 value columns of one head's
 // state in registers (an accumulator tile per 16 keys).  Columns do not meet
 // anywhere in the recurrence, and an accumulator tile is the operand of the
 // next product as it stands, so a wave passes from K S to N to the new state
 // without LDS or another wave; LDS holds only what all columns share (the
-// images of the next chunk arrive in the other buffer meanwhile).
+// images of the next chunk arrive in the other buffer meanwhile).  Bound by the
+// chain of one wave, 1100 instructions a chunk, as long as there are fewer than two
+// to a SIMD: 8 x 2048 tokens of 24 heads of 128 x 64 143 us, 4.5 us a chunk; 16 x
+// 1000 tokens of 16 heads of 128 x 128 94 us.
 #include "ssd_delta.hpp"
 
 #include <math.h>
@@ -162,7 +170,7 @@ __device__ __forceinline__ float exp2_d(double x) {
 template <typename IO, int N, bool GRAD>
 __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
     constexpr bool F32 = sizeof(IO) == 4;
-    constexpr int PL = F32 ? 2 : 1, XB = N / 32, IMG = kDC * N;
+    constexpr int XB = N / 32;
     constexpr int NT = GRAD ? 2 : 1;          // inverses: T, and (I + beta kk)^-1
     constexpr int PPL = F32 || GRAD ? 2 : 1;  // terms of tril(Q K^T)
     __shared__ PrepLds all[4];
@@ -590,7 +598,10 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
 // state and the rows of one of the four row tiles; what it has of K S and Q S
 // goes to the rows' owners, and R, u and e^{G_C - G} u, split, to everyone, through
 // LDS, with a barrier after each.  The powers of two that the waves have to
-// share come from bounds that they exchange with the values before.
+// share come from bounds that they exchange with the values before.  65536 tokens
+// of 64 heads of 128 x 64: 2.36 us a chunk, of them a third waits at the barriers;
+// operands read from LDS a chunk ahead saved 1% of it, a wait for the next chunk's
+// copies moved to the end of this one cost 3%.
 template <typename IO> struct CoopBuf {
     static constexpr int UL = sizeof(IO) == 4 ? 2 : 1;  // terms of u in the read-out
     static constexpr int P = 0, R = P + 12 * 1024, W = R + 4 * 1024, U = W + 4 * 1024;
@@ -864,9 +875,9 @@ template <typename IO, int N> hipError_t run_coop(const DeltaArgs &a, hipStream_
 
 template <typename IO, int N> hipError_t fwd_n(const DeltaArgs &a, hipStream_t s) {
     // Four waves to 16 columns where each such group can have a compute unit of
-    // its own (64 heads of 64 columns: 2459 against 3886 us for 65536 tokens);
+    // its own (64 heads of 64 columns: 2420 against 3886 us for 65536 tokens);
     // with more of them the chains hide each other's waits (8 x 24 heads of 64
-    // columns: 153 against 238 us).
+    // columns: 143 against 238 us).
     return a.b * a.h * (a.p / 16) <= device_cus() ? run_coop<IO, N>(a, s) : run_fwd<IO, N>(a, s);
 }
 
