@@ -175,15 +175,12 @@ __device__ __forceinline__ f32x4 mma16(f16x8 a, f16x8 b, f32x4 c) {
 }
 
 // Power of two that brings magnitudes up to mx into [2^13, 2^14), and its inverse.
-// k_delta_grad's operands stop at 2^60 (kOperand), so that the product of two
-// inverses stays in fp32's range.
-constexpr int kOperand = 187;
 struct Pow2 {
     float sc, inv;
-    __device__ explicit Pow2(float mx, int most = 253) {
+    __device__ explicit Pow2(float mx) {
         const int e = (int)(__builtin_bit_cast(uint32_t, mx) >> 23) & 255;
         int f = 267 - e;
-        f = f > most ? most : f;
+        f = f > 253 ? 253 : f;
         sc = __builtin_bit_cast(float, (uint32_t)f << 23);
         inv = __builtin_bit_cast(float, (uint32_t)(254 - f) << 23);
     }

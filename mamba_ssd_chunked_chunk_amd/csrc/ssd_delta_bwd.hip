@@ -105,7 +105,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_mid(DeltaArgs a) {
     float mx = 0.f;
 #pragma unroll
     for (int x = 0; x < NT; ++x) mx = abs_max(mx, S[x]);
-    const Pow2 ps(tile_max(mx), kOperand);
+    const Pow2 ps(tile_max(mx));
     Split sf[XB];
     OT *simg = static_cast<OT *>(a.simg) + (hi * cts + ct) * (XB * 512);
 #pragma unroll
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_mid(DeltaArgs a) {
         for (int r = 0; r < 4; ++r) R[rt][r] = t[r] * pr.inv;
         mx = abs_max(mx, R[rt]);
     }
-    const Pow2 pn(tile_max(mx), kOperand);
+    const Pow2 pn(tile_max(mx));
     OT *nimg = static_cast<OT *>(a.nimg) + (hi * cts + ct) * kOperandN<IO>;
 #pragma unroll
     for (int tb = 0; tb < 2; ++tb)
@@ -182,7 +182,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_mid(DeltaArgs a) {
         mx = abs_max(mx, R[rt]);
         my = abs_max(my, d);
     }
-    const Pow2 pe(col_max(mx)), py(tile_max(my), kOperand);
+    const Pow2 pe(col_max(mx)), py(tile_max(my));
     OT *yimg = static_cast<OT *>(a.yimg) + (hi * cts + ct) * 1024;
 #pragma unroll
     for (int tb = 0; tb < 2; ++tb) {
@@ -402,7 +402,7 @@ __global__ __launch_bounds__(256, 1) void k_delta_rev(DeltaArgs a) {
         float mx = 0.f;
 #pragma unroll
         for (int x = 0; x < NT; ++x) mx = abs_max(mx, dS[x]);
-        const Pow2 ps(tile_max(mx), kOperand);
+        const Pow2 ps(tile_max(mx));
         Split sf[XB];
         OT *ds = static_cast<OT *>(a.dsimg) + at * (XB * 512);
 #pragma unroll
@@ -483,7 +483,7 @@ __global__ __launch_bounds__(256, 1) void k_delta_rev(DeltaArgs a) {
             }
         }
         in.load_n(a, ahead, lane);
-        const Pow2 pz(tile_max(mz), kOperand);
+        const Pow2 pz(tile_max(mz));
         OT *dz = static_cast<OT *>(a.zimg) + at * kOperandN<IO>;
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb)
@@ -656,20 +656,25 @@ __device__ __forceinline__ double sum16(double v) {
     return dpp_addd<0x121>(v);
 }
 
-// Two tiles' operands under powers of two of their own: the product's common
-// power (its inverse) and what a lane's elements of the second operand take to
-// come under it (lane groups 0, 1 hold the first tile's columns, 2, 3 the
-// second's).
+// Two tiles' operands under powers of two of their own, given by their inverses:
+// what undoes the larger product's, and what a lane's elements of the second
+// operand take to come under it (lane groups 0, 1 hold the first tile's columns,
+// 2, 3 the second's).  In exponents, as the inverses' product can leave fp32's
+// range where the result does not; kDown keeps the products small, so that what
+// undoes them is not too small a number for results near the end of the range.
+// A tile that is far below the other one is lost in it, at 2^-26 of its largest.
 struct Pair {
-    float inv;
+    static constexpr int kDown = 12;
+    int exp;
     f16 part;
     __device__ Pair(const float *s, int x, int y, bool two, int g) {
-        const float e0 = s[x] * s[y], e1 = two ? s[kScales + x] * s[kScales + y] : e0;
-        inv = fmaxf(e0, e1);
-        part = (f16)__builtin_bit_cast(
-            float, __builtin_bit_cast(uint32_t, g < 2 ? e0 : e1) - __builtin_bit_cast(uint32_t, inv) +
-                       0x3f800000u);
+        const auto of = [&](int i) { return (int)(__builtin_bit_cast(uint32_t, s[i]) >> 23); };
+        const int e0 = of(x) + of(y), e1 = two ? of(kScales + x) + of(kScales + y) : e0;
+        const int top = max(e0, e1);
+        exp = top - 254 + kDown;
+        part = (f16)ldexpf(1.f, max((g < 2 ? e0 : e1) - top - kDown, -30));
     }
+    __device__ float undo(float v) const { return ldexpf(v, exp); }
 };
 
 // One stage of k_delta_grad in LDS: 32 value columns of a head (states in front
@@ -803,7 +808,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
                 const Pair sy(sc, kScS, kScY, two, g), sz(sc, kScS, kScZ, two, g),
                     dn(sc, kScD, kScN, two, g);
                 dys = dy * sy.part, zvs = zv * sz.part, nvd = nv * dn.part;
-                gq *= sy.inv, gz *= sz.inv, gn *= dn.inv;
+                gq = sy.undo(gq), gz = sz.undo(gz), gn = dn.undo(gn);
             }
             F dyn = dy, zvn = zv, zvl = zv, nvy = nv, nvz = nv;
             float ny = 1.f, nz = 1.f;
@@ -811,7 +816,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
                 const Pair py(sc, kScN, kScY, two, g), pz(sc, kScN, kScZ, two, g);
                 dyn = dy * py.part, zvn = zv * pz.part, nvy = nv * py.part, nvz = nv * pz.part;
                 zvl = cols_nat(ZV, 2 + (w >> 1), PN, w, lane) * pz.part;
-                ny = py.inv, nz = pz.inv;
+                ny = py.undo(1.f), nz = pz.undo(1.f);
             }
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {

@@ -193,6 +193,22 @@ def test_magnitudes(io, size):
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("v,dy", [(1e-25, 1e6), (1e8, 1e-26), (1e-18, 1.0), (1e15, 1e12)])
+def test_magnitudes_of_values_and_cotangents(io, v, dy):
+    """Values and cotangents of different sizes, a group of 16 value columns of
+    nothing but zeros beside one that is large, and one far below it."""
+    c = delta_case(23, 2, 130, 2, 1, 64, 64, io, normalize=True, init=True, v=lambda t: t * v,
+                   dy=lambda t: t * dy)
+    c["init"], c["d_final"] = c["init"] * v, c["d_final"] * dy
+    for name, axis in (("v", 3), ("dy", 3), ("init", 3), ("d_final", 3)):
+        c[name].narrow(axis, 16, 16).zero_()
+        c[name].narrow(axis, 48, 16).mul_(2.0 ** -40)
+    check_scan(c, io, "sizes %g %g" % (v, dy), normalize=True)
+    got = check_bwd(c, io, "sizes %g %g" % (v, dy), normalize=True)
+    assert (got["dv"][..., 16:32] == 0).all() and (got["d_init"][..., 16:32] == 0).all()
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_repeated_keys(io):
     """One key over and over, and nearly one: the triangle's inverse is furthest
     from the identity.  Errors gather along the chunk: four times the bound."""
