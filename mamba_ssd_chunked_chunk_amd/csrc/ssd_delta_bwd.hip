@@ -3,15 +3,16 @@
 //
 // k_delta_mid, all chunks in parallel: N = v - P^T k of 16 value columns per
 // wave, and what else does not need the adjoint state.  Bound by memory: 4 x 2048
-// tokens of 16 heads of 128 x 128 move 0.5 GB in 120 us.
+// tokens of 16 heads of 128 x 128 move 0.63 GB in 120 us.
 //
 // k_delta_rev, chunk after chunk from the end: the adjoint state of 16 value
 // columns in a wave's registers, as in the forward pass; leaves Z, dV, the
 // adjoint state behind every chunk, and per token the terms of the decays'
 // gradient that reach into the chunk from outside.  What k_delta_mid left, and
-// the state in front, come into registers a chunk ahead.  Bound by the chain of
-// one wave, 1900 instructions a chunk: 186 us for the same call, 5.8 us a chunk
-// (341 us where it formed those values itself and loaded the state at its use).
+// the state in front, come into registers a chunk ahead.  Bound by memory and the
+// chain of one wave, 1900 instructions a chunk, about alike: 186 us and 0.64 GB
+// for the same call, 5.8 us a chunk (341 us where it formed those values itself
+// and loaded the state at its use).
 //
 // k_delta_grad, all chunks in parallel: dq and dk, which contract over the value
 // columns, and the decays' terms inside the chunk.  A wave owns 16 tokens, all
@@ -20,7 +21,7 @@
 // heads that share q and k are walked in order by one workgroup.  With bf16 io
 // its operands are fp16 terms: one of each for dq and dk (2^-12 at most, a
 // sixteenth of their own rounding), two of N and Z where the decays' gradient
-// needs them.  125 us for the same call, which reads 0.3 GB (62 us of a copy).
+// needs them.  125 us for the same call, 0.45 GB (93 us of a copy).
 #include "ssd_delta.hpp"
 
 #include <math.h>

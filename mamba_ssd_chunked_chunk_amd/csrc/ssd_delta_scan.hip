@@ -6,21 +6,21 @@
 // 16 x 16 blocks: the four on the diagonal by substitution (a lane per block and
 // column), the others by distance from it, T_ij = -T_ii sum_k (kk beta)_ik T_kj,
 // on fp32 matrix instructions whose results feed the next product from registers.
-// Bound by its instructions: 4800 for a wave's first head, 1600 for each further
-// one of the group; two waves fit a SIMD.  65536 tokens of 64 heads, eight to a
-// group, keys of 128: 390 us, with 1.3 GB written (275 us of a copy); 8 x 2048
-// tokens of 24 heads with a group each 106 us.  Three waves to a SIMD would leave
-// 168 registers and spill a hundred.
+// Bound by memory, of which its outputs are most (with keys of 128 and bf16 io 32 KB
+// a chunk and group, 20 KB a chunk and head): 65536 tokens of 64 heads, eight to a
+// group, 390 us for 1.9 GB; 8 x 2048 tokens of 24 heads with a group each 106 us
+// for 0.53 GB; a large copy would take 386 and 108.
 //
 // k_delta_fwd, chunk after chunk: a wave owns 16 value columns of one head's
 // state in registers (an accumulator tile per 16 keys).  Columns do not meet
 // anywhere in the recurrence, and an accumulator tile is the operand of the
 // next product as it stands, so a wave passes from K S to N to the new state
 // without LDS or another wave; LDS holds only what all columns share (the
-// images of the next chunk arrive in the other buffer meanwhile).  Bound by the
-// chain of one wave, 1100 instructions a chunk, as long as there are fewer than two
-// to a SIMD: 8 x 2048 tokens of 24 heads of 128 x 64 143 us, 4.5 us a chunk; 16 x
-// 1000 tokens of 16 heads of 128 x 128 94 us.
+// images of the next chunk arrive in the other buffer meanwhile).  Bound by
+// memory where there are columns enough (8 x 2048 tokens of 24 heads of 128 x 64,
+// states kept, 143 us for 0.63 GB), by the chain of one wave, 1100 instructions a
+// chunk, where there are fewer: 16 x 1000 tokens of 16 heads of 128 x 128 94 us,
+// 0.35 GB.
 #include "ssd_delta.hpp"
 
 #include <math.h>
@@ -151,12 +151,6 @@ __device__ __forceinline__ void use_tile(const DeltaArgs &a, const RawTile<IO, N
 
 __device__ __forceinline__ constexpr int tri_tile(int i, int j) { return i * (i + 1) / 2 + j; }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) v = fmaxf(v, __shfl_xor(v, o));
-    return v;
-}
-
 // exp2 of a double, by its value in two floats.
 __device__ __forceinline__ float exp2_d(double x) {
     const float h = (float)x, e = exp2f(h);
@@ -281,7 +275,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
             r[kFq * kDC] = a.scale * fq;
             r[kBeta * kDC] = be;
             r[kRawQ * kDC] = fq;
-            const float most = wave_max(rd * fabsf(fk)), load = wave_max(fabsf(be * fk));
+            const float most = tile_max(rd * fabsf(fk)), load = tile_max(fabsf(be * fk));
             if (lane == 0) r[kCarry * kDC] = cuts ? 0.f : exp2_d(end), r[kCarry * kDC + 1] = most;
             bound = 64.f * load;
             if constexpr (GRAD) {
@@ -382,7 +376,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
                 float most = 0.f;
 #pragma unroll
                 for (int t = 0; t < 10; ++t) most = abs_max(most, T[t]);
-                most = wave_max(most);
+                most = tile_max(most);
                 if (lane == 0) rows[kCarry * kDC + 2] = bound * most;
             }
             f16 *dst = reinterpret_cast<f16 *>(himg + (m ? H::M : H::T)) + lane * 8;
