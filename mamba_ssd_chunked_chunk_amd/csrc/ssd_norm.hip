@@ -11,7 +11,9 @@
 // passes over it (mean, then the squares about it, which do not cancel) cost no
 // traffic.  G is 8 or 32 lanes for short rows, a wave up to 4096 elements, a
 // workgroup up to 16384; longer rows are read again for each pass.  All sums
-// are fp32.
+// are fp32.  16384 rows of 2560 with residual and statistics, bf16: 66 us, 5.1 TB/s;
+// their gradient 88 us, 3.8 TB/s, at two workgroups a compute unit (its registers
+// are the column sums; the next row loaded ahead gave 85 us for 50 more of them).
 //
 // In the gradient a lane keeps the same columns for every row of its
 // workgroup, so the column sums stay in registers too; each workgroup writes
