@@ -591,14 +591,18 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
 // instruction in four cycles).  A wave owns a quarter of the keys' rows of the
 // state and the rows of one of the four row tiles; what it has of K S and Q S
 // goes to the rows' owners, and R, u and e^{G_C - G} u, split, to everyone, through
-// LDS, with a barrier after each.  The powers of two that the waves have to
+// LDS, with a barrier after each.  There are three stretches between barriers (the end
+// of a chunk and the start of the next one are the same), and every place is written in
+// one and read in the one after it, so that no two of them may be the same bytes: a wave
+// still reads Q S while another writes the next chunk's K S.  The powers of two that the waves have to
 // share come from bounds that they exchange with the values before.  65536 tokens
 // of 64 heads of 128 x 64: 2.36 us a chunk, of them a third waits at the barriers;
 // operands read from LDS a chunk ahead saved 1% of it, a wait for the next chunk's
 // copies moved to the end of this one cost 3%.
 template <typename IO> struct CoopBuf {
     static constexpr int UL = sizeof(IO) == 4 ? 2 : 1;  // terms of u in the read-out
-    static constexpr int P = 0, R = P + 12 * 1024, W = R + 4 * 1024, U = W + 4 * 1024;
+    static constexpr int P = 0, Q = P + 12 * 1024, R = Q + 12 * 1024, W = R + 4 * 1024;
+    static constexpr int U = W + 4 * 1024;
     static constexpr int M = U + UL * 2 * 1024, BYTES = M + 3 * 4 * 64;
 };
 
@@ -619,6 +623,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
     const uint32_t base = lds_address(lds);
     char *ex = lds + NB * bufbytes;
     f32x4 *part = reinterpret_cast<f32x4 *>(ex + X::P);        // [to wave][3 others][lane]
+    f32x4 *qpart = reinterpret_cast<f32x4 *>(ex + X::Q);       // the same of Q S
     f16 *rfr = reinterpret_cast<f16 *>(ex + X::R);              // [hi, lo][32 tokens][lane][8]
     f16 *wfr = reinterpret_cast<f16 *>(ex + X::W);
     f16 *ufr = reinterpret_cast<f16 *>(ex + X::U);
@@ -775,7 +780,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
         put_half<F32>(ufr, U, pu.sc, w, lane);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
-            if (rt != w) part[(rt * 3 + (w < rt ? w : w - 1)) * 64 + lane] = qs[rt];
+            if (rt != w) qpart[(rt * 3 + (w < rt ? w : w - 1)) * 64 + lane] = qs[rt];
         vm_wait<0>();
         lds_barrier();
         // this wave's rows of the state
@@ -816,8 +821,8 @@ __global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
                         y = mma16(pf[PL - 1][tb], uh, y);
                     }
                 }
-            const f32x4 p0 = part[(w * 3) * 64 + lane], p1 = part[(w * 3 + 1) * 64 + lane],
-                        p2 = part[(w * 3 + 2) * 64 + lane];
+            const f32x4 p0 = qpart[(w * 3) * 64 + lane], p1 = qpart[(w * 3 + 1) * 64 + lane],
+                        p2 = qpart[(w * 3 + 2) * 64 + lane];
             const Rsrc ry = make_rsrc(static_cast<IO *>(a.y) + ((bb * a.l + t0) * a.h + hh) * a.p + col,
                                       (int64_t)(len - 1) * pitch + 16 * sizeof(IO));
 #pragma unroll
