@@ -594,14 +594,19 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
 // LDS, with a barrier after each.  There are three stretches between barriers (the end
 // of a chunk and the start of the next one are the same), and every place is written in
 // one and read in the one after it, so that no two of them may be the same bytes: a wave
-// still reads Q S while another writes the next chunk's K S.  The powers of two that the waves have to
-// share come from bounds that they exchange with the values before.  65536 tokens
-// of 64 heads of 128 x 64: 2.36 us a chunk, of them a third waits at the barriers;
-// operands read from LDS a chunk ahead saved 1% of it, a wait for the next chunk's
-// copies moved to the end of this one cost 3%.
+// still reads Q S while another writes the next chunk's K S.  With bf16 io Q S has a
+// place of its own (8192 tokens of 32 heads of 64 x 64: 290 us against 306 with a fourth
+// barrier); with fp32 io it takes that of K S, which a fourth barrier in front of its
+// next use allows: LDS then holds two buffers with keys of 64 (361 against 372 us), and
+// with keys of 128 the barrier is the faster one too (446 against 507).  The powers of
+// two that the waves have to share come from bounds that they exchange with the values
+// before.  65536 tokens of 64 heads of 128 x 64: 2.36 us a chunk, of them a third waits
+// at the barriers; operands read from LDS a chunk ahead saved 1% of it, a wait for the
+// next chunk's copies moved to the end of this one cost 3%.
 template <typename IO> struct CoopBuf {
     static constexpr int UL = sizeof(IO) == 4 ? 2 : 1;  // terms of u in the read-out
-    static constexpr int P = 0, Q = P + 12 * 1024, R = Q + 12 * 1024, W = R + 4 * 1024;
+    static constexpr bool SHARED = sizeof(IO) == 4;  // Q S in the place of K S
+    static constexpr int P = 0, Q = SHARED ? P : P + 12 * 1024, R = Q + 12 * 1024, W = R + 4 * 1024;
     static constexpr int U = W + 4 * 1024;
     static constexpr int M = U + UL * 2 * 1024, BYTES = M + 3 * 4 * 64;
 };
@@ -723,6 +728,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
             }
         }
         f32x4 mine = zero4(), myq = zero4();
+        if constexpr (X::SHARED) lds_barrier();  // everyone has read the last chunk's Q S
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
 #pragma unroll
