@@ -675,7 +675,9 @@ size_t ssd_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
  *   dt_softplus, dt_min, dt_max   as for ssd_chunk_scan
  *   scale        factor of y
  *   normalize    nonzero: q and k are divided by sqrt(|.|^2 + norm_eps) first
- *                (norm_eps >= 0, finite; a row of zeros stays zeros)
+ *                (norm_eps >= 0, finite; a row of zeros stays zeros, and its
+ *                gradient is 1 / sqrt(norm_eps) times that of the divided row,
+ *                nothing without norm_eps)
  *   init_state   [batch, heads, key_dim, value_dim] fp32 or NULL (zeros);
  *                16-byte aligned
  *   seq_idx      [batch, seqlen] int32 or NULL, as for ssd_chunk_scan_ex

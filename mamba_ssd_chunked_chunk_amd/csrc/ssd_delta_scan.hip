@@ -129,7 +129,8 @@ __device__ __forceinline__ void use_tile(const DeltaArgs &a, const RawTile<IO, N
         ss += __shfl_xor(ss, 32);
         // |row|^2 = ss / sc^2: the norm without leaving fp32's range
         factor = ss > 0.f ? 1.f / sqrtf(fmaf(a.eps * sc, sc, ss)) : 0.f;
-        norm = factor * sc;
+        // a row of zeros has no factor, but its gradient is divided by sqrt(eps)
+        norm = ss > 0.f ? factor * sc : a.eps > 0.f ? 1.f / sqrtf(a.eps) : 0.f;
     }
     if (g == 0) fac[row] = factor, rn[row] = norm;
     if (img) {

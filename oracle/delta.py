@@ -15,7 +15,8 @@ def _unit(x, normalize, eps):
     if not normalize:
         return x, np.ones(x.shape[:-1] + (1,))
     ss = (x * x).sum(-1, keepdims=True)
-    r = np.where(ss > 0, 1 / np.sqrt(np.where(ss > 0, ss + eps, 1.0)), 0.0)
+    ss = ss + eps
+    r = np.where(ss > 0, 1 / np.sqrt(np.where(ss > 0, ss, 1.0)), 0.0)
     return x * r, r
 
 

@@ -1,0 +1,67 @@
+"""The gated delta rule where rows of q and k are zeros or nearly so: the outputs of
+these rows alone, which next to the others' would not show."""
+import numpy as np
+import pytest
+
+from delta_util import BOUNDS, as64, delta_case, rel
+from gpu_util import log, torch_mod
+from oracle import delta as oracle
+
+pytestmark = pytest.mark.gpu
+
+NAMES = ("q", "k", "v", "dt", "A", "beta")
+
+
+def _rows(seed, n, p, io, size, h=4, g=2):
+    """Every fourth row of q and every fifth of k `size` times as large."""
+    c = delta_case(seed, 2, 150, h, g, n, p, io, normalize=True, init=True, packed=True)
+    for name, step in (("q", 4), ("k", 5)):
+        c[name] = c[name].clone()
+        c[name][:, ::step] *= size
+    return c
+
+
+def _check(c, io, what, step=True, **kw):
+    import mamba_ssd_chunked_chunk_amd as ssd
+    torch = torch_mod()
+    args = [c[k] for k in NAMES]
+    side = dict(dt_bias=c["dt_bias"], normalize=True, **kw)
+    y, fin, st = ssd.delta_scan(*args, initial_state=c["init"], seq_idx=c["seq"],
+                                return_final_state=True, return_states=True, **side)
+    got = ssd.delta_scan_bwd(*args, c["dy"], initial_state=c["init"], seq_idx=c["seq"],
+                             d_final=c["d_final"], states=st, **side)
+    e = as64(c)
+    inputs = dict(init=e["init"], seq=e["seq"], **dict(side, dt_bias=e["dt_bias"]))
+    ref = oracle.scan(*(e[k] for k in NAMES), **inputs)
+    rg = oracle.grad(*(e[k] for k in NAMES), dy=e["dy"], d_final=e["d_final"], **inputs)
+    few = dict(dq=slice(None, None, 4), dk=slice(None, None, 5))
+    rest = {k: [t for t in range(150) if t % s.step] for k, s in few.items()}
+    for name, o in rg.items():
+        for part in ((few[name], rest[name]) if name in few else (slice(None),)):
+            r = rel(got[name][:, part] if name in few else got[name],
+                    o[:, part] if name in few else o)
+            log(what, name, "%.2e" % r)
+            assert r <= BOUNDS[io][name], (what, name, r)
+    for part in (few["dq"], rest["dq"]):
+        r = rel(y[:, part], ref["y"][:, part])
+        assert r <= BOUNDS[io]["y"], (what, "y", r)
+    assert rel(fin, ref["final"]) <= BOUNDS[io]["state"]
+    assert rel(st, ref["states"]) <= BOUNDS[io]["state"]
+    # one token in the manner of a decode step: those of q, of k, and of both
+    for t in (4, 5, 20):
+        state = torch.from_numpy(np.ascontiguousarray(ref["states"][:, 1], np.float32)).cuda()
+        before = state.double().cpu().numpy()
+        tok = [c[k] if k == "A" else c[k][:, t].contiguous() for k in NAMES]
+        ys = ssd.delta_step(state, *tok, **side)
+        yo, so = oracle.step(before, *(e[k] if k == "A" else e[k][:, t] for k in NAMES),
+                             **dict(side, dt_bias=e["dt_bias"]))
+        assert rel(state, so) < 1e-6 and rel(ys, yo) < (2e-6 if io == "f32" else 2.0 ** -8), t
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("n,p", [(32, 16), (64, 64), (128, 128)])
+def test_rows_of_zeros(io, n, p):
+    """x / sqrt(|x|^2 + eps) has the derivative 1 / sqrt(eps) at zero."""
+    _check(_rows(n, n, p, io, 0.0), io, "zeros %d %d" % (n, p))
+    # more columns than one walk's four waves to sixteen of them take
+    _check(_rows(n + 1, n, p, io, 0.0, h=132, g=4), io, "zeros %d %d, many heads" % (n, p))
