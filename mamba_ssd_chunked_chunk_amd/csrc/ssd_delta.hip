@@ -67,7 +67,7 @@ __global__ __launch_bounds__((StepShape<IO, N, P>::THREADS)) void k_delta_step(D
             for (int e = 0; e < E; ++e) v[e] *= sc, ss = fmaf(v[e], v[e], ss);
 #pragma unroll
             for (int o = 1; o < 64; o <<= 1) ss += __shfl_xor(ss, o);
-            unit = ss > 0.f ? 1.f / sqrtf(fmaf(a.eps * sc, sc, ss)) : 0.f;
+            unit = UnitRow(ss, sc, 1.f / sc, a.eps).of_scaled;
         }
 #pragma unroll
         for (int e = 0; e < E; ++e)

@@ -41,6 +41,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "ssd_device.hpp"
@@ -183,6 +184,21 @@ struct Pow2 {
         f = f > 253 ? 253 : f;
         sc = __builtin_bit_cast(float, (uint32_t)f << 23);
         inv = __builtin_bit_cast(float, (uint32_t)(254 - f) << 23);
+    }
+};
+
+// What divides a row x by sqrt(|x|^2 + eps), for x itself and for sc x, whose sum of
+// squares is ss (sc a power of two that brings the row's largest value into [1/2, 1),
+// back its inverse): neither |x|^2 nor eps sc^2 need be in fp32's range.
+struct UnitRow {
+    float of_x, of_scaled;
+    __device__ UnitRow(float ss, float sc, float back, float eps) {
+        const float e = eps * sc * sc;
+        if (ss > 0.f && e < INFINITY) {
+            of_scaled = 1.f / sqrtf(ss + e), of_x = of_scaled * sc;
+        } else {  // |x|^2 is nothing beside eps; a row of zeros without eps stays that
+            of_x = eps > 0.f ? 1.f / sqrtf(eps) : 0.f, of_scaled = ss > 0.f ? of_x * back : 0.f;
+        }
     }
 };
 

@@ -127,10 +127,8 @@ __device__ __forceinline__ void use_tile(const DeltaArgs &a, const RawTile<IO, N
             for (int i = 0; i < 8; ++i) ss = fmaf(v[kb][i], v[kb][i], ss);
         ss += __shfl_xor(ss, 16);
         ss += __shfl_xor(ss, 32);
-        // |row|^2 = ss / sc^2: the norm without leaving fp32's range
-        factor = ss > 0.f ? 1.f / sqrtf(fmaf(a.eps * sc, sc, ss)) : 0.f;
-        // a row of zeros has no factor, but its gradient is divided by sqrt(eps)
-        norm = ss > 0.f ? factor * sc : a.eps > 0.f ? 1.f / sqrtf(a.eps) : 0.f;
+        const UnitRow u(ss, sc, back, a.eps);
+        factor = u.of_scaled, norm = u.of_x;
     }
     if (g == 0) fac[row] = factor, rn[row] = norm;
     if (img) {

@@ -65,3 +65,12 @@ def test_rows_of_zeros(io, n, p):
     _check(_rows(n, n, p, io, 0.0), io, "zeros %d %d" % (n, p))
     # more columns than one walk's four waves to sixteen of them take
     _check(_rows(n + 1, n, p, io, 0.0, h=132, g=4), io, "zeros %d %d, many heads" % (n, p))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size,eps", [(1e-25, 1e-6), (1e-36, 1e-6), (1e-12, 1e-6), (1e-18, 1e-36),
+                                      (1e-18, 1e25)])
+def test_small_rows(io, size, eps):
+    """Rows that eps outweighs by far, by a little or not at all, down to where their
+    squares and eps in units of them leave fp32's range."""
+    _check(_rows(5, 64, 32, io, size), io, "size %g eps %g" % (size, eps), norm_eps=eps)
