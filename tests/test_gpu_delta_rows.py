@@ -55,7 +55,11 @@ def _check(c, io, what, step=True, **kw):
         ys = ssd.delta_step(state, *tok, **side)
         yo, so = oracle.step(before, *(e[k] if k == "A" else e[k][:, t] for k in NAMES),
                              **dict(side, dt_bias=e["dt_bias"]))
-        assert rel(state, so) < 1e-6 and rel(ys, yo) < (2e-6 if io == "f32" else 2.0 ** -8), t
+        # (y of a small q with a small state is below fp32's normal range: there each of
+        # the n products and sums is off by up to 2^-150 of its own, whatever its size)
+        off = np.maximum(np.abs(ys.double().cpu().numpy() - yo) - c["k"].shape[-1] * 2.0 ** -150, 0)
+        assert rel(state, so) < 1e-6, t
+        assert np.linalg.norm(off) <= (2e-6 if io == "f32" else 2.0 ** -8) * np.linalg.norm(yo), t
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
