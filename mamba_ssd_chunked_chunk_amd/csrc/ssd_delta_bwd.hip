@@ -898,8 +898,11 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
         }
         // the terms of the decays' gradient inside the chunk, C_mj for j < m
         {
-            const float fkm = F32 ? r2[kRk * kDC + m] : rows[kFk * kDC + m];
-            const float fqm = F32 ? a.scale * r2[kRq * kDC + m] : rows[kFq * kDC + m];
+            // the products' factors; fp32 rows have theirs (1 / norm) taken first, as the
+            // products of rows as they come can leave fp32's range
+            const float fkm = F32 ? 1.f : rows[kFk * kDC + m];
+            const float fqm = F32 ? a.scale : rows[kFq * kDC + m];
+            const float rkm = r2[kRk * kDC + m], rqm = r2[kRq * kDC + m];
             double sum = 0.0;
             double *cells = a.cells + hi * (5 * kDC);
 #pragma unroll
@@ -907,13 +910,17 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
                 double col[4] = {0.0, 0.0, 0.0, 0.0};
                 if (rt <= w) {
                     f32x4 kk = zero4(), qk = zero4();
+                    const float rkj = r2[kRk * kDC + 16 * rt + j16];
 #pragma unroll
                     for (int kb = 0; kb < XB; ++kb) {
-                        const F kj = img_rows(K, rt * XB + kb, lane);
-                        qk = mma8(kj, img_rows(Q, w * XB + kb, lane), qk);
-                        kk = mma8(kj, img_rows(K, w * XB + kb, lane), kk);
+                        F kj = img_rows(K, rt * XB + kb, lane), qm = img_rows(Q, w * XB + kb, lane),
+                          km = img_rows(K, w * XB + kb, lane);
+                        if constexpr (F32) kj *= rkj, qm *= rqm, km *= rkm;
+                        qk = mma8(kj, qm, qk);
+                        kk = mma8(kj, km, kk);
                     }
-                    const f32x4 bj = row4(rows, kBeta, rt, lane), fk = of_k(rt);
+                    const f32x4 bj = row4(rows, kBeta, rt, lane),
+                                fk = F32 ? f32x4{1.f, 1.f, 1.f, 1.f} : of_k(rt);
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int j = 16 * rt + 4 * g + r;

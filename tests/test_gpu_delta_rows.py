@@ -80,3 +80,15 @@ def test_small_rows(io, size, eps):
     """Rows that eps outweighs by far, by a little or not at all, down to where their
     squares and eps in units of them leave fp32's range."""
     _check(_rows(5, 64, 32, io, size), io, "size %g eps %g" % (size, eps), norm_eps=eps)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [1e-25, 1e25])
+def test_rows_of_every_size_without_eps(io, size):
+    """Divided by their norm, rows of any size are alike, their products among
+    themselves (1e-50, 1e50) too."""
+    c = _rows(6, 64, 32, io, size)
+    _check(c, io, "size %g without eps" % size, norm_eps=0.0)
+    for k in ("q", "k"):
+        c[k] = c[k] * (1 / size if size > 1 else size ** 0.5)
+    _check(c, io, "sizes to %g without eps" % size, norm_eps=0.0)
