@@ -327,7 +327,7 @@ int32_t ssd_delta_scan_bwd(const void *q, const void *k, const void *v, const vo
     if (!states) a.states = reinterpret_cast<float *>(ws + W.states);
     hipError_t e = delta_prep(a, io_dtype, n, true, s);
     if (!states) {
-        a.y = a.nimg;  // not needed: to where N comes later
+        a.y = a.nimg;  // not needed, nor right with these images: to where N comes later
         if (e == hipSuccess) e = delta_forward(a, io_dtype, n, s);
         a.kept = a.states;
     }

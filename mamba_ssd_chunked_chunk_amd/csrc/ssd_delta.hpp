@@ -31,9 +31,11 @@
 //
 // Precision.  The products run on fp16 matrix instructions with fp32
 // accumulation.  Every operand is an fp32 value times a power of two (per row
-// of q and k, per column of a state or of a chunk's rows, so that the largest
-// magnitude fits), written as two fp16 terms hi + lo, 22 significant bits, and
-// multiplied as hi hi + hi lo + lo hi; q and k of bf16 io are exact in one.
+// of q, k and tril(Q K^T), per column of a state or of a chunk's rows, one for an
+// inverse, so that the largest magnitude fits), written as two fp16 terms hi + lo, 22
+// significant bits (fewer below 2^-16 of the largest, of which an element is off by
+// 2^-38 at most), and multiplied as hi hi + hi lo + lo hi; q and k of bf16 io are
+// exact in one.
 // With bf16 io the read-out (Y) and the products of dQ and dK take hi terms alone:
 // their 2^-12 at most is a sixteenth of the result's own rounding.  States, sums,
 // decays and the triangular inverse are fp32, the log decays' sums fp64, and so
@@ -57,13 +59,21 @@ constexpr int kRowsGrad = 8;  // row arrays of the gradient's last pass
 // of two that k and q are stored with (times 1 / norm where the call normalises).
 enum RowOf {
     kReadK,   // e^G fk
-    kFk,      // fk
+    kFk,      // fk; for the scans alone what undoes the row's power of two in tril(Q K^T)
     kWriteK,  // e^{G_C - G} fk
     kReadQ,   // scale e^G fq
-    kFq,      // scale fq
+    kFq,      // scale fq; for the gradient times what undoes that power of two
     kBeta,    // beta
-    kCarry,   // [0]: e^{G_C}; [1], [2]: bounds of kReadK and of beta fk times an inverse's row
+    kCarry,   // see CarryOf
     kRawQ     // fq
+};
+enum CarryOf {
+    kKeep,    // e^{G_C}
+    kMostK,   // the largest kReadK
+    kMostN,   // a bound of N over the largest |R|: the largest sum of a row of |inverse|
+    kMostW,   // the same of beta kWriteK N
+    kInvT,    // what undoes the inverses' powers of two
+    kInvM
 };
 enum RowOfGrad {
     kGhi,    // log2 of e^G, as two floats

@@ -150,6 +150,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_mid(DeltaArgs a) {
     Split rf[2];
 #pragma unroll
     for (int tb = 0; tb < 2; ++tb) rf[tb] = split8(R[2 * tb], R[2 * tb + 1], pr.sc);
+    const float undo = pr.inv * rows[kCarry * kDC + kInvT];
     mx = 0.f;
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
@@ -163,7 +164,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_mid(DeltaArgs a) {
             t = mma16(img_cols(T + kPieces * 512, p0, p1, rt, lane), rf[tb].hi, t);
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) R[rt][r] = t[r] * pr.inv;
+        for (int r = 0; r < 4; ++r) R[rt][r] = t[r] * undo;
         mx = abs_max(mx, R[rt]);
     }
     const Pow2 pn(tile_max(mx));
@@ -384,7 +385,7 @@ __global__ __launch_bounds__(256, 1) void k_delta_rev(DeltaArgs a) {
         const f16 *M = reinterpret_cast<const f16 *>(buf + B::M);
         const float *rows = reinterpret_cast<const float *>(buf + B::R);
         const IO *dY = reinterpret_cast<const IO *>(buf + B::DY);
-        const float carry = rows[kCarry * kDC];
+        const float carry = rows[kCarry * kDC + kKeep];
 
         // e^{G_C} <S, dS> of these columns
         {
@@ -449,6 +450,7 @@ __global__ __launch_bounds__(256, 1) void k_delta_rev(DeltaArgs a) {
         in.load_x(a, ahead, lane);
         // Z, dV = beta Z, and their rows' products
         const Pow2 pu(col_max(mx));
+        const float undo = pu.inv * rows[kCarry * kDC + kInvM];
         Split uf[2];
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) uf[tb] = split8(U[2 * tb], U[2 * tb + 1], pu.sc);
@@ -466,7 +468,7 @@ __global__ __launch_bounds__(256, 1) void k_delta_rev(DeltaArgs a) {
             f32x4 sk, so, sz;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                Z[rt][r] = t[r] * pu.inv;
+                Z[rt][r] = t[r] * undo;
                 const float v = be[r] * Z[rt][r];
                 W[rt][r] = rk[r] * v;
                 buf_put(rv, (16 * rt + 4 * g + r) * pitch + j16 * sizeof(IO), v, IO{});
@@ -874,10 +876,9 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
         // the rows of k and q are the image's times these
         const auto of_k = [&](int rt) { return F32 ? row4(r2, kRk, rt, lane) : row4(rows, kFk, rt, lane); };
         const auto of_q = [&](int rt) {  // and scale
-            f32x4 f = F32 ? row4(r2, kRq, rt, lane) : row4(rows, kFq, rt, lane);
-            if constexpr (F32)
+            f32x4 f = F32 ? row4(r2, kRq, rt, lane) : row4(rows, kRawQ, rt, lane);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) f[r] *= a.scale;
+            for (int r = 0; r < 4; ++r) f[r] *= a.scale;
             return f;
         };
         const float bm = rows[kBeta * kDC + m];
@@ -901,7 +902,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
             // the products' factors; fp32 rows have theirs (1 / norm) taken first, as the
             // products of rows as they come can leave fp32's range
             const float fkm = F32 ? 1.f : rows[kFk * kDC + m];
-            const float fqm = F32 ? a.scale : rows[kFq * kDC + m];
+            const float fqm = F32 ? a.scale : a.scale * rows[kRawQ * kDC + m];
             const float rkm = r2[kRk * kDC + m], rqm = r2[kRq * kDC + m];
             double sum = 0.0;
             double *cells = a.cells + hi * (5 * kDC);

@@ -235,7 +235,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
         char *himg = a.himg + hi * a.hstride;
         float *rows = reinterpret_cast<float *>(himg + H::R);
         // decays: a lane per token
-        float bound;
+        float load;
         {
             const int64_t at = (bb * a.l + t0 + lane) * a.h + hh;
             const bool in = lane < len;
@@ -268,15 +268,16 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
             const float fk = L.fac[0][lane], fq = L.fac[1][lane];
             float *r = rows + lane;
             r[kReadK * kDC] = rd * fk;
-            r[kFk * kDC] = fk;
+            if constexpr (GRAD) r[kFk * kDC] = fk;
             r[kWriteK * kDC] = wr * fk;
             r[kReadQ * kDC] = a.scale * rd * fq;
-            r[kFq * kDC] = a.scale * fq;
+            if constexpr (!GRAD) r[kFq * kDC] = a.scale * fq;
             r[kBeta * kDC] = be;
             r[kRawQ * kDC] = fq;
-            const float most = tile_max(rd * fabsf(fk)), load = tile_max(fabsf(be * fk));
-            if (lane == 0) r[kCarry * kDC] = cuts ? 0.f : exp2_d(end), r[kCarry * kDC + 1] = most;
-            bound = 64.f * load;
+            const float most = tile_max(rd * fabsf(fk));
+            load = tile_max(fabsf(be * wr * fk));
+            float *carry = rows + kCarry * kDC;
+            if (lane == 0) carry[kKeep] = cuts ? 0.f : exp2_d(end), carry[kMostK] = most;
             if constexpr (GRAD) {
                 float *e = a.rows2 + hi * (kRowsGrad * kDC) + lane;
                 e[kGhi * kDC] = gh;
@@ -297,10 +298,13 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
             const int i = 16 * it + j16;
             const float gi = L.ghi[i], li = L.glo[i], di = L.doc[i], fi = L.fac[0][i];
             f32x4 pq[4];
+            float mx = 0.f;
 #pragma unroll
             for (int jt = 0; jt < 4; ++jt) {
                 pq[jt] = zero4();
                 if (jt > it) continue;
+                f32x4 bj = f32x4{1.f, 1.f, 1.f, 1.f};
+                if constexpr (!GRAD) bj = row4(L.bet, 0, jt, lane);
                 const f32x4 gj = row4(L.ghi, 0, jt, lane), lj = row4(L.glo, 0, jt, lane),
                             dj = row4(L.doc, 0, jt, lane), fj = row4(L.fac[0], 0, jt, lane);
                 f32x4 d;
@@ -311,13 +315,18 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
                     d[r] = in ? e : 0.f;
                     const float k = kk[tri_tile(it, jt)][r] * d[r] * (fi * fj[r]);
                     A[tri_tile(it, jt)][r] = jt < it || 4 * g + r < j16 ? k : 0.f;
-                    pq[jt][r] = qk[tri_tile(it, jt)][r] * d[r];
+                    // the read-out takes N: with the factors that make u of it no element
+                    // counts that is multiplied by nothing
+                    pq[jt][r] = qk[tri_tile(it, jt)][r] * d[r] * (GRAD ? 1.f : bj[r] * fj[r]);
                 }
+                mx = abs_max(mx, pq[jt]);
             }
+            const Pow2 pp(col_max(mx));
+            if (g == 0) rows[(GRAD ? kFq : kFk) * kDC + i] = GRAD ? a.scale * L.fac[1][i] * pp.inv : pp.inv;
             f16 *dst = reinterpret_cast<f16 *>(himg + H::P) + lane * 8;
 #pragma unroll
             for (int kb = 0; kb <= it / 2; ++kb) {
-                const Split s = split8(pq[2 * kb], pq[2 * kb + 1], 1.f);
+                const Split s = split8(pq[2 * kb], pq[2 * kb + 1], pp.sc);
                 *reinterpret_cast<f16x8 *>(dst + tri_piece(it, kb) * 512) = s.hi;
                 if constexpr (PPL == 2)
                     *reinterpret_cast<f16x8 *>(dst + (kPieces + tri_piece(it, kb)) * 512) = s.lo;
@@ -371,12 +380,26 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
                         o = Mfma<float>::mma(ti[i][q], m == 0 ? -y[q] : -be[i][q] * y[q], o);
                     T[tri_tile(i, j)] = o;
                 }
-            if (m == 0) {
-                float most = 0.f;
+            float most = 0.f;
 #pragma unroll
-                for (int t = 0; t < 10; ++t) most = abs_max(most, T[t]);
-                most = tile_max(most);
-                if (lane == 0) rows[kCarry * kDC + 2] = bound * most;
+            for (int t = 0; t < 10; ++t) most = abs_max(most, T[t]);
+            const Pow2 pt(tile_max(most));
+            float *carry = rows + kCarry * kDC;
+            if (lane == 0) carry[m == 0 ? kInvT : kInvM] = pt.inv;
+            if (m == 0) {
+                most = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f32x4 sum = zero4();
+#pragma unroll
+                    for (int j = 0; j <= i; ++j)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) sum[r] += fabsf(T[tri_tile(i, j)][r]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) most = fmaxf(most, sum16(sum[r]));
+                }
+                most = col_max(most);
+                if (lane == 0) carry[kMostN] = most, carry[kMostW] = most * load;
             }
             f16 *dst = reinterpret_cast<f16 *>(himg + (m ? H::M : H::T)) + lane * 8;
 #pragma unroll
@@ -384,7 +407,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
 #pragma unroll
                 for (int ib = jt / 2; ib < 2; ++ib) {
                     const f32x4 up = jt > 2 * ib ? zero4() : T[tri_tile(2 * ib, jt > 2 * ib ? 0 : jt)];
-                    const Split s = split8(up, T[tri_tile(2 * ib + 1, jt)], 1.f);
+                    const Split s = split8(up, T[tri_tile(2 * ib + 1, jt)], pt.sc);
                     *reinterpret_cast<f16x8 *>(dst + tri_piece_t(jt, ib) * 512) = s.hi;
                     *reinterpret_cast<f16x8 *>(dst + (kPieces + tri_piece_t(jt, ib)) * 512) = s.lo;
                 }
@@ -477,7 +500,9 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
         Split rf[2];
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) rf[tb] = split8(R[2 * tb], R[2 * tb + 1], pr.sc);
-        f32x4 U[4], W[4];
+        f32x4 U[4], W[4];  // N, and e^{G_C - G} u
+        const float undo = pr.inv * rows[kCarry * kDC + kInvT];
+        float mw = 0.f;
         mx = 0.f;
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
@@ -490,23 +515,21 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
                 t = mma16(th, rf[tb].lo, t);
                 t = mma16(img_cols(T + kPieces * 512, p0, p1, rt, lane), rf[tb].hi, t);
             }
-            const f32x4 be = row4(rows, kBeta, rt, lane), fk = row4(rows, kFk, rt, lane),
-                        wk = row4(rows, kWriteK, rt, lane);
+            const f32x4 be = row4(rows, kBeta, rt, lane), wk = row4(rows, kWriteK, rt, lane);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float v = t[r] * pr.inv;
-                U[rt][r] = v * be[r] * fk[r];
-                W[rt][r] = v * be[r] * wk[r];
+                U[rt][r] = t[r] * undo;
+                W[rt][r] = U[rt][r] * be[r] * wk[r];
             }
             mx = abs_max(mx, U[rt]);
+            mw = abs_max(mw, W[rt]);
         }
-        // e^{G_C - G} <= 1, so one power of two serves both
-        const Pow2 pu(col_max(mx));
-        const float carry = rows[kCarry * kDC];
+        const Pow2 pu(col_max(mx)), pw(col_max(mw));
+        const float carry = rows[kCarry * kDC + kKeep];
         {
             Split wf[2];
 #pragma unroll
-            for (int tb = 0; tb < 2; ++tb) wf[tb] = split8(W[2 * tb], W[2 * tb + 1], pu.sc);
+            for (int tb = 0; tb < 2; ++tb) wf[tb] = split8(W[2 * tb], W[2 * tb + 1], pw.sc);
 #pragma unroll
             for (int x = 0; x < NT; ++x) {
                 f32x4 t = zero4();
@@ -519,10 +542,10 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
                     if constexpr (F32) t = mma16(img_cols(K + IMG, p0, p1, x, lane), wf[tb].hi, t);
                 }
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[x][r] = fmaf(t[r], pu.inv, carry * S[x][r]);
+                for (int r = 0; r < 4; ++r) S[x][r] = fmaf(t[r], pw.inv, carry * S[x][r]);
             }
         }
-        // Y = scale (e^G Q S + tril(Q K^T) U)
+        // Y = scale (e^G Q S + tril(Q K^T) U), the latter's image with what makes u of N
         Split uf[2];
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) uf[tb] = split8(U[2 * tb], U[2 * tb + 1], pu.sc);
@@ -545,10 +568,11 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
                     u = mma16(img_rows(P + kPieces * 512, tri_piece(rt, tb), lane), uf[tb].hi, u);
                 }
             }
-            const f32x4 fr = row4(rows, kReadQ, rt, lane), fp = row4(rows, kFq, rt, lane);
+            const f32x4 fr = row4(rows, kReadQ, rt, lane), fp = row4(rows, kFq, rt, lane),
+                        fi = row4(rows, kFk, rt, lane);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                Y[rt][r] = fmaf(fr[r] * ps.inv, t[r], fp[r] * pu.inv * u[r]);
+                Y[rt][r] = fmaf(fr[r] * ps.inv, t[r], fp[r] * (fi[r] * (pu.inv * u[r])));
         }
         {
             const uint32_t pitch = (uint32_t)(a.h * a.p * sizeof(IO));
@@ -610,8 +634,10 @@ template <typename IO> struct CoopBuf {
     static constexpr int M = U + UL * 2 * 1024, BYTES = M + 3 * 4 * 64;
 };
 
+// LDS leaves room for one workgroup a unit.  (Told so, the compiler spills nothing with
+// fp32 keys of 128, 448 against 492 us; with bf16 it gains nothing by it.)
 template <typename IO, int N, int NB>
-__global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
+__global__ __launch_bounds__(256, sizeof(IO) == 4 ? 1 : 2) void k_delta_coop(DeltaArgs a) {
     typedef FwdBuf<IO, N, false> B;
     typedef CoopBuf<IO> X;
     constexpr bool F32 = sizeof(IO) == 4;
@@ -694,11 +720,12 @@ __global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
                 }
         }
         const f32x4 v = lds_tile(V, 16, w, 0, lane);
-        const f32x4 fr = row4(rows, kReadK, w, lane), fk = row4(rows, kFk, w, lane),
+        const f32x4 fr = row4(rows, kReadK, w, lane), fi = row4(rows, kFk, w, lane),
                     wk = row4(rows, kWriteK, w, lane), be = row4(rows, kBeta, w, lane),
                     yr = row4(rows, kReadQ, w, lane), yp = row4(rows, kFq, w, lane);
-        const float carry = rows[kCarry * kDC], mostf = rows[kCarry * kDC + 1],
-                    mostu = rows[kCarry * kDC + 2];
+        const float *head = rows + kCarry * kDC;
+        const float carry = head[kKeep], mostf = head[kMostK], mostn = head[kMostN],
+                    mostw = head[kMostW], invt = head[kInvT];
 
         // this wave's part of K S and Q S
         float mx = 0.f;
@@ -760,7 +787,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
         if (g == 0) mxs[128 + w * 16 + j16] = mr;
         put_half(rfr, R, pr.sc, w, lane);
         lds_barrier();
-        // N = T R, and u
+        // N = T R, and e^{G_C - G} u
         f32x4 n = zero4();
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb)
@@ -770,19 +797,19 @@ __global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
                 n = mma16(tf[0][tb], rl, n);
                 n = mma16(tf[1][tb], rh, n);
             }
-        f32x4 U, W;
+        f32x4 W;
+        const float undo = pr.inv * invt;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const float u = n[r] * pr.inv * be[r];
-            U[r] = u * fk[r];
-            W[r] = u * wk[r];
+            n[r] *= undo;
+            W[r] = n[r] * be[r] * wk[r];
         }
         top = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) top = fmaxf(top, mxs[128 + i * 16 + j16]);
-        const Pow2 pu(mostu * top);
-        put_half(wfr, W, pu.sc, w, lane);
-        put_half<F32>(ufr, U, pu.sc, w, lane);
+        const Pow2 pu(mostn * top), pw(mostw * top);
+        put_half(wfr, W, pw.sc, w, lane);
+        put_half<F32>(ufr, n, pu.sc, w, lane);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
             if (rt != w) qpart[(rt * 3 + (w < rt ? w : w - 1)) * 64 + lane] = qs[rt];
@@ -805,7 +832,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
 #pragma unroll
         for (int x = 0; x < TPW; ++x)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) S[x][r] = owner ? fmaf(t[x][r], pu.inv, carry * S[x][r]) : 0.f;
+            for (int r = 0; r < 4; ++r) S[x][r] = owner ? fmaf(t[x][r], pw.inv, carry * S[x][r]) : 0.f;
         if (a.states && owner) {
             float *st = a.states + hi * N * a.p + col + j16;
 #pragma unroll
@@ -833,7 +860,8 @@ __global__ __launch_bounds__(256, 2) void k_delta_coop(DeltaArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r)
                 buf_put(ry, (16 * w + 4 * g + r) * pitch + j16 * sizeof(IO),
-                        fmaf(yr[r], (p0[r] + p1[r]) + (p2[r] + myq[r]), yp[r] * pu.inv * y[r]), IO{});
+                        fmaf(yr[r], (p0[r] + p1[r]) + (p2[r] + myq[r]),
+                             yp[r] * (fi[r] * (pu.inv * y[r]))), IO{});
         }
     }
     if (a.fin && owner) {
