@@ -156,11 +156,11 @@ struct DeltaWs {
     }
     DeltaWs(int64_t b, int64_t l, int64_t h, int64_t n, int64_t p, int64_t g, int io, bool grad,
             bool keep) {
-        const size_t el = io == SSD_BF16 ? 2 : 4, planes = el / 2;
+        const size_t el = io == SSD_BF16 ? 2 : 4, planes = el / 2;  // of k and q
         const size_t nc = (size_t)((l + kDC - 1) / kDC), ch = b * nc * h, cg = b * nc * g;
         const size_t tri = kPieces * 1024;
         gimg = add(cg * 2 * planes * kDC * n * 2);
-        hbytes = 2 * tri + kRows * kDC * 4 + (grad ? 4 : planes) * tri;
+        hbytes = 2 * tri + kRows * kDC * 4 + (grad ? 4 : 2) * tri;
         himg = add(ch * hbytes);
         rows2 = nimg = zimg = simg = dsimg = yimg = scales = g0 = x0 = toks = eend = cells = part = states = 0;
         if (!grad) return;

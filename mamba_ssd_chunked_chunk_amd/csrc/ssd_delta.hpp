@@ -36,8 +36,8 @@
 // significant bits (fewer below 2^-16 of the largest, of which an element is off by
 // 2^-38 at most), and multiplied as hi hi + hi lo + lo hi; q and k of bf16 io are
 // exact in one.
-// With bf16 io the read-out (Y) and the products of dQ and dK take hi terms alone:
-// their 2^-12 at most is a sixteenth of the result's own rounding.  States, sums,
+// With bf16 io the products of dQ and dK take hi terms alone, 2^-11 at most of each
+// operand, an eighth of the result's own rounding.  States, sums,
 // decays and the triangular inverse are fp32, the log decays' sums fp64, and so
 // are the sums of C_ij, of which a row's and a column's share all but a few terms.
 #pragma once
@@ -231,16 +231,14 @@ __device__ __forceinline__ Split split8(const f32x4 &a, const f32x4 &b, float sc
 }
 
 // One row tile's share of such fragments in LDS ([hi, lo][2 blocks of 32 rows][lane][8]).
-template <bool LO = true>
 __device__ __forceinline__ void put_half(f16 *dst, const f32x4 &v, float sc, int rt, int lane) {
     const f16x2 h0 = __builtin_convertvector(f32x2{v[0] * sc, v[1] * sc}, f16x2);
     const f16x2 h1 = __builtin_convertvector(f32x2{v[2] * sc, v[3] * sc}, f16x2);
     f16 *p = dst + ((rt >> 1) * 64 + lane) * 8 + 4 * (rt & 1);
     *reinterpret_cast<f16x4 *>(p) = f16x4{h0[0], h0[1], h1[0], h1[1]};
-    if constexpr (LO)
-        *reinterpret_cast<f16x4 *>(p + 1024) =
-            f16x4{(f16)fmaf(v[0], sc, -(float)h0[0]), (f16)fmaf(v[1], sc, -(float)h0[1]),
-                  (f16)fmaf(v[2], sc, -(float)h1[0]), (f16)fmaf(v[3], sc, -(float)h1[1])};
+    *reinterpret_cast<f16x4 *>(p + 1024) =
+        f16x4{(f16)fmaf(v[0], sc, -(float)h0[0]), (f16)fmaf(v[1], sc, -(float)h0[1]),
+              (f16)fmaf(v[2], sc, -(float)h1[0]), (f16)fmaf(v[3], sc, -(float)h1[1])};
 }
 
 // Largest value over the four lane groups that share a column.  (The swaps'
@@ -307,14 +305,14 @@ __device__ __forceinline__ void lds_dma16_at(RsrcW r, uint32_t dst, uint32_t vof
 __device__ __forceinline__ uint32_t lds_address(char *p) { return (uint32_t)(uintptr_t)(lds_void *)p; }
 
 // What k_delta_prep leaves of a chunk and group (k and q, in PL terms each), and
-// of a chunk and head (T, the row arrays, tril(Q K^T) in PPL terms and, for the
-// gradient, (I + beta kk)^-1): the scans copy a range of the latter at once.
+// of a chunk and head (T, the row arrays, tril(Q K^T) and, for the gradient,
+// (I + beta kk)^-1): the scans copy a range of the latter at once.
 template <typename IO, int N> struct GroupImg {
     static constexpr int PL = sizeof(IO) / 2, Q = PL * kDC * N * 2, BYTES = 2 * Q;
 };
-template <typename IO, bool GRAD> struct HeadImg {
-    static constexpr int TRI = kPieces * 1024, PPL = sizeof(IO) == 4 || GRAD ? 2 : 1;
-    static constexpr int T = 0, R = 2 * TRI, P = R + kRows * kDC * 4, M = P + PPL * TRI;
+template <bool GRAD> struct HeadImg {
+    static constexpr int TRI = kPieces * 1024;
+    static constexpr int T = 0, R = 2 * TRI, P = R + kRows * kDC * 4, M = P + 2 * TRI;
     static constexpr int BYTES = M + (GRAD ? 2 * TRI : 0);
 };
 
@@ -369,7 +367,7 @@ __device__ __forceinline__ void copy_rows(const char *src, uint32_t pitch, int r
 // the 64 rows of v (and of dy) of the workgroup's columns.
 template <typename IO, int N, bool GRAD> struct FwdBuf {
     typedef GroupImg<IO, N> G;
-    typedef HeadImg<IO, GRAD> H;
+    typedef HeadImg<GRAD> H;
     static constexpr int K = 0, Q = G::Q, HEAD = H::M;
     static constexpr int T = G::BYTES + H::T, R = G::BYTES + H::R, P = G::BYTES + H::P;
     static constexpr int V = G::BYTES + HEAD;

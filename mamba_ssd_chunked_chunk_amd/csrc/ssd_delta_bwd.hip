@@ -207,7 +207,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_mid(DeltaArgs a) {
 
 template <typename IO, int N> struct RevBuf {
     typedef GroupImg<IO, N> G;
-    typedef HeadImg<IO, true> H;
+    typedef HeadImg<true> H;
     static constexpr int ROWS = H::P - H::R, INV = H::BYTES - H::M;
     static constexpr int K = 0, Q = G::Q, R = G::BYTES, M = R + ROWS, DY = M + INV;
     static __host__ __device__ int bytes(int cols) { return DY + kDC * cols * (int)sizeof(IO); }
@@ -700,7 +700,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
     typedef typename GradOp<IO>::type OT;
     typedef typename Frag8<OT>::type F;
     typedef GradBuf<IO, N> B;
-    typedef HeadImg<IO, true> H;
+    typedef HeadImg<true> H;
     constexpr bool F32 = sizeof(IO) == 4;
     constexpr int XB = N / 32, NT = N / 16, PN = 2 * GradOp<IO>::PL;  // pieces of a tile of N or Z
     __shared__ __align__(1024) char lds[B::ALL];

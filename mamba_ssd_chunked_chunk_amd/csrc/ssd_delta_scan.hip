@@ -165,7 +165,6 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
     constexpr bool F32 = sizeof(IO) == 4;
     constexpr int XB = N / 32;
     constexpr int NT = GRAD ? 2 : 1;          // inverses: T, and (I + beta kk)^-1
-    constexpr int PPL = F32 || GRAD ? 2 : 1;  // terms of tril(Q K^T)
     __shared__ PrepLds all[4];
     const int lane = threadIdx.x & 63, wave = wave_id(), g = lane >> 4, j16 = lane & 15;
     PrepLds &L = all[wave];
@@ -230,7 +229,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
         }
     }
     for (int64_t hh = gg * ratio + part * hs; hh < gg * ratio + (part + 1) * hs; ++hh) {
-        typedef HeadImg<IO, GRAD> H;
+        typedef HeadImg<GRAD> H;
         const int64_t hi = ci * a.h + hh;
         char *himg = a.himg + hi * a.hstride;
         float *rows = reinterpret_cast<float *>(himg + H::R);
@@ -328,8 +327,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_prep(DeltaArgs a, int hs) {
             for (int kb = 0; kb <= it / 2; ++kb) {
                 const Split s = split8(pq[2 * kb], pq[2 * kb + 1], pp.sc);
                 *reinterpret_cast<f16x8 *>(dst + tri_piece(it, kb) * 512) = s.hi;
-                if constexpr (PPL == 2)
-                    *reinterpret_cast<f16x8 *>(dst + (kPieces + tri_piece(it, kb)) * 512) = s.lo;
+                *reinterpret_cast<f16x8 *>(dst + (kPieces + tri_piece(it, kb)) * 512) = s.lo;
             }
             *reinterpret_cast<f32x4 *>(&L.A[it][j16 * kDP + 4 * g]) = A[tri_tile(it, it)];
         }
@@ -556,17 +554,15 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
             for (int kb = 0; kb < XB; ++kb) {
                 const f16x8 q = img_rows(Q, rt * XB + kb, lane);
                 t = mma16(q, sf[kb].hi, t);
-                if constexpr (F32) t = mma16(q, sf[kb].lo, t);
+                t = mma16(q, sf[kb].lo, t);
                 if constexpr (F32) t = mma16(img_rows(Q + IMG, rt * XB + kb, lane), sf[kb].hi, t);
             }
 #pragma unroll
             for (int tb = 0; tb <= rt / 2; ++tb) {
                 const f16x8 p = img_rows(P, tri_piece(rt, tb), lane);
                 u = mma16(p, uf[tb].hi, u);
-                if constexpr (F32) {
-                    u = mma16(p, uf[tb].lo, u);
-                    u = mma16(img_rows(P + kPieces * 512, tri_piece(rt, tb), lane), uf[tb].hi, u);
-                }
+                u = mma16(p, uf[tb].lo, u);
+                u = mma16(img_rows(P + kPieces * 512, tri_piece(rt, tb), lane), uf[tb].hi, u);
             }
             const f32x4 fr = row4(rows, kReadQ, rt, lane), fp = row4(rows, kFq, rt, lane),
                         fi = row4(rows, kFk, rt, lane);
@@ -627,11 +623,10 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
 // at the barriers; operands read from LDS a chunk ahead saved 1% of it, a wait for the
 // next chunk's copies moved to the end of this one cost 3%.
 template <typename IO> struct CoopBuf {
-    static constexpr int UL = sizeof(IO) == 4 ? 2 : 1;  // terms of u in the read-out
     static constexpr bool SHARED = sizeof(IO) == 4;  // Q S in the place of K S
     static constexpr int P = 0, Q = SHARED ? P : P + 12 * 1024, R = Q + 12 * 1024, W = R + 4 * 1024;
     static constexpr int U = W + 4 * 1024;
-    static constexpr int M = U + UL * 2 * 1024, BYTES = M + 3 * 4 * 64;
+    static constexpr int M = U + 4 * 1024, BYTES = M + 3 * 4 * 64;
 };
 
 // LDS leaves room for one workgroup a unit.  (Told so, the compiler spills nothing with
@@ -692,7 +687,7 @@ __global__ __launch_bounds__(256, sizeof(IO) == 4 ? 1 : 2) void k_delta_coop(Del
         const int len = (int)(a.l - t0 < kDC ? a.l - t0 : kDC);
 
         // all of the chunk's operands into registers
-        f16x8 kf[PL][4], qf[PL][4], kc[PL][TPW][2], tf[2][2], pf[PL][2];
+        f16x8 kf[PL][4], qf[PL][4], kc[PL][TPW][2], tf[2][2], pf[2][2];
 #pragma unroll
         for (int i = 0; i < PL; ++i)
 #pragma unroll
@@ -704,12 +699,11 @@ __global__ __launch_bounds__(256, sizeof(IO) == 4 ? 1 : 2) void k_delta_coop(Del
         for (int tb = 0; tb < 2; ++tb) {
             const int b = tb <= w >> 1 ? tb : 0;  // blocks beyond the diagonal are not used
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < 2; ++i) {
                 tf[i][tb] = img_cols(T + i * kPieces * 512, tri_piece_t(2 * b, w >> 1),
                                      tri_piece_t(2 * b + 1, w >> 1), w, lane);
-#pragma unroll
-            for (int i = 0; i < PL; ++i)
                 pf[i][tb] = img_rows(P + i * kPieces * 512, tri_piece(w, b), lane);
+            }
 #pragma unroll
             for (int i = 0; i < PL; ++i)
 #pragma unroll
@@ -747,8 +741,8 @@ __global__ __launch_bounds__(256, sizeof(IO) == 4 ? 1 : 2) void k_delta_coop(Del
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
             ks[rt] = mma16(kf[0][rt], sf.lo, ks[rt]);
+            qs[rt] = mma16(qf[0][rt], sf.lo, qs[rt]);
             if constexpr (F32) {
-                qs[rt] = mma16(qf[0][rt], sf.lo, qs[rt]);
                 ks[rt] = mma16(kf[PL - 1][rt], sf.hi, ks[rt]);
                 qs[rt] = mma16(qf[PL - 1][rt], sf.hi, qs[rt]);
             }
@@ -809,7 +803,7 @@ __global__ __launch_bounds__(256, sizeof(IO) == 4 ? 1 : 2) void k_delta_coop(Del
         for (int i = 0; i < 4; ++i) top = fmaxf(top, mxs[128 + i * 16 + j16]);
         const Pow2 pu(mostn * top), pw(mostw * top);
         put_half(wfr, W, pw.sc, w, lane);
-        put_half<F32>(ufr, n, pu.sc, w, lane);
+        put_half(ufr, n, pu.sc, w, lane);
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
             if (rt != w) qpart[(rt * 3 + (w < rt ? w : w - 1)) * 64 + lane] = qs[rt];
@@ -848,10 +842,8 @@ __global__ __launch_bounds__(256, sizeof(IO) == 4 ? 1 : 2) void k_delta_coop(Del
                 if (tb <= w >> 1) {
                     const f16x8 uh = img_rows(ufr, tb, lane);
                     y = mma16(pf[0][tb], uh, y);
-                    if constexpr (F32) {
-                        y = mma16(pf[0][tb], img_rows(ufr + 1024, tb, lane), y);
-                        y = mma16(pf[PL - 1][tb], uh, y);
-                    }
+                    y = mma16(pf[0][tb], img_rows(ufr + 1024, tb, lane), y);
+                    y = mma16(pf[1][tb], uh, y);
                 }
             const f32x4 p0 = qpart[(w * 3) * 64 + lane], p1 = qpart[(w * 3 + 1) * 64 + lane],
                         p2 = qpart[(w * 3 + 2) * 64 + lane];
