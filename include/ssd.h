@@ -739,11 +739,11 @@ size_t ssd_delta_scan_workspace_bytes(int64_t batch, int64_t seqlen, int64_t hea
  *
  * A time step beyond a limit of the clamp has no gradient, nor has the decay in
  * front of a document's first token or of a zero initial state.  batch and
- * seqlen >= 1, limits and preconditions as for ssd_delta_scan.  bf16 io: the
- * products of dq and dk take one fp16 term (11 bits) of each operand; everything
- * that the other outputs and the adjoint recurrence need keeps 22 bits.  A
- * decay's gradient is the sum of the terms that cross its token, those inside a
- * chunk in fp64, so that nothing larger cancels in it.
+ * seqlen >= 1, limits, preconditions and precision as for ssd_delta_scan; the
+ * products of dq and dk take their operands in fp32 with fp32 io, under one power
+ * of two for 16 value columns of a chunk with bf16 io.  A decay's gradient is the
+ * sum of the terms that cross its token, those inside a chunk in fp64, so that
+ * nothing larger cancels in it.
  */
 int32_t ssd_delta_scan_bwd(const void *q, const void *k, const void *v, const void *dt,
                            const float *A, const float *dt_bias, int32_t dt_softplus,

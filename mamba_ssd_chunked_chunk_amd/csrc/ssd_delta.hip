@@ -167,8 +167,8 @@ struct DeltaWs {
         rows2 = add(ch * kRowsGrad * kDC * 4);
         nimg = add(ch * kDC * p * 4);  // two fp16 terms or one fp32
         zimg = add(ch * kDC * p * 4);
-        simg = add(ch * n * p * el);
-        dsimg = add(ch * n * p * el);
+        simg = add(ch * n * p * 4);
+        dsimg = add(ch * n * p * 4);
         yimg = add(ch * kDC * p * el);
         scales = add(ch * (p / 16) * kScales * 4);
         g0 = add(ch * kDC * p * 4);

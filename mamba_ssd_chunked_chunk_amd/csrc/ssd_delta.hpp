@@ -36,9 +36,7 @@
 // significant bits (fewer below 2^-16 of the largest, of which an element is off by
 // 2^-38 at most), and multiplied as hi hi + hi lo + lo hi; q and k of bf16 io are
 // exact in one.
-// With bf16 io the products of dQ and dK take hi terms alone, 2^-11 at most of each
-// operand, an eighth of the result's own rounding.  States, sums,
-// decays and the triangular inverse are fp32, the log decays' sums fp64, and so
+// States, sums, decays and the triangular inverse are fp32, the log decays' sums fp64, and so
 // are the sums of C_ij, of which a row's and a column's share all but a few terms.
 #pragma once
 
@@ -86,8 +84,8 @@ enum RowOfGrad {
     kStep    // d_t
 };
 
-// k_delta_grad's operands: with bf16 io fp16 terms under one power of two for 16
-// value columns of a chunk (of N and Z both terms, in two planes), fp32 otherwise.
+// k_delta_grad's operands: with bf16 io two fp16 terms, in two planes, under one power
+// of two for 16 value columns of a chunk (of dY, which bf16 holds, one), fp32 otherwise.
 template <typename IO> struct GradOp { typedef f16 type; static constexpr int PL = 2; };
 template <> struct GradOp<float> { typedef float type; static constexpr int PL = 1; };
 enum ScaleOf { kScS, kScD, kScN, kScZ, kScY, kScales = 8 };  // the powers' inverses

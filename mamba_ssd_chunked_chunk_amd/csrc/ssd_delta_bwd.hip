@@ -19,9 +19,8 @@
 // keys of them in registers, transposed ([key][token]), so that the masked
 // products dY U^T and Z N^T are the next product's operands as they stand; the
 // heads that share q and k are walked in order by one workgroup.  With bf16 io
-// its operands are fp16 terms: one of each for dq and dk (2^-12 at most, a
-// sixteenth of their own rounding), two of N and Z where the decays' gradient
-// needs them.  125 us for the same call, 0.45 GB (93 us of a copy).
+// its operands are two fp16 terms, and a step of its products takes both of 16 value
+// columns for the two halves of an instruction's contraction.  125 us for the same call, 0.45 GB (93 us of a copy).
 #include "ssd_delta.hpp"
 
 #include <math.h>
@@ -44,8 +43,9 @@ __device__ __forceinline__ void put_operand(typename GradOp<IO>::type *dst, cons
         *reinterpret_cast<f32x4 *>(dst + f * 512 + lane * 8 + 4) = b;
     }
 }
-// Elements of N or Z of 16 columns of a chunk.
+// Elements of N or Z, and of a state, of 16 columns of a chunk.
 template <typename IO> constexpr int kOperandN = GradOp<IO>::PL * 2 * 512;
+template <typename IO, int N> constexpr int kOperandS = GradOp<IO>::PL * (N / 32) * 512;
 
 // The transposed product of a lower triangle (its hi and lo images at M) with
 // the rows in f: row tile jt.
@@ -108,11 +108,11 @@ __global__ __launch_bounds__(256, 2) void k_delta_mid(DeltaArgs a) {
     for (int x = 0; x < NT; ++x) mx = abs_max(mx, S[x]);
     const Pow2 ps(tile_max(mx));
     Split sf[XB];
-    OT *simg = static_cast<OT *>(a.simg) + (hi * cts + ct) * (XB * 512);
+    OT *simg = static_cast<OT *>(a.simg) + (hi * cts + ct) * kOperandS<IO, N>;
 #pragma unroll
     for (int kb = 0; kb < XB; ++kb) {
         sf[kb] = split8(S[2 * kb], S[2 * kb + 1], ps.sc);
-        put_operand<IO, 1>(simg, S[2 * kb], S[2 * kb + 1], sf[kb], kb, 0, lane);
+        put_operand<IO, 2>(simg, S[2 * kb], S[2 * kb + 1], sf[kb], kb, XB * 512, lane);
     }
     f32x4 R[4];
     f32x4 *g0 = reinterpret_cast<f32x4 *>(a.g0 + (hi * cts + ct) * (16 * kDC)) + lane;
@@ -369,7 +369,7 @@ __global__ __launch_bounds__(256, 1) void k_delta_rev(DeltaArgs a) {
         if (c == a.nc - 1 || NB == 1)
             vm_wait<0>();
         else
-            vm_wait<16 + (F32 ? 2 * XB : XB) + 4 + 12>();
+            vm_wait<16 + 2 * XB + 4 + 12>();
         in.wait();
         lds_barrier();
         const int64_t hi = (bb * a.nc + c) * a.h + hh, t0 = c * kDC, at = hi * cts + ct;
@@ -406,11 +406,11 @@ __global__ __launch_bounds__(256, 1) void k_delta_rev(DeltaArgs a) {
         for (int x = 0; x < NT; ++x) mx = abs_max(mx, dS[x]);
         const Pow2 ps(tile_max(mx));
         Split sf[XB];
-        OT *ds = static_cast<OT *>(a.dsimg) + at * (XB * 512);
+        OT *ds = static_cast<OT *>(a.dsimg) + at * kOperandS<IO, N>;
 #pragma unroll
         for (int kb = 0; kb < XB; ++kb) {
             sf[kb] = split8(dS[2 * kb], dS[2 * kb + 1], ps.sc);
-            put_operand<IO, 1>(ds, dS[2 * kb], dS[2 * kb + 1], sf[kb], kb, 0, lane);
+            put_operand<IO, 2>(ds, dS[2 * kb], dS[2 * kb + 1], sf[kb], kb, XB * 512, lane);
         }
         // scale e^G dY
         f32x4 G[4];
@@ -659,35 +659,26 @@ __device__ __forceinline__ double sum16(double v) {
     return dpp_addd<0x121>(v);
 }
 
-// Two tiles' operands under powers of two of their own, given by their inverses:
-// what undoes the larger product's, and what a lane's elements of the second
-// operand take to come under it (lane groups 0, 1 hold the first tile's columns,
-// 2, 3 the second's).  In exponents, as the inverses' product can leave fp32's
-// range where the result does not; kDown keeps the products small, so that what
-// undoes them is not too small a number for results near the end of the range.
-// A tile that is far below the other one is lost in it, at 2^-26 of its largest.
-struct Pair {
-    static constexpr int kDown = 12;
-    int exp;
-    f16 part;
-    __device__ Pair(const float *s, int x, int y, bool two, int g) {
+// What undoes the powers of two of two operands, given by their inverses: two factors,
+// as the inverses' product can leave fp32's range where the result does not.
+struct Undo {
+    float a, b;
+    __device__ Undo(const float *s, int x, int y) {
         const auto of = [&](int i) { return (int)(__builtin_bit_cast(uint32_t, s[i]) >> 23); };
-        const int e0 = of(x) + of(y), e1 = two ? of(kScales + x) + of(kScales + y) : e0;
-        const int top = max(e0, e1);
-        exp = top - 254 + kDown;
-        part = (f16)ldexpf(1.f, max((g < 2 ? e0 : e1) - top - kDown, -30));
+        const int e = of(x) + of(y) - 254, h = e / 2;
+        a = ldexpf(1.f, h), b = ldexpf(1.f, e - h);
     }
-    __device__ float undo(float v) const { return ldexpf(v, exp); }
 };
 
-// One stage of k_delta_grad in LDS: 32 value columns of a head (states in front
-// and adjoint states behind as [column][key] images, N, Z and dY as
-// [column][token]), or its group's k and q with the head's row arrays.
+// One stage of k_delta_grad in LDS: 16 value columns of a head in two terms, or 32 in
+// fp32 (states in front and adjoint states behind as [column][key] images, N, Z and dY
+// as [column][token]), or its group's k and q with the head's row arrays.
 template <typename IO, int N> struct GradBuf {
     typedef GradOp<IO> O;
-    static constexpr int E = (int)sizeof(typename O::type), TOK = kDC * 32 * E;
-    static constexpr int S = 0, D = S + N * 32 * E, NV = D + N * 32 * E, Z = NV + O::PL * TOK;
-    static constexpr int DY = Z + O::PL * TOK, SC = DY + TOK, END1 = SC + (E == 2 ? 1024 : 0);
+    static constexpr int E = (int)sizeof(typename O::type), TILES = 2 / O::PL;
+    static constexpr int ST = N * 32 * E, TOK = kDC * 32 * E, TOKY = TOK / O::PL;
+    static constexpr int S = 0, D = S + ST, NV = D + ST, Z = NV + TOK;
+    static constexpr int DY = Z + TOK, SC = DY + TOKY, END1 = SC + (E == 2 ? 1024 : 0);
     static constexpr int K = 0, Q = K + kDC * N * E, R = Q + kDC * N * E;
     static constexpr int R2 = R + kRows * kDC * 4, END2 = R2 + kRowsGrad * kDC * 4;
     static constexpr int BYTES = END1 > END2 ? END1 : END2;
@@ -702,7 +693,9 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
     typedef GradBuf<IO, N> B;
     typedef HeadImg<true> H;
     constexpr bool F32 = sizeof(IO) == 4;
-    constexpr int XB = N / 32, NT = N / 16, PN = 2 * GradOp<IO>::PL;  // pieces of a tile of N or Z
+    constexpr int XB = N / 32, NT = N / 16;
+    // an operand's second half in LDS: its low terms (of dY the same ones), or the next tile
+    constexpr int NEXT = 2, NEXTY = F32 ? 2 : 0;
     __shared__ __align__(1024) char lds[B::ALL];
 
     const int w = wave_id(), own = threadIdx.x & 63;
@@ -713,26 +706,26 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
     const int len = (int)(a.l - t0 < kDC ? a.l - t0 : kDC);
     const int cts = a.p >> 4;
     const uint32_t base = lds_address(lds);
-    const int slices = (a.p + 31) >> 5;
+    const int slices = (cts + B::TILES - 1) / B::TILES;
     const int64_t kq = ((bb * a.l + t0) * a.g + gg) * N;
 
     int half = 0;  // the buffer to be read next
     const auto fetch = [&](int64_t hi, int st, int lane) {
         const uint32_t buf = base + half * B::BYTES;
-        const int tiles = cts - 2 * st < 2 ? 1 : 2;
-        const int64_t at = hi * cts + 2 * st;
-        const int whole = tiles * XB * 512 * B::E, tok = tiles * 1024 * B::E;
-        copy_lds(static_cast<const OT *>(a.simg) + at * (XB * 512), whole, N * 32 * B::E, buf + B::S, w,
+        const int tiles = F32 && cts - 2 * st > 1 ? 2 : 1;
+        const int64_t at = hi * cts + B::TILES * st;
+        const int whole = tiles * kOperandS<IO, N> * B::E, tok = tiles * kOperandN<IO> * B::E;
+        copy_lds(static_cast<const OT *>(a.simg) + at * kOperandS<IO, N>, whole, B::ST, buf + B::S, w, 4,
+                 lane);
+        copy_lds(static_cast<const OT *>(a.dsimg) + at * kOperandS<IO, N>, whole, B::ST, buf + B::D, w,
                  4, lane);
-        copy_lds(static_cast<const OT *>(a.dsimg) + at * (XB * 512), whole, N * 32 * B::E, buf + B::D, w,
+        copy_lds(static_cast<const OT *>(a.nimg) + at * kOperandN<IO>, tok, B::TOK, buf + B::NV, w, 4,
+                 lane);
+        copy_lds(static_cast<const OT *>(a.zimg) + at * kOperandN<IO>, tok, B::TOK, buf + B::Z, w, 4,
+                 lane);
+        copy_lds(static_cast<const OT *>(a.yimg) + at * 1024, tiles * 1024 * B::E, B::TOKY, buf + B::DY, w,
                  4, lane);
-        copy_lds(static_cast<const OT *>(a.nimg) + at * kOperandN<IO>, tok * B::O::PL,
-                 B::TOK * B::O::PL, buf + B::NV, w, 4, lane);
-        copy_lds(static_cast<const OT *>(a.zimg) + at * kOperandN<IO>, tok * B::O::PL,
-                 B::TOK * B::O::PL, buf + B::Z, w, 4, lane);
-        copy_lds(static_cast<const OT *>(a.yimg) + at * 1024, tok, B::TOK, buf + B::DY, w, 4, lane);
-        if constexpr (!F32)
-            copy_lds(a.scales + at * kScales, tiles * kScales * 4, 1024, buf + B::SC, w, 4, lane);
+        if constexpr (!F32) copy_lds(a.scales + at * kScales, kScales * 4, 1024, buf + B::SC, w, 4, lane);
         if (st == 0) {
             copy_lds(a.rows2 + hi * (kRowsGrad * kDC), kRowsGrad * kDC * 4, kRowsGrad * kDC * 4,
                      base + B::R0, w, 4, lane);
@@ -798,55 +791,53 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
             const OT *NV = reinterpret_cast<const OT *>(buf + B::NV);
             const OT *ZV = reinterpret_cast<const OT *>(buf + B::Z);
             const OT *DY = reinterpret_cast<const OT *>(buf + B::DY);
-            const F dy = cols_nat(DY, w >> 1, 2, w, lane), nv = cols_nat(NV, w >> 1, PN, w, lane),
-                    zv = cols_nat(ZV, w >> 1, PN, w, lane);
+            // this wave's tokens as second operands: dY; N and Z (`hl`: their two terms);
+            // for products with an operand of two terms hi hi and lo hi, then hi lo
+            const F dy = cols_nat(DY, w >> 1, NEXTY, w, lane), nhl = cols_nat(NV, w >> 1, NEXT, w, lane);
+            F nhh = nhl, zhh = cols_nat(ZV, w >> 1, F32 ? NEXT : 0, w, lane), nl = nhl, zl = zhh;
+            if constexpr (!F32) {
+                const f16 first = g < 2 ? (f16)1.f : (f16)0.f;
+                nhh = cols_nat(NV, w >> 1, 0, w, lane);
+                nl = cols_nat(NV, NEXT + (w >> 1), 0, w, lane) * first;
+                zl = cols_nat(ZV, NEXT + (w >> 1), 0, w, lane) * first;
+            }
+            const auto both = [&](const F &x, const F &hh, const F &l) {
+                f32x4 t = mma8(x, hh, zero4());
+                if constexpr (!F32) t = mma8(x, l, t);
+                return t;
+            };
             const float *sc = reinterpret_cast<const float *>(buf + B::SC);
-            const bool two = cts - 2 * st > 1;
             const float *rows = reinterpret_cast<const float *>(lds + B::R0) + 16 * w + (lane & 15);
             const float be = reinterpret_cast<const float *>(lds + B::BETA)[16 * w + (lane & 15)];
             float gq = a.scale * rows[kRead * kDC], gz = -rows[kRead * kDC] * be,
-                  gn = rows[kWrite * kDC] * be;
-            F dys = dy, zvs = zv, nvd = nv;
+                  gn = rows[kWrite * kDC] * be, ny = 1.f, nz = 1.f;
+            float uq = 1.f, uz = 1.f, un = 1.f, uy = 1.f, uzn = 1.f;
             if constexpr (!F32) {
-                const Pair sy(sc, kScS, kScY, two, g), sz(sc, kScS, kScZ, two, g),
-                    dn(sc, kScD, kScN, two, g);
-                dys = dy * sy.part, zvs = zv * sz.part, nvd = nv * dn.part;
-                gq = sy.undo(gq), gz = sz.undo(gz), gn = dn.undo(gn);
+                const Undo q(sc, kScS, kScY), z(sc, kScS, kScZ), n(sc, kScD, kScN), y(sc, kScN, kScY),
+                    o(sc, kScN, kScZ);
+                gq *= q.a, gz *= z.a, gn *= n.a, ny = y.a, nz = o.a;
+                uq = q.b, uz = z.b, un = n.b, uy = y.b, uzn = o.b;
             }
-            F dyn = dy, zvn = zv, zvl = zv, nvy = nv, nvz = nv;
-            float ny = 1.f, nz = 1.f;
-            if constexpr (!F32) {
-                const Pair py(sc, kScN, kScY, two, g), pz(sc, kScN, kScZ, two, g);
-                dyn = dy * py.part, zvn = zv * pz.part, nvy = nv * py.part, nvz = nv * pz.part;
-                zvl = cols_nat(ZV, 2 + (w >> 1), PN, w, lane) * pz.part;
-                ny = py.undo(1.f), nz = pz.undo(1.f);
-            }
+            // to += f (u t); fp32 operands have no u
+            const auto add = [&](f32x4 &to, float f, float u, const f32x4 &t) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) to[r] = fmaf(f, F32 ? t[r] : u * t[r], to[r]);
+            };
 #pragma unroll
             for (int rt = 0; rt < 4; ++rt) {
-                if (rt <= w) {  // the decays' gradient needs these: both terms
-                    const F n = cols_nat(NV, rt >> 1, PN, rt, lane);
-                    f32x4 t = mma8(n, dyn, zero4()), u = mma8(n, zvn, zero4());
-                    if constexpr (!F32) {
-                        const F l = cols_nat(NV, 2 + (rt >> 1), PN, rt, lane);
-                        t = mma8(l, dyn, t);
-                        u = mma8(n, zvl, u);
-                        u = mma8(l, zvn, u);
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        X[rt][r] = fmaf(ny, t[r], X[rt][r]), Y[rt][r] = fmaf(nz, u[r], Y[rt][r]);
+                if (rt <= w) {
+                    const F n = cols_nat(NV, rt >> 1, NEXT, rt, lane);
+                    add(X[rt], ny, uy, mma8(n, dy, zero4()));
+                    add(Y[rt], nz, uzn, both(n, zhh, zl));
                 }
                 if (rt >= w) {
-                    const F d = cols_nat(DY, rt >> 1, 2, rt, lane);
-                    const F z = cols_nat(ZV, rt >> 1, PN, rt, lane);
-                    const f32x4 t = mma8(d, nvy, zero4()), u = mma8(z, nvz, zero4());
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        if (rt == w)
-                            Xd[r] = fmaf(ny, t[r], Xd[r]), Yd[r] = fmaf(nz, u[r], Yd[r]);
-                        else
-                            X[rt][r] = fmaf(ny, t[r], X[rt][r]), Y[rt][r] = fmaf(nz, u[r], Y[rt][r]);
-                    }
+                    const F d = cols_nat(DY, rt >> 1, NEXTY, rt, lane);
+                    const F z = cols_nat(ZV, rt >> 1, NEXT, rt, lane);
+                    const f32x4 t = mma8(d, nhl, zero4()), u = both(z, nhh, nl);
+                    if (rt == w)
+                        add(Xd, ny, uy, t), add(Yd, nz, uzn, u);
+                    else
+                        add(X[rt], ny, uy, t), add(Y[rt], nz, uzn, u);
                 }
                 sched_fence();
             }
@@ -854,13 +845,9 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
             for (int x = 0; x < NT; ++x) {
                 const F s = cols_nat(S, x >> 1, XB, x, lane);
                 const F d = cols_nat(D, x >> 1, XB, x, lane);
-                const f32x4 t = mma8(s, dys, zero4()), u = mma8(s, zvs, zero4()),
-                            v = mma8(d, nvd, zero4());
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    dQ[x][r] = fmaf(gq, t[r], dQ[x][r]);
-                    dK[x][r] = fmaf(gz, u[r], fmaf(gn, v[r], dK[x][r]));
-                }
+                add(dQ[x], gq, uq, mma8(s, dy, zero4()));
+                add(dK[x], gz, uz, both(s, zhh, zl));
+                add(dK[x], gn, un, both(d, nhh, nl));
                 if (x & 1) sched_fence();
             }
         }
@@ -945,7 +932,7 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
             if (g == 0) cells[m] = sum;
         }
         // the masked products as operands, each token's under a power of two
-        const auto put = [&](F (&f)[2], const f32x4 (&v)[4]) {
+        const auto put = [&](F (&f)[2], F (&l)[2], const f32x4 (&v)[4]) {
             if constexpr (F32) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) f[e >> 3][e & 7] = v[e >> 2][e & 3];
@@ -956,10 +943,9 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
                 for (int rt = 0; rt < 4; ++rt) mx = abs_max(mx, v[rt]);
                 const Pow2 p(col_max(mx));
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                    const f16x2 h = __builtin_convertvector(
-                        f32x2{v[e >> 2][e & 3] * p.sc, v[e >> 2][(e & 3) + 1] * p.sc}, f16x2);
-                    f[e >> 3][e & 7] = h[0], f[e >> 3][(e & 7) + 1] = h[1];
+                for (int tb = 0; tb < 2; ++tb) {
+                    const Split s = split8(v[2 * tb], v[2 * tb + 1], p.sc);
+                    f[tb] = s.hi, l[tb] = s.lo;
                 }
                 return p.inv;
             }
@@ -970,8 +956,15 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
             else
                 return img_cols(img, 2 * tb * XB + (x >> 1), (2 * tb + 1) * XB + (x >> 1), x, lane);
         };
+        // a block of 32 tokens' share of such a product
+        const auto masked = [&](const OT *img, int tb, int x, const F (&f)[2], const F (&l)[2], f32x4 t) {
+            const F k = kcols(img, tb, x);
+            t = mma8(k, f[tb], t);
+            if constexpr (!F32) t = mma8(k, l[tb], t);
+            return t;
+        };
         f32x4 v[4];
-        F f[2];
+        F f[2], l[2];
         // dQ += K^T (rows j <= m of dY U^T)
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
@@ -981,11 +974,11 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
                 v[rt][r] = rt <= w && 16 * rt + 4 * g + r <= m
                                ? a.scale * bj[r] * fk[r] * Dj[rt][r] * X[rt][r] : 0.f;
         }
-        float inv = put(f, v);
+        float inv = put(f, l, v);
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-            f32x4 t = mma8(kcols(K, 0, x), f[0], zero4());
-            if (w >> 1) t = mma8(kcols(K, 1, x), f[1], t);
+            f32x4 t = masked(K, 0, x, f, l, zero4());
+            if (w >> 1) t = masked(K, 1, x, f, l, t);
 #pragma unroll
             for (int r = 0; r < 4; ++r) dQ[x][r] = fmaf(inv, t[r], dQ[x][r]);
             if (x & 1) sched_fence();
@@ -1000,11 +993,11 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
                 v[rt][r] = rt >= w && 16 * rt + 4 * g + r >= m ? bm * fqr[r] * Dj[rt][r] * xv : 0.f;
             }
         }
-        inv = put(f, v);
+        inv = put(f, l, v);
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-            f32x4 t = mma8(kcols(Q, 1, x), f[1], zero4());
-            if (!(w >> 1)) t = mma8(kcols(Q, 0, x), f[0], t);
+            f32x4 t = masked(Q, 1, x, f, l, zero4());
+            if (!(w >> 1)) t = masked(Q, 0, x, f, l, t);
 #pragma unroll
             for (int r = 0; r < 4; ++r) dK[x][r] = fmaf(inv, t[r], dK[x][r]);
             if (x & 1) sched_fence();
@@ -1020,11 +1013,11 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
                 v[rt][r] = j == m ? 0.f : -bj[r] * bm * fk[r] * Dj[rt][r] * yv;
             }
         }
-        inv = put(f, v);
+        inv = put(f, l, v);
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
-            f32x4 t = mma8(kcols(K, 0, x), f[0], zero4());
-            t = mma8(kcols(K, 1, x), f[1], t);
+            f32x4 t = masked(K, 0, x, f, l, zero4());
+            t = masked(K, 1, x, f, l, t);
 #pragma unroll
             for (int r = 0; r < 4; ++r) dK[x][r] = fmaf(inv, t[r], dK[x][r]);
             if (x & 1) sched_fence();

@@ -48,3 +48,20 @@ def test_outputs_of_an_overwritten_state(io, p, h):
         r = rel(x, o)
         log("overwritten", what, io, p, h, "%.2e" % r)
         assert r <= bound, (what, r)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("p,h", [(16, 4), (64, 4), (32, 264), (128, 40)])
+def test_gradients_of_an_overwritten_state(io, p, h):
+    import mamba_ssd_chunked_chunk_amd as ssd
+    c = _case(p + h + 1, io, p, h)
+    args, e = [c[k] for k in NAMES], as64(c)
+    got = ssd.delta_scan_bwd(*args, c["dy"], dt_bias=c["dt_bias"], normalize=True,
+                             initial_state=c["init"], d_final=c["d_final"])
+    ref = oracle.grad(*(e[k] for k in NAMES), dy=e["dy"], dt_bias=e["dt_bias"], normalize=True,
+                      init=e["init"], d_final=e["d_final"])
+    for name in ("dq", "dk", "dbeta"):
+        r = rel(got[name][:, 32:], ref[name][:, 32:])
+        log("overwritten", name, io, p, h, "%.2e" % r)
+        # dk has two such sums over the chunk's tokens, of u and of the state's read
+        assert r <= (2 if name == "dk" else 1) * LIMIT[io], (name, r)
