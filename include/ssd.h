@@ -620,8 +620,9 @@ int32_t ssd_gated_step(float *state, const void *x, const void *gates, const flo
  * y may be x or residual, and sum may be x or residual, y and sum different
  * buffers.  Tensors aligned to their element; 16 bytes move at once where dim
  * and every tensor allow it.  dim up to 2^24, rows * dim up to 2^40, else
- * SSD_ERR_UNSUPPORTED.  The mean and the squares about it are fp32 sums, each
- * output is rounded once.  Deterministic.  rows == 0 is valid.
+ * SSD_ERR_UNSUPPORTED.  The mean and the squares about it are fp32 sums, and what
+ * the mean's rounding leaves of a row far from zero is taken off too; each output
+ * is rounded once.  Deterministic.  rows == 0 is valid.
  */
 int32_t ssd_layer_norm(const void *x, const void *residual, const float *weight,
                        const float *bias, float eps, void *y, void *sum, float *stats,

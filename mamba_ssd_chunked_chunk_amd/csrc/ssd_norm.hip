@@ -66,6 +66,12 @@ template <int G> __device__ __forceinline__ float row_sum(float v, float *red, i
     return v;
 }
 
+// 1 / deviation from the mean square about a value that the mean is u above.
+__device__ __forceinline__ float norm_rstd(float sq, float u, float eps) {
+    const float v = fmaf(-u, u, sq);
+    return 1.f / sqrtf((v < 0.f ? 0.f : v) + eps);  // NaN stays NaN
+}
+
 template <typename IO, int V, int G, int E>
 __global__ __launch_bounds__(kNormThreads) void k_layer_norm(NormArgs a) {
     typedef NVec<IO, V> Vec;
@@ -110,8 +116,11 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm(NormArgs a) {
                 t += s[k * V + e];
             }
         }
-        // divided, not times 1 / dim: rows of one value then have it as their mean
-        const float mean = row_sum<G>(t, red, half) / (float)a.dim;
+        // The mean of a row far from zero is off by roundings of it that can be more than
+        // the row deviates by: what is left of the mean after it is taken off (the
+        // difference is then exact, or nearly so) is taken off too, and from the squares.
+        const float mean = row_sum<G>(t, red, half) * inv;
+        float u = 0.f;
         t = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -119,11 +128,13 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm(NormArgs a) {
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     s[k * V + e] -= mean;
+                    u += s[k * V + e];
                     t = fmaf(s[k * V + e], s[k * V + e], t);
                 }
             }
-        const float rstd = 1.f / sqrtf(row_sum<G>(t, red, half) * inv + a.eps);
-        if (a.stats && lane == 0) a.stats[row] = mean, a.stats[a.rows + row] = rstd;
+        u = row_sum<G>(u, red, half) * inv;
+        const float rstd = norm_rstd(row_sum<G>(t, red, half) * inv, u, a.eps);
+        if (a.stats && lane == 0) a.stats[row] = mean + u, a.stats[a.rows + row] = rstd;
         Vec *py = reinterpret_cast<Vec *>(static_cast<IO *>(a.y) + row * a.dim);
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -137,7 +148,7 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm(NormArgs a) {
                 Vec o;
 #pragma unroll
                 for (int e = 0; e < V; ++e)
-                    o.e[e] = (IO)fmaf(s[k * V + e] * rstd, w.e[e], b.e[e]);
+                    o.e[e] = (IO)fmaf((s[k * V + e] - u) * rstd, w.e[e], b.e[e]);
                 py[c] = o;
             }
     }
@@ -285,16 +296,19 @@ __global__ __launch_bounds__(kNormThreads) void k_layer_norm_wide(NormArgs a) {
         };
         float t = 0.f;
         for (int64_t c = threadIdx.x; c < a.dim; c += kNormThreads) t += value(c, true);
-        const float mean = row_sum<kNormThreads>(t, red, half) / (float)a.dim;
+        const float mean = row_sum<kNormThreads>(t, red, half) * inv;
+        float u = 0.f;
         t = 0.f;
         for (int64_t c = threadIdx.x; c < a.dim; c += kNormThreads) {
             const float d = value(c, false) - mean;
+            u += d;
             t = fmaf(d, d, t);
         }
-        const float rstd = 1.f / sqrtf(row_sum<kNormThreads>(t, red, half) * inv + a.eps);
-        if (a.stats && threadIdx.x == 0) a.stats[row] = mean, a.stats[a.rows + row] = rstd;
+        u = row_sum<kNormThreads>(u, red, half) * inv;
+        const float rstd = norm_rstd(row_sum<kNormThreads>(t, red, half) * inv, u, a.eps);
+        if (a.stats && threadIdx.x == 0) a.stats[row] = mean + u, a.stats[a.rows + row] = rstd;
         for (int64_t c = threadIdx.x; c < a.dim; c += kNormThreads)
-            py[c] = (IO)fmaf((value(c, false) - mean) * rstd, a.weight ? a.weight[c] : 1.f,
+            py[c] = (IO)fmaf((value(c, false) - mean - u) * rstd, a.weight ? a.weight[c] : 1.f,
                              a.bias ? a.bias[c] : 0.f);
     }
 }
