@@ -3,16 +3,15 @@
 //
 // k_delta_mid, all chunks in parallel: N = v - P^T k of 16 value columns per
 // wave, and what else does not need the adjoint state.  Bound by memory: 4 x 2048
-// tokens of 16 heads of 128 x 128 move 0.63 GB in 120 us.
+// tokens of 16 heads of 128 x 128 move 0.69 GB in 130 us.
 //
 // k_delta_rev, chunk after chunk from the end: the adjoint state of 16 value
 // columns in a wave's registers, as in the forward pass; leaves Z, dV, the
 // adjoint state behind every chunk, and per token the terms of the decays'
 // gradient that reach into the chunk from outside.  What k_delta_mid left, and
 // the state in front, come into registers a chunk ahead.  Bound by memory and the
-// chain of one wave, 1900 instructions a chunk, about alike: 186 us and 0.64 GB
-// for the same call, 5.8 us a chunk (341 us where it formed those values itself
-// and loaded the state at its use).
+// chain of one wave, 1900 instructions a chunk, about alike: 205 us and 0.71 GB
+// for the same call, 6.4 us a chunk.
 //
 // k_delta_grad, all chunks in parallel: dq and dk, which contract over the value
 // columns, and the decays' terms inside the chunk.  A wave owns 16 tokens, all
@@ -20,7 +19,8 @@
 // products dY U^T and Z N^T are the next product's operands as they stand; the
 // heads that share q and k are walked in order by one workgroup.  With bf16 io
 // its operands are two fp16 terms, and a step of its products takes both of 16 value
-// columns for the two halves of an instruction's contraction.  125 us for the same call, 0.45 GB (93 us of a copy).
+// columns for the two halves of an instruction's contraction.  178 us for the same
+// call, 0.59 GB (121 us of a copy).
 #include "ssd_delta.hpp"
 
 #include <math.h>
@@ -1118,7 +1118,7 @@ template <typename IO, int N> hipError_t bwd_n(const DeltaArgs &a, hipStream_t s
     const int nw = a.p >= 64 ? 4 : a.p / 16;
     const int64_t walks = a.b * a.h * (a.p / (16 * nw));
     // fewer columns to a workgroup where the walk would leave compute units idle
-    // (4 x 16 heads of 128 columns, 32 columns: 209 us with twice the copies, 341 with 64)
+    // (4 x 16 heads of 128 columns, 32 columns: 205 us with twice the copies, 225 with 64)
     int rw = nw;
     while (rw > 1 && a.b * a.h * (a.p / (16 * rw)) < device_cus()) rw >>= 1;
     const int one = RevBuf<IO, N>::bytes(16 * rw);

@@ -7,9 +7,9 @@
 // column), the others by distance from it, T_ij = -T_ii sum_k (kk beta)_ik T_kj,
 // on fp32 matrix instructions whose results feed the next product from registers.
 // Bound by memory, of which its outputs are most (with keys of 128 and bf16 io 32 KB
-// a chunk and group, 20 KB a chunk and head): 65536 tokens of 64 heads, eight to a
-// group, 390 us for 1.9 GB; 8 x 2048 tokens of 24 heads with a group each 106 us
-// for 0.53 GB; a large copy would take 386 and 108.
+// a chunk and group, 26 KB a chunk and head): 65536 tokens of 64 heads, eight to a
+// group, 456 us for 2.3 GB; 8 x 2048 tokens of 24 heads with a group each 115 us
+// for 0.57 GB; a large copy would take 472 and 117.
 //
 // k_delta_fwd, chunk after chunk: a wave owns 16 value columns of one head's
 // state in registers (an accumulator tile per 16 keys).  Columns do not meet
@@ -18,9 +18,9 @@
 // without LDS or another wave; LDS holds only what all columns share (the
 // images of the next chunk arrive in the other buffer meanwhile).  Bound by
 // memory where there are columns enough (8 x 2048 tokens of 24 heads of 128 x 64,
-// states kept, 143 us for 0.63 GB), by the chain of one wave, 1100 instructions a
-// chunk, where there are fewer: 16 x 1000 tokens of 16 heads of 128 x 128 94 us,
-// 0.35 GB.
+// states kept, 160 us for 0.67 GB), by the chain of one wave, 1200 instructions a
+// chunk, where there are fewer: 16 x 1000 tokens of 16 heads of 128 x 128 106 us,
+// 0.37 GB.
 #include "ssd_delta.hpp"
 
 #include <math.h>
@@ -609,19 +609,19 @@ __global__ __launch_bounds__(512) void k_delta_fwd(DeltaArgs a) {
 // chain of chunks is then all there is to wait for, and a wave alone issues one
 // instruction in four cycles).  A wave owns a quarter of the keys' rows of the
 // state and the rows of one of the four row tiles; what it has of K S and Q S
-// goes to the rows' owners, and R, u and e^{G_C - G} u, split, to everyone, through
+// goes to the rows' owners, and R, N and e^{G_C - G} u, split, to everyone, through
 // LDS, with a barrier after each.  There are three stretches between barriers (the end
 // of a chunk and the start of the next one are the same), and every place is written in
 // one and read in the one after it, so that no two of them may be the same bytes: a wave
 // still reads Q S while another writes the next chunk's K S.  With bf16 io Q S has a
-// place of its own (8192 tokens of 32 heads of 64 x 64: 290 us against 306 with a fourth
-// barrier); with fp32 io it takes that of K S, which a fourth barrier in front of its
-// next use allows: LDS then holds two buffers with keys of 64 (361 against 372 us), and
-// with keys of 128 the barrier is the faster one too (446 against 507).  The powers of
-// two that the waves have to share come from bounds that they exchange with the values
-// before.  65536 tokens of 64 heads of 128 x 64: 2.36 us a chunk, of them a third waits
-// at the barriers; operands read from LDS a chunk ahead saved 1% of it, a wait for the
-// next chunk's copies moved to the end of this one cost 3%.
+// place of its own (65536 tokens of 64 heads of 128 x 64: 3.03 ms against 3.10 with a
+// fourth barrier); with fp32 io it takes that of K S, which a fourth barrier in front of
+// its next use allows: LDS then holds two buffers with keys of 64 (8192 tokens of 32
+// heads of 64 x 64: 365 against 371 us), and with keys of 128 the barrier is the faster
+// one too (447 against 452).  The powers of two that the waves have to share come from
+// bounds that they exchange with the values before.  65536 tokens of 64 heads of 128 x
+// 64: 2.51 us a chunk; operands read from LDS a chunk ahead saved 1% of it, a wait for
+// the next chunk's copies moved to the end of this one cost 3%.
 template <typename IO> struct CoopBuf {
     static constexpr bool SHARED = sizeof(IO) == 4;  // Q S in the place of K S
     static constexpr int P = 0, Q = SHARED ? P : P + 12 * 1024, R = Q + 12 * 1024, W = R + 4 * 1024;
@@ -899,9 +899,11 @@ template <typename IO, int N> hipError_t run_coop(const DeltaArgs &a, hipStream_
 
 template <typename IO, int N> hipError_t fwd_n(const DeltaArgs &a, hipStream_t s) {
     // Four waves to 16 columns where each such group can have a compute unit of
-    // its own (64 heads of 64 columns: 2420 against 3886 us for 65536 tokens);
-    // with more of them the chains hide each other's waits (8 x 24 heads of 64
-    // columns: 143 against 238 us).
+    // its own; with more of them the chains hide each other's waits.  4096 tokens,
+    // keys of 128, heads of 64 columns, 256 compute units: 128, 256, 320 and 768
+    // groups take 197, 221, 399 and 661 us by four waves each, 285, 305, 333 and 427
+    // by one (fp32 256, 339, 593, 964 and 404, 492, 538, 680; with other widths of
+    // keys and columns the two cross between 256 and 320 groups too).
     return a.b * a.h * (a.p / 16) <= device_cus() ? run_coop<IO, N>(a, s) : run_fwd<IO, N>(a, s);
 }
 

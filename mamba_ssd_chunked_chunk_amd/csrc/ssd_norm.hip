@@ -8,8 +8,8 @@
 //
 // Bound by memory.  A row is read once and stays in the registers of the G
 // lanes that own it (E elements each) until its outputs are written, so both
-// passes over it (mean, then the squares about it, which do not cancel) cost no
-// traffic.  G is 8 or 32 lanes for short rows, a wave up to 4096 elements, a
+// passes over it (mean, then the squares about it, which do not cancel, and what is
+// left of the mean) cost no traffic.  G is 8 or 32 lanes for short rows, a wave up to 4096 elements, a
 // workgroup up to 16384; longer rows are read again for each pass.  All sums
 // are fp32.  16384 rows of 2560 with residual and statistics, bf16: 66 us, 5.1 TB/s;
 // their gradient 88 us, 3.8 TB/s, at two workgroups a compute unit (its registers
@@ -478,17 +478,19 @@ bool norm_sizes(int64_t rows, int64_t dim) {
     return dim <= ((int64_t)1 << 24) && rows <= ((int64_t)1 << 40) / dim;
 }
 
-// Workgroups of the gradient: as many as run at once (a lane's 16 columns and
-// fewer leave room for four on a compute unit, up to 64 for two), so that none
-// waits for a place: 16384 rows of 2560 take 93 us in 512 workgroups, 114 in 768
-// or 1024.  Fewer rows than that go one to each of G lanes, though a row of
-// partial sums is then written for few of them: 1999 rows of 771 take 20 us so,
-// 27 us with four rows to each.
+// Workgroups of the gradient: four on a compute unit where a lane has 16 columns or
+// fewer, else two.  Two do run at once up to 48 columns a lane with bf16 io and 40 with
+// fp32, up to 32 where elements move one at a time; above that, and where 256 lanes
+// have a row whose elements do, the registers of the column sums leave room for one.
+// 16384 rows of 2560 take 93 us in 512 workgroups, 114 in 768 or 1024.  Fewer rows than
+// that go one to each of G lanes, though a row of partial sums is then written for few
+// of them: 1999 rows of 771 take 20 us so, 27 us with four rows to each.
 int norm_blocks(int64_t rows, int64_t dim) {
     const NormShape n(dim);
     const int64_t slots = n.e <= 16 ? kMostBlocks : kMostBlocks / 2;
     const int64_t b = (rows + n.rows_per_block() - 1) / n.rows_per_block();
-    // beyond 16 MB of partial sums fewer workgroups run
+    // beyond 16 MB of partial sums (rows wider than 4096) fewer workgroups run: 198 of
+    // them, less than one a compute unit, for rows of 10576
     const int64_t most = ((int64_t)1 << 24) / (8 * dim);
     const int64_t cap = most < 1 ? 1 : most > slots ? slots : most;
     return (int)(b < cap ? b : cap);
