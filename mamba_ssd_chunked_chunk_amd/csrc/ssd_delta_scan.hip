@@ -119,7 +119,8 @@ __device__ __forceinline__ void use_tile(const DeltaArgs &a, const RawTile<IO, N
             }
         }
     }
-    float factor = back, norm = 1.f;
+    // a row of zeros (one behind the last token too) takes no part in bounds of rows
+    float factor = mx == 0.f ? 0.f : back, norm = 1.f;
     if (a.norm) {
 #pragma unroll
         for (int kb = 0; kb < XB; ++kb)

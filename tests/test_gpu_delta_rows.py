@@ -92,3 +92,26 @@ def test_rows_of_every_size_without_eps(io, size):
     for k in ("q", "k"):
         c[k] = c[k] * (1 / size if size > 1 else size ** 0.5)
     _check(c, io, "sizes to %g without eps" % size, norm_eps=0.0)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("l", [200, 65, 64 + 63])
+def test_small_keys_in_a_chunk_that_ends_early(io, l):
+    """Keys of 1e-8 that are not normalised (beta 1e16 times as large), in a last chunk
+    of few tokens: the rows that are not there do not count as keys of one, nor do
+    rows of zeros among the others."""
+    import mamba_ssd_chunked_chunk_amd as ssd
+    for h, g in ((4, 2), (136, 4)):
+        c = delta_case(l, 2, l, h, g, 64, 32, io, init=True)
+        c["k"], c["beta"], c["init"] = c["k"] * 1e-8, c["beta"] * 1e16, c["init"] * 1e8
+        c["k"][:, l - 1] = 0
+        args, e = [c[k] for k in NAMES], as64(c)
+        y, fin = ssd.delta_scan(*args, dt_bias=c["dt_bias"], initial_state=c["init"],
+                                return_final_state=True)
+        ref = oracle.scan(*(e[k] for k in NAMES), dt_bias=e["dt_bias"], init=e["init"])
+        for t in range(l - l % 64, l):
+            r = rel(y[:, t], ref["y"][:, t])
+            assert r <= BOUNDS[io]["y"], (h, t, r)
+        r = rel(fin, ref["final"])
+        log("small keys", io, l, h, "%.2e" % r)
+        assert r <= BOUNDS[io]["state"], (h, r)
