@@ -1002,7 +1002,8 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
             for (int r = 0; r < 4; ++r) dK[x][r] = fmaf(inv, t[r], dK[x][r]);
             if (x & 1) sched_fence();
         }
-        // dK -= K^T (dV U^T and its transpose)
+        // dK -= K^T (dV U^T and its transpose), this token's beta last: beta's square can
+        // leave fp32's range where keys are small or large
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
             const f32x4 bj = row4(rows, kBeta, rt, lane), fk = of_k(rt);
@@ -1010,10 +1011,10 @@ __global__ __launch_bounds__(256, 2) void k_delta_grad(DeltaArgs a) {
             for (int r = 0; r < 4; ++r) {
                 const int j = 16 * rt + 4 * g + r;
                 const float yv = rt == w && j > m ? Yd[r] : Y[rt][r];
-                v[rt][r] = j == m ? 0.f : -bj[r] * bm * fk[r] * Dj[rt][r] * yv;
+                v[rt][r] = j == m ? 0.f : -bj[r] * fk[r] * Dj[rt][r] * yv;
             }
         }
-        inv = put(f, l, v);
+        inv = put(f, l, v) * bm;
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
             f32x4 t = masked(K, 0, x, f, l, zero4());

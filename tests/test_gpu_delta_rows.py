@@ -115,3 +115,23 @@ def test_small_keys_in_a_chunk_that_ends_early(io, l):
         r = rel(fin, ref["final"])
         log("small keys", io, l, h, "%.2e" % r)
         assert r <= BOUNDS[io]["state"], (h, r)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [1e-10, 1.0, 1e12])
+def test_gradient_of_keys_of_every_size(io, size):
+    """Keys that are not normalised, some of them zeros, with a beta of the inverse
+    square of their size: beta's square (1e40, 1e-48) need not be in fp32's range."""
+    import mamba_ssd_chunked_chunk_amd as ssd
+    for h, g in ((4, 2), (136, 4)):
+        c = delta_case(9, 1, 150, h, g, 64, 32, io, init=True)
+        c["k"], c["beta"] = c["k"] * size, c["beta"] / size / size
+        c["init"] = c["init"] / size
+        c["k"][:, 3::7] = 0
+        args, e = [c[k] for k in NAMES], as64(c)
+        got = ssd.delta_scan_bwd(*args, c["dy"], dt_bias=c["dt_bias"], initial_state=c["init"])
+        ref = oracle.grad(*(e[k] for k in NAMES), dy=e["dy"], dt_bias=e["dt_bias"], init=e["init"])
+        for name, o in ref.items():
+            r = rel(got[name], o)
+            log("keys of", size, name, io, h, "%.2e" % r)
+            assert r <= BOUNDS[io][name], (name, h, r)
