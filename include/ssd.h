@@ -702,8 +702,9 @@ size_t ssd_layer_norm_bwd_workspace_bytes(int64_t rows, int64_t dim);
  *
  * Precision: operands of the matrix products formed inside the call are split
  * into two fp16 terms with a power of two per row or column (one for the 64 x 64
- * inverse), 22 significant bits, fewer below 2^-16 of the largest of them, of which
- * an element is off by 2^-38 at most (q and k of bf16 io are exact).  States, sums,
+ * inverse), 22 significant bits, fewer below 2^-16 of the largest of them (calls of
+ * few columns: of a bound of it), of which an element is off by 2^-38 at most (q and
+ * k of bf16 io are exact).  States, sums,
  * decays and the triangular inverse are fp32 (log decays are summed in fp64);
  * y is rounded to nearest even.  Deterministic.  seqlen == 0 gives final_state =
  * init_state or zeros.

@@ -34,10 +34,10 @@
 // of q, k and tril(Q K^T), per column of a state or of a chunk's rows, one for an
 // inverse, so that the largest magnitude fits), written as two fp16 terms hi + lo, 22
 // significant bits (fewer below 2^-16 of the largest, of which an element is off by
-// 2^-38 at most), and multiplied as hi hi + hi lo + lo hi; q and k of bf16 io are
-// exact in one.
-// States, sums, decays and the triangular inverse are fp32, the log decays' sums fp64, and so
-// are the sums of C_ij, of which a row's and a column's share all but a few terms.
+// 2^-38 at most; the four-wave walk takes bounds for the largest of R, N and the
+// update), and multiplied as hi hi + hi lo + lo hi; q and k of bf16 io are exact in
+// one.  States, sums, decays and the triangular inverse are fp32, the log decays' sums
+// fp64, and so are the sums of C_ij, of which a row's and a column's share all but a few terms.
 #pragma once
 
 #include <hip/hip_runtime.h>
